@@ -1,5 +1,6 @@
-"""The measured cases of the training-side operators: embedding lookup with scaling, its gradient by
-sorted ids, and the orthogonalisation of a weight matrix's update by Newton-Schulz products.
+"""The measured cases of the learned side of the path: embedding lookup with scaling, its gradient by
+sorted ids, cross attention of queries to a mini-batch's states and its backward pass, and the
+orthogonalisation of a weight matrix's update by Newton-Schulz products.
 
 `run` computes them with the library's calls where `own` is true and in plain torch operations
 where it is not; `exact` gives the same results in 64 bits.
@@ -22,9 +23,6 @@ PAD = 0   # the padding id of the cases with padding: its rows are zero and get 
 
 def listed():
     return [
-        # the seeds of one mini-batch read their learned node vectors: one short launch
-        dict(name="lookup seeds", op="lookup", n=1024, rows=233_000, d=602, table="f32", out="f32",
-             ids="frontier", pad=False),
         # text tokens of a batch of sequences with padding at their ends, scaled by sqrt(d)
         dict(name="lookup tokens", op="lookup", n=16_384, rows=50_257, d=768, table="bf16",
              out="bf16", ids="zipf", pad=True),
@@ -41,15 +39,20 @@ def listed():
         # repeat; only the touched rows of a large table come back
         dict(name="grad edges", op="grad", n=901_120, rows=2_450_000, d=100, dout="f32", out="f32",
              form="rows", ids="edges", nodes=400_000, pad=False),
-        # odd width, so that rows are not aligned, and a ragged number of tokens
-        dict(name="grad odd", op="grad", n=33_333, rows=100_003, d=515, dout="bf16", out="bf16",
-             form="dense", ids="zipf", pad=True),
+        # one token of each of the group's sequences attends to its mini-batch's first-hop states
+        dict(name="attend one token", op="attend", batch=16, lq=1, lk=16_384, heads=16, kv=4, d=128,
+             dtype="bf16", train=False, empty=False),
+        # prompts of a few tokens over short neighbourhoods, one of them without a neighbour
+        dict(name="attend short odd", op="attend", batch=12, lq=19, lk=333, heads=8, kv=2, d=80,
+             dtype="f32", train=False, empty=True),
+        # a training step over ragged states, grouped heads
+        dict(name="attend train", op="attend", batch=4, lq=1024, lk=2600, heads=16, kv=4, d=128,
+             dtype="bf16", train=True, empty=False),
+        # the same in single precision, one sequence without states
+        dict(name="attend train f32", op="attend", batch=3, lq=201, lk=1025, heads=8, kv=8, d=64,
+             dtype="f32", train=True, empty=True),
         # the weights [2 d, d_out] of one mean-aggregating layer
         dict(name="ortho layer", op="ortho", batch=1, m=256, n=256, dtype="f32"),
-        # many equal small matrices at once (the projections of the heads of a model)
-        dict(name="ortho heads", op="ortho", batch=24, m=128, n=768, dtype="bf16"),
-        # one wide projection of a mid-sized model
-        dict(name="ortho wide", op="ortho", batch=1, m=1024, n=4096, dtype="bf16"),
         # tall, odd in both directions, single precision
         dict(name="ortho tall odd", op="ortho", batch=2, m=2571, n=1030, dtype="f32"),
         # the largest square weights
@@ -63,7 +66,18 @@ def _spread(rng, lo, hi):
 
 
 def draw(rng):
-    op = rng.choice(["lookup", "grad", "ortho"])
+    op = rng.choice(["lookup", "grad", "attend", "ortho"])
+    if op == "attend":
+        train = rng.random() < 0.5
+        while True:
+            heads = rng.choice([4, 8, 16])
+            case = dict(op=op, batch=_spread(rng, 1, 16), lq=_spread(rng, 1, 1024),
+                        lk=_spread(rng, 1, 16_384), heads=heads,
+                        kv=heads // rng.choice([1, 2, 4]), d=rng.choice([32, 40, 64, 80, 128]),
+                        dtype=rng.choice(["f32", "bf16"]), train=train, empty=rng.random() < 0.3)
+            case["empty"] = case["empty"] and case["batch"] > 1
+            if case["batch"] * heads * case["lq"] * case["lk"] <= (50e6 if train else 150e6):
+                return case
     if op == "ortho":
         dtype = rng.choice(["f32", "bf16"])
         m, n = _spread(rng, 64, 4096), _spread(rng, 64, 4096)
@@ -126,10 +140,47 @@ def _scale(case):
     return float(torch.tensor(math.sqrt(case["d"]), dtype=torch.float32))
 
 
+def _lengths(case):
+    """Queries and states of each sequence, from the case alone: between a quarter and all of lk."""
+    lq, lk = [], []
+    for b in range(case["batch"]):
+        part = (0.618034 * (b + 1)) % 1.0 if b else 1.0
+        lk.append(max(1, round(case["lk"] * (0.25 + 0.75 * part))))
+        lq.append(max(1, round(case["lq"] * (0.5 + 0.5 * (0.7548777 * b % 1.0)))) if b else case["lq"])
+    if case["empty"]:
+        lk[case["batch"] // 2] = 0
+    return lq, lk
+
+
+def _indptr(lengths):
+    return torch.tensor([0] + lengths, device="cuda").cumsum(0).to(torch.int32)
+
+
 def prepare(case, seed):
     gen = torch.Generator(device="cuda")
     gen.manual_seed(seed)
     s = dict(case=case)
+    if case["op"] == "attend":
+        lq, lk = _lengths(case)
+        h, kv, d, dtype = case["heads"], case["kv"], case["d"], DTYPES[case["dtype"]]
+
+        def rows(n, heads):
+            return torch.randn(n, heads, d, generator=gen, device="cuda", dtype=dtype)
+
+        s["q"], s["k"], s["v"] = rows(sum(lq), h), rows(sum(lk), kv), rows(sum(lk), kv)
+        s["q_indptr"], s["k_indptr"] = _indptr(lq), _indptr(lk)
+        s["max_q"], s["max_k"], s["scale"] = max(lq), max(lk), d ** -0.5
+        s["out"] = torch.empty_like(s["q"])
+        s["lse"] = torch.empty(sum(lq), h, device="cuda")
+        if case["train"]:
+            s["dout"] = rows(sum(lq), h)
+            s["dq"], s["dk"], s["dv"] = (torch.empty_like(s[x]) for x in "qkv")
+        if own:
+            import graph_mini_pipeline_amd as gm
+            s["ws"] = torch.empty(gm.gnn_cross_attention_workspace_size(
+                case["batch"], sum(lq), sum(lk), s["max_q"], s["max_k"], h, kv, d, dtype,
+                backward=case["train"]), dtype=torch.uint8, device="cuda")
+        return s
     if case["op"] == "ortho":
         b, m, n = case["batch"], case["m"], case["n"]
         k = max(1, min(m, n) // 8)
@@ -169,7 +220,7 @@ def prepare(case, seed):
 
 
 def run(s):
-    return {"lookup": _lookup, "grad": _grad, "ortho": _ortho}[s["case"]["op"]](s)
+    return {"lookup": _lookup, "grad": _grad, "attend": _attend, "ortho": _ortho}[s["case"]["op"]](s)
 
 
 def _lookup(s):
@@ -211,6 +262,64 @@ def _grad(s):
     return nodes, count, (acc * s["scale"]).to(s["grad"].dtype)
 
 
+def _padded(indptr, most, x, heads):
+    """Rows of a packed x as [batch, heads, most, d] in 32 bits, and which of them there are."""
+    at = indptr[:-1, None].long() + torch.arange(most, device="cuda")
+    there = at < indptr[1:, None]
+    if x.shape[0] == 0:
+        return x.new_zeros(at.shape[0], heads, most, x.shape[2], dtype=torch.float32), there
+    y = torch.where(there[:, :, None, None], x[at.clamp(max=x.shape[0] - 1)].float(), 0.0)
+    return y.transpose(1, 2).contiguous(), there
+
+
+def _attend(s):
+    case = s["case"]
+    if own:
+        import graph_mini_pipeline_amd as gm
+        gm.gnn_cross_attention(s["q"], s["k"], s["v"], s["q_indptr"], s["k_indptr"], s["max_q"],
+                               s["max_k"], s["scale"], s["out"], s["ws"], lse=s["lse"])
+        if not case["train"]:
+            return s["out"], s["lse"]
+        gm.gnn_cross_attention_backward(s["q"], s["k"], s["v"], s["q_indptr"], s["k_indptr"],
+                                        s["max_q"], s["max_k"], s["scale"], s["out"], s["lse"],
+                                        s["dout"], s["dq"], s["dk"], s["dv"], s["ws"])
+        return s["out"], s["lse"], s["dq"], s["dk"], s["dv"]
+    b, h, kv, d = case["batch"], case["heads"], case["kv"], case["d"]
+    lq, lk, dtype = s["max_q"], s["max_k"], s["q"].dtype
+
+    def shared(x):      # [b, h, lq, d] with the heads that share states in one matrix
+        return x.reshape(b * kv, h // kv * lq, d)
+
+    def times(x, y):    # batched x @ y^T
+        return x @ y.transpose(1, 2).contiguous()
+
+    q, there_q = _padded(s["q_indptr"], lq, s["q"], h)
+    k, there_k = _padded(s["k_indptr"], lk, s["k"], kv)
+    v, _ = _padded(s["k_indptr"], lk, s["v"], kv)
+    q, k, v = shared(q), k.reshape(b * kv, lk, d), v.reshape(b * kv, lk, d)
+    live = there_k[:, None, None, :].expand(b, kv, 1, lk).reshape(b * kv, 1, lk)
+    score = torch.where(live, times(q, k) * s["scale"], -math.inf)
+    top = score.amax(2, keepdim=True)
+    p = torch.exp(score - torch.where(top == -math.inf, 0.0, top))
+    total = p.sum(2, keepdim=True)
+    lse = torch.where(top == -math.inf, -math.inf, top + torch.log(total))
+    p = p / torch.where(total == 0, 1.0, total)
+    out = p @ v
+
+    def packed(x, there, heads, most):
+        return x.reshape(b, heads, most, -1).transpose(1, 2)[there]
+
+    answer = (packed(out, there_q, h, lq).to(dtype), packed(lse, there_q, h, lq)[:, :, 0])
+    if not case["train"]:
+        return answer
+    g = shared(_padded(s["q_indptr"], lq, s["dout"], h)[0])
+    dv = p.transpose(1, 2).contiguous() @ g
+    ds = p * (times(g, v) - (g * out).sum(2, keepdim=True)) * s["scale"]
+    dq, dk = ds @ k, ds.transpose(1, 2).contiguous() @ q
+    return answer + (packed(dq, there_q, h, lq).to(dtype), packed(dk, there_k, kv, lk).to(dtype),
+                     packed(dv, there_k, kv, lk).to(dtype))
+
+
 def _ortho(s):
     if own:
         import graph_mini_pipeline_amd as gm
@@ -246,6 +355,14 @@ def _distinct(case):
 
 def work(case):
     size = {"f32": 4, "bf16": 2}
+    if case["op"] == "attend":
+        lq, lk = _lengths(case)
+        h, d, z = case["heads"], case["d"], size[case["dtype"]]
+        pairs = sum(x * y for x, y in zip(lq, lk)) * h * d
+        rows_q, rows_k = sum(lq) * h * d * z, sum(lk) * case["kv"] * d * z
+        if case["train"]:       # seven products of every query with every state
+            return dict(bytes=4 * rows_q + 4 * rows_k + sum(lq) * h * 4, flops=14 * pairs)
+        return dict(bytes=2 * rows_q + 2 * rows_k + sum(lq) * h * 4, flops=4 * pairs)
     if case["op"] == "ortho":
         s, l = sorted((case["m"], case["n"]))
         # of the two symmetric products one triangle is needed, with its diagonal
@@ -268,6 +385,8 @@ def exact(case, seed):
     s = prepare(case, seed)
     if case["op"] == "ortho":
         return _exact_ortho(s["g"].double())
+    if case["op"] == "attend":
+        return _exact_attend(s)
     ids, scale = s["ids"].long(), torch.tensor(s["scale"], dtype=torch.float64, device="cuda")
     if case["op"] == "lookup":
         out = torch.zeros(case["n"], case["d"], dtype=torch.float64, device="cuda")
@@ -289,6 +408,35 @@ def exact(case, seed):
     out = torch.zeros(case["rows"], case["d"], dtype=torch.float64, device="cuda")
     out[nodes] = sums
     return out
+
+
+def _exact_attend(s):
+    """Sequence by sequence and head by head."""
+    case = s["case"]
+    group, scale = case["heads"] // case["kv"], s["scale"]
+    names = ("out", "lse", "dq", "dk", "dv") if case["train"] else ("out", "lse")
+    r = {x: torch.zeros(s[x].shape, dtype=torch.float64, device="cuda") for x in names}
+    q_at, k_at = s["q_indptr"].tolist(), s["k_indptr"].tolist()
+    for b in range(case["batch"]):
+        i, j = slice(q_at[b], q_at[b + 1]), slice(k_at[b], k_at[b + 1])
+        for h in range(case["heads"]):
+            q, k, v = s["q"][i, h].double(), s["k"][j, h // group].double(), s["v"][j, h // group].double()
+            if k.shape[0] == 0:
+                r["lse"][i, h] = -math.inf
+                continue
+            score = scale * torch.mm(q, k.t())
+            lse = torch.logsumexp(score, 1)
+            p = torch.exp(score - lse[:, None])
+            r["out"][i, h], r["lse"][i, h] = torch.mm(p, v), lse
+            if not case["train"]:
+                continue
+            g = s["dout"][i, h].double()
+            r["dv"][j, h // group] += torch.mm(p.t(), g)
+            dp = torch.mm(g, v.t())
+            ds = scale * p * (dp - (p * dp).sum(1, keepdim=True))
+            r["dq"][i, h] = torch.mm(ds, k)
+            r["dk"][j, h // group] += torch.mm(ds.t(), q)
+    return tuple(r[x] for x in names)
 
 
 def _exact_ortho(g):
