@@ -29,6 +29,8 @@ __all__ = [
     "gnn_feature_store_destroy", "gnn_gather_features", "gnn_mean_aggregate", "gnn_sage_layer",
     "gnn_sage_update", "gnn_minibatch", "gnn_unique_relabel_noalloc", "AdjacencyCache", "gnn_adjacency_cache_create",
     "gnn_host_mapped_pointer",
+    "gnn_embedding_lookup", "gnn_embedding_grad", "gnn_embedding_grad_rows",
+    "gnn_embedding_grad_workspace_size",
     "gnn_read_device_status", "gnn_timer_create", "gnn_timer_destroy", "gnn_timer_reset",
     "gnn_timer_elapsed", "gnn_copy_probe", "gnn_copy_probe_host", "gnn_hash_probe", "lib",
 ]
@@ -629,6 +631,107 @@ def gnn_minibatch(graph: DeviceGraph, fs: FeatureStore, seeds: torch.Tensor,
                              _stream(stream), timer.handle if timer else None)
     _ok(st, "gnn_minibatch")
     return st
+
+
+_TYPES = {torch.float32: _abi.GNN_F32, torch.bfloat16: _abi.GNN_BF16}
+
+
+def _type(dtype, name: str) -> int:
+    t = _TYPES.get(dtype)
+    if t is None:
+        raise TypeError(f"{name}: expected float32 or bfloat16, got {dtype}")
+    return t
+
+
+def _need_rows(t: torch.Tensor, name: str) -> int:
+    """Checks a device matrix of float32 or bfloat16 whose rows are contiguous; its element type."""
+    kind = _type(t.dtype, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or \
+            (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name}: must be a matrix with contiguous rows that do not overlap")
+    return kind
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Elements from one row of a matrix to the next."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def gnn_embedding_lookup(table: torch.Tensor, ids: torch.Tensor, scale: float, out: torch.Tensor,
+                         pad_id: int = -1, d_n: Optional[torch.Tensor] = None,
+                         d_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out[i] = scale * table[ids[i]], a zero row where ids[i] == pad_id.  table: [num_rows, d],
+    out: [>= len(ids), d], float32 or bfloat16 each."""
+    _need(ids, torch.int32, "ids")
+    tt, ot = _need_rows(table, "table"), _need_rows(out, "out")
+    n, d = ids.numel(), table.shape[1]
+    if out.shape[0] < n or out.shape[1] != d:
+        raise ValueError("out: [>= len(ids), d]")
+    if d_n is not None:
+        _need(d_n, torch.int64, "d_n")
+    if d_status is not None:
+        _need(d_status, torch.int32, "d_status")
+    _ok(lib().gnn_embedding_lookup(table.data_ptr(), tt, table.shape[0], d, _ld(table),
+                                   ids.data_ptr(), _ptr(d_n), n, scale, pad_id, out.data_ptr(), ot,
+                                   _ld(out), _ptr(d_status), _stream(stream)),
+        "gnn_embedding_lookup")
+
+
+def gnn_embedding_grad_workspace_size(n: int, num_rows: int, d: int) -> int:
+    b = ctypes.c_size_t(0)
+    _ok(lib().gnn_embedding_grad_workspace_size(n, num_rows, d, ctypes.byref(b)),
+        "gnn_embedding_grad_workspace_size")
+    return int(b.value)
+
+
+def _need_grad(ids, dout, grad, d_n, d_status, ws):
+    _need(ids, torch.int32, "ids")
+    dt, gt = _need_rows(dout, "dout"), _need_rows(grad, "grad")
+    if dout.shape[0] < ids.numel() or grad.shape[1] != dout.shape[1]:
+        raise ValueError("dout: [>= len(ids), d]; grad: [*, d]")
+    if d_n is not None:
+        _need(d_n, torch.int64, "d_n")
+    if d_status is not None:
+        _need(d_status, torch.int32, "d_status")
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws: must be a contiguous device tensor")
+    return dt, gt
+
+
+def gnn_embedding_grad(ids: torch.Tensor, dout: torch.Tensor, scale: float, grad: torch.Tensor,
+                       ws: torch.Tensor, pad_id: int = -1, accumulate: bool = False,
+                       d_n: Optional[torch.Tensor] = None,
+                       d_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """grad[t] = scale * sum of dout[i] over ids[i] == t (accumulate: added to grad's rows), for the
+    whole table grad [num_rows, d]."""
+    dt, gt = _need_grad(ids, dout, grad, d_n, d_status, ws)
+    _ok(lib().gnn_embedding_grad(ids.data_ptr(), _ptr(d_n), ids.numel(), dout.data_ptr(), dt,
+                                 _ld(dout), scale, pad_id, grad.shape[0], grad.shape[1],
+                                 grad.data_ptr(), gt, _ld(grad), 1 if accumulate else 0,
+                                 _ptr(d_status), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                 _stream(stream)), "gnn_embedding_grad")
+
+
+def gnn_embedding_grad_rows(ids: torch.Tensor, dout: torch.Tensor, scale: float, num_rows: int,
+                            uniq: torch.Tensor, d_n_uniq: torch.Tensor, grad: torch.Tensor,
+                            ws: torch.Tensor, pad_id: int = -1,
+                            d_n: Optional[torch.Tensor] = None,
+                            d_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The gradient rows of the distinct ids only: uniq (int32, ascending), d_n_uniq (int64 [1])
+    their number, grad[p] the row of uniq[p]."""
+    dt, gt = _need_grad(ids, dout, grad, d_n, d_status, ws)
+    _need(uniq, torch.int32, "uniq")
+    _need(d_n_uniq, torch.int64, "d_n_uniq")
+    if grad.shape[0] < uniq.numel() or d_n_uniq.numel() < 1:
+        raise ValueError("grad: [>= len(uniq), d]; d_n_uniq: [1]")
+    _ok(lib().gnn_embedding_grad_rows(ids.data_ptr(), _ptr(d_n), ids.numel(), dout.data_ptr(), dt,
+                                      _ld(dout), scale, pad_id, num_rows, grad.shape[1],
+                                      uniq.data_ptr(), uniq.numel(), d_n_uniq.data_ptr(),
+                                      grad.data_ptr(), gt, _ld(grad), _ptr(d_status),
+                                      ws.data_ptr(), ws.numel() * ws.element_size(),
+                                      _stream(stream)), "gnn_embedding_grad_rows")
 
 
 def gnn_copy_probe(src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:

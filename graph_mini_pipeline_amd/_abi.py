@@ -24,6 +24,8 @@ GNN_SAMPLE_EXACT_RANK = 128
 GNN_NOALLOC_MAX_IDS = 1 << 26
 GNN_NOALLOC_SCRATCH_BYTES = (24 << 20) + (64 << 10)
 GNN_DYN_AUTO = 1
+GNN_F32 = 0
+GNN_BF16 = 1
 
 GNN_OK = 0
 GNN_ERR_INVALID_ARG = -1
@@ -33,6 +35,7 @@ GNN_ERR_HIP = -4
 GNN_ERR_UNSUPPORTED = -5
 GNN_ERR_INTERNAL = -6
 
+f32 = ctypes.c_float
 i32, i64, u32, u64, vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_void_p
 size_t = ctypes.c_size_t
 
@@ -112,6 +115,12 @@ SIGNATURES = {
                              vp, i64, vp, vp]),
     "gnn_minibatch": (i32, [P(gnn_graph), vp, vp, P(i64), i32, P(i32), i32, u64,
                             P(gnn_minibatch_out), vp, size_t, P(gnn_options), vp, vp]),
+    "gnn_embedding_lookup": (i32, [vp, i32, i64, i64, i64, vp, vp, i64, f32, i32, vp, i32, i64, vp, vp]),
+    "gnn_embedding_grad_workspace_size": (i32, [i64, i64, i64, P(size_t)]),
+    "gnn_embedding_grad": (i32, [vp, vp, i64, vp, i32, i64, f32, i32, i64, i64, vp, i32, i64, i32, vp,
+                                 vp, size_t, vp]),
+    "gnn_embedding_grad_rows": (i32, [vp, vp, i64, vp, i32, i64, f32, i32, i64, i64, vp, i64, vp, vp,
+                                      i32, i64, vp, vp, size_t, vp]),
     "gnn_read_device_status": (i32, [vp, vp, P(i32)]),
     "gnn_timer_create": (i32, [i32, P(vp)]),
     "gnn_timer_destroy": (i32, [vp]),

@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "common.hpp"
+#include "learn.hpp"
 
 using namespace gnnmb;
 
@@ -1641,6 +1642,126 @@ gnn_status gnn_minibatch(const gnn_graph *g, const gnn_feature_store *fs, const 
     if (ev) GNN_TRY_HIP(hipEventRecord(ev[2 + 2 * group], s));
     GNN_TRY(dyn_auto_refresh(fs, w.status, s));
     return finish(o, w, s);
+}
+
+// ---- embedding lookup and gradient ---------------------------------------------------------------
+
+namespace {
+bool known_type(int32_t t) { return t == GNN_F32 || t == GNN_BF16; }
+// Bounds of the kernels' grids: rows * columns, and the columns of one row.
+constexpr int64_t kEmbedMax = int64_t(1) << 40;
+constexpr int64_t kEmbedMaxCols = int64_t(1) << 24;
+
+gnn_status check_embed_sizes(int64_t n, int64_t num_rows, int64_t d) {
+    if (n < 0 || num_rows < 1 || d < 1) return GNN_ERR_INVALID_ARG;
+    if (n > kInt32Max || num_rows > kInt32Max || d > kEmbedMaxCols || n > kEmbedMax / d)
+        return GNN_ERR_UNSUPPORTED;
+    return GNN_OK;
+}
+
+gnn_status embedding_grad(EmbedGradArgs a, void *ws, size_t ws_bytes, gnn_stream stream) {
+    GNN_TRY(check_embed_sizes(a.n, a.num_rows, a.d));
+    if (!known_type(a.dout_type) || !known_type(a.out_type)) return GNN_ERR_UNSUPPORTED;
+    if (a.ld_dout < a.d || a.ld_out < a.d || a.pad_id < -1) return GNN_ERR_INVALID_ARG;
+    if (a.n > 0 && (!a.ids || !a.dout)) return GNN_ERR_INVALID_ARG;
+    if (!ws) return GNN_ERR_INVALID_ARG;
+    if (ws_bytes < embedding_grad_bytes(a.n, a.num_rows, a.d)) return GNN_ERR_CAPACITY;
+    if (fault(kFaultLaunch)) return GNN_ERR_HIP;
+    a.ws = static_cast<char *>(ws);
+    GNN_TRY_HIP(launch_embedding_grad(a, static_cast<hipStream_t>(stream)));
+    return GNN_OK;
+}
+}  // namespace
+
+gnn_status gnn_embedding_lookup(const void *table, int32_t table_type, int64_t num_rows, int64_t d,
+                                int64_t ld, const int32_t *ids, const int64_t *d_n, int64_t n,
+                                float scale, int32_t pad_id, void *out, int32_t out_type,
+                                int64_t ld_out, int32_t *d_status, gnn_stream stream) {
+    GNN_TRY(check_embed_sizes(n, num_rows, d));
+    if (!known_type(table_type) || !known_type(out_type)) return GNN_ERR_UNSUPPORTED;
+    if (ld < d || ld_out < d || pad_id < -1) return GNN_ERR_INVALID_ARG;
+    if (!table || (n > 0 && (!ids || !out))) return GNN_ERR_INVALID_ARG;
+    if (fault(kFaultLaunch)) return GNN_ERR_HIP;
+    LookupArgs a{};
+    a.table = table;
+    a.table_type = table_type;
+    a.out_type = out_type;
+    a.num_rows = num_rows;
+    a.d = d;
+    a.ld = ld;
+    a.ids = ids;
+    a.d_n = d_n;
+    a.n = n;
+    a.scale = scale;
+    a.pad_id = pad_id;
+    a.out = out;
+    a.ld_out = ld_out;
+    a.status = d_status;
+    GNN_TRY_HIP(launch_embedding_lookup(a, static_cast<hipStream_t>(stream)));
+    return GNN_OK;
+}
+
+gnn_status gnn_embedding_grad_workspace_size(int64_t n, int64_t num_rows, int64_t d,
+                                             size_t *out_bytes) {
+    if (!out_bytes) return GNN_ERR_INVALID_ARG;
+    GNN_TRY(check_embed_sizes(n, num_rows, d));
+    *out_bytes = embedding_grad_bytes(n, num_rows, d);
+    return GNN_OK;
+}
+
+gnn_status gnn_embedding_grad(const int32_t *ids, const int64_t *d_n, int64_t n, const void *dout,
+                              int32_t dout_type, int64_t ld_dout, float scale, int32_t pad_id,
+                              int64_t num_rows, int64_t d, void *grad, int32_t grad_type,
+                              int64_t ld_grad, int32_t accumulate, int32_t *d_status, void *ws,
+                              size_t ws_bytes, gnn_stream stream) {
+    if (!grad) return GNN_ERR_INVALID_ARG;
+    EmbedGradArgs a{};
+    a.ids = ids;
+    a.d_n = d_n;
+    a.n = n;
+    a.dout = dout;
+    a.dout_type = dout_type;
+    a.ld_dout = ld_dout;
+    a.scale = scale;
+    a.pad_id = pad_id;
+    a.num_rows = num_rows;
+    a.d = d;
+    a.out = grad;
+    a.out_type = grad_type;
+    a.ld_out = ld_grad;
+    a.accumulate = accumulate ? 1 : 0;
+    a.status = d_status;
+    return embedding_grad(a, ws, ws_bytes, stream);
+}
+
+gnn_status gnn_embedding_grad_rows(const int32_t *ids, const int64_t *d_n, int64_t n,
+                                   const void *dout, int32_t dout_type, int64_t ld_dout,
+                                   float scale, int32_t pad_id, int64_t num_rows, int64_t d,
+                                   int32_t *uniq, int64_t uniq_cap, int64_t *d_n_uniq, void *grad,
+                                   int32_t grad_type, int64_t ld_grad, int32_t *d_status, void *ws,
+                                   size_t ws_bytes, gnn_stream stream) {
+    if (uniq_cap < 0 || !d_n_uniq) return GNN_ERR_INVALID_ARG;
+    if (uniq_cap > 0 && (!uniq || !grad)) return GNN_ERR_INVALID_ARG;
+    EmbedGradArgs a{};
+    a.ids = ids;
+    a.d_n = d_n;
+    a.n = n;
+    a.dout = dout;
+    a.dout_type = dout_type;
+    a.ld_dout = ld_dout;
+    a.scale = scale;
+    a.pad_id = pad_id;
+    a.num_rows = num_rows;
+    a.d = d;
+    a.out = grad;
+    a.out_type = grad_type;
+    a.ld_out = ld_grad;
+    a.rows = 1;
+    a.uniq = uniq;
+    a.d_n_uniq = d_n_uniq;
+    a.row_cap = uniq_cap;
+    a.status = d_status;
+    return embedding_grad(a, ws, ws_bytes, stream);
 }
 
 gnn_status gnn_read_device_status(const void *ws, gnn_stream stream, gnn_status *out) {

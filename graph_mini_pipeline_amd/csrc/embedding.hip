@@ -1,0 +1,840 @@
+// Embedding lookup with scaling, and its gradient by sorted ids.
+//
+// Lookup: out[i, :] = scale * table[ids[i], :], one rounding to the output's type.  Memory-bound: a
+// thread holds kLookUnroll independent 16-byte row pieces in flight.
+//
+// Gradient: G[t, :] = scale * sum over the positions i with ids[i] = t of dout[i, :], for a dense
+// table or for the distinct ids only.  The (id, position) pairs are sorted by id, stably, so that
+// each id's positions follow each other in ascending order; then
+//   - the sorted list is cut into chunks of equal length, whatever the ids' frequencies, so a word
+//     that holds a tenth of all positions costs no more than any other tenth: a lane group walks
+//     one chunk, keeps one fp32 sum per column in registers, and stores it whenever the id changes.
+//     A run that lies within the chunk is final; the chunk's first and last run may go on beyond
+//     it, and their sums go to the workspace;
+//   - runs over several chunks are joined from these partial sums in chunk order.
+// No atomic touches a sum, so results do not depend on timing.
+#include "learn.hpp"
+
+namespace gnnmb {
+
+namespace {
+
+constexpr int kLookThreads = 256;
+constexpr int kLookUnroll = 4;
+
+template <typename TI, typename TO, int VE>
+__global__ __launch_bounds__(kLookThreads) void k_embedding_lookup(LookupArgs a) {
+    const int64_t n = load_count(a.d_n, a.n);
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * (kLookThreads * kLookUnroll);
+    const int64_t row0 = base / a.cpr;
+    if (row0 >= n) return;
+    const uint32_t rem = static_cast<uint32_t>(base - row0 * a.cpr);
+    const TI *table = static_cast<const TI *>(a.table);
+    typename loose<TI, VE>::type v[kLookUnroll];
+    int64_t row[kLookUnroll];
+    int64_t col[kLookUnroll];
+    bool live[kLookUnroll];
+    // Every load is made, of a row that exists, so that none waits for a branch.
+#pragma unroll
+    for (int u = 0; u < kLookUnroll; ++u) {
+        const uint32_t off = rem + u * kLookThreads + threadIdx.x;
+        const uint32_t q = fast_div(off, a.by_cpr);
+        row[u] = row0 + q;
+        // the last piece of a row ends at its end: it overlaps the one before where VE does not
+        // divide d, and both store the same values there
+        col[u] = static_cast<int64_t>(off - q * a.cpr) * VE;
+        if (col[u] > a.d - VE) col[u] = a.d - VE;
+        const int32_t id = a.ids[row[u] < n ? row[u] : n - 1];
+        const bool good = id >= 0 && id < a.num_rows;
+        live[u] = good && id != a.pad_id;
+        if (!good && row[u] < n) set_status(a.status, GNN_ERR_OUT_OF_RANGE);
+        v[u] = *reinterpret_cast<const typename loose<TI, VE>::type *>(
+            table + static_cast<int64_t>(good ? id : 0) * a.ld + col[u]);
+    }
+    TO *out = static_cast<TO *>(a.out);
+#pragma unroll
+    for (int u = 0; u < kLookUnroll; ++u)
+        if (row[u] < n) {
+            const vec<float, VE> x = __builtin_convertvector(v[u], vec<float, VE>) * a.scale;
+            store_f32<TO, VE>(out + row[u] * a.ld_out + col[u], live[u] ? x : vec<float, VE>(0.f));
+        }
+}
+
+template <typename TI, typename TO, int VE>
+hipError_t run_lookup(LookupArgs a, hipStream_t s) {
+    a.cpr = static_cast<uint32_t>((a.d + VE - 1) / VE);
+    a.by_cpr = make_fastdiv(a.cpr);
+    const int64_t per = kLookThreads * kLookUnroll;
+    const int64_t grid = (a.n * a.cpr + per - 1) / per;
+    hipLaunchKernelGGL((k_embedding_lookup<TI, TO, VE>), dim3(static_cast<unsigned>(grid)),
+                       dim3(kLookThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename TI, typename TO>
+hipError_t pick_lookup(const LookupArgs &a, hipStream_t s) {
+    // 16 bytes of the narrower type, unless rows end in a half-filled piece of 8
+    constexpr bool wide = sizeof(TI) == 2 || sizeof(TO) == 2;
+    if (wide && a.d >= 8 && (a.d % 8 == 0 || a.d % 8 > 4)) return run_lookup<TI, TO, 8>(a, s);
+    if (a.d >= 4) return run_lookup<TI, TO, 4>(a, s);
+    return run_lookup<TI, TO, 1>(a, s);
+}
+
+// ---- the sort -----------------------------------------------------------------------------------
+//
+// Least-significant-digit radix sort of (key, position) by digits of at most 8 bits, stable.  A
+// workgroup of 16 wavefronts takes a tile of 8192 keys, 8 per thread; a wavefront's keys lie next
+// to each other, 64 a round, so the order (wavefront, round, lane) is the order of the positions.
+// Lanes with the same digit find each other by one ballot per bit of the digit.  Up to one tile of
+// keys is sorted by one workgroup in LDS in one launch.  Beyond that, each digit takes two
+// launches: digit counts of every tile, then the placement, where every tile sums the counts of the
+// tiles before it (beyond kSumTiles tiles a third launch does that once for all).
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kSortRounds = 8;
+constexpr int kSortTile = kSortThreads * kSortRounds;
+constexpr int kSortBits = 8;
+constexpr int kDigits = 1 << kSortBits;
+constexpr int kSumTiles = 256;
+constexpr int64_t kChunkMin = 8;      // shortest chunk of the sums
+
+struct SortArgs {
+    const int32_t *ids;
+    const int64_t *d_n;
+    int64_t n;
+    int32_t pad_id;
+    uint32_t num_rows;      // also the key of positions without a gradient row: they sort last
+    int32_t *status;
+    const uint32_t *key_in, *pos_in;   // NULL: the first digit, read from ids
+    uint32_t *key_out, *pos_out;
+    uint32_t *hist;         // [tiles, kDigits], then (scanned) the digits' totals
+    int32_t tiles;
+    int32_t scanned;
+    int32_t shift, bits;
+    // work of other parts of the gradient that rides along
+    uint32_t *touched;      // bitmap over the table's rows: cleared by the first count, marked by
+    int64_t touched_words;  // the first placement; NULL: none
+    // run heads (one-tile sort of the rows form)
+    int32_t rows;
+    int32_t *uniq;
+    int64_t *d_n_uniq;
+    int64_t row_cap;
+    uint32_t *chunk_rank;
+    int32_t chunk;
+    int32_t passes;
+};
+
+__device__ __forceinline__ uint32_t make_key(const SortArgs &a, int64_t i, int64_t n_act) {
+    if (i >= n_act) return a.num_rows;
+    const int32_t id = a.ids[i];
+    if (id < 0 || static_cast<uint32_t>(id) >= a.num_rows) {
+        set_status(a.status, GNN_ERR_OUT_OF_RANGE);
+        return a.num_rows;
+    }
+    return id == a.pad_id ? a.num_rows : static_cast<uint32_t>(id);
+}
+
+__device__ __forceinline__ void mark_touched(const SortArgs &a, uint32_t key) {
+    if (key >= a.num_rows) return;
+    uint32_t *w = a.touched + (key >> 5);
+    const uint32_t bit = 1u << (key & 31);
+    if (!(__hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) & bit)) atomicOr(w, bit);
+}
+
+// Ranks each round's keys among the wavefront's earlier keys of the same digit; cnt (this
+// wavefront's digit counts, zero before) receives the counts.
+__device__ __forceinline__ void rank_rounds(const uint32_t (&key)[kSortRounds], int rounds,
+                                            int shift, int bits, uint32_t *cnt,
+                                            uint32_t (&rank)[kSortRounds]) {
+    const uint64_t below = (1ull << lane_id()) - 1ull;
+#pragma unroll
+    for (int j = 0; j < kSortRounds; ++j) {
+        if (j >= rounds) break;
+        const uint32_t dg = (key[j] >> shift) & ((1u << bits) - 1u);
+        uint64_t same = ~0ull;
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t m = __ballot((dg >> b) & 1u);
+            same &= ((dg >> b) & 1u) ? m : ~m;
+        }
+        const uint32_t before = cnt[dg];
+        rank[j] = before + __popcll(same & below);
+        wave_lds_sync();
+        if ((same & below) == 0) cnt[dg] = before + __popcll(same);
+        wave_lds_sync();
+    }
+}
+
+// Exclusive scan of 256 values, one per thread of the first four wavefronts; every thread of the
+// workgroup calls it (the others' v is ignored).
+__device__ __forceinline__ uint32_t scan_digits(uint32_t v, uint32_t *s4) {
+    const int w = threadIdx.x >> 6;
+    const uint32_t inc = wave_inclusive_scan(v);
+    if (w < 4 && lane_id() == 63) s4[w] = inc;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int i = 0; i < 3; ++i)
+        if (i < w) before += s4[i];
+    __syncthreads();
+    return before + inc - v;
+}
+
+__global__ __launch_bounds__(kSortThreads) void k_sort_count(SortArgs a) {
+    __shared__ uint32_t h[kDigits];
+    const int t = threadIdx.x;
+    if (t < kDigits) h[t] = 0;
+    if (a.touched != nullptr && a.key_in == nullptr)
+        for (int64_t w = static_cast<int64_t>(blockIdx.x) * kSortThreads + t; w < a.touched_words;
+             w += static_cast<int64_t>(gridDim.x) * kSortThreads)
+            a.touched[w] = 0;
+    __syncthreads();
+    const int64_t n_act = load_count(a.d_n, a.n);
+    const int64_t tile0 = static_cast<int64_t>(blockIdx.x) * kSortTile;
+#pragma unroll
+    for (int j = 0; j < kSortRounds; ++j) {
+        const int64_t i = tile0 + j * kSortThreads + t;
+        if (i >= a.n) continue;
+        const uint32_t key = a.key_in ? a.key_in[i] : make_key(a, i, n_act);
+        atomicAdd(&h[(key >> a.shift) & ((1u << a.bits) - 1u)], 1u);
+    }
+    __syncthreads();
+    if (t < kDigits) a.hist[static_cast<int64_t>(blockIdx.x) * kDigits + t] = h[t];
+}
+
+// One workgroup per digit: exclusive prefix over the tiles, in place; the total at [tiles].
+__global__ __launch_bounds__(256) void k_sort_scan(SortArgs a) {
+    __shared__ uint32_t sm[4];
+    const int dg = blockIdx.x;
+    uint32_t carry = 0;
+    for (int64_t t0 = 0; t0 < a.tiles; t0 += 256) {
+        const int64_t t = t0 + threadIdx.x;
+        const uint32_t v = t < a.tiles ? a.hist[t * kDigits + dg] : 0u;
+        uint32_t total;
+        const uint32_t ex = block_exclusive_scan<uint32_t, 256>(v, &total, sm);
+        if (t < a.tiles) a.hist[t * kDigits + dg] = carry + ex;
+        carry += total;
+    }
+    if (threadIdx.x == 0) a.hist[static_cast<int64_t>(a.tiles) * kDigits + dg] = carry;
+}
+
+__global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs a) {
+    __shared__ uint32_t cnt[kSortWaves][kDigits];
+    __shared__ uint32_t sums[2][kSortThreads / kDigits][kDigits];
+    __shared__ uint32_t base[kDigits];
+    __shared__ uint32_t s4[4];
+    const int t = threadIdx.x, w = t >> 6;
+    for (int i = t; i < kSortWaves * kDigits; i += kSortThreads) (&cnt[0][0])[i] = 0;
+    const int64_t n_act = load_count(a.d_n, a.n);
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortTile + w * (64 * kSortRounds) +
+                       lane_id();
+    uint32_t key[kSortRounds], pos[kSortRounds], rank[kSortRounds];
+#pragma unroll
+    for (int j = 0; j < kSortRounds; ++j) {
+        const int64_t i = i0 + j * 64;
+        key[j] = 0xffffffffu;        // beyond the end: ranked after every key of the last tile
+        pos[j] = 0;
+        if (i < a.n) {
+            if (a.key_in) {
+                key[j] = a.key_in[i];
+                pos[j] = a.pos_in[i];
+            } else {
+                key[j] = make_key(a, i, n_act);
+                pos[j] = static_cast<uint32_t>(i);
+                if (a.touched) mark_touched(a, key[j]);
+            }
+        }
+    }
+    // counts of the tiles before this one and of all tiles, four threads per digit
+    const int dg = t & (kDigits - 1), part = t / kDigits;
+    uint32_t before = 0, total = 0;
+    if (a.scanned) {
+        if (part == 0) {
+            before = a.hist[static_cast<int64_t>(blockIdx.x) * kDigits + dg];
+            total = a.hist[static_cast<int64_t>(a.tiles) * kDigits + dg];
+        }
+    } else {
+#pragma unroll 8
+        for (int k = part; k < a.tiles; k += kSortThreads / kDigits) {
+            const uint32_t c = a.hist[k * kDigits + dg];
+            total += c;
+            if (k < static_cast<int>(blockIdx.x)) before += c;
+        }
+    }
+    sums[0][part][dg] = before;
+    sums[1][part][dg] = total;
+    __syncthreads();
+    rank_rounds(key, kSortRounds, a.shift, a.bits, cnt[w], rank);
+    __syncthreads();
+    before = total = 0;
+    if (t < kDigits) {
+        for (int q = 0; q < kSortThreads / kDigits; ++q) {
+            before += sums[0][q][t];
+            total += sums[1][q][t];
+        }
+        uint32_t run = 0;
+        for (int q = 0; q < kSortWaves; ++q) {
+            const uint32_t c = cnt[q][t];
+            cnt[q][t] = run;
+            run += c;
+        }
+    }
+    const uint32_t ex = scan_digits(total, s4);
+    if (t < kDigits) base[t] = ex + before;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kSortRounds; ++j) {
+        if (i0 + j * 64 >= a.n) continue;
+        const uint32_t g = (key[j] >> a.shift) & ((1u << a.bits) - 1u);
+        const uint32_t to = base[g] + cnt[w][g] + rank[j];
+        a.key_out[to] = key[j];
+        a.pos_out[to] = pos[j];
+    }
+}
+
+// Writes the distinct ids among sorted positions [i0, i0 + 8 * threads), given the number of run
+// heads before i0, and the rank of the run at each chunk's start.  Returns the tile's heads.
+__device__ __forceinline__ bool is_head(uint32_t key, uint32_t prev, bool first, uint32_t rows) {
+    return key < rows && (first || key != prev);
+}
+
+__global__ __launch_bounds__(kSortThreads) void k_sort_tile(SortArgs a) {
+    __shared__ uint32_t skey[kSortTile];
+    __shared__ uint16_t spos[kSortTile];
+    __shared__ uint32_t cnt[kSortWaves][kDigits];
+    __shared__ uint32_t base[kDigits];
+    __shared__ uint32_t s4[4];
+    __shared__ uint32_t sw[kSortWaves];
+    const int t = threadIdx.x, w = t >> 6;
+    const int n = static_cast<int>(a.n);
+    const int64_t n_act = load_count(a.d_n, a.n);
+    const int rounds = (n + kSortThreads - 1) / kSortThreads;
+    const int i0 = w * 64 * rounds + lane_id();
+    if (a.touched != nullptr) {
+        for (int64_t i = t; i < a.touched_words; i += kSortThreads) a.touched[i] = 0;
+        __threadfence();
+        __syncthreads();
+    }
+    uint32_t key[kSortRounds], rank[kSortRounds];
+    uint32_t pos[kSortRounds];
+#pragma unroll
+    for (int j = 0; j < kSortRounds; ++j) {
+        key[j] = a.num_rows;        // slots beyond n: after every position of the same key
+        pos[j] = 0;
+        if (j >= rounds) continue;
+        const int i = i0 + j * 64;
+        pos[j] = static_cast<uint32_t>(i);
+        if (i < n) key[j] = make_key(a, i, n_act);
+        if (a.touched) mark_touched(a, key[j]);
+    }
+    for (int p = 0; p < a.passes; ++p) {
+        const int shift = p * a.bits;
+        for (int i = t; i < kSortWaves * kDigits; i += kSortThreads) (&cnt[0][0])[i] = 0;
+        __syncthreads();
+        rank_rounds(key, rounds, shift, a.bits, cnt[w], rank);
+        __syncthreads();
+        uint32_t total = 0;
+        if (t < kDigits)
+            for (int q = 0; q < kSortWaves; ++q) {
+                const uint32_t c = cnt[q][t];
+                cnt[q][t] = total;
+                total += c;
+            }
+        const uint32_t ex = scan_digits(total, s4);
+        if (t < kDigits) base[t] = ex;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kSortRounds; ++j) {
+            if (j >= rounds) continue;
+            const uint32_t g = (key[j] >> shift) & ((1u << a.bits) - 1u);
+            const uint32_t to = base[g] + cnt[w][g] + rank[j];
+            skey[to] = key[j];
+            spos[to] = static_cast<uint16_t>(pos[j]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kSortRounds; ++j) {
+            if (j >= rounds) continue;
+            key[j] = skey[i0 + j * 64];
+            pos[j] = spos[i0 + j * 64];
+        }
+    }
+    // the last pass left the sorted list in LDS too
+#pragma unroll
+    for (int j = 0; j < kSortRounds; ++j) {
+        const int i = i0 + j * 64;
+        if (j >= rounds || i >= n) continue;
+        a.key_out[i] = key[j];
+        a.pos_out[i] = pos[j];
+    }
+    if (!a.rows) return;
+    uint32_t carry = 0;
+    for (int r0 = 0; r0 < n; r0 += kSortThreads) {
+        const int i = r0 + t;
+        const uint32_t k = i < n ? skey[i] : a.num_rows;
+        const uint32_t head = is_head(k, i > 0 ? skey[i < n ? i - 1 : 0] : 0u, i == 0, a.num_rows);
+        uint32_t total;
+        const uint32_t at = carry + block_exclusive_scan<uint32_t, kSortThreads>(head, &total, sw);
+        if (head && at < a.row_cap) a.uniq[at] = static_cast<int32_t>(k);
+        if (i < n && i % a.chunk == 0) a.chunk_rank[i / a.chunk] = at + head - 1u;
+        carry += total;
+    }
+    if (t == 0) {
+        *a.d_n_uniq = carry;
+        if (carry > a.row_cap) set_status(a.status, GNN_ERR_CAPACITY);
+    }
+}
+
+// The rows form beyond one tile: run heads of every tile, then the distinct ids.
+struct HeadArgs {
+    const uint32_t *key;
+    int64_t n;
+    uint32_t num_rows;
+    uint32_t *heads;        // [tiles]
+    int32_t tiles;
+    int32_t *uniq;
+    int64_t *d_n_uniq;
+    int64_t row_cap;
+    uint32_t *chunk_rank;
+    int32_t chunk;
+    int32_t *status;
+};
+
+__device__ __forceinline__ uint32_t tile_heads(const HeadArgs &a, int64_t i0, uint32_t &flags) {
+    flags = 0;
+    uint32_t prev = i0 > 0 && i0 < a.n ? a.key[i0 - 1] : 0u;
+#pragma unroll
+    for (int j = 0; j < kSortRounds; ++j) {
+        if (i0 + j >= a.n) break;
+        const uint32_t k = a.key[i0 + j];
+        if (is_head(k, prev, i0 + j == 0, a.num_rows)) flags |= 1u << j;
+        prev = k;
+    }
+    return __popc(flags);
+}
+
+__global__ __launch_bounds__(kSortThreads) void k_count_heads(HeadArgs a) {
+    __shared__ uint32_t sm[kSortWaves];
+    uint32_t flags, total;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortTile + threadIdx.x * kSortRounds;
+    const uint32_t c = tile_heads(a, i0, flags);
+    block_exclusive_scan<uint32_t, kSortThreads>(c, &total, sm);
+    if (threadIdx.x == 0) a.heads[blockIdx.x] = total;
+}
+
+__global__ __launch_bounds__(kSortThreads) void k_emit_heads(HeadArgs a) {
+    __shared__ uint32_t sm[kSortWaves];
+    uint32_t mine = 0, before, flags, total;
+    for (int k = threadIdx.x; k < static_cast<int>(blockIdx.x); k += kSortThreads) mine += a.heads[k];
+    block_exclusive_scan<uint32_t, kSortThreads>(mine, &before, sm);
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortTile + threadIdx.x * kSortRounds;
+    const uint32_t c = tile_heads(a, i0, flags);
+    uint32_t at = before + block_exclusive_scan<uint32_t, kSortThreads>(c, &total, sm);
+#pragma unroll
+    for (int j = 0; j < kSortRounds; ++j) {
+        if (i0 + j >= a.n) break;
+        const bool head = (flags >> j) & 1u;
+        if (head && at < a.row_cap) a.uniq[at] = static_cast<int32_t>(a.key[i0 + j]);
+        at += head;
+        if ((i0 + j) % a.chunk == 0) a.chunk_rank[(i0 + j) / a.chunk] = at - 1u;
+    }
+    if (static_cast<int>(blockIdx.x) == a.tiles - 1 && threadIdx.x == 0) {
+        *a.d_n_uniq = static_cast<int64_t>(before) + total;
+        if (static_cast<int64_t>(before) + total > a.row_cap) set_status(a.status, GNN_ERR_CAPACITY);
+    }
+}
+
+// ---- the sums -----------------------------------------------------------------------------------
+
+constexpr int kSumThreads = 256;
+constexpr int kSumUnroll = 8;     // rows of dout in flight per lane
+
+struct SumArgs {
+    const uint32_t *key, *pos;
+    int64_t n;
+    uint32_t num_rows;
+    const void *dout;
+    int64_t ld_dout, d;
+    float scale;
+    void *out;
+    int64_t ld_out;
+    int32_t accumulate;
+    const uint32_t *chunk_rank;    // rows form
+    int64_t row_cap;
+    float *part;                   // [2 * chunks, d] sums of a chunk's first run (even) where it
+                                   // began earlier, and of its last run (odd) where it goes on
+    int32_t chunk;
+    int64_t chunks;
+    int32_t lanes;                 // lanes per chunk, a power of two
+    int32_t slabs;                 // groups of lanes side by side along a row
+    const uint32_t *touched;       // dense, written: rows without a bit are zeroed
+    int64_t sum_blocks;            // blocks beyond these zero rows
+};
+
+// The columns of one lane: VE from `at`, of which the first `skip` belong to its neighbour.
+struct Cols {
+    int64_t at;
+    int skip;
+    bool on;
+};
+
+template <int VE>
+__device__ __forceinline__ Cols lane_cols(int64_t slab, int lanes, int lane, int64_t d) {
+    Cols c;
+    const int64_t c0 = (slab * lanes + lane) * VE;
+    c.on = c0 < d;
+    c.at = c0 > d - VE ? d - VE : c0;
+    c.skip = static_cast<int>(c0 - c.at);
+    return c;
+}
+
+template <typename TO, int VE>
+__device__ __forceinline__ void put_row(const SumArgs &a, int64_t row, const Cols &c,
+                                        vec<float, VE> v) {
+    if (row >= a.row_cap || !c.on) return;
+    TO *p = static_cast<TO *>(a.out) + row * a.ld_out + c.at;
+    v *= a.scale;
+    if (a.accumulate) v += load_f32<TO, VE>(p);
+    if (c.skip == 0) {
+        store_f32<TO, VE>(p, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+            if (e >= c.skip) p[e] = static_cast<TO>(v[e]);
+    }
+}
+
+template <int VE>
+__device__ __forceinline__ void put_part(const SumArgs &a, int64_t row, const Cols &c,
+                                         vec<float, VE> v) {
+    if (!c.on) return;
+    store_f32<float, VE>(a.part + row * a.d + c.at, v);   // neighbours store equal values
+}
+
+template <typename TI, typename TO, int VE>
+__global__ __launch_bounds__(kSumThreads) void k_embedding_sums(SumArgs a) {
+    const int per = kSumThreads / a.lanes;
+    const int lane = threadIdx.x & (a.lanes - 1);
+    if (static_cast<int64_t>(blockIdx.x) >= a.sum_blocks) {
+        // zero the rows of the table that no id names: one row per lane group and turn
+        const int64_t groups = (static_cast<int64_t>(gridDim.x) - a.sum_blocks) * per;
+        int64_t r = (static_cast<int64_t>(blockIdx.x) - a.sum_blocks) * per + threadIdx.x / a.lanes;
+        for (; r < a.num_rows; r += groups) {
+            if ((a.touched[r >> 5] >> (r & 31)) & 1u) continue;
+            TO *p = static_cast<TO *>(a.out) + r * a.ld_out;
+            for (int64_t s = 0; s < a.slabs; ++s) {
+                const Cols c = lane_cols<VE>(s, a.lanes, lane, a.d);
+                if (c.on) store_f32<TO, VE>(p + c.at, vec<float, VE>(0.f));
+            }
+        }
+        return;
+    }
+    const int64_t g = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / a.lanes;
+    const int64_t chunk = g / a.slabs;
+    if (chunk >= a.chunks) return;
+    const Cols c = lane_cols<VE>(g - chunk * a.slabs, a.lanes, lane, a.d);
+    const int64_t e0 = chunk * a.chunk;
+    const int64_t e1 = e0 + a.chunk < a.n ? e0 + a.chunk : a.n;
+    uint32_t cur = a.key[e0];
+    if (cur >= a.num_rows) return;
+    bool earlier = e0 > 0 && a.key[e0 - 1] == cur;
+    int64_t rank = a.chunk_rank ? static_cast<int64_t>(a.chunk_rank[chunk]) : 0;
+    const TI *dout = static_cast<const TI *>(a.dout) + (c.on ? c.at : 0);
+    vec<float, VE> acc(0.f);
+    bool ended = false;      // reached the positions without a gradient row
+    for (int64_t e = e0; e < e1 && !ended; e += kSumUnroll) {
+        uint32_t k[kSumUnroll];
+        typename loose<TI, VE>::type v[kSumUnroll];
+        // every load is made (of the chunk's last row beyond its end), so that none waits for a
+        // branch
+#pragma unroll
+        for (int u = 0; u < kSumUnroll; ++u) {
+            const int64_t i = e + u < e1 ? e + u : e1 - 1;
+            k[u] = e + u < e1 ? a.key[i] : a.num_rows;
+            v[u] = *reinterpret_cast<const typename loose<TI, VE>::type *>(
+                dout + static_cast<int64_t>(a.pos[i]) * a.ld_dout);
+        }
+#pragma unroll
+        for (int u = 0; u < kSumUnroll; ++u) {
+            if (k[u] >= a.num_rows) {
+                ended = true;
+                break;
+            }
+            if (k[u] != cur) {
+                if (earlier)
+                    put_part<VE>(a, 2 * chunk, c, acc);
+                else
+                    put_row<TO, VE>(a, a.chunk_rank ? rank : cur, c, acc);
+                earlier = false;
+                cur = k[u];
+                ++rank;
+                acc = vec<float, VE>(0.f);
+            }
+            acc += __builtin_convertvector(v[u], vec<float, VE>);
+        }
+    }
+    const bool on = e1 < a.n && a.key[e1] == cur;
+    if (earlier)
+        put_part<VE>(a, 2 * chunk, c, acc);
+    else if (on)
+        put_part<VE>(a, 2 * chunk + 1, c, acc);
+    else
+        put_row<TO, VE>(a, a.chunk_rank ? rank : cur, c, acc);
+}
+
+// Joins the runs that begin in one chunk and go on in later ones: lane groups of a workgroup take
+// the run's partial sums in turn, then their sums are added in the groups' order.
+template <typename TO, int VE>
+__global__ __launch_bounds__(kSumThreads) void k_embedding_join(SumArgs a) {
+    __shared__ float sm[kSumThreads * VE];
+    const int64_t chunk = blockIdx.x / a.slabs;
+    const int64_t slab = blockIdx.x - chunk * a.slabs;
+    const int64_t e0 = chunk * a.chunk, e1 = e0 + a.chunk;
+    // whole workgroup
+    if (e1 >= a.n) return;
+    const uint32_t cur = a.key[e1 - 1];
+    if (cur >= a.num_rows || a.key[e1] != cur) return;
+    if (e0 > 0 && a.key[e0 - 1] == cur) return;       // it began earlier
+    // the last chunk whose first key is cur
+    int64_t last = chunk + 1, step = 1;
+    while (last + step < a.chunks && a.key[(last + step) * a.chunk] == cur) {
+        last += step;
+        step *= 2;
+    }
+    for (; step > 0; step /= 2)
+        if (last + step < a.chunks && a.key[(last + step) * a.chunk] == cur) last += step;
+    const int groups = kSumThreads / a.lanes;
+    const int grp = threadIdx.x / a.lanes, lane = threadIdx.x & (a.lanes - 1);
+    const Cols c = lane_cols<VE>(slab, a.lanes, lane, a.d);
+    vec<float, VE> acc(0.f);
+    if (c.on) {
+        const float *p = a.part + c.at;
+        if (grp == 0) acc = load_f32<float, VE>(p + (2 * chunk + 1) * a.d);
+#pragma unroll 8
+        for (int64_t q = chunk + 1 + grp; q <= last; q += groups)
+            acc += load_f32<float, VE>(p + 2 * q * a.d);
+    }
+#pragma unroll
+    for (int e = 0; e < VE; ++e) sm[e * kSumThreads + threadIdx.x] = acc[e];
+    __syncthreads();
+    if (grp != 0) return;
+    for (int q = 1; q < groups; ++q)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) acc[e] += sm[e * kSumThreads + q * a.lanes + lane];
+    int64_t row = cur;
+    if (a.chunk_rank) {
+        // the run's rank: that of the next chunk's first run
+        row = a.chunk_rank[chunk + 1];
+    }
+    put_row<TO, VE>(a, row, c, acc);
+}
+
+__global__ __launch_bounds__(256) void k_zero_rows(char *out, int64_t row_bytes, int64_t ld_bytes,
+                                                   int64_t rows) {
+    // one row per wavefront and turn, 16 bytes a lane, then the row's last 2-byte pieces
+    const int lane = lane_id();
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); r < rows;
+         r += static_cast<int64_t>(gridDim.x) * 4) {
+        char *p = out + r * ld_bytes;
+        int64_t b = static_cast<int64_t>(lane) * 16;
+        for (; b + 16 <= row_bytes; b += 1024)
+            *reinterpret_cast<loose<uint16_t, 8>::type *>(p + b) = vec<uint16_t, 8>(uint16_t(0));
+        for (int64_t q = (row_bytes & ~int64_t(15)) + 2 * lane; q < row_bytes; q += 128)
+            *reinterpret_cast<uint16_t *>(p + q) = 0;
+    }
+}
+
+// What the gradient keeps in the workspace.
+struct GradSpace {
+    uint32_t *key[2], *pos[2], *hist, *heads, *chunk_rank, *touched;
+    float *part;
+    int32_t chunk;
+    int64_t chunks, touched_words;
+    int32_t tiles;
+    size_t bytes;
+};
+
+// Chunk length: 64 positions, so that the partial sums of a chunk's two ends cost at most a
+// sixteenth of its rows of fp32, or shorter where that leaves fewer than kMinGroups lane groups.
+int32_t chunk_for(int64_t n) {
+    int64_t c = 64;
+    while (c > kChunkMin && n / c < 2048) c /= 2;
+    return static_cast<int32_t>(c);
+}
+
+GradSpace carve_grad(int64_t n, int64_t num_rows, int64_t d, char *base) {
+    GradSpace g{};
+    size_t off = 0;
+    auto take = [&](int64_t words) {
+        off = (off + 255) & ~static_cast<size_t>(255);
+        uint32_t *p = base ? reinterpret_cast<uint32_t *>(base + off) : nullptr;
+        off += static_cast<size_t>(words < 1 ? 1 : words) * 4;
+        return p;
+    };
+    g.chunk = chunk_for(n);
+    g.chunks = (n + g.chunk - 1) / g.chunk;
+    g.tiles = static_cast<int32_t>((n + kSortTile - 1) / kSortTile);
+    g.touched_words = (num_rows + 31) / 32;
+    for (int i = 0; i < 2; ++i) {
+        g.key[i] = take(n);
+        g.pos[i] = take(n);
+    }
+    g.hist = take(static_cast<int64_t>(g.tiles + 1) * kDigits);
+    g.heads = take(g.tiles);
+    g.chunk_rank = take(g.chunks);
+    g.touched = take(g.touched_words);
+    g.part = reinterpret_cast<float *>(take(2 * g.chunks * d));
+    g.bytes = off;
+    return g;
+}
+
+template <typename TI, typename TO, int VE>
+hipError_t run_sums(const EmbedGradArgs &a, const GradSpace &g, const uint32_t *key,
+                    const uint32_t *pos, bool zero_untouched, hipStream_t s) {
+    SumArgs p{};
+    p.key = key;
+    p.pos = pos;
+    p.n = a.n;
+    p.num_rows = static_cast<uint32_t>(a.num_rows);
+    p.dout = a.dout;
+    p.ld_dout = a.ld_dout;
+    p.d = a.d;
+    p.scale = a.scale;
+    p.out = a.out;
+    p.ld_out = a.ld_out;
+    p.accumulate = a.accumulate;
+    p.chunk_rank = a.rows ? g.chunk_rank : nullptr;
+    p.row_cap = a.rows ? a.row_cap : a.num_rows;
+    p.part = g.part;
+    p.chunk = g.chunk;
+    p.chunks = g.chunks;
+    const int64_t cpr = (a.d + VE - 1) / VE;
+    p.lanes = 1;
+    while (p.lanes < cpr && p.lanes < 64) p.lanes *= 2;
+    p.slabs = static_cast<int32_t>((cpr + p.lanes - 1) / p.lanes);
+    const int per = kSumThreads / p.lanes;
+    p.sum_blocks = (g.chunks * p.slabs + per - 1) / per;
+    int64_t zero_blocks = 0;
+    if (zero_untouched) {
+        p.touched = g.touched;
+        zero_blocks = (a.num_rows + per * 8 - 1) / (per * 8);
+        if (zero_blocks > 16384) zero_blocks = 16384;
+    }
+    if (p.sum_blocks + zero_blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL((k_embedding_sums<TI, TO, VE>),
+                       dim3(static_cast<unsigned>(p.sum_blocks + zero_blocks)), dim3(kSumThreads),
+                       0, s, p);
+    if (g.chunks > 1)
+        hipLaunchKernelGGL((k_embedding_join<TO, VE>),
+                           dim3(static_cast<unsigned>((g.chunks - 1) * p.slabs)),
+                           dim3(kSumThreads), 0, s, p);
+    return hipGetLastError();
+}
+
+template <typename TI, typename TO>
+hipError_t pick_sums(const EmbedGradArgs &a, const GradSpace &g, const uint32_t *key,
+                     const uint32_t *pos, bool zero, hipStream_t s) {
+    constexpr int kWide = sizeof(TI) == 2 ? 8 : 4;      // 16 bytes of dout a lane
+    if (a.d >= kWide) return run_sums<TI, TO, kWide>(a, g, key, pos, zero, s);
+    return run_sums<TI, TO, 1>(a, g, key, pos, zero, s);
+}
+
+}  // namespace
+
+hipError_t launch_embedding_lookup(LookupArgs a, hipStream_t s) {
+    if (a.n <= 0) return hipSuccess;
+    if (a.table_type == GNN_F32)
+        return a.out_type == GNN_F32 ? pick_lookup<float, float>(a, s) : pick_lookup<float, bf16>(a, s);
+    return a.out_type == GNN_F32 ? pick_lookup<bf16, float>(a, s) : pick_lookup<bf16, bf16>(a, s);
+}
+
+size_t embedding_grad_bytes(int64_t n, int64_t num_rows, int64_t d) {
+    return carve_grad(n, num_rows, d, nullptr).bytes;
+}
+
+hipError_t launch_embedding_grad(const EmbedGradArgs &a, hipStream_t s) {
+    const int elem = a.out_type == GNN_F32 ? 4 : 2;
+    const bool dense = !a.rows;
+    // A written dense table: rows that no id names are zeroed from a bitmap of the named ones, or,
+    // where at most one row in 16 can be named, the whole table is cleared first (the rows written
+    // twice are then fewer than the bitmap's test is worth).
+    const bool written = dense && !a.accumulate;
+    const bool clear_all = written && a.n <= a.num_rows / 16;
+    if (clear_all) {
+        const int64_t blocks = (a.num_rows + 15) / 16;
+        hipLaunchKernelGGL(k_zero_rows, dim3(static_cast<unsigned>(blocks < 32768 ? blocks : 32768)),
+                           dim3(256), 0, s, static_cast<char *>(a.out), a.d * elem, a.ld_out * elem,
+                           a.num_rows);
+    }
+    if (a.n == 0 && (!written || clear_all) && dense) return hipGetLastError();
+    const GradSpace g = carve_grad(a.n, a.num_rows, a.d, a.ws);
+    SortArgs q{};
+    q.ids = a.ids;
+    q.d_n = a.d_n;
+    q.n = a.n;
+    q.pad_id = a.pad_id;
+    q.num_rows = static_cast<uint32_t>(a.num_rows);
+    q.status = a.status;
+    q.hist = g.hist;
+    q.tiles = g.tiles;
+    q.scanned = g.tiles > kSumTiles;
+    if (written && !clear_all) {
+        q.touched = g.touched;
+        q.touched_words = g.touched_words;
+    }
+    int nb = 1;
+    while ((static_cast<uint64_t>(a.num_rows) >> nb) != 0) ++nb;
+    q.passes = (nb + kSortBits - 1) / kSortBits;
+    q.bits = (nb + q.passes - 1) / q.passes;
+    q.rows = a.rows;
+    q.uniq = a.uniq;
+    q.d_n_uniq = a.d_n_uniq;
+    q.row_cap = a.row_cap;
+    q.chunk_rank = g.chunk_rank;
+    q.chunk = g.chunk;
+    const uint32_t *key, *pos;
+    if (a.n <= kSortTile) {
+        q.key_out = g.key[0];
+        q.pos_out = g.pos[0];
+        hipLaunchKernelGGL(k_sort_tile, dim3(1), dim3(kSortThreads), 0, s, q);
+        key = g.key[0];
+        pos = g.pos[0];
+    } else {
+        for (int p = 0; p < q.passes; ++p) {
+            q.shift = p * q.bits;
+            q.key_in = p ? g.key[(p + 1) & 1] : nullptr;
+            q.pos_in = p ? g.pos[(p + 1) & 1] : nullptr;
+            q.key_out = g.key[p & 1];
+            q.pos_out = g.pos[p & 1];
+            const dim3 grid(static_cast<unsigned>(g.tiles));
+            hipLaunchKernelGGL(k_sort_count, grid, dim3(kSortThreads), 0, s, q);
+            if (q.scanned) hipLaunchKernelGGL(k_sort_scan, dim3(kDigits), dim3(256), 0, s, q);
+            hipLaunchKernelGGL(k_sort_place, grid, dim3(kSortThreads), 0, s, q);
+        }
+        key = g.key[(q.passes - 1) & 1];
+        pos = g.pos[(q.passes - 1) & 1];
+        if (!dense) {
+            HeadArgs h{};
+            h.key = key;
+            h.n = a.n;
+            h.num_rows = q.num_rows;
+            h.heads = g.heads;
+            h.tiles = g.tiles;
+            h.uniq = a.uniq;
+            h.d_n_uniq = a.d_n_uniq;
+            h.row_cap = a.row_cap;
+            h.chunk_rank = g.chunk_rank;
+            h.chunk = g.chunk;
+            h.status = a.status;
+            const dim3 grid(static_cast<unsigned>(g.tiles));
+            hipLaunchKernelGGL(k_count_heads, grid, dim3(kSortThreads), 0, s, h);
+            hipLaunchKernelGGL(k_emit_heads, grid, dim3(kSortThreads), 0, s, h);
+        }
+    }
+    const bool zero = written && !clear_all;
+    if (a.dout_type == GNN_F32)
+        return a.out_type == GNN_F32 ? pick_sums<float, float>(a, g, key, pos, zero, s)
+                                     : pick_sums<float, bf16>(a, g, key, pos, zero, s);
+    return a.out_type == GNN_F32 ? pick_sums<bf16, float>(a, g, key, pos, zero, s)
+                                 : pick_sums<bf16, bf16>(a, g, key, pos, zero, s);
+}
+
+}  // namespace gnnmb

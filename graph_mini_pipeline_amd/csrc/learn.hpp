@@ -1,0 +1,75 @@
+// Launchers of the learned side of the path (embedding lookup and gradient, cross attention,
+// orthogonalised updates), and the element types they share.  Internal; not part of the ABI.
+#pragma once
+
+#include "common.hpp"
+
+namespace gnnmb {
+
+typedef __bf16 bf16;
+
+template <typename T, int N>
+using vec = T __attribute__((ext_vector_type(N)));
+// The same vector at any address that is aligned for one element: global loads and stores of gfx950
+// need no more than the element's alignment.
+template <typename T, int N>
+struct loose {
+    typedef T type __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+};
+
+template <typename T, int N>
+__device__ __forceinline__ vec<float, N> load_f32(const T *p) {
+    const typename loose<T, N>::type v = *reinterpret_cast<const typename loose<T, N>::type *>(p);
+    return __builtin_convertvector(v, vec<float, N>);
+}
+
+// Rounds to nearest even where T is bf16.
+template <typename T, int N>
+__device__ __forceinline__ void store_f32(T *p, vec<float, N> v) {
+    *reinterpret_cast<typename loose<T, N>::type *>(p) = __builtin_convertvector(v, vec<T, N>);
+}
+
+// ---- embedding ----------------------------------------------------------------------------------
+
+struct LookupArgs {
+    const void *table;
+    int32_t table_type, out_type;
+    int64_t num_rows, d, ld;
+    const int32_t *ids;
+    const int64_t *d_n;
+    int64_t n;
+    float scale;
+    int32_t pad_id;
+    void *out;
+    int64_t ld_out;
+    int32_t *status;
+    uint32_t cpr;       // vectors per row (set by the launcher, with its divisor)
+    FastDiv by_cpr;
+};
+hipError_t launch_embedding_lookup(LookupArgs a, hipStream_t s);
+
+struct EmbedGradArgs {
+    const int32_t *ids;
+    const int64_t *d_n;
+    int64_t n;
+    const void *dout;
+    int32_t dout_type, out_type;
+    int64_t ld_dout;
+    float scale;
+    int32_t pad_id;
+    int64_t num_rows, d;
+    void *out;              // dense: [num_rows, ld_out]; rows: [row_cap, ld_out]
+    int64_t ld_out;
+    int32_t accumulate;     // dense only
+    int32_t rows;           // 1: the rows form, 0: dense
+    int32_t *uniq;          // rows: [row_cap] distinct ids, ascending
+    int64_t *d_n_uniq;
+    int64_t row_cap;
+    int32_t *status;
+    char *ws;
+};
+// Bytes of workspace that launch_embedding_grad needs for these sizes.
+size_t embedding_grad_bytes(int64_t n, int64_t num_rows, int64_t d);
+hipError_t launch_embedding_grad(const EmbedGradArgs &a, hipStream_t s);
+
+}  // namespace gnnmb

@@ -57,6 +57,10 @@ typedef int32_t gnn_status;
 
 typedef void *gnn_stream; /* hipStream_t */
 
+/* Element types of the calls that take one. */
+#define GNN_F32 0
+#define GNN_BF16 1
+
 /* Flags for gnn_options.flags. */
 #define GNN_SYNC 1u /* synchronise the stream at the end of the call and return the device status */
 /* How gnn_minibatch relabels the sub-batches of a super-batch (results are identical; at most one
@@ -503,6 +507,53 @@ gnn_status gnn_minibatch(const gnn_graph *g, const gnn_feature_store *fs, const 
                          int32_t num_hops, uint64_t seed64, gnn_minibatch_out *outs, void *ws,
                          size_t ws_bytes, const gnn_options *opt, gnn_stream stream,
                          gnn_timer *timer);
+
+/*
+ * Embedding lookup with scaling (learned node or token vectors; the gather of a table that is
+ * trained): out[i, 0..d) = scale * table[ids[i], 0..d), i < n, computed in fp32 and rounded once to
+ * out's type.  ids[i] = pad_id (pad_id >= 0; -1: none) gives a zero row.
+ *   table: device [num_rows, ld], out: device [n, ld_out], types GNN_F32 or GNN_BF16 (any pair);
+ *   rows may start at any multiple of their element; out must not overlap table.
+ *   n and d_n as in gnn_gather_features: rows at or past *d_n are left as they are.
+ * Device errors: GNN_ERR_OUT_OF_RANGE (an id outside [0, num_rows); its row is zero), written to
+ * *d_status if not NULL.
+ * Errors: GNN_ERR_INVALID_ARG; GNN_ERR_UNSUPPORTED for another type, n or num_rows over 2^31 - 1,
+ * d over 2^24 or n * d over 2^40.
+ */
+gnn_status gnn_embedding_lookup(const void *table, int32_t table_type, int64_t num_rows, int64_t d,
+                                int64_t ld, const int32_t *ids, const int64_t *d_n, int64_t n,
+                                float scale, int32_t pad_id, void *out, int32_t out_type,
+                                int64_t ld_out, int32_t *d_status, gnn_stream stream);
+
+/*
+ * The gradient of that lookup: grad[t, 0..d) = scale * sum over i < n with ids[i] = t of
+ * dout[i, 0..d), summed in fp32 in an order that the ids alone decide (the same bits every time),
+ * rounded once.  Positions that hold pad_id add nothing.  The positions are sorted by id in ws.
+ *   gnn_embedding_grad: the dense table grad [num_rows, ld_grad].  accumulate = 0: every row is
+ *     written, zero where no id names it; accumulate != 0: the sums are added to the named rows
+ *     (fp32 addition, then one rounding), the others are not touched.
+ *   gnn_embedding_grad_rows: the distinct ids only, as gnn_unique_relabel lists them: *d_n_uniq
+ *     (device int64) their number U, uniq[0..U) (device int32) the ids, ascending, and
+ *     grad[p, 0..d) the row of uniq[p]; nothing is written at or past U or uniq_cap.
+ *   dout: device [n, ld_dout]; types GNN_F32 or GNN_BF16 (any pair).  grad must not overlap dout.
+ *   ws: ws_bytes >= gnn_embedding_grad_workspace_size(n, num_rows, d).
+ * Device errors (in *d_status if not NULL): GNN_ERR_OUT_OF_RANGE (an id outside [0, num_rows), which
+ * then adds nothing), GNN_ERR_CAPACITY (U > uniq_cap; *d_n_uniq still holds U).
+ * Errors: as gnn_embedding_lookup; GNN_ERR_CAPACITY when ws is too small.
+ */
+gnn_status gnn_embedding_grad_workspace_size(int64_t n, int64_t num_rows, int64_t d,
+                                             size_t *out_bytes);
+gnn_status gnn_embedding_grad(const int32_t *ids, const int64_t *d_n, int64_t n, const void *dout,
+                              int32_t dout_type, int64_t ld_dout, float scale, int32_t pad_id,
+                              int64_t num_rows, int64_t d, void *grad, int32_t grad_type,
+                              int64_t ld_grad, int32_t accumulate, int32_t *d_status, void *ws,
+                              size_t ws_bytes, gnn_stream stream);
+gnn_status gnn_embedding_grad_rows(const int32_t *ids, const int64_t *d_n, int64_t n,
+                                   const void *dout, int32_t dout_type, int64_t ld_dout,
+                                   float scale, int32_t pad_id, int64_t num_rows, int64_t d,
+                                   int32_t *uniq, int64_t uniq_cap, int64_t *d_n_uniq, void *grad,
+                                   int32_t grad_type, int64_t ld_grad, int32_t *d_status, void *ws,
+                                   size_t ws_bytes, gnn_stream stream);
 
 /*
  * Device status word of a workspace: synchronises `stream`, returns the first device error
