@@ -30,7 +30,7 @@ __all__ = [
     "gnn_sage_update", "gnn_minibatch", "gnn_unique_relabel_noalloc", "AdjacencyCache", "gnn_adjacency_cache_create",
     "gnn_host_mapped_pointer",
     "gnn_embedding_lookup", "gnn_embedding_grad", "gnn_embedding_grad_rows",
-    "gnn_embedding_grad_workspace_size",
+    "gnn_embedding_grad_workspace_size", "gnn_orthogonalize", "gnn_orthogonalize_workspace_size",
     "gnn_read_device_status", "gnn_timer_create", "gnn_timer_destroy", "gnn_timer_reset",
     "gnn_timer_elapsed", "gnn_copy_probe", "gnn_copy_probe_host", "gnn_hash_probe", "lib",
 ]
@@ -732,6 +732,50 @@ def gnn_embedding_grad_rows(ids: torch.Tensor, dout: torch.Tensor, scale: float,
                                       grad.data_ptr(), gt, _ld(grad), _ptr(d_status),
                                       ws.data_ptr(), ws.numel() * ws.element_size(),
                                       _stream(stream)), "gnn_embedding_grad_rows")
+
+
+def gnn_orthogonalize_workspace_size(batch: int, rows: int, cols: int, dtype) -> int:
+    b = ctypes.c_size_t(0)
+    _ok(lib().gnn_orthogonalize_workspace_size(batch, rows, cols, _type(dtype, "dtype"),
+                                               ctypes.byref(b)),
+        "gnn_orthogonalize_workspace_size")
+    return int(b.value)
+
+
+def _matrices(t: torch.Tensor, name: str):
+    """(type, batch, rows, cols, row stride, matrix stride) of a device matrix or batch of them."""
+    kind = _type(t.dtype, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    if t.dim() == 2:
+        t = t.unsqueeze(0)
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name}: must be [rows, cols] or [batch, rows, cols] with contiguous rows")
+    b, m, n = t.shape
+    ld = t.stride(1) if m > 1 else n
+    return kind, b, m, n, ld, t.stride(0) if b > 1 else m * ld
+
+
+def gnn_orthogonalize(g: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, steps: int = 5,
+                      coefs: Optional[Sequence[float]] = None, eps: float = 1e-7,
+                      scale: float = 1.0, stream=None) -> None:
+    """out = scale * X after `steps` Newton-Schulz steps X <- (c0 I + c1 A + c2 A^2) X, A = X X^T, from
+    X = g / (|g|_F + eps).  g, out: [rows, cols] or [batch, rows, cols], float32 or bfloat16."""
+    kind, b, m, n, ld, stride = _matrices(g, "g")
+    okind, ob, om, on, old, ostride = _matrices(out, "out")
+    if okind != kind or (ob, om, on) != (b, m, n):
+        raise ValueError("out: g's shape and type")
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws: must be a contiguous device tensor")
+    c = None
+    if coefs is not None:
+        if len(coefs) != 3:
+            raise ValueError("coefs: three numbers")
+        c = (ctypes.c_float * 3)(*coefs)
+    _ok(lib().gnn_orthogonalize(g.data_ptr(), kind, b, m, n, ld, stride, steps, c, eps, scale,
+                                out.data_ptr(), old, ostride, ws.data_ptr(),
+                                ws.numel() * ws.element_size(), _stream(stream)),
+        "gnn_orthogonalize")
 
 
 def gnn_copy_probe(src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:

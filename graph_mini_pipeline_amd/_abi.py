@@ -121,6 +121,9 @@ SIGNATURES = {
                                  vp, size_t, vp]),
     "gnn_embedding_grad_rows": (i32, [vp, vp, i64, vp, i32, i64, f32, i32, i64, i64, vp, i64, vp, vp,
                                       i32, i64, vp, vp, size_t, vp]),
+    "gnn_orthogonalize_workspace_size": (i32, [i64, i64, i64, i32, P(size_t)]),
+    "gnn_orthogonalize": (i32, [vp, i32, i64, i64, i64, i64, i64, i32, P(f32), f32, f32, vp, i64, i64,
+                                vp, size_t, vp]),
     "gnn_read_device_status": (i32, [vp, vp, P(i32)]),
     "gnn_timer_create": (i32, [i32, P(vp)]),
     "gnn_timer_destroy": (i32, [vp]),

@@ -1764,6 +1764,62 @@ gnn_status gnn_embedding_grad_rows(const int32_t *ids, const int64_t *d_n, int64
     return embedding_grad(a, ws, ws_bytes, stream);
 }
 
+// ---- orthogonalised updates -----------------------------------------------------------------------
+
+namespace {
+constexpr int64_t kNewtonMaxEdge = 32768;
+constexpr int32_t kNewtonMaxSteps = 16;
+
+gnn_status check_newton_sizes(int64_t rows, int64_t cols, int64_t batch, int32_t type) {
+    if (rows < 1 || cols < 1 || batch < 0) return GNN_ERR_INVALID_ARG;
+    if (!known_type(type) || rows > kNewtonMaxEdge || cols > kNewtonMaxEdge || batch > 65535)
+        return GNN_ERR_UNSUPPORTED;
+    return GNN_OK;
+}
+}  // namespace
+
+gnn_status gnn_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64_t cols, int32_t type,
+                                            size_t *out_bytes) {
+    if (!out_bytes) return GNN_ERR_INVALID_ARG;
+    GNN_TRY(check_newton_sizes(rows, cols, batch, type));
+    *out_bytes = newton_bytes(rows, cols, batch, type);
+    return GNN_OK;
+}
+
+gnn_status gnn_orthogonalize(const void *g, int32_t type, int64_t batch, int64_t rows, int64_t cols,
+                             int64_t ld_g, int64_t stride_g, int32_t steps, const float *coefs,
+                             float eps, float scale, void *out, int64_t ld_out, int64_t stride_out,
+                             void *ws, size_t ws_bytes, gnn_stream stream) {
+    GNN_TRY(check_newton_sizes(rows, cols, batch, type));
+    if (steps < 1 || !(eps >= 0) || ld_g < cols || ld_out < cols) return GNN_ERR_INVALID_ARG;
+    if (batch > 1 && (stride_g < (rows - 1) * ld_g + cols || stride_out < (rows - 1) * ld_out + cols))
+        return GNN_ERR_INVALID_ARG;
+    if (!ws || (batch > 0 && (!g || !out))) return GNN_ERR_INVALID_ARG;
+    NewtonArgs a{};
+    const float quintic[3] = {3.4445f, -4.7750f, 2.0315f};
+    for (int i = 0; i < 3; ++i) a.coefs[i] = coefs ? coefs[i] : quintic[i];
+    if (steps > kNewtonMaxSteps || !newton_in_range(a.coefs, steps)) return GNN_ERR_UNSUPPORTED;
+    if (ws_bytes < newton_bytes(rows, cols, batch, type)) return GNN_ERR_CAPACITY;
+    if (fault(kFaultLaunch)) return GNN_ERR_HIP;
+    if (batch == 0) return GNN_OK;
+    a.g = g;
+    a.type = type;
+    a.rows = rows;
+    a.cols = cols;
+    a.ld_g = ld_g;
+    a.batch = batch;
+    a.batch_g = stride_g;
+    a.steps = steps;
+    a.eps = eps;
+    a.scale = scale;
+    a.out = out;
+    a.ld_out = ld_out;
+    a.batch_out = stride_out;
+    a.ws = static_cast<char *>(ws);
+    GNN_TRY_HIP(launch_newton(a, static_cast<hipStream_t>(stream)));
+    return GNN_OK;
+}
+
 gnn_status gnn_read_device_status(const void *ws, gnn_stream stream, gnn_status *out) {
     if (!ws || !out) return GNN_ERR_INVALID_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);

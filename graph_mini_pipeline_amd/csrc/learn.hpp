@@ -72,4 +72,22 @@ struct EmbedGradArgs {
 size_t embedding_grad_bytes(int64_t n, int64_t num_rows, int64_t d);
 hipError_t launch_embedding_grad(const EmbedGradArgs &a, hipStream_t s);
 
+// ---- orthogonalised updates -----------------------------------------------------------------------
+
+struct NewtonArgs {
+    const void *g;          // [batch][rows, ld_g]
+    int32_t type;
+    int64_t rows, cols, ld_g, batch, batch_g;
+    int32_t steps;
+    float coefs[3];
+    float eps, scale;
+    void *out;              // [batch][rows, ld_out], g's type
+    int64_t ld_out, batch_out;
+    char *ws;
+};
+size_t newton_bytes(int64_t rows, int64_t cols, int64_t batch, int32_t type);
+// Whether the values of these steps fit the planes they are kept in.
+bool newton_in_range(const float *coefs, int steps);
+hipError_t launch_newton(const NewtonArgs &a, hipStream_t s);
+
 }  // namespace gnnmb

@@ -1,0 +1,516 @@
+// Orthogonalising a weight matrix's update by Newton-Schulz products (the step of the Muon optimiser).
+//
+// With X = G / (|G|_F + eps), every step applies the odd polynomial p(s) = a s + b s^3 + c s^5 to the
+// singular values of X, by products alone:
+//   A = X X^T,   Q = a I + b A + c A^2,   X <- Q X,
+// X taken wide (s rows, l >= s columns), so that A and Q are s x s.  A and Q are symmetric: one
+// triangle of their tiles is computed, and each tile is stored a second time, mirrored.
+//
+// Numbers.  The products run on the 16-bit matrix instructions with fp32 accumulation.  X, A and Q
+// are stored in fp16, times 2^12: the singular values stay below 3 (newton_in_range), so that
+// every entry fits, and entries down to 2^-26 keep fp16's 11 bits.  For a bf16 update one fp16 plane carries
+// eight times the precision of the result's type; the fp32 update takes two planes, x = hi + lo (22
+// bits), and three matrix products, hi hi + hi lo + lo hi (all four for small matrices); the dropped
+// product is below 2^-22 of a term.  The first X is G times a power of two, so nothing is rounded that need not be, and the rest
+// of 1 / (|G|_F + eps) multiplies the first A and the first Q X.
+//
+// Layout.  The matrix instructions want both operands with the summed index contiguous: X for A, the
+// symmetric A for A^2, and, since (Q X)^T = X^T Q, X^T and Q for the last product, which therefore
+// stores X and X^T.  The planes are padded with zeros to whole tiles, and zeros stay zeros.
+#include <math.h>
+
+#include "learn.hpp"
+
+namespace gnnmb {
+
+namespace {
+
+typedef _Float16 f16;
+typedef vec<f16, 8> h8;
+typedef vec<float, 16> f16x;
+
+constexpr float kUp = 4096.f;                 // the stored planes' factor, 2^12
+constexpr float kDown = 1.f / 4096.f;
+
+// Where the tile's 16-byte piece c of row r lies in LDS, in pieces: a row's pieces are permuted by the
+// row, so that the 32 rows which one operand read touches at the same c spread over the banks.
+template <int CPR>
+__device__ __forceinline__ int piece(int r, int c) {
+    return r * CPR + (c ^ ((CPR == 8 ? r : r >> 1) & (CPR - 1)));
+}
+
+enum : int32_t { kGram, kPoly, kApply, kLast };
+
+struct ProductArgs {
+    const f16 *a, *b;            // [rows, ld] planes, summed index contiguous
+    int64_t ld_a, ld_b, plane_a, plane_b, batch_a, batch_b;
+    f16 *c, *t;                  // the product, and its transpose (symmetric: the mirrored tiles)
+    int64_t ld_c, ld_t, plane_c, plane_t, batch_c, batch_t;
+    int64_t k;                   // summed length, a multiple of 64
+    int32_t m_tiles, n_tiles;
+    int32_t what;
+    float ca, cb, cc;            // kPoly
+    const float *first;          // [batch] factor of X in the first step, NULL: 1
+    // kLast
+    void *out;
+    int64_t ld_out, batch_out;
+    int64_t m, n;                // rows and columns of the product that exist
+    int32_t out_rows;            // 1: out[m][n], 0: out[n][m]
+    float scale;
+};
+
+template <int PL>
+struct PolyOf {
+    typedef float type;
+};
+// The terms of a + b A + c A^2 cancel to a fraction of their size, so for fp32 updates they are added
+// in 64 bits (an s x s epilogue: no time that shows).
+template <>
+struct PolyOf<2> {
+    typedef double type;
+};
+
+template <int BM, int BN, int WM, int WN, int PL, typename TO>
+__global__ __launch_bounds__(WM *WN * 64) void k_newton_product(ProductArgs p) {
+    constexpr int T = WM * WN * 64;
+    constexpr int BK = PL == 1 ? 64 : 32;
+    constexpr int CPR = BK / 8;                     // 16-byte pieces per row
+    // Small matrices are not bound by the products, and their sums are too short for the dropped one
+    // to average out (1.2e-6 of a 5 x 1 update's norm without it, 1e-7 with it).
+    constexpr bool kAllFour = BM == 64;
+    typedef typename PolyOf<PL>::type Poly;
+    constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
+    constexpr int LA = BM * CPR / T, LB = BN * CPR / T;   // pieces per thread and plane
+    __shared__ h8 lds[2][PL * (BM + BN) * CPR];
+    const bool symmetric = p.what == kGram || p.what == kPoly;
+    int tm, tn;
+    if (symmetric) {
+        const int q = static_cast<int>(blockIdx.x);
+        tm = static_cast<int>((sqrtf(8.f * q + 1.f) - 1.f) * 0.5f);
+        while ((tm + 1) * (tm + 2) / 2 <= q) ++tm;
+        while (tm * (tm + 1) / 2 > q) --tm;
+        tn = q - tm * (tm + 1) / 2;
+    } else {
+        tm = static_cast<int>(blockIdx.x) / p.n_tiles;
+        tn = static_cast<int>(blockIdx.x) - tm * p.n_tiles;
+    }
+    const int64_t z = blockIdx.y;
+    const int t = threadIdx.x, lane = lane_id(), w = t >> 6;
+    const int wm = w / WN, wn = w % WN;
+    const f16 *ga = p.a + z * p.batch_a + static_cast<int64_t>(tm) * BM * p.ld_a;
+    const f16 *gb = p.b + z * p.batch_b + static_cast<int64_t>(tn) * BN * p.ld_b;
+
+    h8 ra[PL][LA], rb[PL][LB];
+    auto load = [&](int64_t k0) {
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+#pragma unroll
+            for (int i = 0; i < LA; ++i) {
+                const int e = i * T + t, r = e / CPR, c = e % CPR;
+                ra[q][i] = *reinterpret_cast<const h8 *>(ga + q * p.plane_a + r * p.ld_a + k0 + c * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < LB; ++i) {
+                const int e = i * T + t, r = e / CPR, c = e % CPR;
+                rb[q][i] = *reinterpret_cast<const h8 *>(gb + q * p.plane_b + r * p.ld_b + k0 + c * 8);
+            }
+        }
+    };
+    auto store = [&](int buf) {
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+            h8 *at = &lds[buf][q * (BM + BN) * CPR];
+#pragma unroll
+            for (int i = 0; i < LA; ++i) {
+                const int e = i * T + t;
+                at[piece<CPR>(e / CPR, e % CPR)] = ra[q][i];
+            }
+#pragma unroll
+            for (int i = 0; i < LB; ++i) {
+                const int e = i * T + t;
+                at[BM * CPR + piece<CPR>(e / CPR, e % CPR)] = rb[q][i];
+            }
+        }
+    };
+    f16x acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = f16x(0.f);
+
+    const int row = lane & 31, half = lane >> 5;
+    const int steps = static_cast<int>(p.k / BK);
+    load(0);
+    store(0);
+    __syncthreads();
+    for (int s = 0; s < steps; ++s) {
+        if (s + 1 < steps) load(static_cast<int64_t>(s + 1) * BK);
+        const h8 *at = lds[s & 1];
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk) {
+            h8 a[PL][TM], b[PL][TN];
+#pragma unroll
+            for (int q = 0; q < PL; ++q) {
+                const h8 *pl = at + q * (BM + BN) * CPR;
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    a[q][i] = pl[piece<CPR>((wm * TM + i) * 32 + row, kk * 2 + half)];
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    b[q][j] = pl[BM * CPR + piece<CPR>((wn * TN + j) * 32 + row, kk * 2 + half)];
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    if (PL == 2) {
+                        if (kAllFour)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[PL - 1][i], b[PL - 1][j], acc[i][j], 0, 0, 0);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[0][i], b[PL - 1][j], acc[i][j], 0, 0, 0);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[PL - 1][i], b[0][j], acc[i][j], 0, 0, 0);
+                    }
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[0][i], b[0][j], acc[i][j], 0, 0, 0);
+                }
+        }
+        if (s + 1 < steps) store((s + 1) & 1);
+        __syncthreads();
+    }
+
+    // A lane holds column lane % 32 and rows 8 g + 4 (lane / 32) + 0..3 of each 32 x 32 accumulator.
+    const float first = p.first ? p.first[z] : 1.f;
+    const bool mirror = !symmetric || tm != tn;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int64_t n = static_cast<int64_t>(tn) * BN + (wn * TN + j) * 32 + row;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int64_t m = static_cast<int64_t>(tm) * BM + (wm * TM + i) * 32 + 8 * g + 4 * half;
+                vec<float, 4> v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e];
+                if (p.what == kLast) {
+                    v *= kDown * kDown * first * p.scale;
+                    TO *out = static_cast<TO *>(p.out) + z * p.batch_out;
+                    if (n >= p.n) continue;
+                    if (p.out_rows) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (m + e < p.m) out[(m + e) * p.ld_out + n] = static_cast<TO>(v[e]);
+                    } else if (m + 4 <= p.m) {
+                        store_f32<TO, 4>(out + n * p.ld_out + m, v);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (m + e < p.m) out[n * p.ld_out + m + e] = static_cast<TO>(v[e]);
+                    }
+                    continue;
+                }
+                if (p.what == kGram) {
+                    v *= kDown * first * first;
+                } else if (p.what == kPoly) {
+                    // the product's operand is A itself; A[n][m..] = A[m..][n]
+                    const f16 *old = p.a + z * p.batch_a + n * p.ld_a + m;
+                    vec<Poly, 4> u = __builtin_convertvector(v, vec<Poly, 4>) * static_cast<Poly>(kDown * p.cc);
+#pragma unroll
+                    for (int q = 0; q < PL; ++q) {
+                        const vec<f16, 4> x = *reinterpret_cast<const vec<f16, 4> *>(old + q * p.plane_a);
+                        u += static_cast<Poly>(p.cb) * __builtin_convertvector(x, vec<Poly, 4>);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (m + e == n) u[e] += static_cast<Poly>(p.ca * kUp);
+                    v = __builtin_convertvector(u, vec<float, 4>);
+                } else {
+                    v *= kDown * first;
+                }
+#pragma unroll
+                for (int q = 0; q < PL; ++q) {
+                    const vec<f16, 4> x = __builtin_convertvector(v, vec<f16, 4>);
+                    f16 *c = p.c + z * p.batch_c + q * p.plane_c + m * p.ld_c + n;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[e * p.ld_c] = x[e];
+                    if (mirror)
+                        *reinterpret_cast<vec<f16, 4> *>(p.t + z * p.batch_t + q * p.plane_t +
+                                                         n * p.ld_t + m) = x;
+                    v -= __builtin_convertvector(x, vec<float, 4>);
+                }
+            }
+        }
+}
+
+// ---- the norm and the first X ---------------------------------------------------------------------
+
+constexpr int kNormThreads = 256;
+constexpr int kNormBlocks = 256;     // most partial sums per matrix: one per thread of the reader
+
+struct PrepArgs {
+    const void *g;
+    int64_t rows, cols, ld, batch_g;
+    double *partial;        // [batch, blocks] sums of squares
+    int32_t blocks;
+    float eps;
+    float *first;           // [batch]
+    f16 *same, *turned;     // G's orientation, and transposed; padded
+    int64_t ld_same, ld_turned, plane, batch;   // elements
+};
+
+// Squares are summed in 64 bits, which neither overflow nor vanish for any fp32 update.
+template <typename TI>
+__global__ __launch_bounds__(kNormThreads) void k_norm_squares(PrepArgs p) {
+    __shared__ double sm[kNormThreads / 64];
+    const TI *g = static_cast<const TI *>(p.g) + blockIdx.y * p.batch_g;
+    const int w = threadIdx.x >> 6;
+    double sum = 0;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + w; r < p.rows;
+         r += static_cast<int64_t>(gridDim.x) * 4)
+#pragma unroll 8
+        for (int64_t c = lane_id(); c < p.cols; c += 64) {
+            const double x = static_cast<float>(g[r * p.ld + c]);
+            sum += x * x;
+        }
+    sum = wave_sum(sum);
+    if (lane_id() == 0) sm[w] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) p.partial[blockIdx.y * p.blocks + blockIdx.x] = (sm[0] + sm[1]) + (sm[2] + sm[3]);
+}
+
+template <typename TI, int PL>
+__global__ __launch_bounds__(kNormThreads) void k_first_planes(PrepArgs p) {
+    __shared__ double sm[kNormThreads / 64];
+    __shared__ f16 tile[PL][64][66];
+    const int t = threadIdx.x, w = t >> 6;
+    const int64_t z = blockIdx.z;
+    const double s = wave_sum(t < p.blocks ? p.partial[z * p.blocks + t] : 0.0);
+    if (lane_id() == 0) sm[w] = s;
+    __syncthreads();
+    const double norm = sqrt((sm[0] + sm[1]) + (sm[2] + sm[3]));
+    int e = 0;
+    if (norm > 0 && norm <= 1.7e308) frexp(norm, &e);     // norm 2^-e in [0.5, 1)
+    if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) {
+        // the rest of the division, exactly 0 for a zero update and NaN where G is not finite
+        double rest = norm > 0 ? 1.0 / ldexp(norm + static_cast<double>(p.eps), -e) : 0.0;
+        if (!(norm <= 1.7e308)) rest = __builtin_nan("");
+        p.first[z] = static_cast<float>(rest);
+    }
+    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64, c0 = static_cast<int64_t>(blockIdx.x) * 64;
+    const TI *g = static_cast<const TI *>(p.g) + z * p.batch_g;
+    const int c = t & 63;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int r = w * 16 + i;
+        float v = 0.f;
+        if (r0 + r < p.rows && c0 + c < p.cols)
+            v = ldexpf(static_cast<float>(g[(r0 + r) * p.ld + c0 + c]), 12 - e);
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+            const f16 x = static_cast<f16>(v);
+            p.same[z * p.batch + q * p.plane + (r0 + r) * p.ld_same + c0 + c] = x;
+            tile[q][c][r] = x;
+            v -= static_cast<float>(x);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < PL; ++q)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int r = w * 16 + i;
+            p.turned[z * p.batch + q * p.plane + (c0 + r) * p.ld_turned + r0 + c] = tile[q][r][c];
+        }
+}
+
+// ---- host -------------------------------------------------------------------------------------------
+
+struct NewtonSpace {
+    f16 *x, *xt[2], *a, *q;
+    float *first;
+    double *partial;
+    int64_t s, l;           // padded
+    int64_t plane_x, plane_a;
+    int32_t planes;
+    int32_t tile;
+    size_t bytes;
+};
+
+// Tile edge: 128 keeps a compute unit's matrix units busy from one LDS read per two products; 64 where
+// 128 would leave most compute units without a tile.
+int32_t tile_for(int64_t rows, int64_t cols, int64_t batch) {
+    const int64_t s = rows < cols ? rows : cols, l = rows < cols ? cols : rows;
+    return batch * ((s + 127) / 128) * ((l + 127) / 128) >= 128 ? 128 : 64;
+}
+
+NewtonSpace carve_newton(int64_t rows, int64_t cols, int64_t batch, int32_t type, char *base) {
+    NewtonSpace n{};
+    n.planes = type == GNN_F32 ? 2 : 1;
+    n.tile = tile_for(rows, cols, batch);
+    const int64_t s = rows < cols ? rows : cols, l = rows < cols ? cols : rows;
+    n.s = (s + n.tile - 1) / n.tile * n.tile;
+    n.l = (l + n.tile - 1) / n.tile * n.tile;
+    n.plane_x = n.s * n.l;
+    n.plane_a = n.s * n.s;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        off = (off + 255) & ~static_cast<size_t>(255);
+        char *p = base ? base + off : nullptr;
+        off += bytes;
+        return p;
+    };
+    const size_t x = static_cast<size_t>(batch * n.planes * n.plane_x) * sizeof(f16);
+    const size_t a = static_cast<size_t>(batch * n.planes * n.plane_a) * sizeof(f16);
+    n.x = reinterpret_cast<f16 *>(take(x));
+    n.xt[0] = reinterpret_cast<f16 *>(take(x));
+    n.xt[1] = reinterpret_cast<f16 *>(take(x));
+    n.a = reinterpret_cast<f16 *>(take(a));
+    n.q = reinterpret_cast<f16 *>(take(a));
+    n.partial = reinterpret_cast<double *>(take(static_cast<size_t>(batch) * kNormBlocks * 8));
+    n.first = reinterpret_cast<float *>(take(static_cast<size_t>(batch) * 4));
+    n.bytes = off;
+    return n;
+}
+
+template <int PL, typename TO>
+hipError_t launch_product(const ProductArgs &p, int tile, int64_t batch, hipStream_t s) {
+    const bool symmetric = p.what == kGram || p.what == kPoly;
+    const int64_t tiles = symmetric ? static_cast<int64_t>(p.m_tiles) * (p.m_tiles + 1) / 2
+                                    : static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(batch));
+    if (tile == 128)
+        hipLaunchKernelGGL((k_newton_product<128, 128, 2, 2, PL, TO>), grid, dim3(256), 0, s, p);
+    else
+        hipLaunchKernelGGL((k_newton_product<64, 64, 2, 2, PL, TO>), grid, dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+template <int PL, typename T>
+hipError_t run_newton(const NewtonArgs &a, hipStream_t s) {
+    const NewtonSpace n = carve_newton(a.rows, a.cols, a.batch, a.type, a.ws);
+    const bool wide = a.rows <= a.cols;
+    const int64_t bx = PL * n.plane_x, ba = PL * n.plane_a;
+    PrepArgs p{};
+    p.g = a.g;
+    p.rows = a.rows;
+    p.cols = a.cols;
+    p.ld = a.ld_g;
+    p.batch_g = a.batch_g;
+    p.partial = n.partial;
+    const int64_t want = (a.rows + 3) / 4;
+    p.blocks = static_cast<int32_t>(want < kNormBlocks ? want : kNormBlocks);
+    p.eps = a.eps;
+    p.first = n.first;
+    p.same = wide ? n.x : n.xt[0];
+    p.turned = wide ? n.xt[0] : n.x;
+    p.ld_same = wide ? n.l : n.s;
+    p.ld_turned = wide ? n.s : n.l;
+    p.plane = n.plane_x;
+    p.batch = bx;
+    const unsigned nb = static_cast<unsigned>(a.batch);
+    hipLaunchKernelGGL((k_norm_squares<T>), dim3(static_cast<unsigned>(p.blocks), nb),
+                       dim3(kNormThreads), 0, s, p);
+    const int64_t pr = wide ? n.s : n.l, pc = wide ? n.l : n.s;
+    hipLaunchKernelGGL((k_first_planes<T, PL>),
+                       dim3(static_cast<unsigned>(pc / 64), static_cast<unsigned>(pr / 64), nb),
+                       dim3(kNormThreads), 0, s, p);
+    hipError_t err = hipGetLastError();
+    for (int step = 0; step < a.steps && err == hipSuccess; ++step) {
+        const float *first = step == 0 ? n.first : nullptr;
+        const bool last = step + 1 == a.steps;
+        ProductArgs g{};
+        g.what = kGram;
+        g.a = g.b = n.x;
+        g.ld_a = g.ld_b = g.k = n.l;
+        g.plane_a = g.plane_b = n.plane_x;
+        g.batch_a = g.batch_b = bx;
+        g.c = g.t = n.a;
+        g.ld_c = g.ld_t = n.s;
+        g.plane_c = g.plane_t = n.plane_a;
+        g.batch_c = g.batch_t = ba;
+        g.m_tiles = g.n_tiles = static_cast<int32_t>(n.s / n.tile);
+        g.first = first;
+        err = launch_product<PL, T>(g, n.tile, a.batch, s);
+        if (err != hipSuccess) return err;
+        ProductArgs q = g;
+        q.what = kPoly;
+        q.a = q.b = n.a;
+        q.ld_a = q.ld_b = q.k = n.s;
+        q.plane_a = q.plane_b = n.plane_a;
+        q.batch_a = q.batch_b = ba;
+        q.c = q.t = n.q;
+        q.ca = a.coefs[0];
+        q.cb = a.coefs[1];
+        q.cc = a.coefs[2];
+        q.first = nullptr;
+        err = launch_product<PL, T>(q, n.tile, a.batch, s);
+        if (err != hipSuccess) return err;
+        ProductArgs y{};
+        y.what = last ? kLast : kApply;
+        y.a = n.xt[step & 1];
+        y.ld_a = y.k = n.s;
+        y.plane_a = n.plane_x;
+        y.batch_a = bx;
+        y.b = n.q;
+        y.ld_b = n.s;
+        y.plane_b = n.plane_a;
+        y.batch_b = ba;
+        y.c = n.xt[(step + 1) & 1];
+        y.ld_c = n.s;
+        y.plane_c = y.plane_t = n.plane_x;
+        y.batch_c = y.batch_t = bx;
+        y.t = n.x;
+        y.ld_t = n.l;
+        y.m_tiles = static_cast<int32_t>(n.l / n.tile);
+        y.n_tiles = static_cast<int32_t>(n.s / n.tile);
+        y.first = first;
+        y.out = a.out;
+        y.ld_out = a.ld_out;
+        y.batch_out = a.batch_out;
+        y.m = wide ? a.cols : a.rows;
+        y.n = wide ? a.rows : a.cols;
+        y.out_rows = wide ? 0 : 1;
+        y.scale = a.scale;
+        err = launch_product<PL, T>(y, n.tile, a.batch, s);
+    }
+    return err;
+}
+
+}  // namespace
+
+size_t newton_bytes(int64_t rows, int64_t cols, int64_t batch, int32_t type) {
+    return carve_newton(rows, cols, batch, type, nullptr).bytes;
+}
+
+// The largest singular value that the steps can reach from [0, 1], and the largest of
+// |a + b t + c t^2| on their squares; both bound the stored entries.
+bool newton_in_range(const float *coefs, int steps) {
+    const double a = coefs[0], b = coefs[1], c = coefs[2];
+    double top = 1.0;
+    for (int k = 0; k < steps; ++k) {
+        double next = 0.0, q = 0.0;
+        auto look = [&](double s) {
+            if (!(s >= 0 && s <= top)) return;
+            const double t = s * s, v = a + b * t + c * t * t;
+            next = fmax(next, fabs(s * v));
+            q = fmax(q, fabs(v));
+        };
+        look(0.0);
+        look(top);
+        if (c != 0) {
+            look(sqrt(fmax(0.0, -b / (2 * c))));                 // of a + b t + c t^2
+            const double root = sqrt(fmax(0.0, 9 * b * b - 20 * a * c));
+            look(sqrt(fmax(0.0, (-3 * b + root) / (10 * c))));   // of a s + b s^3 + c s^5
+            look(sqrt(fmax(0.0, (-3 * b - root) / (10 * c))));
+        } else if (b != 0) {
+            look(sqrt(fmax(0.0, -a / (3 * b))));
+        }
+        if (!(next <= 3.0 && q <= 15.0)) return false;
+        top = fmax(next, 1e-30);
+    }
+    return true;
+}
+
+hipError_t launch_newton(const NewtonArgs &a, hipStream_t s) {
+    return a.type == GNN_F32 ? run_newton<2, float>(a, s) : run_newton<1, bf16>(a, s);
+}
+
+}  // namespace gnnmb

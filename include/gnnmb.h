@@ -556,6 +556,29 @@ gnn_status gnn_embedding_grad_rows(const int32_t *ids, const int64_t *d_n, int64
                                    size_t ws_bytes, gnn_stream stream);
 
 /*
+ * Orthogonalises the updates of `batch` weight matrices of one shape, as the Muon optimiser does
+ * with its momentum.  With X = G / (|G|_F + eps), `steps` times (1..16):
+ *   A = X X^T,  X <- (c[0] I + c[1] A + c[2] A^2) X      (X^T X on the right where rows > cols),
+ * then out = scale * X.  Every singular value s of X goes to c[0] s + c[1] s^3 + c[2] s^5; the
+ * default coefficients (coefs = NULL: 3.4445, -4.7750, 2.0315) bring those above about 1/500 near 1
+ * in five steps.  coefs: host [3].
+ *   g, out: device, batch matrices [rows, ld] with stride elements from one to the next, of type
+ *     GNN_F32 or GNN_BF16; out may be g.  Sums are fp32; the products carry 22 bits of X for
+ *     GNN_F32 and 11 for GNN_BF16.  A zero update gives zeros; one that is not finite gives NaN.
+ *     Entries are kept relative to max(1, eps / |G|_F): precision falls where |G|_F < eps / 256.
+ *   ws: ws_bytes >= gnn_orthogonalize_workspace_size(batch, rows, cols, type).
+ * Errors: GNN_ERR_INVALID_ARG; GNN_ERR_CAPACITY (ws too small); GNN_ERR_UNSUPPORTED for another
+ * type, rows or cols over 32768, batch over 65535, steps over 16, or coefficients that can drive
+ * a singular value of at most 1 beyond 3 or have |c[0] + c[1] s^2 + c[2] s^4| beyond 15.
+ */
+gnn_status gnn_orthogonalize_workspace_size(int64_t batch, int64_t rows, int64_t cols, int32_t type,
+                                            size_t *out_bytes);
+gnn_status gnn_orthogonalize(const void *g, int32_t type, int64_t batch, int64_t rows, int64_t cols,
+                             int64_t ld_g, int64_t stride_g, int32_t steps, const float *coefs,
+                             float eps, float scale, void *out, int64_t ld_out, int64_t stride_out,
+                             void *ws, size_t ws_bytes, gnn_stream stream);
+
+/*
  * Device status word of a workspace: synchronises `stream`, returns the first device error
  * recorded by the last call that used ws (GNN_OK if none) in *out (host).
  */
