@@ -484,6 +484,7 @@ size_t newton_bytes(int64_t rows, int64_t cols, int64_t batch, int32_t type) {
 // |a + b t + c t^2| on their squares; both bound the stored entries.
 bool newton_in_range(const float *coefs, int steps) {
     const double a = coefs[0], b = coefs[1], c = coefs[2];
+    if (!isfinite(a) || !isfinite(b) || !isfinite(c)) return false;
     double top = 1.0;
     for (int k = 0; k < steps; ++k) {
         double next = 0.0, q = 0.0;
