@@ -31,6 +31,7 @@ __all__ = [
     "gnn_host_mapped_pointer",
     "gnn_embedding_lookup", "gnn_embedding_grad", "gnn_embedding_grad_rows",
     "gnn_embedding_grad_workspace_size", "gnn_orthogonalize", "gnn_orthogonalize_workspace_size",
+    "gnn_cross_attention", "gnn_cross_attention_backward", "gnn_cross_attention_workspace_size",
     "gnn_read_device_status", "gnn_timer_create", "gnn_timer_destroy", "gnn_timer_reset",
     "gnn_timer_elapsed", "gnn_copy_probe", "gnn_copy_probe_host", "gnn_hash_probe", "lib",
 ]
@@ -732,6 +733,101 @@ def gnn_embedding_grad_rows(ids: torch.Tensor, dout: torch.Tensor, scale: float,
                                       grad.data_ptr(), gt, _ld(grad), _ptr(d_status),
                                       ws.data_ptr(), ws.numel() * ws.element_size(),
                                       _stream(stream)), "gnn_embedding_grad_rows")
+
+
+def gnn_cross_attention_workspace_size(n_seq: int, n_q: int, n_k: int, max_q: int, max_k: int,
+                                       heads: int, kv_heads: int, head_dim: int, dtype,
+                                       backward: bool = False) -> int:
+    x = _abi.gnn_attention(_type(dtype, "dtype"), heads, kv_heads, head_dim, n_seq, n_q, n_k, max_q,
+                           max_k)
+    b = ctypes.c_size_t(0)
+    _ok(lib().gnn_cross_attention_workspace_size(ctypes.byref(x), 1 if backward else 0,
+                                                 ctypes.byref(b)),
+        "gnn_cross_attention_workspace_size")
+    return int(b.value)
+
+
+def _head_rows(t: torch.Tensor, dtype, heads: int, head_dim: int, name: str) -> int:
+    """Checks a [rows, heads, head_dim] device tensor whose rows are contiguous; its row stride."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or \
+            (head_dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{name}: must be [rows, {heads}, {head_dim}] with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else heads * head_dim
+
+
+def _attention(q, k, v, q_indptr, k_indptr, max_q, max_k, scale, out, lse, k_count, d_status):
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q: [n_q, heads, head_dim]; k: [n_k, kv_heads, head_dim]")
+    heads, d, kv = q.shape[1], q.shape[2], k.shape[1]
+    kind = _type(q.dtype, "q")
+    ld_q = _head_rows(q, q.dtype, heads, d, "q")
+    ld_k = _head_rows(k, q.dtype, kv, d, "k")
+    ld_v = _head_rows(v, q.dtype, kv, d, "v")
+    ld_out = _head_rows(out, q.dtype, heads, d, "out")
+    _need(q_indptr, torch.int32, "q_indptr")
+    _need(k_indptr, torch.int32, "k_indptr")
+    n_seq = q_indptr.numel() - 1
+    if n_seq < 0 or k_indptr.numel() != n_seq + 1:
+        raise ValueError("q_indptr, k_indptr: [n_seq + 1] each")
+    if v.shape[0] != k.shape[0] or out.shape[0] != q.shape[0]:
+        raise ValueError("v: as many rows as k; out: as many rows as q")
+    if k_count is not None:
+        _need(k_count, torch.int64, "k_count")
+        if k_count.numel() != n_seq:
+            raise ValueError("k_count: [n_seq]")
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        if lse.numel() != q.shape[0] * heads:
+            raise ValueError("lse: [n_q, heads]")
+    if d_status is not None:
+        _need(d_status, torch.int32, "d_status")
+    return _abi.gnn_attention(
+        kind, heads, kv, d, n_seq, q.shape[0], k.shape[0], max_q, max_k, scale, q_indptr.data_ptr(),
+        k_indptr.data_ptr(), None if k_count is None else k_count.data_ptr(), q.data_ptr(),
+        k.data_ptr(), v.data_ptr(), ld_q, ld_k, ld_v, out.data_ptr(), ld_out,
+        None if lse is None else lse.data_ptr(), None if d_status is None else d_status.data_ptr())
+
+
+def gnn_cross_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_indptr: torch.Tensor,
+                        k_indptr: torch.Tensor, max_q: int, max_k: int, scale: float,
+                        out: torch.Tensor, ws: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                        k_count: Optional[torch.Tensor] = None,
+                        d_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out[i, h] = softmax(scale q[i, h] . k) v over the states of i's sequence; lse [n_q, heads] the
+    log of the weights' sum.  q, out: [n_q, heads, head_dim]; k, v: [n_k, kv_heads, head_dim]."""
+    x = _attention(q, k, v, q_indptr, k_indptr, max_q, max_k, scale, out, lse, k_count, d_status)
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws: must be a contiguous device tensor")
+    _ok(lib().gnn_cross_attention(ctypes.byref(x), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                  _stream(stream)), "gnn_cross_attention")
+
+
+def gnn_cross_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                 q_indptr: torch.Tensor, k_indptr: torch.Tensor, max_q: int,
+                                 max_k: int, scale: float, out: torch.Tensor, lse: torch.Tensor,
+                                 dout: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor,
+                                 dv: torch.Tensor, ws: torch.Tensor,
+                                 k_count: Optional[torch.Tensor] = None,
+                                 d_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dq, dk, dv of gnn_cross_attention from its out and lse and the gradient dout of out."""
+    x = _attention(q, k, v, q_indptr, k_indptr, max_q, max_k, scale, out, lse, k_count, d_status)
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws: must be a contiguous device tensor")
+    heads, d, kv = q.shape[1], q.shape[2], k.shape[1]
+    g = _abi.gnn_attention_grad(
+        dout.data_ptr(), _head_rows(dout, q.dtype, heads, d, "dout"), dq.data_ptr(), dk.data_ptr(),
+        dv.data_ptr(), _head_rows(dq, q.dtype, heads, d, "dq"),
+        _head_rows(dk, q.dtype, kv, d, "dk"), _head_rows(dv, q.dtype, kv, d, "dv"))
+    if dout.shape[0] != q.shape[0] or dq.shape[0] != q.shape[0] or dk.shape[0] != k.shape[0] or \
+            dv.shape[0] != k.shape[0]:
+        raise ValueError("dout, dq: as many rows as q; dk, dv: as many rows as k")
+    _ok(lib().gnn_cross_attention_backward(ctypes.byref(x), ctypes.byref(g), ws.data_ptr(),
+                                           ws.numel() * ws.element_size(), _stream(stream)),
+        "gnn_cross_attention_backward")
 
 
 def gnn_orthogonalize_workspace_size(batch: int, rows: int, cols: int, dtype) -> int:

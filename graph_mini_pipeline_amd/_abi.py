@@ -80,6 +80,19 @@ class gnn_minibatch_out(ctypes.Structure):
     _fields_ = [("blocks", gnn_blocks), ("x", vp), ("h", vp * GNN_MAX_HOPS), ("ld_h", i64)]
 
 
+class gnn_attention(ctypes.Structure):
+    _fields_ = [("type", i32), ("heads", i32), ("kv_heads", i32), ("head_dim", i32), ("n_seq", i64),
+                ("n_q", i64), ("n_k", i64), ("max_q", i64), ("max_k", i64), ("scale", f32),
+                ("q_indptr", vp), ("k_indptr", vp), ("k_count", vp), ("q", vp), ("k", vp), ("v", vp),
+                ("ld_q", i64), ("ld_k", i64), ("ld_v", i64), ("out", vp), ("ld_out", i64),
+                ("lse", vp), ("d_status", vp)]
+
+
+class gnn_attention_grad(ctypes.Structure):
+    _fields_ = [("dout", vp), ("ld_dout", i64), ("dq", vp), ("dk", vp), ("dv", vp), ("ld_dq", i64),
+                ("ld_dk", i64), ("ld_dv", i64)]
+
+
 P = ctypes.POINTER
 
 # name -> (restype, argtypes); every entry point the header declares
@@ -121,6 +134,9 @@ SIGNATURES = {
                                  vp, size_t, vp]),
     "gnn_embedding_grad_rows": (i32, [vp, vp, i64, vp, i32, i64, f32, i32, i64, i64, vp, i64, vp, vp,
                                       i32, i64, vp, vp, size_t, vp]),
+    "gnn_cross_attention_workspace_size": (i32, [P(gnn_attention), i32, P(size_t)]),
+    "gnn_cross_attention": (i32, [P(gnn_attention), vp, size_t, vp]),
+    "gnn_cross_attention_backward": (i32, [P(gnn_attention), P(gnn_attention_grad), vp, size_t, vp]),
     "gnn_orthogonalize_workspace_size": (i32, [i64, i64, i64, i32, P(size_t)]),
     "gnn_orthogonalize": (i32, [vp, i32, i64, i64, i64, i64, i64, i32, P(f32), f32, f32, vp, i64, i64,
                                 vp, size_t, vp]),

@@ -1764,6 +1764,107 @@ gnn_status gnn_embedding_grad_rows(const int32_t *ids, const int64_t *d_n, int64
     return embedding_grad(a, ws, ws_bytes, stream);
 }
 
+// ---- cross attention ------------------------------------------------------------------------------
+
+namespace {
+constexpr int32_t kAttendMaxDim = 128;
+constexpr int32_t kAttendMaxHeads = 1024;
+
+gnn_status attend_sizes(const gnn_attention *x, AttendArgs *a) {
+    if (!x || x->heads < 1 || x->kv_heads < 1 || x->head_dim < 1 || x->n_seq < 0 || x->n_q < 0 ||
+        x->n_k < 0 || x->max_q < 0 || x->max_k < 0)
+        return GNN_ERR_INVALID_ARG;
+    if (x->heads % x->kv_heads != 0) return GNN_ERR_INVALID_ARG;
+    if (!known_type(x->type) || x->head_dim % 8 != 0 || x->head_dim > kAttendMaxDim ||
+        x->heads > kAttendMaxHeads || x->n_seq > 65535 || x->n_q > kInt32Max || x->n_k > kInt32Max)
+        return GNN_ERR_UNSUPPORTED;
+    *a = AttendArgs{};
+    a->type = x->type;
+    a->heads = x->heads;
+    a->kv = x->kv_heads;
+    a->group = x->heads / x->kv_heads;
+    a->d = x->head_dim;
+    a->n_seq = x->n_seq;
+    a->n_q = x->n_q;
+    a->n_k = x->n_k;
+    // no sequence is longer than all rows
+    a->max_q = x->max_q < x->n_q ? x->max_q : x->n_q;
+    a->max_k = x->max_k < x->n_k ? x->max_k : x->n_k;
+    if (x->n_q * x->heads > kInt32Max || x->n_k * x->kv_heads > kInt32Max) return GNN_ERR_UNSUPPORTED;
+    return GNN_OK;
+}
+
+gnn_status attend_args(const gnn_attention *x, AttendArgs *a) {
+    GNN_TRY(attend_sizes(x, a));
+    const int64_t wq = static_cast<int64_t>(x->heads) * x->head_dim;
+    const int64_t wk = static_cast<int64_t>(x->kv_heads) * x->head_dim;
+    if (x->ld_q < wq || x->ld_out < wq || x->ld_k < wk || x->ld_v < wk) return GNN_ERR_INVALID_ARG;
+    if (x->n_seq > 0 && (!x->q_indptr || !x->k_indptr)) return GNN_ERR_INVALID_ARG;
+    if (x->n_q > 0 && (!x->q || !x->out)) return GNN_ERR_INVALID_ARG;
+    if (x->n_k > 0 && (!x->k || !x->v)) return GNN_ERR_INVALID_ARG;
+    if (x->scale != x->scale) return GNN_ERR_INVALID_ARG;
+    a->scale = x->scale;
+    a->q_indptr = x->q_indptr;
+    a->k_indptr = x->k_indptr;
+    a->k_count = x->k_count;
+    a->q = x->q;
+    a->k = x->k;
+    a->v = x->v;
+    a->ld_q = x->ld_q;
+    a->ld_k = x->ld_k;
+    a->ld_v = x->ld_v;
+    a->out = x->out;
+    a->ld_out = x->ld_out;
+    a->lse = x->lse;
+    a->status = x->d_status;
+    return GNN_OK;
+}
+}  // namespace
+
+gnn_status gnn_cross_attention_workspace_size(const gnn_attention *x, int32_t backward,
+                                              size_t *out_bytes) {
+    if (!out_bytes) return GNN_ERR_INVALID_ARG;
+    AttendArgs a;
+    GNN_TRY(attend_sizes(x, &a));
+    const size_t f = attend_bytes(a, false), b = backward ? attend_bytes(a, true) : 0;
+    *out_bytes = f > b ? f : b;
+    return GNN_OK;
+}
+
+gnn_status gnn_cross_attention(const gnn_attention *x, void *ws, size_t ws_bytes, gnn_stream stream) {
+    AttendArgs a;
+    GNN_TRY(attend_args(x, &a));
+    if (!ws) return GNN_ERR_INVALID_ARG;
+    if (ws_bytes < attend_bytes(a, false)) return GNN_ERR_CAPACITY;
+    if (fault(kFaultLaunch)) return GNN_ERR_HIP;
+    GNN_TRY_HIP(launch_attend(a, false, static_cast<char *>(ws), static_cast<hipStream_t>(stream)));
+    return GNN_OK;
+}
+
+gnn_status gnn_cross_attention_backward(const gnn_attention *x, const gnn_attention_grad *g, void *ws,
+                                        size_t ws_bytes, gnn_stream stream) {
+    AttendArgs a;
+    GNN_TRY(attend_args(x, &a));
+    if (!g || !ws) return GNN_ERR_INVALID_ARG;
+    const int64_t wq = static_cast<int64_t>(x->heads) * x->head_dim;
+    const int64_t wk = static_cast<int64_t>(x->kv_heads) * x->head_dim;
+    if (g->ld_dout < wq || g->ld_dq < wq || g->ld_dk < wk || g->ld_dv < wk) return GNN_ERR_INVALID_ARG;
+    if (x->n_q > 0 && (!x->lse || !g->dout || !g->dq)) return GNN_ERR_INVALID_ARG;
+    if (x->n_k > 0 && (!g->dk || !g->dv)) return GNN_ERR_INVALID_ARG;
+    if (ws_bytes < attend_bytes(a, true)) return GNN_ERR_CAPACITY;
+    if (fault(kFaultLaunch)) return GNN_ERR_HIP;
+    a.dout = g->dout;
+    a.ld_dout = g->ld_dout;
+    a.dq = g->dq;
+    a.dk = g->dk;
+    a.dv = g->dv;
+    a.ld_dq = g->ld_dq;
+    a.ld_dk = g->ld_dk;
+    a.ld_dv = g->ld_dv;
+    GNN_TRY_HIP(launch_attend(a, true, static_cast<char *>(ws), static_cast<hipStream_t>(stream)));
+    return GNN_OK;
+}
+
 // ---- orthogonalised updates -----------------------------------------------------------------------
 
 namespace {

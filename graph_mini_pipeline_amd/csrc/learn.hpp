@@ -72,6 +72,35 @@ struct EmbedGradArgs {
 size_t embedding_grad_bytes(int64_t n, int64_t num_rows, int64_t d);
 hipError_t launch_embedding_grad(const EmbedGradArgs &a, hipStream_t s);
 
+// ---- cross attention ------------------------------------------------------------------------------
+
+struct AttendArgs {
+    int32_t type, heads, kv, group, d;     // group = heads / kv
+    int64_t n_seq, n_q, n_k, max_q, max_k;
+    float scale, scale2;                   // scale2 = scale * log2(e)
+    const int32_t *q_indptr, *k_indptr;
+    const int64_t *k_count;
+    const void *q, *k, *v;
+    int64_t ld_q, ld_k, ld_v;
+    void *out;                             // backward: read
+    int64_t ld_out;
+    float *lse;                            // [n_q, heads]; backward: read
+    int32_t *status;
+    // backward
+    const void *dout;
+    int64_t ld_dout;
+    void *dq, *dk, *dv;
+    int64_t ld_dq, ld_dk, ld_dv;
+    // set by the launcher
+    FastDiv by_group;
+    int32_t splits;
+    float2 *stat;          // [n_q * heads] {lse log2(e), dout . out}
+    float *part;           // partial sums of the splits
+    float2 *part_stat;     // [splits, n_q * heads] {maximum, sum}
+};
+size_t attend_bytes(const AttendArgs &a, bool backward);
+hipError_t launch_attend(AttendArgs a, bool backward, char *ws, hipStream_t s);
+
 // ---- orthogonalised updates -----------------------------------------------------------------------
 
 struct NewtonArgs {

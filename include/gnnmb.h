@@ -556,6 +556,60 @@ gnn_status gnn_embedding_grad_rows(const int32_t *ids, const int64_t *d_n, int64
                                    size_t ws_bytes, gnn_stream stream);
 
 /*
+ * Cross attention of queries to the states of their own sequence, whose number is another one for
+ * each (a sub-batch's text or readout attending to the nodes that were sampled for it).  Rows are
+ * packed: sequence b's queries are rows q_indptr[b] .. q_indptr[b+1]-1 of q, its states rows
+ * k_indptr[b] .. k_indptr[b+1]-1 of k and v (device int32 [n_seq+1]; a block's indptr is one), of which
+ * the first k_count[b] count (device int64 [n_seq]; NULL: all).  For every query row i and head h:
+ *   S_j = scale q[i, h] . k[j, h'],  h' = h / (heads / kv_heads),
+ *   lse[i, h] = log sum_j exp(S_j),  out[i, h] = sum_j exp(S_j - lse) v[j, h'];
+ * without a state, out = 0 and lse = -inf.  States that do not count have no effect, whatever they
+ *   hold.
+ *   q, out: [n_q, ld] with heads * head_dim elements a row; k, v: [n_k, ld] with kv_heads * head_dim;
+ *   type GNN_F32 or GNN_BF16 (products and sums in fp32; for GNN_BF16 the weights exp(S - lse) are
+ *   rounded to bf16 before they multiply v).  lse: float [n_q, heads], may be NULL for
+ *   gnn_cross_attention.  max_q, max_k: host bounds on a sequence's queries and state rows.
+ *   Rows that belong to no sequence are left as they are.
+ * gnn_cross_attention_backward: with out and lse of the forward call and dout [n_q, ld_dout], writes
+ * dq, dk, dv of the same shapes (dk and dv zero for states that do not count), each summed in fp32
+ * in a fixed order and rounded once.  No output may overlap an input or another output.
+ *   ws: ws_bytes >= gnn_cross_attention_workspace_size(x, backward); x->type, heads, kv_heads,
+ *   head_dim, n_seq, n_q, n_k, max_q and max_k decide it.
+ * Device errors (in *d_status if not NULL): GNN_ERR_OUT_OF_RANGE (an indptr that decreases or
+ * leaves [0, n]; it is clamped), GNN_ERR_CAPACITY (a sequence longer than max_q or max_k; the rows
+ * beyond are left out).
+ * Errors: GNN_ERR_INVALID_ARG; GNN_ERR_CAPACITY (ws too small); GNN_ERR_UNSUPPORTED for another
+ * type, a head_dim that is no multiple of 8 or over 128, heads over 1024, n_seq over 65535, or
+ * n_q * heads or n_k * kv_heads over 2^31 - 1.
+ */
+typedef struct gnn_attention {
+    int32_t type, heads, kv_heads, head_dim;
+    int64_t n_seq, n_q, n_k, max_q, max_k;
+    float scale;
+    const int32_t *q_indptr, *k_indptr;
+    const int64_t *k_count;
+    const void *q, *k, *v;
+    int64_t ld_q, ld_k, ld_v;
+    void *out;
+    int64_t ld_out;
+    float *lse;
+    int32_t *d_status;
+} gnn_attention;
+
+typedef struct gnn_attention_grad {
+    const void *dout;
+    int64_t ld_dout;
+    void *dq, *dk, *dv;
+    int64_t ld_dq, ld_dk, ld_dv;
+} gnn_attention_grad;
+
+gnn_status gnn_cross_attention_workspace_size(const gnn_attention *x, int32_t backward,
+                                              size_t *out_bytes);
+gnn_status gnn_cross_attention(const gnn_attention *x, void *ws, size_t ws_bytes, gnn_stream stream);
+gnn_status gnn_cross_attention_backward(const gnn_attention *x, const gnn_attention_grad *g, void *ws,
+                                        size_t ws_bytes, gnn_stream stream);
+
+/*
  * Orthogonalises the updates of `batch` weight matrices of one shape, as the Muon optimiser does
  * with its momentum.  With X = G / (|G|_F + eps), `steps` times (1..16):
  *   A = X X^T,  X <- (c[0] I + c[1] A + c[2] A^2) X      (X^T X on the right where rows > cols),
