@@ -10,8 +10,9 @@
 //     that holds a tenth of all positions costs no more than any other tenth: a lane group walks
 //     one chunk, keeps one fp32 sum per column in registers, and stores it whenever the id changes.
 //     A run that lies within the chunk is final; the chunk's first and last run may go on beyond
-//     it, and their sums go to the workspace;
-//   - runs over several chunks are joined from these partial sums in chunk order.
+//     it, and leave a partial sum per chunk in the workspace;
+//   - those are joined in chunk order: a run of two chunks by a lane group, a longer one, which the
+//     first pass lists, by a workgroup.
 // No atomic touches a sum, so results do not depend on timing.
 #include "learn.hpp"
 
@@ -83,15 +84,17 @@ hipError_t pick_lookup(const LookupArgs &a, hipStream_t s) {
 // ---- the sort -----------------------------------------------------------------------------------
 //
 // Least-significant-digit radix sort of (key, position) by digits of at most 8 bits, stable.  A
-// workgroup of 16 wavefronts takes a tile of 8192 keys, 8 per thread; a wavefront's keys lie next
-// to each other, 64 a round, so the order (wavefront, round, lane) is the order of the positions.
-// Lanes with the same digit find each other by one ballot per bit of the digit.  Up to one tile of
-// keys is sorted by one workgroup in LDS in one launch.  Beyond that, each digit takes two
-// launches: digit counts of every tile, then the placement, where every tile sums the counts of the
-// tiles before it (beyond kSumTiles tiles a third launch does that once for all).
-constexpr int kSortThreads = 1024;
-constexpr int kSortWaves = kSortThreads / 64;
+// workgroup takes a tile of keys, 8 per thread; a wavefront's keys lie next to each other, 64 a
+// round, so the order (wavefront, round, lane) is the order of the positions.  Lanes with the same
+// digit find each other by one ballot per bit of the digit.  Up to 8192 keys are sorted by one
+// workgroup of 16 wavefronts in LDS in one launch.  Beyond that, each digit takes two launches over
+// tiles of 4096 keys: digit counts of every tile, then the placement, where every tile sums the
+// counts of the tiles before it (beyond kSumTiles tiles a third launch does that once for all).
 constexpr int kSortRounds = 8;
+constexpr int kOneThreads = 1024;                       // the one-workgroup sort
+constexpr int kOneTile = kOneThreads * kSortRounds;
+constexpr int kSortThreads = 512;                       // the tiled sort
+constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortTile = kSortThreads * kSortRounds;
 constexpr int kSortBits = 8;
 constexpr int kDigits = 1 << kSortBits;
@@ -112,8 +115,9 @@ struct SortArgs {
     int32_t scanned;
     int32_t shift, bits;
     // work of other parts of the gradient that rides along
-    uint32_t *touched;      // bitmap over the table's rows: cleared by the first count, marked by
-    int64_t touched_words;  // the first placement; NULL: none
+    uint8_t *touched;       // [num_rows] 1: some id names the row; cleared by the first count, marked
+    int64_t touched_words;  // by the first placement; NULL: none
+    uint32_t *long_runs;    // their number is cleared by the first count
     // run heads (one-tile sort of the rows form)
     int32_t rows;
     int32_t *uniq;
@@ -124,9 +128,9 @@ struct SortArgs {
     int32_t passes;
 };
 
-__device__ __forceinline__ uint32_t make_key(const SortArgs &a, int64_t i, int64_t n_act) {
+// The key of position i, which holds id.
+__device__ __forceinline__ uint32_t make_key(const SortArgs &a, int64_t i, int64_t n_act, int32_t id) {
     if (i >= n_act) return a.num_rows;
-    const int32_t id = a.ids[i];
     if (id < 0 || static_cast<uint32_t>(id) >= a.num_rows) {
         set_status(a.status, GNN_ERR_OUT_OF_RANGE);
         return a.num_rows;
@@ -134,21 +138,23 @@ __device__ __forceinline__ uint32_t make_key(const SortArgs &a, int64_t i, int64
     return id == a.pad_id ? a.num_rows : static_cast<uint32_t>(id);
 }
 
-__device__ __forceinline__ void mark_touched(const SortArgs &a, uint32_t key) {
-    if (key >= a.num_rows) return;
-    uint32_t *w = a.touched + (key >> 5);
-    const uint32_t bit = 1u << (key & 31);
-    if (!(__hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) & bit)) atomicOr(w, bit);
+// Clears the marks and the number of long runs; the grid's threads share the work.
+__device__ __forceinline__ void clear_marks(const SortArgs &a) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (t == 0) *a.long_runs = 0;
+    if (a.touched == nullptr) return;
+    uint32_t *w = reinterpret_cast<uint32_t *>(a.touched);
+    for (int64_t i = t; i < a.touched_words; i += static_cast<int64_t>(gridDim.x) * blockDim.x) w[i] = 0;
 }
 
 // Ranks each round's keys among the wavefront's earlier keys of the same digit; cnt (this
 // wavefront's digit counts, zero before) receives the counts.
-__device__ __forceinline__ void rank_rounds(const uint32_t (&key)[kSortRounds], int rounds,
-                                            int shift, int bits, uint32_t *cnt,
-                                            uint32_t (&rank)[kSortRounds]) {
+template <int ROUNDS>
+__device__ __forceinline__ void rank_rounds(const uint32_t (&key)[ROUNDS], int rounds, int shift,
+                                            int bits, uint32_t *cnt, uint32_t (&rank)[ROUNDS]) {
     const uint64_t below = (1ull << lane_id()) - 1ull;
 #pragma unroll
-    for (int j = 0; j < kSortRounds; ++j) {
+    for (int j = 0; j < ROUNDS; ++j) {
         if (j >= rounds) break;
         const uint32_t dg = (key[j] >> shift) & ((1u << bits) - 1u);
         uint64_t same = ~0ull;
@@ -182,18 +188,22 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(SortArgs a) {
     __shared__ uint32_t h[kDigits];
     const int t = threadIdx.x;
     if (t < kDigits) h[t] = 0;
-    if (a.touched != nullptr && a.key_in == nullptr)
-        for (int64_t w = static_cast<int64_t>(blockIdx.x) * kSortThreads + t; w < a.touched_words;
-             w += static_cast<int64_t>(gridDim.x) * kSortThreads)
-            a.touched[w] = 0;
-    __syncthreads();
+    if (a.key_in == nullptr) clear_marks(a);
     const int64_t n_act = load_count(a.d_n, a.n);
     const int64_t tile0 = static_cast<int64_t>(blockIdx.x) * kSortTile;
+    const int32_t *in = a.key_in ? reinterpret_cast<const int32_t *>(a.key_in) : a.ids;
+    int32_t x[kSortRounds];
+#pragma unroll
+    for (int j = 0; j < kSortRounds; ++j) {
+        const int64_t i = tile0 + j * kSortThreads + t;
+        x[j] = in[i < a.n ? i : a.n - 1];
+    }
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < kSortRounds; ++j) {
         const int64_t i = tile0 + j * kSortThreads + t;
         if (i >= a.n) continue;
-        const uint32_t key = a.key_in ? a.key_in[i] : make_key(a, i, n_act);
+        const uint32_t key = a.key_in ? static_cast<uint32_t>(x[j]) : make_key(a, i, n_act, x[j]);
         atomicAdd(&h[(key >> a.shift) & ((1u << a.bits) - 1u)], 1u);
     }
     __syncthreads();
@@ -227,20 +237,22 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs a) {
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortTile + w * (64 * kSortRounds) +
                        lane_id();
     uint32_t key[kSortRounds], pos[kSortRounds], rank[kSortRounds];
+    const bool given = a.key_in != nullptr;
+    const int32_t *in = given ? reinterpret_cast<const int32_t *>(a.key_in) : a.ids;
+#pragma unroll
+    for (int j = 0; j < kSortRounds; ++j) {
+        const int64_t i = i0 + j * 64 < a.n ? i0 + j * 64 : a.n - 1;
+        key[j] = static_cast<uint32_t>(in[i]);
+        pos[j] = given ? a.pos_in[i] : static_cast<uint32_t>(i);
+    }
 #pragma unroll
     for (int j = 0; j < kSortRounds; ++j) {
         const int64_t i = i0 + j * 64;
-        key[j] = 0xffffffffu;        // beyond the end: ranked after every key of the last tile
-        pos[j] = 0;
-        if (i < a.n) {
-            if (a.key_in) {
-                key[j] = a.key_in[i];
-                pos[j] = a.pos_in[i];
-            } else {
-                key[j] = make_key(a, i, n_act);
-                pos[j] = static_cast<uint32_t>(i);
-                if (a.touched) mark_touched(a, key[j]);
-            }
+        if (i >= a.n) {
+            key[j] = 0xffffffffu;        // beyond the end: ranked after every key of the last tile
+        } else if (!given) {
+            key[j] = make_key(a, i, n_act, static_cast<int32_t>(key[j]));
+            if (a.touched && key[j] < a.num_rows) a.touched[key[j]] = 1;
         }
     }
     // counts of the tiles before this one and of all tiles, four threads per digit
@@ -262,7 +274,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs a) {
     sums[0][part][dg] = before;
     sums[1][part][dg] = total;
     __syncthreads();
-    rank_rounds(key, kSortRounds, a.shift, a.bits, cnt[w], rank);
+    rank_rounds<kSortRounds>(key, kSortRounds, a.shift, a.bits, cnt[w], rank);
     __syncthreads();
     before = total = 0;
     if (t < kDigits) {
@@ -290,89 +302,105 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs a) {
     }
 }
 
-// Writes the distinct ids among sorted positions [i0, i0 + 8 * threads), given the number of run
-// heads before i0, and the rank of the run at each chunk's start.  Returns the tile's heads.
 __device__ __forceinline__ bool is_head(uint32_t key, uint32_t prev, bool first, uint32_t rows) {
     return key < rows && (first || key != prev);
 }
 
-__global__ __launch_bounds__(kSortThreads) void k_sort_tile(SortArgs a) {
-    __shared__ uint32_t skey[kSortTile];
-    __shared__ uint16_t spos[kSortTile];
-    __shared__ uint32_t cnt[kSortWaves][kDigits];
-    __shared__ uint32_t base[kDigits];
-    __shared__ uint32_t s4[4];
-    __shared__ uint32_t sw[kSortWaves];
+// The one-workgroup sort: n <= ROUNDS * 1024 positions, sorted, in key and pos.
+template <int ROUNDS>
+struct OneSort {
+    static constexpr int kWaves = kOneThreads / 64;
+    uint32_t key[ROUNDS * kOneThreads];
+    uint16_t pos[ROUNDS * kOneThreads];
+    uint32_t cnt[kWaves][kDigits];
+    uint32_t base[kDigits];
+    uint32_t s4[4];
+};
+
+// mark: every named row's mark is set.  Every thread of the workgroup calls it.
+template <int ROUNDS>
+__device__ __forceinline__ void sort_one(const SortArgs &a, OneSort<ROUNDS> &m, bool mark) {
+    constexpr int kWaves = OneSort<ROUNDS>::kWaves;
     const int t = threadIdx.x, w = t >> 6;
     const int n = static_cast<int>(a.n);
     const int64_t n_act = load_count(a.d_n, a.n);
-    const int rounds = (n + kSortThreads - 1) / kSortThreads;
+    const int rounds = (n + kOneThreads - 1) / kOneThreads;
     const int i0 = w * 64 * rounds + lane_id();
-    if (a.touched != nullptr) {
-        for (int64_t i = t; i < a.touched_words; i += kSortThreads) a.touched[i] = 0;
-        __threadfence();
-        __syncthreads();
-    }
-    uint32_t key[kSortRounds], rank[kSortRounds];
-    uint32_t pos[kSortRounds];
+    uint32_t key[ROUNDS], pos[ROUNDS], rank[ROUNDS];
 #pragma unroll
-    for (int j = 0; j < kSortRounds; ++j) {
-        key[j] = a.num_rows;        // slots beyond n: after every position of the same key
-        pos[j] = 0;
+    for (int j = 0; j < ROUNDS; ++j)
+        if (j < rounds) key[j] = static_cast<uint32_t>(a.ids[i0 + j * 64 < n ? i0 + j * 64 : n - 1]);
+#pragma unroll
+    for (int j = 0; j < ROUNDS; ++j) {
         if (j >= rounds) continue;
         const int i = i0 + j * 64;
         pos[j] = static_cast<uint32_t>(i);
-        if (i < n) key[j] = make_key(a, i, n_act);
-        if (a.touched) mark_touched(a, key[j]);
+        // slots beyond n: after every position of the same key
+        key[j] = i < n ? make_key(a, i, n_act, static_cast<int32_t>(key[j])) : a.num_rows;
+        if (mark && key[j] < a.num_rows) a.touched[key[j]] = 1;
     }
     for (int p = 0; p < a.passes; ++p) {
         const int shift = p * a.bits;
-        for (int i = t; i < kSortWaves * kDigits; i += kSortThreads) (&cnt[0][0])[i] = 0;
+        for (int i = t; i < kWaves * kDigits; i += kOneThreads) (&m.cnt[0][0])[i] = 0;
         __syncthreads();
-        rank_rounds(key, rounds, shift, a.bits, cnt[w], rank);
+        rank_rounds<ROUNDS>(key, rounds, shift, a.bits, m.cnt[w], rank);
         __syncthreads();
         uint32_t total = 0;
-        if (t < kDigits)
-            for (int q = 0; q < kSortWaves; ++q) {
-                const uint32_t c = cnt[q][t];
-                cnt[q][t] = total;
-                total += c;
+        if (t < kDigits) {
+            uint32_t c[kWaves];
+#pragma unroll
+            for (int q = 0; q < kWaves; ++q) c[q] = m.cnt[q][t];
+#pragma unroll
+            for (int q = 0; q < kWaves; ++q) {
+                m.cnt[q][t] = total;
+                total += c[q];
             }
-        const uint32_t ex = scan_digits(total, s4);
-        if (t < kDigits) base[t] = ex;
+        }
+        const uint32_t ex = scan_digits(total, m.s4);
+        if (t < kDigits) m.base[t] = ex;
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kSortRounds; ++j) {
+        for (int j = 0; j < ROUNDS; ++j) {
             if (j >= rounds) continue;
             const uint32_t g = (key[j] >> shift) & ((1u << a.bits) - 1u);
-            const uint32_t to = base[g] + cnt[w][g] + rank[j];
-            skey[to] = key[j];
-            spos[to] = static_cast<uint16_t>(pos[j]);
+            const uint32_t to = m.base[g] + m.cnt[w][g] + rank[j];
+            m.key[to] = key[j];
+            m.pos[to] = static_cast<uint16_t>(pos[j]);
         }
         __syncthreads();
+        if (p + 1 == a.passes) break;
 #pragma unroll
-        for (int j = 0; j < kSortRounds; ++j) {
+        for (int j = 0; j < ROUNDS; ++j) {
             if (j >= rounds) continue;
-            key[j] = skey[i0 + j * 64];
-            pos[j] = spos[i0 + j * 64];
+            key[j] = m.key[i0 + j * 64];
+            pos[j] = m.pos[i0 + j * 64];
         }
     }
-    // the last pass left the sorted list in LDS too
-#pragma unroll
-    for (int j = 0; j < kSortRounds; ++j) {
-        const int i = i0 + j * 64;
-        if (j >= rounds || i >= n) continue;
-        a.key_out[i] = key[j];
-        a.pos_out[i] = pos[j];
+}
+
+__global__ __launch_bounds__(kOneThreads) void k_sort_one(SortArgs a) {
+    __shared__ OneSort<kSortRounds> m;
+    __shared__ uint32_t sw[kOneThreads / 64];
+    const int t = threadIdx.x;
+    const int n = static_cast<int>(a.n);
+    clear_marks(a);
+    if (a.touched != nullptr) {
+        __threadfence();        // before the marks
+        __syncthreads();
+    }
+    sort_one<kSortRounds>(a, m, a.touched != nullptr);
+    for (int i = t; i < n; i += kOneThreads) {
+        a.key_out[i] = m.key[i];
+        a.pos_out[i] = m.pos[i];
     }
     if (!a.rows) return;
     uint32_t carry = 0;
-    for (int r0 = 0; r0 < n; r0 += kSortThreads) {
+    for (int r0 = 0; r0 < n; r0 += kOneThreads) {
         const int i = r0 + t;
-        const uint32_t k = i < n ? skey[i] : a.num_rows;
-        const uint32_t head = is_head(k, i > 0 ? skey[i < n ? i - 1 : 0] : 0u, i == 0, a.num_rows);
+        const uint32_t k = i < n ? m.key[i] : a.num_rows;
+        const uint32_t head = is_head(k, i > 0 ? m.key[i < n ? i - 1 : 0] : 0u, i == 0, a.num_rows);
         uint32_t total;
-        const uint32_t at = carry + block_exclusive_scan<uint32_t, kSortThreads>(head, &total, sw);
+        const uint32_t at = carry + block_exclusive_scan<uint32_t, kOneThreads>(head, &total, sw);
         if (head && at < a.row_cap) a.uniq[at] = static_cast<int32_t>(k);
         if (i < n && i % a.chunk == 0) a.chunk_rank[i / a.chunk] = at + head - 1u;
         carry += total;
@@ -446,6 +474,7 @@ __global__ __launch_bounds__(kSortThreads) void k_emit_heads(HeadArgs a) {
 
 constexpr int kSumThreads = 256;
 constexpr int kSumUnroll = 8;     // rows of dout in flight per lane
+constexpr int kJoinRuns = 512;    // workgroups per slab that share the listed runs
 
 struct SumArgs {
     const uint32_t *key, *pos;
@@ -465,7 +494,8 @@ struct SumArgs {
     int64_t chunks;
     int32_t lanes;                 // lanes per chunk, a power of two
     int32_t slabs;                 // groups of lanes side by side along a row
-    const uint32_t *touched;       // dense, written: rows without a bit are zeroed
+    const uint8_t *touched;        // dense, written: rows without a mark are zeroed
+    uint32_t *long_runs;           // number of listed runs, then their first chunks
     int64_t sum_blocks;            // blocks beyond these zero rows
 };
 
@@ -518,7 +548,7 @@ __global__ __launch_bounds__(kSumThreads) void k_embedding_sums(SumArgs a) {
         const int64_t groups = (static_cast<int64_t>(gridDim.x) - a.sum_blocks) * per;
         int64_t r = (static_cast<int64_t>(blockIdx.x) - a.sum_blocks) * per + threadIdx.x / a.lanes;
         for (; r < a.num_rows; r += groups) {
-            if ((a.touched[r >> 5] >> (r & 31)) & 1u) continue;
+            if (a.touched[r]) continue;
             TO *p = static_cast<TO *>(a.out) + r * a.ld_out;
             for (int64_t s = 0; s < a.slabs; ++s) {
                 const Cols c = lane_cols<VE>(s, a.lanes, lane, a.d);
@@ -531,26 +561,32 @@ __global__ __launch_bounds__(kSumThreads) void k_embedding_sums(SumArgs a) {
     const int64_t chunk = g / a.slabs;
     if (chunk >= a.chunks) return;
     const Cols c = lane_cols<VE>(g - chunk * a.slabs, a.lanes, lane, a.d);
-    const int64_t e0 = chunk * a.chunk;
+    const int64_t e0 = chunk * a.chunk, far = e0 + 2 * a.chunk;
     const int64_t e1 = e0 + a.chunk < a.n ? e0 + a.chunk : a.n;
+    const uint32_t none = a.num_rows;
     uint32_t cur = a.key[e0];
+    const uint32_t after = e1 < a.n ? a.key[e1] : none;
+    const uint32_t after2 = far < a.n ? a.key[far] : none;
+    bool earlier = e0 > 0 && a.key[e0 - 1] == cur;       // the first run began in an earlier chunk
     if (cur >= a.num_rows) return;
-    bool earlier = e0 > 0 && a.key[e0 - 1] == cur;
     int64_t rank = a.chunk_rank ? static_cast<int64_t>(a.chunk_rank[chunk]) : 0;
     const TI *dout = static_cast<const TI *>(a.dout) + (c.on ? c.at : 0);
+    typedef typename loose<TI, VE>::type Raw;
+    const auto row = [&](uint32_t p) {
+        return *reinterpret_cast<const Raw *>(dout + static_cast<int64_t>(p) * a.ld_dout);
+    };
     vec<float, VE> acc(0.f);
     bool ended = false;      // reached the positions without a gradient row
     for (int64_t e = e0; e < e1 && !ended; e += kSumUnroll) {
         uint32_t k[kSumUnroll];
-        typename loose<TI, VE>::type v[kSumUnroll];
+        Raw v[kSumUnroll];
         // every load is made (of the chunk's last row beyond its end), so that none waits for a
         // branch
 #pragma unroll
         for (int u = 0; u < kSumUnroll; ++u) {
             const int64_t i = e + u < e1 ? e + u : e1 - 1;
-            k[u] = e + u < e1 ? a.key[i] : a.num_rows;
-            v[u] = *reinterpret_cast<const typename loose<TI, VE>::type *>(
-                dout + static_cast<int64_t>(a.pos[i]) * a.ld_dout);
+            k[u] = e + u < e1 ? a.key[i] : none;
+            v[u] = row(a.pos[i]);
         }
 #pragma unroll
         for (int u = 0; u < kSumUnroll; ++u) {
@@ -571,60 +607,186 @@ __global__ __launch_bounds__(kSumThreads) void k_embedding_sums(SumArgs a) {
             acc += __builtin_convertvector(v[u], vec<float, VE>);
         }
     }
-    const bool on = e1 < a.n && a.key[e1] == cur;
-    if (earlier)
+    if (earlier) {
         put_part<VE>(a, 2 * chunk, c, acc);
-    else if (on)
+    } else if (after == cur) {
         put_part<VE>(a, 2 * chunk + 1, c, acc);
-    else
+        if (after2 == cur && lane == 0 && g == chunk * a.slabs)     // beyond the next chunk as well
+            a.long_runs[1 + atomicAdd(a.long_runs, 1u)] = static_cast<uint32_t>(chunk);
+    } else {
         put_row<TO, VE>(a, a.chunk_rank ? rank : cur, c, acc);
+    }
 }
 
-// Joins the runs that begin in one chunk and go on in later ones: lane groups of a workgroup take
-// the run's partial sums in turn, then their sums are added in the groups' order.
+// Joins the partial sums: a lane group takes a chunk's last run where it ends in the next chunk, and
+// the workgroups of the grid's last row take the listed longer runs, whose partial sums their lane
+// groups add in turn, and then each other's sums in the groups' order.
 template <typename TO, int VE>
 __global__ __launch_bounds__(kSumThreads) void k_embedding_join(SumArgs a) {
     __shared__ float sm[kSumThreads * VE];
-    const int64_t chunk = blockIdx.x / a.slabs;
-    const int64_t slab = blockIdx.x - chunk * a.slabs;
-    const int64_t e0 = chunk * a.chunk, e1 = e0 + a.chunk;
-    // whole workgroup
-    if (e1 >= a.n) return;
-    const uint32_t cur = a.key[e1 - 1];
-    if (cur >= a.num_rows || a.key[e1] != cur) return;
-    if (e0 > 0 && a.key[e0 - 1] == cur) return;       // it began earlier
-    // the last chunk whose first key is cur
-    int64_t last = chunk + 1, step = 1;
-    while (last + step < a.chunks && a.key[(last + step) * a.chunk] == cur) {
-        last += step;
-        step *= 2;
-    }
-    for (; step > 0; step /= 2)
-        if (last + step < a.chunks && a.key[(last + step) * a.chunk] == cur) last += step;
     const int groups = kSumThreads / a.lanes;
     const int grp = threadIdx.x / a.lanes, lane = threadIdx.x & (a.lanes - 1);
-    const Cols c = lane_cols<VE>(slab, a.lanes, lane, a.d);
-    vec<float, VE> acc(0.f);
-    if (c.on) {
+    if (static_cast<int64_t>(blockIdx.x) < a.sum_blocks) {
+        const int64_t g = static_cast<int64_t>(blockIdx.x) * groups + grp;
+        const int64_t chunk = g / a.slabs;
+        const int64_t e0 = chunk * a.chunk, e1 = e0 + a.chunk, far = e1 + a.chunk;
+        if (e1 >= a.n) return;
+        const uint32_t none = a.num_rows;
+        const uint32_t cur = a.key[e1 - 1], after = a.key[e1];
+        const uint32_t before = e0 > 0 ? a.key[e0 - 1] : none;
+        const uint32_t after2 = far < a.n ? a.key[far] : none;
+        if (cur >= none || after != cur || before == cur || after2 == cur) return;
+        const Cols c = lane_cols<VE>(g - chunk * a.slabs, a.lanes, lane, a.d);
+        if (!c.on) return;
         const float *p = a.part + c.at;
-        if (grp == 0) acc = load_f32<float, VE>(p + (2 * chunk + 1) * a.d);
+        const vec<float, VE> acc = load_f32<float, VE>(p + (2 * chunk + 1) * a.d) +
+                                   load_f32<float, VE>(p + (2 * chunk + 2) * a.d);
+        put_row<TO, VE>(a, a.chunk_rank ? static_cast<int64_t>(a.chunk_rank[chunk + 1]) : cur, c, acc);
+        return;
+    }
+    const int64_t b = static_cast<int64_t>(blockIdx.x) - a.sum_blocks;
+    const int64_t wide = (static_cast<int64_t>(gridDim.x) - a.sum_blocks) / a.slabs;
+    const Cols c = lane_cols<VE>(b % a.slabs, a.lanes, lane, a.d);
+    const uint32_t count = *a.long_runs;
+    for (uint32_t r = static_cast<uint32_t>(b / a.slabs); r < count; r += static_cast<uint32_t>(wide)) {
+        const int64_t chunk = a.long_runs[1 + r];
+        const uint32_t cur = a.key[(chunk + 1) * a.chunk];
+        // chunks after `chunk` whose first key is cur, a workgroup's width at a time
+        int64_t last = chunk;
+        for (;;) {
+            const int64_t q = last + 1 + threadIdx.x;
+            const int in = __syncthreads_count(q < a.chunks && a.key[q * a.chunk] == cur);
+            last += in;
+            if (in < kSumThreads) break;
+        }
+        vec<float, VE> acc(0.f);
+        if (c.on) {
+            const float *p = a.part + c.at;
+            if (grp == 0) acc = load_f32<float, VE>(p + (2 * chunk + 1) * a.d);
 #pragma unroll 8
-        for (int64_t q = chunk + 1 + grp; q <= last; q += groups)
-            acc += load_f32<float, VE>(p + 2 * q * a.d);
-    }
+            for (int64_t q = chunk + 1 + grp; q <= last; q += groups)
+                acc += load_f32<float, VE>(p + 2 * q * a.d);
+        }
 #pragma unroll
-    for (int e = 0; e < VE; ++e) sm[e * kSumThreads + threadIdx.x] = acc[e];
-    __syncthreads();
-    if (grp != 0) return;
-    for (int q = 1; q < groups; ++q)
+        for (int e = 0; e < VE; ++e) sm[e * kSumThreads + threadIdx.x] = acc[e];
+        __syncthreads();
+        if (grp == 0) {
+            for (int q = 1; q < groups; ++q)
 #pragma unroll
-        for (int e = 0; e < VE; ++e) acc[e] += sm[e * kSumThreads + q * a.lanes + lane];
-    int64_t row = cur;
-    if (a.chunk_rank) {
-        // the run's rank: that of the next chunk's first run
-        row = a.chunk_rank[chunk + 1];
+                for (int e = 0; e < VE; ++e) acc[e] += sm[e * kSumThreads + q * a.lanes + lane];
+            // the run's rank is that of the next chunk's first run
+            put_row<TO, VE>(a, a.chunk_rank ? static_cast<int64_t>(a.chunk_rank[chunk + 1]) : cur, c, acc);
+        }
+        __syncthreads();
     }
-    put_row<TO, VE>(a, row, c, acc);
+}
+
+// ---- few positions --------------------------------------------------------------------------------
+//
+// Up to kFewMost positions the launches cost more than the work: one launch does it all.  Every
+// workgroup sorts all positions for itself and then takes its share: the runs that begin in its part
+// of the sorted list (short ones by a lane group each, long ones by all groups in turn) and, for a
+// written dense table, the unnamed rows in its part of the table.
+constexpr int kFewRounds = 2;
+constexpr int kFewMost = kFewRounds * kOneThreads;
+constexpr int kFewShare = 16;      // sorted positions per workgroup
+constexpr int kFewRun = 32;        // longest run that one lane group takes
+
+template <typename TI, typename TO, int VE>
+__global__ __launch_bounds__(kOneThreads) void k_embedding_few(SortArgs q, SumArgs a, int zero) {
+    __shared__ OneSort<kFewRounds> m;
+    __shared__ uint32_t sw[kOneThreads / 64];
+    __shared__ uint32_t rank_of[kFewShare];
+    __shared__ float sm[kOneThreads * VE];
+    const int t = threadIdx.x, n = static_cast<int>(q.n);
+    sort_one<kFewRounds>(q, m, false);
+    const int lo = static_cast<int>(blockIdx.x) * kFewShare;
+    const auto head = [&](int i) { return is_head(m.key[i], i > 0 ? m.key[i - 1] : 0u, i == 0, q.num_rows); };
+    if (q.rows) {
+        // ranks of the runs; the first workgroup writes the list
+        uint32_t carry = 0;
+        for (int r0 = 0; r0 < n; r0 += kOneThreads) {
+            const int i = r0 + t;
+            const uint32_t h = i < n && head(i);
+            uint32_t total;
+            const uint32_t at = carry + block_exclusive_scan<uint32_t, kOneThreads>(h, &total, sw);
+            if (i >= lo && i < lo + kFewShare) rank_of[i - lo] = at;
+            if (blockIdx.x == 0 && h && at < q.row_cap) q.uniq[at] = static_cast<int32_t>(m.key[i]);
+            carry += total;
+        }
+        if (blockIdx.x == 0 && t == 0) {
+            *q.d_n_uniq = carry;
+            if (carry > q.row_cap) set_status(q.status, GNN_ERR_CAPACITY);
+        }
+        __syncthreads();
+    }
+    const int groups = kOneThreads / a.lanes, grp = t / a.lanes, lane = t & (a.lanes - 1);
+    const TI *dout = static_cast<const TI *>(a.dout);
+    typedef typename loose<TI, VE>::type Raw;
+    // the sum of positions i0, i0 + step, ... below end of the sorted list
+    const auto sum = [&](int i0, int end, int step, const Cols &c) {
+        vec<float, VE> acc(0.f);
+        for (int i = i0; i < end; i += kSumUnroll * step) {
+            Raw v[kSumUnroll];
+#pragma unroll
+            for (int u = 0; u < kSumUnroll; ++u) {
+                const int at = i + u * step < end ? i + u * step : i;
+                v[u] = *reinterpret_cast<const Raw *>(dout + static_cast<int64_t>(m.pos[at]) * a.ld_dout +
+                                                      (c.on ? c.at : 0));
+            }
+#pragma unroll
+            for (int u = 0; u < kSumUnroll; ++u)
+                if (i + u * step < end) acc += __builtin_convertvector(v[u], vec<float, VE>);
+        }
+        return acc;
+    };
+    const int hi = lo + kFewShare < n ? lo + kFewShare : n;
+    for (int item = grp; item < (hi - lo) * a.slabs; item += groups) {
+        const int i = lo + item / a.slabs;
+        if (!head(i)) continue;
+        int end = i + 1;
+        while (end < n && end <= i + kFewRun && m.key[end] == m.key[i]) ++end;
+        if (end > i + kFewRun) continue;
+        const Cols c = lane_cols<VE>(item % a.slabs, a.lanes, lane, a.d);
+        put_row<TO, VE>(a, q.rows ? static_cast<int64_t>(rank_of[i - lo]) : m.key[i], c, sum(i, end, 1, c));
+    }
+    for (int i = lo; i < hi; ++i) {      // whole workgroup
+        if (!head(i) || i + kFewRun >= n || m.key[i + kFewRun] != m.key[i]) continue;
+        int end = i + kFewRun + 1, over = n;     // the first position of another key
+        while (end < over) {
+            const int mid = (end + over) / 2;
+            if (m.key[mid] == m.key[i]) end = mid + 1; else over = mid;
+        }
+        for (int slab = 0; slab < a.slabs; ++slab) {
+            const Cols c = lane_cols<VE>(slab, a.lanes, lane, a.d);
+            vec<float, VE> acc = sum(i + grp, end, groups, c);
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < VE; ++e) sm[e * kOneThreads + t] = acc[e];
+            __syncthreads();
+            if (grp == 0) {
+                for (int g = 1; g < groups; ++g)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) acc[e] += sm[e * kOneThreads + g * a.lanes + lane];
+                put_row<TO, VE>(a, q.rows ? static_cast<int64_t>(rank_of[i - lo]) : m.key[i], c, acc);
+            }
+        }
+    }
+    if (!zero) return;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * groups + grp; r < q.num_rows;
+         r += static_cast<int64_t>(gridDim.x) * groups) {
+        int from = 0, to = n;      // the first position whose key is at least r
+        while (from < to) {
+            const int mid = (from + to) / 2;
+            if (m.key[mid] < r) from = mid + 1; else to = mid;
+        }
+        if (from < n && m.key[from] == r) continue;
+        TO *p = static_cast<TO *>(a.out) + r * a.ld_out;
+        for (int s = 0; s < a.slabs; ++s) {
+            const Cols c = lane_cols<VE>(s, a.lanes, lane, a.d);
+            if (c.on) store_f32<TO, VE>(p + c.at, vec<float, VE>(0.f));
+        }
+    }
 }
 
 __global__ __launch_bounds__(256) void k_zero_rows(char *out, int64_t row_bytes, int64_t ld_bytes,
@@ -644,7 +806,8 @@ __global__ __launch_bounds__(256) void k_zero_rows(char *out, int64_t row_bytes,
 
 // What the gradient keeps in the workspace.
 struct GradSpace {
-    uint32_t *key[2], *pos[2], *hist, *heads, *chunk_rank, *touched;
+    uint32_t *key[2], *pos[2], *hist, *heads, *chunk_rank, *long_runs;
+    uint8_t *touched;
     float *part;
     int32_t chunk;
     int64_t chunks, touched_words;
@@ -660,6 +823,11 @@ int32_t chunk_for(int64_t n) {
     return static_cast<int32_t>(c);
 }
 
+// A written dense table: rows that no id names are zeroed by their marks, or, where at most one row in
+// 16 can be named, the whole table is cleared first (the rows then written twice are fewer than the
+// marks are worth).
+bool clears_all(int64_t n, int64_t num_rows) { return n <= num_rows / 16; }
+
 GradSpace carve_grad(int64_t n, int64_t num_rows, int64_t d, char *base) {
     GradSpace g{};
     size_t off = 0;
@@ -672,7 +840,7 @@ GradSpace carve_grad(int64_t n, int64_t num_rows, int64_t d, char *base) {
     g.chunk = chunk_for(n);
     g.chunks = (n + g.chunk - 1) / g.chunk;
     g.tiles = static_cast<int32_t>((n + kSortTile - 1) / kSortTile);
-    g.touched_words = (num_rows + 31) / 32;
+    g.touched_words = (num_rows + 3) / 4;
     for (int i = 0; i < 2; ++i) {
         g.key[i] = take(n);
         g.pos[i] = take(n);
@@ -680,15 +848,16 @@ GradSpace carve_grad(int64_t n, int64_t num_rows, int64_t d, char *base) {
     g.hist = take(static_cast<int64_t>(g.tiles + 1) * kDigits);
     g.heads = take(g.tiles);
     g.chunk_rank = take(g.chunks);
-    g.touched = take(g.touched_words);
+    g.long_runs = take(1 + g.chunks);
+    g.touched = reinterpret_cast<uint8_t *>(take(clears_all(n, num_rows) ? 0 : g.touched_words));
     g.part = reinterpret_cast<float *>(take(2 * g.chunks * d));
     g.bytes = off;
     return g;
 }
 
 template <typename TI, typename TO, int VE>
-hipError_t run_sums(const EmbedGradArgs &a, const GradSpace &g, const uint32_t *key,
-                    const uint32_t *pos, bool zero_untouched, hipStream_t s) {
+hipError_t run_sums(const EmbedGradArgs &a, const GradSpace &g, const SortArgs &sort,
+                    const uint32_t *key, const uint32_t *pos, bool zero_untouched, hipStream_t s) {
     SumArgs p{};
     p.key = key;
     p.pos = pos;
@@ -704,12 +873,22 @@ hipError_t run_sums(const EmbedGradArgs &a, const GradSpace &g, const uint32_t *
     p.chunk_rank = a.rows ? g.chunk_rank : nullptr;
     p.row_cap = a.rows ? a.row_cap : a.num_rows;
     p.part = g.part;
+    p.long_runs = g.long_runs;
     p.chunk = g.chunk;
     p.chunks = g.chunks;
     const int64_t cpr = (a.d + VE - 1) / VE;
     p.lanes = 1;
     while (p.lanes < cpr && p.lanes < 64) p.lanes *= 2;
     p.slabs = static_cast<int32_t>((cpr + p.lanes - 1) / p.lanes);
+    if (key == nullptr) {
+        int64_t grid = (a.n + kFewShare - 1) / kFewShare;
+        const int64_t clear = a.num_rows / 32 < 128 ? a.num_rows / 32 : 128;
+        if (zero_untouched && grid < clear) grid = clear;     // more workgroups, for the unnamed rows
+        hipLaunchKernelGGL((k_embedding_few<TI, TO, VE>), dim3(static_cast<unsigned>(grid)),
+                           dim3(kOneThreads), 0, s, sort, p,
+                           zero_untouched ? 1 : 0);
+        return hipGetLastError();
+    }
     const int per = kSumThreads / p.lanes;
     p.sum_blocks = (g.chunks * p.slabs + per - 1) / per;
     int64_t zero_blocks = 0;
@@ -722,19 +901,22 @@ hipError_t run_sums(const EmbedGradArgs &a, const GradSpace &g, const uint32_t *
     hipLaunchKernelGGL((k_embedding_sums<TI, TO, VE>),
                        dim3(static_cast<unsigned>(p.sum_blocks + zero_blocks)), dim3(kSumThreads),
                        0, s, p);
-    if (g.chunks > 1)
+    if (g.chunks > 1) {
+        // a listed run holds a whole chunk
+        const int64_t most = g.chunks / 2 < kJoinRuns ? g.chunks / 2 : kJoinRuns;
         hipLaunchKernelGGL((k_embedding_join<TO, VE>),
-                           dim3(static_cast<unsigned>((g.chunks - 1) * p.slabs)),
+                           dim3(static_cast<unsigned>(p.sum_blocks + most * p.slabs)),
                            dim3(kSumThreads), 0, s, p);
+    }
     return hipGetLastError();
 }
 
 template <typename TI, typename TO>
-hipError_t pick_sums(const EmbedGradArgs &a, const GradSpace &g, const uint32_t *key,
+hipError_t pick_sums(const EmbedGradArgs &a, const GradSpace &g, const SortArgs &q, const uint32_t *key,
                      const uint32_t *pos, bool zero, hipStream_t s) {
     constexpr int kWide = sizeof(TI) == 2 ? 8 : 4;      // 16 bytes of dout a lane
-    if (a.d >= kWide) return run_sums<TI, TO, kWide>(a, g, key, pos, zero, s);
-    return run_sums<TI, TO, 1>(a, g, key, pos, zero, s);
+    if (a.d >= kWide) return run_sums<TI, TO, kWide>(a, g, q, key, pos, zero, s);
+    return run_sums<TI, TO, 1>(a, g, q, key, pos, zero, s);
 }
 
 }  // namespace
@@ -753,11 +935,8 @@ size_t embedding_grad_bytes(int64_t n, int64_t num_rows, int64_t d) {
 hipError_t launch_embedding_grad(const EmbedGradArgs &a, hipStream_t s) {
     const int elem = a.out_type == GNN_F32 ? 4 : 2;
     const bool dense = !a.rows;
-    // A written dense table: rows that no id names are zeroed from a bitmap of the named ones, or,
-    // where at most one row in 16 can be named, the whole table is cleared first (the rows written
-    // twice are then fewer than the bitmap's test is worth).
     const bool written = dense && !a.accumulate;
-    const bool clear_all = written && a.n <= a.num_rows / 16;
+    const bool clear_all = written && clears_all(a.n, a.num_rows);
     if (clear_all) {
         const int64_t blocks = (a.num_rows + 15) / 16;
         hipLaunchKernelGGL(k_zero_rows, dim3(static_cast<unsigned>(blocks < 32768 ? blocks : 32768)),
@@ -791,10 +970,13 @@ hipError_t launch_embedding_grad(const EmbedGradArgs &a, hipStream_t s) {
     q.chunk_rank = g.chunk_rank;
     q.chunk = g.chunk;
     const uint32_t *key, *pos;
-    if (a.n <= kSortTile) {
+    q.long_runs = g.long_runs;
+    if (a.n > 0 && a.n <= kFewMost) {
+        key = pos = nullptr;        // sorted by the kernel that adds
+    } else if (a.n <= kOneTile) {
         q.key_out = g.key[0];
         q.pos_out = g.pos[0];
-        hipLaunchKernelGGL(k_sort_tile, dim3(1), dim3(kSortThreads), 0, s, q);
+        hipLaunchKernelGGL(k_sort_one, dim3(1), dim3(kOneThreads), 0, s, q);
         key = g.key[0];
         pos = g.pos[0];
     } else {
@@ -831,10 +1013,10 @@ hipError_t launch_embedding_grad(const EmbedGradArgs &a, hipStream_t s) {
     }
     const bool zero = written && !clear_all;
     if (a.dout_type == GNN_F32)
-        return a.out_type == GNN_F32 ? pick_sums<float, float>(a, g, key, pos, zero, s)
-                                     : pick_sums<float, bf16>(a, g, key, pos, zero, s);
-    return a.out_type == GNN_F32 ? pick_sums<bf16, float>(a, g, key, pos, zero, s)
-                                 : pick_sums<bf16, bf16>(a, g, key, pos, zero, s);
+        return a.out_type == GNN_F32 ? pick_sums<float, float>(a, g, q, key, pos, zero, s)
+                                     : pick_sums<float, bf16>(a, g, q, key, pos, zero, s);
+    return a.out_type == GNN_F32 ? pick_sums<bf16, float>(a, g, q, key, pos, zero, s)
+                                 : pick_sums<bf16, bf16>(a, g, q, key, pos, zero, s);
 }
 
 }  // namespace gnnmb
