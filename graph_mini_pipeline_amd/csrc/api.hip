@@ -1769,6 +1769,8 @@ gnn_status gnn_embedding_grad_rows(const int32_t *ids, const int64_t *d_n, int64
 namespace {
 constexpr int32_t kAttendMaxDim = 128;
 constexpr int32_t kAttendMaxHeads = 1024;
+// A tile of up to 128 rows spans fewer than 2^31 bytes.
+constexpr int64_t kAttendMaxLd = int64_t(1) << 21;
 
 gnn_status attend_sizes(const gnn_attention *x, AttendArgs *a) {
     if (!x || x->heads < 1 || x->kv_heads < 1 || x->head_dim < 1 || x->n_seq < 0 || x->n_q < 0 ||
@@ -1799,6 +1801,8 @@ gnn_status attend_args(const gnn_attention *x, AttendArgs *a) {
     const int64_t wq = static_cast<int64_t>(x->heads) * x->head_dim;
     const int64_t wk = static_cast<int64_t>(x->kv_heads) * x->head_dim;
     if (x->ld_q < wq || x->ld_out < wq || x->ld_k < wk || x->ld_v < wk) return GNN_ERR_INVALID_ARG;
+    if (x->ld_q > kAttendMaxLd || x->ld_k > kAttendMaxLd || x->ld_v > kAttendMaxLd)
+        return GNN_ERR_UNSUPPORTED;
     if (x->n_seq > 0 && (!x->q_indptr || !x->k_indptr)) return GNN_ERR_INVALID_ARG;
     if (x->n_q > 0 && (!x->q || !x->out)) return GNN_ERR_INVALID_ARG;
     if (x->n_k > 0 && (!x->k || !x->v)) return GNN_ERR_INVALID_ARG;
@@ -1849,6 +1853,7 @@ gnn_status gnn_cross_attention_backward(const gnn_attention *x, const gnn_attent
     const int64_t wq = static_cast<int64_t>(x->heads) * x->head_dim;
     const int64_t wk = static_cast<int64_t>(x->kv_heads) * x->head_dim;
     if (g->ld_dout < wq || g->ld_dq < wq || g->ld_dk < wk || g->ld_dv < wk) return GNN_ERR_INVALID_ARG;
+    if (g->ld_dout > kAttendMaxLd) return GNN_ERR_UNSUPPORTED;
     if (x->n_q > 0 && (!x->lse || !g->dout || !g->dq)) return GNN_ERR_INVALID_ARG;
     if (x->n_k > 0 && (!g->dk || !g->dv)) return GNN_ERR_INVALID_ARG;
     if (ws_bytes < attend_bytes(a, true)) return GNN_ERR_CAPACITY;

@@ -60,64 +60,96 @@ __device__ __forceinline__ void mma(f32x16 &acc, Piece<float> a, Piece<float> b)
     for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], acc, 0, 0, 0);
 }
 
-// A row-major LDS tile of DP columns: 16-byte pieces, those of a row permuted by the row so that
-// lanes reading the same piece of different rows use different banks.
+// A row-major LDS tile of DP columns, in 16-byte pieces.  A row is one piece longer than its columns, so
+// that the 32 rows which a read touches at the same piece spread over the banks, and every other
+// distance within a tile is a constant.
 template <typename T, int DP>
 struct Tile {
     static constexpr int NP = DP / Kind<T>::kPiece;      // pieces per row
-    static constexpr int kMask = (NP < 16 ? NP : 16) - 1;
+    static constexpr int kStride = NP + 1;
+    static constexpr int pieces(int rows) { return rows * kStride; }
     Piece<T> *p;
-    __device__ __forceinline__ Piece<T> *at(int r, int c) const {
-        return p + r * NP + (c ^ (r & kMask));
-    }
+    __device__ __forceinline__ Piece<T> *at(int r, int c) const { return p + r * kStride + c; }
     // element d of row r
     __device__ __forceinline__ T *element(int r, int d) const {
-        return reinterpret_cast<T *>(at(r, d / Kind<T>::kPiece)) + d % Kind<T>::kPiece;
+        return reinterpret_cast<T *>(at(r, 0)) + d;
     }
 };
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-// acc[db] += (columns 32 db .. of the tile's rows row0 .. row0+31)^T p, p being a 32 x 32 result
-// whose rows are those 32.
-template <int DP>
-__device__ __forceinline__ void mma_turned(f32x16 (&acc)[DP / 32], const Tile<bf16, DP> &tile,
-                                           int row0, const f32x16 &p) {
-    const int lane = lane_id();
-    // the transposing read: 16 lanes name a 4 x 16 block, 4 elements each, and get a column each
-    const int r = 4 * (lane >> 5) + ((lane & 15) >> 2);
-    const int d = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+// Operands come from LDS through a ring of RING registers sets, each read RING steps before the matrix
+// instructions that use it (left alone, the compiler reads one, waits for it, multiplies, and reads
+// the next).  use(s, v) may carry other work, which the matrix instructions hide.
+template <int RING, int STEPS, typename V, typename L>
+__device__ __forceinline__ void prime(V (&v)[RING], L load) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        Piece<bf16> b;
+    for (int s = 0; s < RING && s < STEPS; ++s) v[s] = load(s);
+    __builtin_amdgcn_sched_barrier(0);
+}
+template <int RING, int STEPS, typename V, typename L, typename U>
+__device__ __forceinline__ void stream(V (&v)[RING], L load, U use) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) b[e] = static_cast<bf16>(p[8 * t + e]);
-#pragma unroll
-        for (int db = 0; db < DP / 32; ++db) {
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4 *)tile.element(row0 + 16 * t + r, 32 * db + d));
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4 *)tile.element(row0 + 16 * t + 8 + r, 32 * db + d));
-            const vec<short, 8> a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-            mma(acc[db], __builtin_bit_cast(Piece<bf16>, a), b);
-        }
+    for (int s = 0; s < STEPS; ++s) {
+        use(s, v[s % RING]);
+        if (s + RING < STEPS) v[s % RING] = load(s + RING);
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
+
+// The transposed operand of acc[db] += (columns 32 db .. of the tile's rows row0 .. row0+31)^T p, p
+// being a 32 x 32 result whose rows are those 32: kSteps steps, each with a read of its own.
+template <typename T, int DP>
+struct Turned;
+
 template <int DP>
-__device__ __forceinline__ void mma_turned(f32x16 (&acc)[DP / 32], const Tile<float, DP> &tile,
-                                           int row0, const f32x16 &p) {
-    const int lane = lane_id();
+struct Turned<bf16, DP> {
+    static constexpr int DB = DP / 32, kSteps = 2 * DB, kRing = 6;
+    struct V {
+        s16x4 lo, hi;
+    };
+    static __device__ __forceinline__ V load(const Tile<bf16, DP> &tile, int row0, int s) {
+        const int lane = lane_id();
+        // the transposing read: 16 lanes name a 4 x 16 block, 4 elements each, and get a column each
+        const int r = 4 * (lane >> 5) + ((lane & 15) >> 2);
+        const int d = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+        bf16 *at = tile.element(r, d) + (row0 + 16 * (s / DB)) * Tile<bf16, DP>::kStride * 8 + 32 * (s % DB);
+        return V{__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at),
+                 __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + 8 * Tile<bf16, DP>::kStride * 8))};
+    }
+    Piece<bf16> b;      // p's half that the current steps multiply
+    __device__ __forceinline__ void use(f32x16 (&acc)[DB], const V &v, int s, const f32x16 &p) {
+        if (s % DB == 0) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g)
+            for (int e = 0; e < 8; ++e) b[e] = static_cast<bf16>(p[8 * (s / DB) + e]);
+        }
+        const vec<short, 8> a = __builtin_shufflevector(v.lo, v.hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        mma(acc[s % DB], __builtin_bit_cast(Piece<bf16>, a), b);
+    }
+};
+
+template <int DP>
+struct Turned<float, DP> {
+    static constexpr int DB = DP / 32, kSteps = 16, kRing = 4;
+    struct V {
+        float a[DB];
+    };
+    static __device__ __forceinline__ V load(const Tile<float, DP> &tile, int row0, int s) {
+        const int lane = lane_id();
+        const float *at = tile.element(4 * (lane >> 5), lane & 31) +
+                          (row0 + 8 * (s >> 2) + (s & 3)) * Tile<float, DP>::kStride * 4;
+        V v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int db = 0; db < DB; ++db) v.a[db] = at[32 * db];
+        return v;
+    }
+    __device__ __forceinline__ void use(f32x16 (&acc)[DB], const V &v, int s, const f32x16 &p) {
 #pragma unroll
-            for (int db = 0; db < DP / 32; ++db) {
-                const float a = *tile.element(row0 + 8 * g + 4 * (lane >> 5) + e, 32 * db + (lane & 31));
-                acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p[4 * g + e], acc[db], 0, 0, 0);
-            }
-}
+        for (int db = 0; db < DB; ++db)
+            acc[db] = __builtin_amdgcn_mfma_f32_32x32x2f32(v.a[db], p[s], acc[db], 0, 0, 0);
+    }
+};
 
 struct Seq {
     int64_t q0, nq;      // first query row, queries
@@ -161,30 +193,36 @@ __device__ __forceinline__ GroupRow group_row(const AttendArgs &a, const Seq &s,
     return g;
 }
 
-// Loads R rows of DP columns into registers, rows at or past `rows` and columns at or past d as zeros;
-// put() stores them to the tile.  ptr(r) is row r's first element; row 0 exists.
+// Loads R rows of DP columns into registers, and puts them into a tile a turn later, rows at or past
+// `rows` and columns at or past d as zeros (only there, so that nothing waits for the loads before).
+// at(r) is row r's distance in elements from `base`, which is the same for all threads, so that an
+// address is a scalar pair and one 32-bit register (a tile's rows span fewer than 2^31 bytes); row 0
+// exists.
 template <typename T, int DP, int R>
 struct Stage {
     static constexpr int NP = DP / Kind<T>::kPiece;
-    static constexpr int N = R * NP / kThreads;
+    static constexpr int kAll = R * NP;
+    static constexpr int N = (kAll + kThreads - 1) / kThreads;     // the last turn may be a part of one
     Piece<T> v[N];
     template <typename F>
-    __device__ __forceinline__ void load(int64_t rows, int d, F ptr) {
+    __device__ __forceinline__ void load(const T *base, int64_t rows, int d, F at) {
+        const char *from = reinterpret_cast<const char *>(base);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int e = i * kThreads + static_cast<int>(threadIdx.x);
             const int r = e / NP, c = e % NP * Kind<T>::kPiece;
             // every load is made, of a place that exists, so that none waits for a branch
-            const T *p = ptr(r < rows ? r : 0) + (c < d ? c : 0);
-            const Piece<T> x = *reinterpret_cast<const typename loose<T, Kind<T>::kPiece>::type *>(p);
-            v[i] = r < rows && c < d ? x : Piece<T>(static_cast<T>(0.f));
+            const uint32_t off = (at(r < rows ? r : 0) + (c < d ? c : 0)) * static_cast<uint32_t>(sizeof(T));
+            v[i] = *reinterpret_cast<const typename loose<T, Kind<T>::kPiece>::type *>(from + off);
         }
     }
-    __device__ __forceinline__ void put(const Tile<T, DP> &tile) const {
+    __device__ __forceinline__ void put(const Tile<T, DP> &tile, int64_t rows, int d) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int e = i * kThreads + static_cast<int>(threadIdx.x);
-            *tile.at(e / NP, e % NP) = v[i];
+            const int r = e / NP, c = e % NP;
+            const Piece<T> x = r < rows && c * Kind<T>::kPiece < d ? v[i] : Piece<T>(static_cast<T>(0.f));
+            if (kAll % kThreads == 0 || e < kAll) *tile.at(r, c) = x;
         }
     }
 };
@@ -205,16 +243,15 @@ struct RowPieces {
     }
 };
 
-// The 32 x 32 product of tile rows row0 .. row0+31 with the registers' rows.
+// Step s of the product of tile rows row0 .. row0+31 with the registers' rows.
+template <typename T>
+constexpr int row_ring() {
+    return sizeof(T) == 2 ? 6 : 3;      // an fp32 step is four long instructions
+}
 template <typename T, int DP>
-__device__ __forceinline__ f32x16 product(const Tile<T, DP> &tile, int row0,
-                                          const RowPieces<T, DP> &b) {
-    f32x16 acc(0.f);
+__device__ __forceinline__ Piece<T> row_piece(const Tile<T, DP> &tile, int row0, int s) {
     const int lane = lane_id();
-#pragma unroll
-    for (int kk = 0; kk < RowPieces<T, DP>::KK; ++kk)
-        mma(acc, *tile.at(row0 + (lane & 31), 2 * kk + (lane >> 5)), b.v[kk]);
-    return acc;
+    return tile.at(lane & 31, lane >> 5)[row0 * Tile<T, DP>::kStride + 2 * s];
 }
 
 // Writes the four consecutive elements d0 .. d0+3 of a row (of d elements, a multiple of 8).
@@ -223,13 +260,20 @@ __device__ __forceinline__ void put4(T *row, int d0, int d, f32x4 v) {
     if (d0 < d) store_f32<T, 4>(row + d0, v);
 }
 
-// The states of one split of a sequence: [begin, end).
-__device__ __forceinline__ void split_range(int64_t n, int split, int splits, int unit, int64_t &begin,
-                                            int64_t &end) {
-    int64_t per = (n + splits - 1) / splits;
-    per = (per + unit - 1) / unit * unit;
-    begin = per * split < n ? per * split : n;
-    end = begin + per < n ? begin + per : n;
+// A sequence's states (or rows) are split into as many parts of at most `per` as they need (an empty
+// sequence has one part, which is empty), of equal length up to a multiple of `unit`.
+__device__ __forceinline__ int64_t parts_of(int64_t n, int64_t per) {
+    return n <= per ? 1 : (n + per - 1) / per;
+}
+__device__ __forceinline__ void part_range(int64_t n, int64_t per, int part, int unit, int64_t &begin,
+                                           int64_t &end) {
+    int64_t len = per;
+    if (n > per) {
+        const int64_t parts = (n + per - 1) / per;
+        len = ((n + parts - 1) / parts + unit - 1) / unit * unit;
+    }
+    begin = len * part < n ? len * part : n;
+    end = begin + len < n ? begin + len : n;
 }
 
 // States per wavefront and turn.
@@ -238,92 +282,133 @@ constexpr int keys_per_wave() {
     return sizeof(T) == 2 && WK == 1 ? 64 : 32;
 }
 
+// Wavefronts that share the states where rows are few: four, or two where four wavefronts' tiles, twice,
+// exceed the LDS.
+template <typename T, int DP>
+constexpr int sharing() {
+    return sizeof(T) * DP <= 256 ? 4 : 2;
+}
+
 // ---- forward --------------------------------------------------------------------------------------
 //
 // WQ wavefronts take 32 rows each of a tile of rows, WK wavefronts share the states among them (for
 // a sequence's few rows: four wavefronts read four times as many states a turn).  splits > 1: the
 // states are shared among workgroups as well, whose sums the combining kernel joins.
 template <typename T, int DP, int WQ, int WK>
-__global__ __launch_bounds__(kThreads, 2) void k_attend(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, WK == 1 ? 2 : 1) void k_attend(AttendArgs a) {
     constexpr int KW = keys_per_wave<T, WK>(), BK = KW * WK, BQ = 32 * WQ, KB = KW / 32;
     constexpr int DB = DP / 32;
     typedef Tile<T, DP> Tl;
-    __shared__ Piece<T> smem[2 * BK * Tl::NP];
-    const Tl tk{smem}, tv{smem + BK * Tl::NP};
+    typedef Turned<T, DP> Tu;
+    // two pairs of tiles of k and v: one is read while the next one is on its way
+    constexpr int kPair = 2 * Tl::pieces(BK);
+    __shared__ Piece<T> smem[2 * kPair];
     const Seq s = sequence(a, blockIdx.z);
     const int hk = static_cast<int>(blockIdx.y) / a.splits, split = static_cast<int>(blockIdx.y) % a.splits;
     const int64_t rows = s.nq * a.group, r0 = static_cast<int64_t>(blockIdx.x) * BQ;
-    if (r0 >= rows) return;      // whole workgroup
+    if (r0 >= rows || split >= parts_of(s.nk, a.per)) return;      // whole workgroup
+    int64_t kb, ke;
+    part_range(s.nk, a.per, split, BK, kb, ke);
     const int lane = lane_id(), w = threadIdx.x >> 6, wq = w / WK, wk = w % WK;
     const int64_t r = r0 + wq * 32 + (lane & 31);
     const GroupRow me = group_row(a, s, hk, r < rows ? r : rows - 1);
     RowPieces<T, DP> q;
     q.load(static_cast<const T *>(a.q) + me.pos * a.ld_q + me.head * a.d, r < rows, a.d);
 
-    int64_t kb, ke;
-    split_range(s.nk, split, a.splits, BK, kb, ke);
     const T *kp = static_cast<const T *>(a.k) + s.k0 * a.ld_k + hk * a.d;
     const T *vp = static_cast<const T *>(a.v) + s.k0 * a.ld_v + hk * a.d;
     f32x16 o[DB];
 #pragma unroll
     for (int i = 0; i < DB; ++i) o[i] = f32x16(0.f);
     float top = -INFINITY, sum = 0.f;       // of scale * log2(e) * S
+    const auto k_row = [&](int i) { return static_cast<uint32_t>(i) * static_cast<uint32_t>(a.ld_k); };
+    const auto v_row = [&](int i) { return static_cast<uint32_t>(i) * static_cast<uint32_t>(a.ld_v); };
     Stage<T, DP, BK> sk, sv;
-    if (kb < ke) {
-        sk.load(ke - kb, a.d, [&](int i) { return kp + (kb + i) * a.ld_k; });
-        sv.load(ke - kb, a.d, [&](int i) { return vp + (kb + i) * a.ld_v; });
-    }
-    for (int64_t k0 = kb; k0 < ke; k0 += BK) {
-        __syncthreads();          // the last turn's reads are done
-        sk.put(tk);
-        sv.put(tv);
+    const auto load = [&](int64_t at) {
+        sk.load(kp + at * a.ld_k, ke - at, a.d, k_row);
+        sv.load(vp + at * a.ld_v, ke - at, a.d, v_row);
+    };
+    const auto put = [&](Piece<T> *pair, int64_t at) {
+        sk.put(Tl{pair}, ke - at, a.d);
+        sv.put(Tl{pair + kPair / 2}, ke - at, a.d);
         __syncthreads();
+    };
+    const auto turn = [&](Piece<T> *pair, Piece<T> *next, int64_t k0) {
+        const Tl tk{pair}, tv{pair + kPair / 2};
         const int64_t k1 = k0 + BK;
-        if (k1 < ke) {
-            sk.load(ke - k1, a.d, [&](int i) { return kp + (k1 + i) * a.ld_k; });
-            sv.load(ke - k1, a.d, [&](int i) { return vp + (k1 + i) * a.ld_v; });
-        }
+        if (k1 < ke) load(k1);
+        constexpr int KK = RowPieces<T, DP>::KK, kR = row_ring<T>();
         f32x16 x[KB];
         float most = -INFINITY;
+        const auto settle = [&](int b, int i) {       // the scaled score, -inf past the end
+            x[b][i] *= a.scale2;
+            if (k1 > ke && k0 + wk * KW + b * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= ke)
+                x[b][i] = -INFINITY;
+            most = fmaxf(most, x[b][i]);
+        };
+        Piece<T> ring[kR];
+        const auto piece = [&](int st) { return row_piece<T, DP>(tk, wk * KW + st / KK * 32, st % KK); };
+        prime<kR, KB * KK>(ring, piece);
 #pragma unroll
-        for (int b = 0; b < KB; ++b) {
-            x[b] = product<T, DP>(tk, wk * KW + b * 32, q) * a.scale2;
-            if (k1 > ke) {        // the last turn: states past the end
+        for (int b = 0; b < KB; ++b) x[b] = f32x16(0.f);
+        stream<kR, KB * KK>(ring, piece, [&](int st, const Piece<T> &v) {
+            mma(x[st / KK], v, q.v[st % KK]);
+            if (st >= KK) {                           // the block before, meanwhile
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (k0 + wk * KW + b * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= ke)
-                        x[b][i] = -INFINITY;
+                for (int i = st % KK * 16 / KK; i < (st % KK + 1) * 16 / KK; ++i) settle(st / KK - 1, i);
             }
+        });
+        typename Tu::V turned[Tu::kRing];
+        const auto column = [&](int st) {
+            return Tu::load(tv, wk * KW + st / Tu::kSteps * 32, st % Tu::kSteps);
+        };
+        prime<Tu::kRing, KB * Tu::kSteps>(turned, column);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) most = fmaxf(most, x[b][i]);
-        }
+        for (int i = 0; i < 16; ++i) settle(KB - 1, i);
         most = fmaxf(most, __shfl_xor(most, 32, 64));
         most = fmaxf(most, top);
         const float base = most == -INFINITY ? 0.f : most;
-        const float keep = __builtin_amdgcn_exp2f(top - base);
-        top = most;
-        sum *= keep;
+        if (__any(most > top)) {     // the sums so far are kept relative to the largest so far
+            const float keep = __builtin_amdgcn_exp2f(top - base);
+            sum *= keep;
 #pragma unroll
-        for (int i = 0; i < DB; ++i) o[i] *= keep;
-#pragma unroll
-        for (int b = 0; b < KB; ++b) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                x[b][i] = __builtin_amdgcn_exp2f(x[b][i] - base);
-                sum += x[b][i];
-            }
-            mma_turned<DP>(o, tv, wk * KW + b * 32, x[b]);
+            for (int i = 0; i < DB; ++i) o[i] *= keep;
+            top = most;
         }
+        const auto weigh = [&](int b, int i) {
+            x[b][i] = __builtin_amdgcn_exp2f(x[b][i] - base);
+            sum += x[b][i];
+        };
+#pragma unroll
+        for (int i = 0; i < 16; ++i) weigh(0, i);
+        Tu tu;
+        stream<Tu::kRing, KB * Tu::kSteps>(turned, column, [&](int st, const typename Tu::V &v) {
+            const int b = st / Tu::kSteps, t = st % Tu::kSteps;
+            tu.use(o, v, t, x[b]);
+            if (b + 1 < KB) {                         // the next block's weights, meanwhile
+#pragma unroll
+                for (int i = t * 16 / Tu::kSteps; i < (t + 1) * 16 / Tu::kSteps; ++i) weigh(b + 1, i);
+            }
+        });
+        if (k1 < ke) put(next, k1);
+    };
+    if (kb < ke) {
+        load(kb);
+        put(smem, kb);
+    }
+    for (int64_t k0 = kb; k0 < ke; k0 += 2 * BK) {
+        turn(smem, smem + kPair, k0);
+        if (k0 + BK < ke) turn(smem + kPair, smem, k0 + BK);
     }
     sum += __shfl_xor(sum, 32, 64);
     if (WK > 1) {
         // join the wavefronts' sums: [WK - 1][32 rows][DP + 2] floats in the tiles' memory
         constexpr int kRow = DP + 4;
-        static_assert((WK - 1) * 32 * kRow * 4 <= static_cast<int>(sizeof(smem)), "join area");
-        float *join = reinterpret_cast<float *>(smem);
+        static_assert((WK - 1) * WQ * 32 * kRow * 4 <= static_cast<int>(sizeof(smem)), "join area");
+        float *join = reinterpret_cast<float *>(smem) + (wq * (WK - 1) * 32 + (lane & 31)) * kRow;
         __syncthreads();
         if (wk > 0) {
-            float *row = join + ((wk - 1) * 32 + (lane & 31)) * kRow;
+            float *row = join + (wk - 1) * 32 * kRow;
 #pragma unroll
             for (int i = 0; i < DB; ++i)
 #pragma unroll
@@ -338,7 +423,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend(AttendArgs a) {
         __syncthreads();
         if (wk > 0) return;
         for (int u = 0; u < WK - 1; ++u) {
-            const float *row = join + (u * 32 + (lane & 31)) * kRow;
+            const float *row = join + u * 32 * kRow;
             const float t = row[DP], most = fmaxf(top, t);
             const float base = most == -INFINITY ? 0.f : most;
             const float mine = __builtin_amdgcn_exp2f(top - base), its = __builtin_amdgcn_exp2f(t - base);
@@ -386,30 +471,40 @@ __global__ __launch_bounds__(kThreads) void k_attend_combine(AttendArgs a) {
     const int64_t line0 = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
     if (line0 >= s.nq * a.heads) return;
     const int64_t line = s.q0 * a.heads + line0, all = a.n_q * a.heads;
-    float top = -INFINITY;
-    for (int i = 0; i < a.splits; ++i) top = fmaxf(top, a.part_stat[i * all + line].x);
+    // each lane looks after one part's maximum and sum; kMaxSplits = 64
+    const int parts = static_cast<int>(parts_of(s.nk, a.per));
+    const int lane = lane_id();
+    const float2 st = a.part_stat[(lane < parts ? lane : 0) * all + line];
+    float top = lane < parts ? st.x : -INFINITY;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
     const float base = top == -INFINITY ? 0.f : top;
-    const int c = 2 * lane_id();
-    float sum = 0.f, x = 0.f, y = 0.f;
-    for (int i = 0; i < a.splits; ++i) {
-        const float2 st = a.part_stat[i * all + line];
-        const float f = __builtin_amdgcn_exp2f(st.x - base);
-        sum += st.y * f;
-        if (c < a.d) {
-            const float2 v = *reinterpret_cast<const float2 *>(a.part + (i * all + line) * a.d + c);
-            x += v.x * f;
-            y += v.y * f;
-        }
+    const float mine = lane < parts ? __builtin_amdgcn_exp2f(st.x - base) : 0.f;
+    const float sum = wave_sum(lane < parts ? st.y * mine : 0.f);
+    const int c = 2 * lane;
+    float x = 0.f, y = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < parts; ++i) {
+        const float f = __shfl(mine, i, 64);
+        const float2 v = *reinterpret_cast<const float2 *>(a.part + (i * all + line) * a.d + (c < a.d ? c : 0));
+        x += v.x * f;
+        y += v.y * f;
     }
     const int64_t pos = s.q0 + line0 / a.heads, head = line0 % a.heads;
     const float each = sum == 0.f ? 0.f : 1.f / sum;
     if (c < a.d) store_f32<T, 2>(static_cast<T *>(a.out) + pos * a.ld_out + head * a.d + c, vec<float, 2>{x * each, y * each});
-    if (a.lse && lane_id() == 0) a.lse[line] = (top + log2f(sum)) * kLn2;
+    if (a.lse && lane == 0) a.lse[line] = (top + log2f(sum)) * kLn2;
 }
 
 // ---- backward -------------------------------------------------------------------------------------
 
-// stat[line] = {lse log2(e), D}; a row without weights (lse = -inf) gets +inf, which marks it.
+// Where the statistics of a query row's head are kept: by state head, then as the group's rows.
+__device__ __forceinline__ int64_t stat_at(const AttendArgs &a, int64_t pos, int32_t head) {
+    const int32_t hk = static_cast<int32_t>(fast_div(static_cast<uint32_t>(head), a.by_group));
+    return (hk * a.n_q + pos) * a.group + (head - hk * a.group);
+}
+
+// stat = {lse log2(e), D}; a row without weights (lse = -inf) gets +inf, which marks it.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_attend_stat(AttendArgs a) {
     // eight lanes a row, 16 columns a lane
@@ -429,20 +524,23 @@ __global__ __launch_bounds__(kThreads) void k_attend_stat(AttendArgs a) {
     sum += __shfl_xor(sum, 4, 64);
     if ((threadIdx.x & 7) == 0) {
         const float l = a.lse[line];
-        a.stat[line] = float2{l == -INFINITY ? INFINITY : l * kLog2E, sum};
+        a.stat[stat_at(a, pos, static_cast<int32_t>(head))] = float2{l == -INFINITY ? INFINITY : l * kLog2E, sum};
     }
 }
 
 template <typename T, int DP, int WQ, int WK>
-__global__ __launch_bounds__(kThreads) void k_attend_dq(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, WK == 1 && sizeof(T) == 2 ? 2 : 1) void k_attend_dq(AttendArgs a) {
     constexpr int KW = 32, BK = KW * WK, BQ = 32 * WQ, DB = DP / 32;
     typedef Tile<T, DP> Tl;
-    __shared__ Piece<T> smem[2 * BK * Tl::NP];
-    const Tl tk{smem}, tv{smem + BK * Tl::NP};
+    typedef Turned<T, DP> Tu;
+    constexpr int kPair = 2 * Tl::pieces(BK);
+    __shared__ Piece<T> smem[2 * kPair];
     const Seq s = sequence(a, blockIdx.z);
     const int hk = static_cast<int>(blockIdx.y) / a.splits, split = static_cast<int>(blockIdx.y) % a.splits;
     const int64_t rows = s.nq * a.group, r0 = static_cast<int64_t>(blockIdx.x) * BQ;
-    if (r0 >= rows) return;      // whole workgroup
+    if (r0 >= rows || split >= parts_of(s.nk, a.per)) return;      // whole workgroup
+    int64_t kb, ke;
+    part_range(s.nk, a.per, split, BK, kb, ke);
     const int lane = lane_id(), w = threadIdx.x >> 6, wq = w / WK, wk = w % WK;
     const int64_t r = r0 + wq * 32 + (lane & 31);
     const GroupRow me = group_row(a, s, hk, r < rows ? r : rows - 1);
@@ -450,45 +548,70 @@ __global__ __launch_bounds__(kThreads) void k_attend_dq(AttendArgs a) {
     RowPieces<T, DP> q, g;
     q.load(static_cast<const T *>(a.q) + me.pos * a.ld_q + me.head * a.d, r < rows, a.d);
     g.load(static_cast<const T *>(a.dout) + me.pos * a.ld_dout + me.head * a.d, r < rows, a.d);
-    const float2 st = a.stat[line];
-    int64_t kb, ke;
-    split_range(s.nk, split, a.splits, BK, kb, ke);
+    const float2 st = a.stat[stat_at(a, me.pos, me.head)];
+    const bool live = st.x != INFINITY;      // a row without weights has zeros, whatever is not finite
     const T *kp = static_cast<const T *>(a.k) + s.k0 * a.ld_k + hk * a.d;
     const T *vp = static_cast<const T *>(a.v) + s.k0 * a.ld_v + hk * a.d;
     f32x16 dq[DB];
 #pragma unroll
     for (int i = 0; i < DB; ++i) dq[i] = f32x16(0.f);
+    const auto k_row = [&](int i) { return static_cast<uint32_t>(i) * static_cast<uint32_t>(a.ld_k); };
+    const auto v_row = [&](int i) { return static_cast<uint32_t>(i) * static_cast<uint32_t>(a.ld_v); };
     Stage<T, DP, BK> sk, sv;
-    if (kb < ke) {
-        sk.load(ke - kb, a.d, [&](int i) { return kp + (kb + i) * a.ld_k; });
-        sv.load(ke - kb, a.d, [&](int i) { return vp + (kb + i) * a.ld_v; });
-    }
-    for (int64_t k0 = kb; k0 < ke; k0 += BK) {
-        __syncthreads();
-        sk.put(tk);
-        sv.put(tv);
-        __syncthreads();
-        const int64_t k1 = k0 + BK;
-        if (k1 < ke) {
-            sk.load(ke - k1, a.d, [&](int i) { return kp + (k1 + i) * a.ld_k; });
-            sv.load(ke - k1, a.d, [&](int i) { return vp + (k1 + i) * a.ld_v; });
-        }
-        f32x16 x = product<T, DP>(tk, wk * KW, q);
-        const f32x16 dp = product<T, DP>(tv, wk * KW, g);
+    const auto load = [&](int64_t at) {
+        sk.load(kp + at * a.ld_k, ke - at, a.d, k_row);
+        sv.load(vp + at * a.ld_v, ke - at, a.d, v_row);
+    };
+    const auto put = [&](Piece<T> *pair, int64_t at) {
         // states past the end: k and v are zeros there, and add nothing to dq
+        sk.put(Tl{pair}, ke - at, a.d);
+        sv.put(Tl{pair + kPair / 2}, ke - at, a.d);
+        __syncthreads();
+    };
+    const auto turn = [&](Piece<T> *pair, Piece<T> *next, int64_t k0) {
+        const Tl tk{pair}, tv{pair + kPair / 2};
+        const int64_t k1 = k0 + BK;
+        if (k1 < ke) load(k1);
+        constexpr int KK = RowPieces<T, DP>::KK, kR = row_ring<T>();
+        f32x16 x(0.f), dp(0.f);
+        Piece<T> ring[kR];
+        const auto piece = [&](int i) { return row_piece<T, DP>(i < KK ? tk : tv, wk * KW, i % KK); };
+        prime<kR, 2 * KK>(ring, piece);
+        typename Tu::V turned[Tu::kRing];
+        const auto column = [&](int i) { return Tu::load(tk, wk * KW, i); };
+        stream<kR, 2 * KK>(ring, piece, [&](int i, const Piece<T> &v) {
+            if (i < KK) {
+                mma(x, v, q.v[i]);
+            } else {
+                mma(dp, v, g.v[i - KK]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            x[i] = st.x == INFINITY ? 0.f
-                                    : __builtin_amdgcn_exp2f(x[i] * a.scale2 - st.x) * (dp[i] - st.y);
-        mma_turned<DP>(dq, tk, wk * KW, x);
+                for (int j = (i - KK) * 16 / KK; j < (i - KK + 1) * 16 / KK; ++j)      // the weights, meanwhile
+                    x[j] = __builtin_amdgcn_exp2f(live ? x[j] * a.scale2 - st.x : -INFINITY);
+            }
+        });
+        prime<Tu::kRing, Tu::kSteps>(turned, column);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] *= live ? dp[i] - st.y : 0.f;
+        Tu tu;
+        stream<Tu::kRing, Tu::kSteps>(turned, column,
+                                      [&](int i, const typename Tu::V &v) { tu.use(dq, v, i, x); });
+        if (k1 < ke) put(next, k1);
+    };
+    if (kb < ke) {
+        load(kb);
+        put(smem, kb);
+    }
+    for (int64_t k0 = kb; k0 < ke; k0 += 2 * BK) {
+        turn(smem, smem + kPair, k0);
+        if (k0 + BK < ke) turn(smem + kPair, smem, k0 + BK);
     }
     if (WK > 1) {
         constexpr int kRow = DP + 4;
-        static_assert((WK - 1) * 32 * kRow * 4 <= static_cast<int>(sizeof(smem)), "join area");
-        float *join = reinterpret_cast<float *>(smem);
+        static_assert((WK - 1) * WQ * 32 * kRow * 4 <= static_cast<int>(sizeof(smem)), "join area");
+        float *join = reinterpret_cast<float *>(smem) + (wq * (WK - 1) * 32 + (lane & 31)) * kRow;
         __syncthreads();
         if (wk > 0) {
-            float *row = join + ((wk - 1) * 32 + (lane & 31)) * kRow;
+            float *row = join + (wk - 1) * 32 * kRow;
 #pragma unroll
             for (int i = 0; i < DB; ++i)
 #pragma unroll
@@ -499,7 +622,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_dq(AttendArgs a) {
         __syncthreads();
         if (wk > 0) return;
         for (int u = 0; u < WK - 1; ++u) {
-            const float *row = join + (u * 32 + (lane & 31)) * kRow;
+            const float *row = join + u * 32 * kRow;
 #pragma unroll
             for (int i = 0; i < DB; ++i)
 #pragma unroll
@@ -528,16 +651,21 @@ __global__ __launch_bounds__(kThreads) void k_attend_dq(AttendArgs a) {
 
 // dk and dv of 128 states, 32 a wavefront; splits > 1 shares the query rows among workgroups.
 template <typename T, int DP>
-__global__ __launch_bounds__(kThreads) void k_attend_dkv(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, 1) void k_attend_dkv(AttendArgs a) {
     constexpr int BR = 32, DB = DP / 32;
     typedef Tile<T, DP> Tl;
-    __shared__ Piece<T> smem[2 * BR * Tl::NP];
-    __shared__ float2 sstat[BR];
-    const Tl tq{smem}, tg{smem + BR * Tl::NP};
+    typedef Turned<T, DP> Tu;
+    constexpr int kPair = 2 * Tl::pieces(BR);
+    __shared__ Piece<T> smem[2 * kPair];
+    __shared__ f32x4 sstat[2][BR / 2];      // {lse, D} of two rows
     const Seq s = sequence(a, blockIdx.z);
     const int hk = static_cast<int>(blockIdx.y) / a.splits, split = static_cast<int>(blockIdx.y) % a.splits;
     const int64_t c0 = static_cast<int64_t>(blockIdx.x) * 128;
-    if (c0 >= s.span) return;      // whole workgroup
+    const int64_t rows = s.nq * a.group;
+    if (c0 >= s.span || split >= parts_of(rows, a.per)) return;      // whole workgroup
+    int64_t rb, re;
+    part_range(rows, a.per, split, BR, rb, re);
+    if (c0 >= s.nk) re = rb;                         // nothing counts
     const int lane = lane_id(), w = threadIdx.x >> 6;
     const int64_t key = c0 + w * 32 + (lane & 31);
     const bool counts = key < s.nk;
@@ -548,47 +676,83 @@ __global__ __launch_bounds__(kThreads) void k_attend_dkv(AttendArgs a) {
     f32x16 dk[DB], dv[DB];
 #pragma unroll
     for (int i = 0; i < DB; ++i) dk[i] = dv[i] = f32x16(0.f);
-    int64_t rb = 0, re = 0;
-    if (c0 < s.nk) split_range(s.nq * a.group, split, a.splits, BR, rb, re);   // else: nothing counts
+    // the statistics of this state head's rows lie next to each other
+    const float2 *stat = a.stat + (static_cast<int64_t>(hk) * a.n_q + s.q0) * a.group;
     Stage<T, DP, BR> sq, sg;
-    float2 st{INFINITY, 0.f};
-    auto load = [&](int64_t r0) {
-        const auto q_row = [&](int i) {
-            const GroupRow g = group_row(a, s, hk, r0 + i);
-            return static_cast<const T *>(a.q) + g.pos * a.ld_q + g.head * a.d;
+    float2 st;
+    const auto load = [&](int64_t r0) {
+        // the tile's first query row, and the rows' distances from its first head of the group
+        const uint32_t p0 = fast_div(static_cast<uint32_t>(r0), a.by_group);
+        const auto row = [&](int i, int64_t ld) {
+            const uint32_t r = static_cast<uint32_t>(r0) + i, p = fast_div(r, a.by_group);
+            return (p - p0) * static_cast<uint32_t>(ld) + (r - p * a.group) * static_cast<uint32_t>(a.d);
         };
-        const auto g_row = [&](int i) {
-            const GroupRow g = group_row(a, s, hk, r0 + i);
-            return static_cast<const T *>(a.dout) + g.pos * a.ld_dout + g.head * a.d;
-        };
-        sq.load(re - r0, a.d, q_row);
-        sg.load(re - r0, a.d, g_row);
-        st = float2{INFINITY, 0.f};          // rows past the end: P = 0
-        if (threadIdx.x < BR && r0 + threadIdx.x < re) {
-            const GroupRow g = group_row(a, s, hk, r0 + threadIdx.x);
-            st = a.stat[g.pos * a.heads + g.head];
-        }
+        sq.load(static_cast<const T *>(a.q) + (s.q0 + p0) * a.ld_q + hk * a.group * a.d, re - r0, a.d,
+                [&](int i) { return row(i, a.ld_q); });
+        sg.load(static_cast<const T *>(a.dout) + (s.q0 + p0) * a.ld_dout + hk * a.group * a.d, re - r0,
+                a.d, [&](int i) { return row(i, a.ld_dout); });
+        const int64_t r = r0 + (threadIdx.x & (BR - 1));
+        st = stat[r < re ? r : re - 1];
     };
-    if (rb < re) load(rb);
-    for (int64_t r0 = rb; r0 < re; r0 += BR) {
+    const auto put = [&](int pair, int64_t r0) {
+        sq.put(Tl{smem + pair * kPair}, re - r0, a.d);
+        sg.put(Tl{smem + pair * kPair + kPair / 2}, re - r0, a.d);
+        if (threadIdx.x < BR)      // rows past the end are marked as without weights
+            reinterpret_cast<float2 *>(sstat[pair])[threadIdx.x] =
+                r0 + threadIdx.x < re ? st : float2{INFINITY, 0.f};
         __syncthreads();
-        sq.put(tq);
-        sg.put(tg);
-        if (threadIdx.x < BR) sstat[threadIdx.x] = st;
-        __syncthreads();
-        if (r0 + BR < re) load(r0 + BR);
-        f32x16 p = product<T, DP>(tq, 0, k);
-        f32x16 ds = product<T, DP>(tg, 0, v);
+    };
+    const auto turn = [&](int pair, int64_t r0) {
+        const Tl tq{smem + pair * kPair}, tg{smem + pair * kPair + kPair / 2};
+        const int64_t r1 = r0 + BR;
+        if (r1 < re) load(r1);
+        constexpr int KK = RowPieces<T, DP>::KK, kR = row_ring<T>();
+        f32x16 p(0.f), ds(0.f);
+        Piece<T> ring[kR];
+        const auto piece = [&](int i) { return row_piece<T, DP>(i < KK ? tq : tg, 0, i % KK); };
+        prime<kR, 2 * KK>(ring, piece);
+        f32x4 x[8];      // rows 8 g + 4 half + 0..3
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float2 x = sstat[8 * (i >> 2) + 4 * (lane >> 5) + (i & 3)];
-            // a row without weights, or past the end: zero, also against states that are not finite
-            const bool live = x.x != INFINITY;
-            p[i] = live ? __builtin_amdgcn_exp2f(p[i] * a.scale2 - x.x) : 0.f;
-            ds[i] = live ? p[i] * (ds[i] - x.y) : 0.f;
-        }
-        mma_turned<DP>(dv, tg, 0, p);
-        mma_turned<DP>(dk, tq, 0, ds);
+        for (int i = 0; i < 8; ++i) x[i] = sstat[pair][4 * (i >> 1) + 2 * (lane >> 5) + (i & 1)];
+        typename Tu::V turned[Tu::kRing];
+        const auto column = [&](int i) {
+            return Tu::load(i < Tu::kSteps ? tg : tq, 0, i % Tu::kSteps);
+        };
+        stream<kR, 2 * KK>(ring, piece, [&](int i, const Piece<T> &u) {
+            if (i < KK) {
+                mma(p, u, k.v[i]);
+            } else {
+                mma(ds, u, v.v[i - KK]);
+                // the weights, meanwhile; a row without weights has zeros, also against states that are
+                // not finite
+#pragma unroll
+                for (int j = (i - KK) * 16 / KK; j < (i - KK + 1) * 16 / KK; ++j) {
+                    const float l = x[j >> 1][2 * (j & 1)];
+                    p[j] = __builtin_amdgcn_exp2f(l != INFINITY ? p[j] * a.scale2 - l : -INFINITY);
+                }
+            }
+        });
+        prime<Tu::kRing, 2 * Tu::kSteps>(turned, column);
+        Tu tu;
+        stream<Tu::kRing, 2 * Tu::kSteps>(turned, column, [&](int i, const typename Tu::V &u) {
+            if (i < Tu::kSteps) {
+                tu.use(dv, u, i, p);
+#pragma unroll
+                for (int j = i * 16 / Tu::kSteps; j < (i + 1) * 16 / Tu::kSteps; ++j)
+                    ds[j] = p[j] * (x[j >> 1][2 * (j & 1)] != INFINITY ? ds[j] - x[j >> 1][2 * (j & 1) + 1] : 0.f);
+            } else {
+                tu.use(dk, u, i - Tu::kSteps, ds);
+            }
+        });
+        if (r1 < re) put(pair ^ 1, r1);
+    };
+    if (rb < re) {
+        load(rb);
+        put(0, rb);
+    }
+    for (int64_t r0 = rb; r0 < re; r0 += 2 * BR) {
+        turn(0, r0);
+        if (r0 + BR < re) turn(1, r0 + BR);
     }
     if (key >= s.span) return;
     // a state past the count has no gradient
@@ -627,9 +791,11 @@ __global__ __launch_bounds__(kThreads) void k_attend_reduce(AttendArgs a, int st
     const int64_t all = (states ? a.n_k : a.n_q) * per;
     const int64_t pos = first + line0 / per, head = line0 % per;
     const int wide = states ? 2 * a.d : a.d;
+    const int parts = static_cast<int>(parts_of(states ? s.nq * a.group : s.nk, a.per));
     for (int c = 2 * lane_id(); c < wide; c += 128) {
         float x = 0.f, y = 0.f;
-        for (int i = 0; i < a.splits; ++i) {
+#pragma unroll 8
+        for (int i = 0; i < parts; ++i) {
             const float2 v = *reinterpret_cast<const float2 *>(a.part + (i * all + line) * wide + c);
             x += v.x;
             y += v.y;
@@ -648,35 +814,42 @@ __global__ __launch_bounds__(kThreads) void k_attend_reduce(AttendArgs a, int st
 // ---- host -------------------------------------------------------------------------------------------
 
 constexpr int64_t kWantGroups = 1024;     // workgroups that fill the card
-constexpr int64_t kMaxSplits = 64;
+constexpr int64_t kFewTiles = 256;        // fewer tiles of 128 rows than compute units: tiles of 32
+constexpr int64_t kMaxSplits = 64;        // one lane each in the combining kernel
 
 // The plan of a call, from its host-side sizes alone.
 struct Plan {
-    bool few;                 // at most 32 rows a sequence: the wavefronts share the states
+    bool few;                 // tiles of few rows, the wavefronts share the states
     int64_t q_tiles, k_tiles;
-    int splits, dq_splits, dkv_splits;
+    int splits, dkv_splits;   // of the states (forward, dq) and of the rows (dk, dv)
+    int64_t per, dkv_per;     // their lengths
     size_t stat, part_stat, part, bytes;      // byte offsets
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-int pick_splits(int64_t groups, int64_t length, int64_t least) {
-    if (groups >= kWantGroups || groups < 1) return 1;
-    int64_t s = ceil_div(kWantGroups, groups), most = length / least;
-    if (s > most) s = most;
+// Splits `length` among workgroups until `groups` of them fill the card, in parts of whole multiples of
+// `least`.
+void pick_splits(int64_t groups, int64_t length, int64_t least, int &splits, int64_t &per) {
+    int64_t s = groups < 1 ? 1 : ceil_div(kWantGroups, groups);
     if (s > kMaxSplits) s = kMaxSplits;
-    return static_cast<int>(s < 1 ? 1 : s);
+    if (s < 1) s = 1;
+    per = ceil_div(ceil_div(length, s), least) * least;
+    if (per < least) per = least;
+    splits = length <= per ? 1 : static_cast<int>(ceil_div(length, per));
 }
 
 Plan plan_for(const AttendArgs &a, bool backward) {
     Plan p{};
     const int64_t rows = a.max_q * a.group;
-    p.few = rows <= 32;
-    p.q_tiles = ceil_div(rows, p.few ? 32 : 128);
-    p.k_tiles = ceil_div(a.max_k, 128);
     const int64_t side = a.n_seq * a.kv;
-    p.splits = p.dq_splits = pick_splits(side * p.q_tiles, a.max_k, 256);
-    p.dkv_splits = pick_splits(side * p.k_tiles, rows, 128);
+    p.few = rows <= 32 || side * ceil_div(rows, 128) < kFewTiles;
+    // (sharing(): two wavefronts' rows for wide fp32 heads)
+    const int few_rows = a.type == GNN_F32 && a.d > 64 ? 64 : 32;
+    p.q_tiles = ceil_div(rows, p.few ? few_rows : 128);
+    p.k_tiles = ceil_div(a.max_k, 128);
+    pick_splits(side * p.q_tiles, a.max_k, p.few ? 128 : 256, p.splits, p.per);
+    pick_splits(side * p.k_tiles, rows, 128, p.dkv_splits, p.dkv_per);
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -699,10 +872,11 @@ Plan plan_for(const AttendArgs &a, bool backward) {
 template <typename T, int DP>
 hipError_t forward(AttendArgs a, const Plan &p, hipStream_t s) {
     a.splits = p.splits;
+    a.per = p.per;
     const dim3 grid(static_cast<unsigned>(p.q_tiles), static_cast<unsigned>(a.kv * p.splits),
                     static_cast<unsigned>(a.n_seq));
     if (p.few)
-        hipLaunchKernelGGL((k_attend<T, DP, 1, 4>), grid, dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL((k_attend<T, DP, 4 / sharing<T, DP>(), sharing<T, DP>()>), grid, dim3(kThreads), 0, s, a);
     else
         hipLaunchKernelGGL((k_attend<T, DP, 4, 1>), grid, dim3(kThreads), 0, s, a);
     if (p.splits > 1)
@@ -721,10 +895,11 @@ hipError_t backward(AttendArgs a, const Plan &p, hipStream_t s) {
                            dim3(static_cast<unsigned>(ceil_div(a.n_q * a.heads, 32))),
                            dim3(kThreads), 0, s, a);
     if (a.max_q > 0) {
-        a.splits = p.dq_splits;
+        a.splits = p.splits;
+        a.per = p.per;
         const dim3 grid(static_cast<unsigned>(p.q_tiles), static_cast<unsigned>(a.kv * a.splits), z);
         if (p.few)
-            hipLaunchKernelGGL((k_attend_dq<T, DP, 1, 4>), grid, dim3(kThreads), 0, s, a);
+            hipLaunchKernelGGL((k_attend_dq<T, DP, 4 / sharing<T, DP>(), sharing<T, DP>()>), grid, dim3(kThreads), 0, s, a);
         else
             hipLaunchKernelGGL((k_attend_dq<T, DP, 4, 1>), grid, dim3(kThreads), 0, s, a);
         if (a.splits > 1)
@@ -734,6 +909,7 @@ hipError_t backward(AttendArgs a, const Plan &p, hipStream_t s) {
     }
     if (a.max_k > 0) {
         a.splits = p.dkv_splits;
+        a.per = p.dkv_per;
         const dim3 grid(static_cast<unsigned>(p.k_tiles), static_cast<unsigned>(a.kv * a.splits), z);
         hipLaunchKernelGGL((k_attend_dkv<T, DP>), grid, dim3(kThreads), 0, s, a);
         if (a.splits > 1)
@@ -746,7 +922,9 @@ hipError_t backward(AttendArgs a, const Plan &p, hipStream_t s) {
 
 template <typename T>
 hipError_t run(const AttendArgs &a, const Plan &p, bool back, hipStream_t s) {
+    if (a.d <= 32) return back ? backward<T, 32>(a, p, s) : forward<T, 32>(a, p, s);
     if (a.d <= 64) return back ? backward<T, 64>(a, p, s) : forward<T, 64>(a, p, s);
+    if (a.d <= 96) return back ? backward<T, 96>(a, p, s) : forward<T, 96>(a, p, s);
     return back ? backward<T, 128>(a, p, s) : forward<T, 128>(a, p, s);
 }
 

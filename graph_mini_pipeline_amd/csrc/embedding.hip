@@ -306,25 +306,25 @@ __device__ __forceinline__ bool is_head(uint32_t key, uint32_t prev, bool first,
     return key < rows && (first || key != prev);
 }
 
-// The one-workgroup sort: n <= ROUNDS * 1024 positions, sorted, in key and pos.
-template <int ROUNDS>
+// The one-workgroup sort: n <= ROUNDS * THREADS positions, sorted, in key and pos.
+template <int ROUNDS, int THREADS>
 struct OneSort {
-    static constexpr int kWaves = kOneThreads / 64;
-    uint32_t key[ROUNDS * kOneThreads];
-    uint16_t pos[ROUNDS * kOneThreads];
+    static constexpr int kWaves = THREADS / 64;
+    uint32_t key[ROUNDS * THREADS];
+    uint16_t pos[ROUNDS * THREADS];
     uint32_t cnt[kWaves][kDigits];
     uint32_t base[kDigits];
     uint32_t s4[4];
 };
 
 // mark: every named row's mark is set.  Every thread of the workgroup calls it.
-template <int ROUNDS>
-__device__ __forceinline__ void sort_one(const SortArgs &a, OneSort<ROUNDS> &m, bool mark) {
-    constexpr int kWaves = OneSort<ROUNDS>::kWaves;
+template <int ROUNDS, int THREADS>
+__device__ __forceinline__ void sort_one(const SortArgs &a, OneSort<ROUNDS, THREADS> &m, bool mark) {
+    constexpr int kWaves = THREADS / 64;
     const int t = threadIdx.x, w = t >> 6;
     const int n = static_cast<int>(a.n);
     const int64_t n_act = load_count(a.d_n, a.n);
-    const int rounds = (n + kOneThreads - 1) / kOneThreads;
+    const int rounds = (n + THREADS - 1) / THREADS;
     const int i0 = w * 64 * rounds + lane_id();
     uint32_t key[ROUNDS], pos[ROUNDS], rank[ROUNDS];
 #pragma unroll
@@ -341,7 +341,7 @@ __device__ __forceinline__ void sort_one(const SortArgs &a, OneSort<ROUNDS> &m, 
     }
     for (int p = 0; p < a.passes; ++p) {
         const int shift = p * a.bits;
-        for (int i = t; i < kWaves * kDigits; i += kOneThreads) (&m.cnt[0][0])[i] = 0;
+        for (int i = t; i < kWaves * kDigits; i += THREADS) (&m.cnt[0][0])[i] = 0;
         __syncthreads();
         rank_rounds<ROUNDS>(key, rounds, shift, a.bits, m.cnt[w], rank);
         __syncthreads();
@@ -379,7 +379,7 @@ __device__ __forceinline__ void sort_one(const SortArgs &a, OneSort<ROUNDS> &m, 
 }
 
 __global__ __launch_bounds__(kOneThreads) void k_sort_one(SortArgs a) {
-    __shared__ OneSort<kSortRounds> m;
+    __shared__ OneSort<kSortRounds, kOneThreads> m;
     __shared__ uint32_t sw[kOneThreads / 64];
     const int t = threadIdx.x;
     const int n = static_cast<int>(a.n);
@@ -388,7 +388,7 @@ __global__ __launch_bounds__(kOneThreads) void k_sort_one(SortArgs a) {
         __threadfence();        // before the marks
         __syncthreads();
     }
-    sort_one<kSortRounds>(a, m, a.touched != nullptr);
+    sort_one(a, m, a.touched != nullptr);
     for (int i = t; i < n; i += kOneThreads) {
         a.key_out[i] = m.key[i];
         a.pos_out[i] = m.pos[i];
@@ -687,29 +687,32 @@ __global__ __launch_bounds__(kSumThreads) void k_embedding_join(SumArgs a) {
 // workgroup sorts all positions for itself and then takes its share: the runs that begin in its part
 // of the sorted list (short ones by a lane group each, long ones by all groups in turn) and, for a
 // written dense table, the unnamed rows in its part of the table.
-constexpr int kFewRounds = 2;
-constexpr int kFewMost = kFewRounds * kOneThreads;
+constexpr int kFewThreads = 512;   // (workgroups of 1024 start up to 6 us apart, of 512 half that)
+constexpr int kFewRounds = 4;
+constexpr int kFewMost = kFewRounds * kFewThreads;
 constexpr int kFewShare = 16;      // sorted positions per workgroup
 constexpr int kFewRun = 32;        // longest run that one lane group takes
 
 template <typename TI, typename TO, int VE>
-__global__ __launch_bounds__(kOneThreads) void k_embedding_few(SortArgs q, SumArgs a, int zero) {
-    __shared__ OneSort<kFewRounds> m;
-    __shared__ uint32_t sw[kOneThreads / 64];
+__global__ __launch_bounds__(kFewThreads) void k_embedding_few(SortArgs q, SumArgs a, int zero) {
+    __shared__ OneSort<kFewRounds, kFewThreads> m;
+    __shared__ uint32_t sw[kFewThreads / 64];
     __shared__ uint32_t rank_of[kFewShare];
-    __shared__ float sm[kOneThreads * VE];
+    __shared__ uint32_t long_runs;       // one bit per position of the share
+    __shared__ float sm[kFewThreads * VE];
     const int t = threadIdx.x, n = static_cast<int>(q.n);
-    sort_one<kFewRounds>(q, m, false);
+    if (t == 0) long_runs = 0;
+    sort_one(q, m, false);
     const int lo = static_cast<int>(blockIdx.x) * kFewShare;
     const auto head = [&](int i) { return is_head(m.key[i], i > 0 ? m.key[i - 1] : 0u, i == 0, q.num_rows); };
     if (q.rows) {
         // ranks of the runs; the first workgroup writes the list
         uint32_t carry = 0;
-        for (int r0 = 0; r0 < n; r0 += kOneThreads) {
+        for (int r0 = 0; r0 < n; r0 += kFewThreads) {
             const int i = r0 + t;
             const uint32_t h = i < n && head(i);
             uint32_t total;
-            const uint32_t at = carry + block_exclusive_scan<uint32_t, kOneThreads>(h, &total, sw);
+            const uint32_t at = carry + block_exclusive_scan<uint32_t, kFewThreads>(h, &total, sw);
             if (i >= lo && i < lo + kFewShare) rank_of[i - lo] = at;
             if (blockIdx.x == 0 && h && at < q.row_cap) q.uniq[at] = static_cast<int32_t>(m.key[i]);
             carry += total;
@@ -720,7 +723,7 @@ __global__ __launch_bounds__(kOneThreads) void k_embedding_few(SortArgs q, SumAr
         }
         __syncthreads();
     }
-    const int groups = kOneThreads / a.lanes, grp = t / a.lanes, lane = t & (a.lanes - 1);
+    const int groups = kFewThreads / a.lanes, grp = t / a.lanes, lane = t & (a.lanes - 1);
     const TI *dout = static_cast<const TI *>(a.dout);
     typedef typename loose<TI, VE>::type Raw;
     // the sum of positions i0, i0 + step, ... below end of the sorted list
@@ -744,14 +747,18 @@ __global__ __launch_bounds__(kOneThreads) void k_embedding_few(SortArgs q, SumAr
     for (int item = grp; item < (hi - lo) * a.slabs; item += groups) {
         const int i = lo + item / a.slabs;
         if (!head(i)) continue;
+        if (i + kFewRun < n && m.key[i + kFewRun] == m.key[i]) {
+            if (lane == 0) atomicOr(&long_runs, 1u << (i - lo));
+            continue;
+        }
         int end = i + 1;
-        while (end < n && end <= i + kFewRun && m.key[end] == m.key[i]) ++end;
-        if (end > i + kFewRun) continue;
+        while (end < n && m.key[end] == m.key[i]) ++end;
         const Cols c = lane_cols<VE>(item % a.slabs, a.lanes, lane, a.d);
         put_row<TO, VE>(a, q.rows ? static_cast<int64_t>(rank_of[i - lo]) : m.key[i], c, sum(i, end, 1, c));
     }
-    for (int i = lo; i < hi; ++i) {      // whole workgroup
-        if (!head(i) || i + kFewRun >= n || m.key[i + kFewRun] != m.key[i]) continue;
+    __syncthreads();
+    for (uint32_t left = long_runs; left != 0; left &= left - 1) {      // whole workgroup
+        const int i = lo + __ffs(static_cast<int>(left)) - 1;
         int end = i + kFewRun + 1, over = n;     // the first position of another key
         while (end < over) {
             const int mid = (end + over) / 2;
@@ -762,12 +769,12 @@ __global__ __launch_bounds__(kOneThreads) void k_embedding_few(SortArgs q, SumAr
             vec<float, VE> acc = sum(i + grp, end, groups, c);
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < VE; ++e) sm[e * kOneThreads + t] = acc[e];
+            for (int e = 0; e < VE; ++e) sm[e * kFewThreads + t] = acc[e];
             __syncthreads();
             if (grp == 0) {
                 for (int g = 1; g < groups; ++g)
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) acc[e] += sm[e * kOneThreads + g * a.lanes + lane];
+                    for (int e = 0; e < VE; ++e) acc[e] += sm[e * kFewThreads + g * a.lanes + lane];
                 put_row<TO, VE>(a, q.rows ? static_cast<int64_t>(rank_of[i - lo]) : m.key[i], c, acc);
             }
         }
@@ -885,7 +892,7 @@ hipError_t run_sums(const EmbedGradArgs &a, const GradSpace &g, const SortArgs &
         const int64_t clear = a.num_rows / 32 < 128 ? a.num_rows / 32 : 128;
         if (zero_untouched && grid < clear) grid = clear;     // more workgroups, for the unnamed rows
         hipLaunchKernelGGL((k_embedding_few<TI, TO, VE>), dim3(static_cast<unsigned>(grid)),
-                           dim3(kOneThreads), 0, s, sort, p,
+                           dim3(kFewThreads), 0, s, sort, p,
                            zero_untouched ? 1 : 0);
         return hipGetLastError();
     }

@@ -94,6 +94,7 @@ struct AttendArgs {
     // set by the launcher
     FastDiv by_group;
     int32_t splits;
+    int64_t per;           // states (or rows) per split
     float2 *stat;          // [n_q * heads] {lse log2(e), dout . out}
     float *part;           // partial sums of the splits
     float2 *part_stat;     // [splits, n_q * heads] {maximum, sum}

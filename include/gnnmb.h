@@ -579,8 +579,8 @@ gnn_status gnn_embedding_grad_rows(const int32_t *ids, const int64_t *d_n, int64
  * leaves [0, n]; it is clamped), GNN_ERR_CAPACITY (a sequence longer than max_q or max_k; the rows
  * beyond are left out).
  * Errors: GNN_ERR_INVALID_ARG; GNN_ERR_CAPACITY (ws too small); GNN_ERR_UNSUPPORTED for another
- * type, a head_dim that is no multiple of 8 or over 128, heads over 1024, n_seq over 65535, or
- * n_q * heads or n_k * kv_heads over 2^31 - 1.
+ * type, a head_dim that is no multiple of 8 or over 128, heads over 1024, n_seq over 65535,
+ * n_q * heads or n_k * kv_heads over 2^31 - 1, or rows of q, k, v or dout over 2^21 elements apart.
  */
 typedef struct gnn_attention {
     int32_t type, heads, kv_heads, head_dim;

@@ -34,7 +34,8 @@ SIZES = [("heads", 0, BAD), ("kv_heads", 0, BAD), ("kv_heads", 3, BAD), ("head_d
          ("heads", 2048, UNS)]
 POINTERS = [("q_indptr", None, BAD), ("k_indptr", None, BAD), ("q", None, BAD), ("k", None, BAD),
             ("v", None, BAD), ("out", None, BAD), ("ld_q", 511, BAD), ("ld_k", 127, BAD),
-            ("ld_v", 127, BAD), ("ld_out", 511, BAD), ("scale", float("nan"), BAD)]
+            ("ld_v", 127, BAD), ("ld_out", 511, BAD), ("ld_q", 2 ** 21 + 1, UNS),
+            ("ld_k", 2 ** 21 + 1, UNS), ("ld_v", 2 ** 21 + 1, UNS), ("scale", float("nan"), BAD)]
 
 
 @pytest.mark.parametrize("field,value,want", SIZES + POINTERS)
