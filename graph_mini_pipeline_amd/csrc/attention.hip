@@ -62,17 +62,23 @@ __device__ __forceinline__ void mma(f32x16 &acc, Piece<float> a, Piece<float> b)
 
 // A row-major LDS tile of DP columns, in 16-byte pieces.  A row is one piece longer than its columns, so
 // that the 32 rows which a read touches at the same piece spread over the banks, and every other
-// distance within a tile is a constant.
+// distance within a tile is a constant.  Row r lies at place(r): the rows 4 h + 0..3 of every sixteen
+// are four places apart, so that the 4 x 16 blocks of a transposing read, two beside each other, fill
+// the 64 banks exactly.
+__device__ __forceinline__ int place(int r) {
+    return (r & ~15) | ((r & 3) << 2) | ((r >> 3 & 1) << 1) | (r >> 2 & 1);
+}
 template <typename T, int DP>
 struct Tile {
     static constexpr int NP = DP / Kind<T>::kPiece;      // pieces per row
     static constexpr int kStride = NP + 1;
     static constexpr int pieces(int rows) { return rows * kStride; }
     Piece<T> *p;
-    __device__ __forceinline__ Piece<T> *at(int r, int c) const { return p + r * kStride + c; }
-    // element d of row r
-    __device__ __forceinline__ T *element(int r, int d) const {
-        return reinterpret_cast<T *>(at(r, 0)) + d;
+    // piece c of row r
+    __device__ __forceinline__ Piece<T> *at(int r, int c) const { return p + place(r) * kStride + c; }
+    // element d of row 4 h, 4 h of a tile's first sixteen rows
+    __device__ __forceinline__ T *quad(int h, int d) const {
+        return reinterpret_cast<T *>(p + h * kStride) + d;
     }
 };
 
@@ -82,6 +88,7 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // Operands come from LDS through a ring of RING registers sets, each read RING steps before the matrix
 // instructions that use it (left alone, the compiler reads one, waits for it, multiplies, and reads
 // the next).  use(s, v) may carry other work, which the matrix instructions hide.
+constexpr int kOthersMove = 0x406;      // scalar, vector and transcendental arithmetic may cross
 template <int RING, int STEPS, typename V, typename L>
 __device__ __forceinline__ void prime(V (&v)[RING], L load) {
 #pragma unroll
@@ -94,7 +101,7 @@ __device__ __forceinline__ void stream(V (&v)[RING], L load, U use) {
     for (int s = 0; s < STEPS; ++s) {
         use(s, v[s % RING]);
         if (s + RING < STEPS) v[s % RING] = load(s + RING);
-        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(kOthersMove);
     }
 }
 
@@ -105,18 +112,20 @@ struct Turned;
 
 template <int DP>
 struct Turned<bf16, DP> {
-    static constexpr int DB = DP / 32, kSteps = 2 * DB, kRing = 6;
+    static constexpr int DB = DP / 32, kSteps = 2 * DB, kRing = 4;
     struct V {
         s16x4 lo, hi;
     };
     static __device__ __forceinline__ V load(const Tile<bf16, DP> &tile, int row0, int s) {
         const int lane = lane_id();
-        // the transposing read: 16 lanes name a 4 x 16 block, 4 elements each, and get a column each
-        const int r = 4 * (lane >> 5) + ((lane & 15) >> 2);
+        // the transposing read: 16 lanes name a 4 x 16 block, 4 elements each, and get a column each;
+        // a row's successor is four places on, the row eight below it two
+        constexpr int kRow = Tile<bf16, DP>::kStride * 8;
         const int d = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-        bf16 *at = tile.element(r, d) + (row0 + 16 * (s / DB)) * Tile<bf16, DP>::kStride * 8 + 32 * (s % DB);
+        bf16 *at = tile.quad(lane >> 5, d) + ((lane & 15) >> 2) * 4 * kRow + (row0 + 16 * (s / DB)) * kRow +
+                   32 * (s % DB);
         return V{__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at),
-                 __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + 8 * Tile<bf16, DP>::kStride * 8))};
+                 __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + 2 * kRow))};
     }
     Piece<bf16> b;      // p's half that the current steps multiply
     __device__ __forceinline__ void use(f32x16 (&acc)[DB], const V &v, int s, const f32x16 &p) {
@@ -137,8 +146,9 @@ struct Turned<float, DP> {
     };
     static __device__ __forceinline__ V load(const Tile<float, DP> &tile, int row0, int s) {
         const int lane = lane_id();
-        const float *at = tile.element(4 * (lane >> 5), lane & 31) +
-                          (row0 + 8 * (s >> 2) + (s & 3)) * Tile<float, DP>::kStride * 4;
+        // row 8 (s / 4) + 4 half + s % 4
+        const float *at = tile.quad(lane >> 5, lane & 31) +
+                          (row0 + 16 * (s >> 3) + 2 * (s >> 2 & 1) + 4 * (s & 3)) * Tile<float, DP>::kStride * 4;
         V v;
 #pragma unroll
         for (int db = 0; db < DB; ++db) v.a[db] = at[32 * db];
@@ -193,11 +203,11 @@ __device__ __forceinline__ GroupRow group_row(const AttendArgs &a, const Seq &s,
     return g;
 }
 
-// Loads R rows of DP columns into registers, and puts them into a tile a turn later, rows at or past
-// `rows` and columns at or past d as zeros (only there, so that nothing waits for the loads before).
-// at(r) is row r's distance in elements from `base`, which is the same for all threads, so that an
-// address is a scalar pair and one 32-bit register (a tile's rows span fewer than 2^31 bytes); row 0
-// exists.
+// Loads R rows of DP columns into registers, and puts them into a tile a turn later, columns at or past d
+// as zeros and rows at or past `rows` as zeros too or as row 0 (only there, so that nothing waits for
+// the loads before).  at(r) is row r's distance in elements from `base`, which is the same for all
+// threads, so that an address is a scalar pair and one 32-bit register (a tile's rows span fewer than
+// 2^31 bytes); row 0 exists.  The first 256 threads of the workgroup call it.
 template <typename T, int DP, int R>
 struct Stage {
     static constexpr int NP = DP / Kind<T>::kPiece;
@@ -246,7 +256,7 @@ struct RowPieces {
 // Step s of the product of tile rows row0 .. row0+31 with the registers' rows.
 template <typename T>
 constexpr int row_ring() {
-    return sizeof(T) == 2 ? 6 : 3;      // an fp32 step is four long instructions
+    return sizeof(T) == 2 ? 4 : 3;      // an fp32 step is four long instructions
 }
 template <typename T, int DP>
 __device__ __forceinline__ Piece<T> row_piece(const Tile<T, DP> &tile, int row0, int s) {
@@ -549,7 +559,6 @@ __global__ __launch_bounds__(kThreads, WK == 1 && sizeof(T) == 2 ? 2 : 1) void k
     q.load(static_cast<const T *>(a.q) + me.pos * a.ld_q + me.head * a.d, r < rows, a.d);
     g.load(static_cast<const T *>(a.dout) + me.pos * a.ld_dout + me.head * a.d, r < rows, a.d);
     const float2 st = a.stat[stat_at(a, me.pos, me.head)];
-    const bool live = st.x != INFINITY;      // a row without weights has zeros, whatever is not finite
     const T *kp = static_cast<const T *>(a.k) + s.k0 * a.ld_k + hk * a.d;
     const T *vp = static_cast<const T *>(a.v) + s.k0 * a.ld_v + hk * a.d;
     f32x16 dq[DB];
@@ -563,7 +572,6 @@ __global__ __launch_bounds__(kThreads, WK == 1 && sizeof(T) == 2 ? 2 : 1) void k
         sv.load(vp + at * a.ld_v, ke - at, a.d, v_row);
     };
     const auto put = [&](Piece<T> *pair, int64_t at) {
-        // states past the end: k and v are zeros there, and add nothing to dq
         sk.put(Tl{pair}, ke - at, a.d);
         sv.put(Tl{pair + kPair / 2}, ke - at, a.d);
         __syncthreads();
@@ -586,12 +594,17 @@ __global__ __launch_bounds__(kThreads, WK == 1 && sizeof(T) == 2 ? 2 : 1) void k
                 mma(dp, v, g.v[i - KK]);
 #pragma unroll
                 for (int j = (i - KK) * 16 / KK; j < (i - KK + 1) * 16 / KK; ++j)      // the weights, meanwhile
-                    x[j] = __builtin_amdgcn_exp2f(live ? x[j] * a.scale2 - st.x : -INFINITY);
+                    x[j] = __builtin_amdgcn_exp2f(x[j] * a.scale2 - st.x);      // (lse = +inf: 0)
             }
         });
         prime<Tu::kRing, Tu::kSteps>(turned, column);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] *= live ? dp[i] - st.y : 0.f;
+        for (int i = 0; i < 16; ++i) x[i] *= dp[i] - st.y;
+        if (k1 > ke) {        // the last turn: states past the end
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (k0 + wk * KW + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= ke) x[i] = 0.f;
+        }
         Tu tu;
         stream<Tu::kRing, Tu::kSteps>(turned, column,
                                       [&](int i, const typename Tu::V &v) { tu.use(dq, v, i, x); });
@@ -649,15 +662,21 @@ __global__ __launch_bounds__(kThreads, WK == 1 && sizeof(T) == 2 ? 2 : 1) void k
         }
 }
 
-// dk and dv of 128 states, 32 a wavefront; splits > 1 shares the query rows among workgroups.
-template <typename T, int DP>
-__global__ __launch_bounds__(kThreads, 1) void k_attend_dkv(AttendArgs a) {
+// dk and dv of 128 states, 32 a wavefront; splits > 1 shares the query rows among workgroups.  For bf16
+// (SIDES = 2) four wavefronts take dv and four more dk of the same states: S is computed twice, 40
+// products in place of 32, but each side's operands and sums leave room for two wavefronts per SIMD,
+// whose waits overlap (one side's 258 us for both became SIDES2_US at 4 x 1024 queries of 16 heads
+// over up to 2600 states).  For fp32, whose operands take twice the registers and whose products
+// take sixteen times as long, one wavefront does both.
+template <typename T, int DP, int SIDES>
+__global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArgs a) {
     constexpr int BR = 32, DB = DP / 32;
     typedef Tile<T, DP> Tl;
     typedef Turned<T, DP> Tu;
     constexpr int kPair = 2 * Tl::pieces(BR);
     __shared__ Piece<T> smem[2 * kPair];
-    __shared__ f32x4 sstat[2][BR / 2];      // {lse, D} of two rows
+    __shared__ float sstat[2][2][BR];       // lse, then D
+    __shared__ Piece<T> own[SIDES == 2 ? Tl::pieces(128) : 1];     // the states' v rows (dk's side)
     const Seq s = sequence(a, blockIdx.z);
     const int hk = static_cast<int>(blockIdx.y) / a.splits, split = static_cast<int>(blockIdx.y) % a.splits;
     const int64_t c0 = static_cast<int64_t>(blockIdx.x) * 128;
@@ -666,21 +685,37 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_dkv(AttendArgs a) {
     int64_t rb, re;
     part_range(rows, a.per, split, BR, rb, re);
     if (c0 >= s.nk) re = rb;                         // nothing counts
-    const int lane = lane_id(), w = threadIdx.x >> 6;
-    const int64_t key = c0 + w * 32 + (lane & 31);
+    const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool do_v = SIDES == 1 || w < 4, do_k = SIDES == 1 || w >= 4;
+    const int64_t key = c0 + (w & 3) * 32 + (lane & 31);
     const bool counts = key < s.nk;
     const int64_t kr = s.k0 + (key < s.span ? key : 0);
     RowPieces<T, DP> k, v;
     k.load(static_cast<const T *>(a.k) + kr * a.ld_k + hk * a.d, counts, a.d);
     v.load(static_cast<const T *>(a.v) + kr * a.ld_v + hk * a.d, counts, a.d);
-    f32x16 dk[DB], dv[DB];
+    const Tl tv{own};
+    if (SIDES == 2 && do_k) {
+        // read again in every turn (its registers are the sums'), by the wavefront that wrote them
 #pragma unroll
-    for (int i = 0; i < DB; ++i) dk[i] = dv[i] = f32x16(0.f);
+        for (int i = 0; i < RowPieces<T, DP>::KK; ++i)
+            *tv.at((w & 3) * 32 + (lane & 31), 2 * i + (lane >> 5)) = v.v[i];
+        wave_lds_sync();
+    }
+    // the sums: dv and dk, or this side's
+    f32x16 sums[2 / SIDES][DB];
+#pragma unroll
+    for (int i = 0; i < DB; ++i) {
+        sums[0][i] = f32x16(0.f);
+        sums[2 / SIDES - 1][i] = f32x16(0.f);
+    }
+    auto &dv = sums[0], &dk = sums[2 / SIDES - 1];
     // the statistics of this state head's rows lie next to each other
     const float2 *stat = a.stat + (static_cast<int64_t>(hk) * a.n_q + s.q0) * a.group;
+    // dv's side, which has less to do, brings the tiles
     Stage<T, DP, BR> sq, sg;
     float2 st;
     const auto load = [&](int64_t r0) {
+        if (!do_v) return;
         // the tile's first query row, and the rows' distances from its first head of the group
         const uint32_t p0 = fast_div(static_cast<uint32_t>(r0), a.by_group);
         const auto row = [&](int i, int64_t ld) {
@@ -695,11 +730,16 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_dkv(AttendArgs a) {
         st = stat[r < re ? r : re - 1];
     };
     const auto put = [&](int pair, int64_t r0) {
-        sq.put(Tl{smem + pair * kPair}, re - r0, a.d);
-        sg.put(Tl{smem + pair * kPair + kPair / 2}, re - r0, a.d);
-        if (threadIdx.x < BR)      // rows past the end are marked as without weights
-            reinterpret_cast<float2 *>(sstat[pair])[threadIdx.x] =
-                r0 + threadIdx.x < re ? st : float2{INFINITY, 0.f};
+        if (do_v) {
+            // rows past the end are row 0 again, without weights (zeros would make NaN of states that
+            // are not finite)
+            sq.put(Tl{smem + pair * kPair}, BR, a.d);
+            sg.put(Tl{smem + pair * kPair + kPair / 2}, BR, a.d);
+            if (threadIdx.x < BR) {
+                sstat[pair][0][threadIdx.x] = r0 + threadIdx.x < re ? st.x : INFINITY;
+                sstat[pair][1][threadIdx.x] = st.y;
+            }
+        }
         __syncthreads();
     };
     const auto turn = [&](int pair, int64_t r0) {
@@ -710,40 +750,72 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_dkv(AttendArgs a) {
         f32x16 p(0.f), ds(0.f);
         Piece<T> ring[kR];
         const auto piece = [&](int i) { return row_piece<T, DP>(i < KK ? tq : tg, 0, i % KK); };
-        prime<kR, 2 * KK>(ring, piece);
-        f32x4 x[8];      // rows 8 g + 4 half + 0..3
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = sstat[pair][4 * (i >> 1) + 2 * (lane >> 5) + (i & 1)];
-        typename Tu::V turned[Tu::kRing];
-        const auto column = [&](int i) {
-            return Tu::load(i < Tu::kSteps ? tg : tq, 0, i % Tu::kSteps);
+        // a step's row piece, and in dP's steps the piece of v
+        struct Both {
+            Piece<T> u, v;
         };
-        stream<kR, 2 * KK>(ring, piece, [&](int i, const Piece<T> &u) {
-            if (i < KK) {
-                mma(p, u, k.v[i]);
-            } else {
-                mma(ds, u, v.v[i - KK]);
-                // the weights, meanwhile; a row without weights has zeros, also against states that are
-                // not finite
+        const auto both = [&](int i) {
+            Both x;
+            x.u = piece(i);
+            if (SIDES == 2 && i >= KK) x.v = row_piece<T, DP>(tv, (w & 3) * 32, i - KK);
+            return x;
+        };
+        f32x4 lse[4], dd[4];      // rows 8 g + 4 half + 0..3
+        const auto read_stat = [&](int which, f32x4 (&x)[4]) {
 #pragma unroll
-                for (int j = (i - KK) * 16 / KK; j < (i - KK + 1) * 16 / KK; ++j) {
-                    const float l = x[j >> 1][2 * (j & 1)];
-                    p[j] = __builtin_amdgcn_exp2f(l != INFINITY ? p[j] * a.scale2 - l : -INFINITY);
-                }
-            }
-        });
-        prime<Tu::kRing, 2 * Tu::kSteps>(turned, column);
+            for (int g = 0; g < 4; ++g)
+                x[g] = *reinterpret_cast<const f32x4 *>(&sstat[pair][which][8 * g + 4 * (lane >> 5)]);
+        };
+        // lse = +inf, a row without weights: p = 0
+        const auto weigh = [&](int j) {
+            p[j] = __builtin_amdgcn_exp2f(p[j] * a.scale2 - lse[j >> 2][j & 3]);
+        };
+        const auto differ = [&](int j) { ds[j] = p[j] * (ds[j] - dd[j >> 2][j & 3]); };
+        typename Tu::V turned[Tu::kRing];
         Tu tu;
-        stream<Tu::kRing, 2 * Tu::kSteps>(turned, column, [&](int i, const typename Tu::V &u) {
-            if (i < Tu::kSteps) {
-                tu.use(dv, u, i, p);
+        if (SIDES == 2 && do_v) {
+            prime<kR, KK>(ring, piece);
+            read_stat(0, lse);
+            stream<kR, KK>(ring, piece, [&](int i, const Piece<T> &u) { mma(p, u, k.v[i]); });
+            const auto column = [&](int i) { return Tu::load(tg, 0, i); };
+            prime<Tu::kRing, Tu::kSteps>(turned, column);
 #pragma unroll
-                for (int j = i * 16 / Tu::kSteps; j < (i + 1) * 16 / Tu::kSteps; ++j)
-                    ds[j] = p[j] * (x[j >> 1][2 * (j & 1)] != INFINITY ? ds[j] - x[j >> 1][2 * (j & 1) + 1] : 0.f);
-            } else {
-                tu.use(dk, u, i - Tu::kSteps, ds);
+            for (int j = 0; j < 16; ++j) weigh(j);
+            stream<Tu::kRing, Tu::kSteps>(turned, column,
+                                          [&](int i, const typename Tu::V &u) { tu.use(dv, u, i, p); });
+        } else {
+            Both pairs[kR];
+            prime<kR, 2 * KK>(pairs, both);
+            read_stat(0, lse);
+            stream<kR, 2 * KK>(pairs, both, [&](int i, const Both &x) {
+                if (i < KK) {
+                    mma(p, x.u, k.v[i]);
+                } else {
+                    mma(ds, x.u, SIDES == 2 ? x.v : v.v[i - KK]);
+#pragma unroll
+                    for (int j = (i - KK) * 16 / KK; j < (i - KK + 1) * 16 / KK; ++j) weigh(j);   // meanwhile
+                }
+            });
+            constexpr int kSteps = (3 - SIDES) * Tu::kSteps, kFirst = kSteps - Tu::kSteps;
+            const auto column = [&](int i) {
+                return Tu::load(i < kFirst ? tg : tq, 0, i % Tu::kSteps);
+            };
+            read_stat(1, dd);
+            prime<Tu::kRing, kSteps>(turned, column);
+            if (SIDES == 2) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) differ(j);
             }
-        });
+            stream<Tu::kRing, kSteps>(turned, column, [&](int i, const typename Tu::V &u) {
+                if (i < kFirst) {
+                    tu.use(dv, u, i, p);
+#pragma unroll
+                    for (int j = i * 16 / Tu::kSteps; j < (i + 1) * 16 / Tu::kSteps; ++j) differ(j);
+                } else {
+                    tu.use(dk, u, i - kFirst, ds);
+                }
+            });
+        }
         if (r1 < re) put(pair ^ 1, r1);
     };
     if (rb < re) {
@@ -758,25 +830,22 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_dkv(AttendArgs a) {
     // a state past the count has no gradient
     const int64_t line = kr * a.kv + hk, all = a.n_k * a.kv;
     float *part = a.part + (static_cast<int64_t>(split) * all + line) * 2 * a.d;
-    T *ok = static_cast<T *>(a.dk) + kr * a.ld_dk + hk * a.d;
-    T *ov = static_cast<T *>(a.dv) + kr * a.ld_dv + hk * a.d;
+    const auto write = [&](const f32x16 (&sum)[DB], float factor, T *to, float *part_to) {
 #pragma unroll
-    for (int i = 0; i < DB; ++i)
+        for (int i = 0; i < DB; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f32x4 x{dk[i][4 * j], dk[i][4 * j + 1], dk[i][4 * j + 2], dk[i][4 * j + 3]};
-            f32x4 y{dv[i][4 * j], dv[i][4 * j + 1], dv[i][4 * j + 2], dv[i][4 * j + 3]};
-            x = counts ? x * a.scale : f32x4(0.f);
-            y = counts ? y : f32x4(0.f);
-            const int d0 = 32 * i + 8 * j + 4 * (lane >> 5);
-            if (a.splits > 1) {
-                put4<float>(part, d0, a.d, x);
-                put4<float>(part + a.d, d0, a.d, y);
-            } else {
-                put4<T>(ok, d0, a.d, x);
-                put4<T>(ov, d0, a.d, y);
+            for (int j = 0; j < 4; ++j) {
+                f32x4 x{sum[i][4 * j], sum[i][4 * j + 1], sum[i][4 * j + 2], sum[i][4 * j + 3]};
+                x = counts ? x * factor : f32x4(0.f);
+                const int d0 = 32 * i + 8 * j + 4 * (lane >> 5);
+                if (a.splits > 1)
+                    put4<float>(part_to, d0, a.d, x);
+                else
+                    put4<T>(to, d0, a.d, x);
             }
-        }
+    };
+    if (do_k) write(dk, a.scale, static_cast<T *>(a.dk) + kr * a.ld_dk + hk * a.d, part);
+    if (do_v) write(dv, 1.f, static_cast<T *>(a.dv) + kr * a.ld_dv + hk * a.d, part + a.d);
 }
 
 // Adds the splits of dq (states = 0) or of dk and dv (states = 1), a wavefront a row.
@@ -813,7 +882,8 @@ __global__ __launch_bounds__(kThreads) void k_attend_reduce(AttendArgs a, int st
 
 // ---- host -------------------------------------------------------------------------------------------
 
-constexpr int64_t kWantGroups = 1024;     // workgroups that fill the card
+constexpr int64_t kWantGroups = 256;      // a workgroup per compute unit: more, for which states have to be
+                                          // split further, cost more in partial sums than they even out
 constexpr int64_t kFewTiles = 256;        // fewer tiles of 128 rows than compute units: tiles of 32
 constexpr int64_t kMaxSplits = 64;        // one lane each in the combining kernel
 
@@ -911,7 +981,8 @@ hipError_t backward(AttendArgs a, const Plan &p, hipStream_t s) {
         a.splits = p.dkv_splits;
         a.per = p.dkv_per;
         const dim3 grid(static_cast<unsigned>(p.k_tiles), static_cast<unsigned>(a.kv * a.splits), z);
-        hipLaunchKernelGGL((k_attend_dkv<T, DP>), grid, dim3(kThreads), 0, s, a);
+        constexpr int kSides = sizeof(T) == 2 ? 2 : 1;
+        hipLaunchKernelGGL((k_attend_dkv<T, DP, kSides>), grid, dim3(kThreads * kSides), 0, s, a);
         if (a.splits > 1)
             hipLaunchKernelGGL((k_attend_reduce<T>),
                                dim3(static_cast<unsigned>(ceil_div(a.max_k * a.kv, 4)), z),

@@ -213,6 +213,27 @@ def test_minus_infinity_scores():
     assert torch.all(got["dv"] == 0)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("nq", [3, 200])
+def test_all_scores_far_below_zero(nq, dtype):
+    """lse near -600: what lies past a sequence's end has a score of zero, far above it."""
+    c = Call([nq, nq], [45, 7], 2, 1, 32, dtype, scale=1.0, seed=31)
+    c.q[:, :, 0], c.k[:, :, 0] = 25.0, -25.0
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_infinite_states_stay_in_their_rows_and_gradients(dtype):
+    """A state of -inf scores (its weight is zero), with a row count that ends inside a tile."""
+    c = Call([5], [70], 1, 1, 16, dtype, scale=1.0, seed=33)
+    c.q[:, 0, 0] = 1.0
+    c.k[9, 0, 0] = -math.inf
+    got = c.run()
+    assert torch.isfinite(got["out"]).all() and torch.isfinite(got["dv"]).all()
+    assert torch.all(got["dv"][9] == 0)
+    assert torch.isfinite(got["dk"]).all() and torch.all(got["dk"][9] == 0)
+
+
 def test_same_bits_every_time_and_other_bounds():
     c = Call([1, 60], [3000, 1200], 8, 2, 64, BF16, seed=17)
     a, b = c.run(), c.run()
