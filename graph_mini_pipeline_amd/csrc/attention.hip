@@ -848,35 +848,56 @@ __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArg
     if (do_v) write(dv, 1.f, static_cast<T *>(a.dv) + kr * a.ld_dv + hk * a.d, part + a.d);
 }
 
-// Adds the splits of dq (states = 0) or of dk and dv (states = 1), a wavefront a row.
+// What the reducing kernel takes: the splits of the states' sums, whose partial sums lie at part_kv, and
+// those of dq (0: none to add).
+struct ReduceArgs {
+    int64_t dq_per, dkv_per;
+    const float *part_kv;
+    int32_t dq, dkv;
+};
+
+// Adds the splits of dq and (the grid's second layer, or the only one) of dk and dv.  A sequence's
+// partial sums of one split are one stretch of memory: kReduceFours pieces of four a thread.
+constexpr int kReduceFours = 4;
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_attend_reduce(AttendArgs a, int states) {
+__global__ __launch_bounds__(kThreads) void k_attend_reduce(AttendArgs a, ReduceArgs z) {
+    const bool states = z.dkv && (!z.dq || blockIdx.z == 1);
     const Seq s = sequence(a, blockIdx.y);
-    const int64_t per = states ? a.kv : a.heads;
-    const int64_t line0 = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (line0 >= (states ? s.span : s.nq) * per) return;
     const int64_t first = states ? s.k0 : s.q0;
-    const int64_t line = first * per + line0;
-    const int64_t all = (states ? a.n_k : a.n_q) * per;
-    const int64_t pos = first + line0 / per, head = line0 % per;
-    const int wide = states ? 2 * a.d : a.d;
-    const int parts = static_cast<int>(parts_of(states ? s.nq * a.group : s.nk, a.per));
-    for (int c = 2 * lane_id(); c < wide; c += 128) {
-        float x = 0.f, y = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < parts; ++i) {
-            const float2 v = *reinterpret_cast<const float2 *>(a.part + (i * all + line) * wide + c);
-            x += v.x;
-            y += v.y;
+    const uint32_t per = states ? a.kv : a.heads;               // lines of a row
+    const uint32_t fours = (states ? 2 * a.d : a.d) / 4;        // pieces of a line
+    const int64_t count = (states ? s.span : s.nq) * per * fours;
+    const int64_t f0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kReduceFours) + threadIdx.x;
+    if (static_cast<int64_t>(blockIdx.x) * (kThreads * kReduceFours) >= count) return;
+    const int64_t all = (states ? a.n_k : a.n_q) * per * fours;
+    const f32x4 *part = reinterpret_cast<const f32x4 *>(states ? z.part_kv : a.part) + first * per * fours;
+    const int parts = states ? static_cast<int>(parts_of(s.nq * a.group, z.dkv_per))
+                             : static_cast<int>(parts_of(s.nk, z.dq_per));
+    f32x4 sum[kReduceFours];
+#pragma unroll
+    for (int u = 0; u < kReduceFours; ++u) sum[u] = f32x4(0.f);
+#pragma unroll 2
+    for (int i = 0; i < parts; ++i)
+#pragma unroll
+        for (int u = 0; u < kReduceFours; ++u) {
+            const int64_t f = f0 + u * kThreads;
+            sum[u] += part[i * all + (f < count ? f : 0)];
         }
+#pragma unroll
+    for (int u = 0; u < kReduceFours; ++u) {
+        const int64_t f = f0 + u * kThreads;
+        if (f >= count) continue;
+        const int64_t line = f / fours;
+        const int c = static_cast<int>(f - line * fours) * 4;
+        const int64_t pos = line / per, head = line - pos * per, row = first + pos;
         T *to;
         if (!states)
-            to = static_cast<T *>(a.dq) + pos * a.ld_dq + head * a.d + c;
+            to = static_cast<T *>(a.dq) + row * a.ld_dq + head * a.d + c;
         else if (c < a.d)
-            to = static_cast<T *>(a.dk) + pos * a.ld_dk + head * a.d + c;
+            to = static_cast<T *>(a.dk) + row * a.ld_dk + head * a.d + c;
         else
-            to = static_cast<T *>(a.dv) + pos * a.ld_dv + head * a.d + c - a.d;
-        store_f32<T, 2>(to, vec<float, 2>{x, y});
+            to = static_cast<T *>(a.dv) + row * a.ld_dv + head * a.d + c - a.d;
+        store_f32<T, 4>(to, sum[u]);
     }
 }
 
@@ -893,13 +914,13 @@ struct Plan {
     int64_t q_tiles, k_tiles;
     int splits, dkv_splits;   // of the states (forward, dq) and of the rows (dk, dv)
     int64_t per, dkv_per;     // their lengths
-    size_t stat, part_stat, part, bytes;      // byte offsets
+    size_t stat, part_stat, part, part_kv, bytes;      // byte offsets
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Splits `length` among workgroups until `groups` of them fill the card, in parts of whole multiples of
-// `least`.
+// Splits `length` among workgroups until `groups` of them times the splits fill the card, in parts of
+// whole multiples of `least`.
 void pick_splits(int64_t groups, int64_t length, int64_t least, int &splits, int64_t &per) {
     int64_t s = groups < 1 ? 1 : ceil_div(kWantGroups, groups);
     if (s > kMaxSplits) s = kMaxSplits;
@@ -928,13 +949,11 @@ Plan plan_for(const AttendArgs &a, bool backward) {
     };
     const size_t lines = static_cast<size_t>(a.n_q) * a.heads;
     if (backward) p.stat = take(lines * 8);
-    size_t part = p.splits > 1 ? lines * a.d * 4 * p.splits : 0;
+    const size_t part = p.splits > 1 ? lines * a.d * 4 * p.splits : 0;
     if (p.splits > 1) p.part_stat = take(lines * 8 * p.splits);
-    if (backward && p.dkv_splits > 1) {
-        const size_t kv = static_cast<size_t>(a.n_k) * a.kv * 2 * a.d * 4 * p.dkv_splits;
-        part = kv > part ? kv : part;
-    }
     p.part = take(part);
+    if (backward && p.dkv_splits > 1)
+        p.part_kv = take(static_cast<size_t>(a.n_k) * a.kv * 2 * a.d * 4 * p.dkv_splits);
     p.bytes = off < 256 ? 256 : off;
     return p;
 }
@@ -972,21 +991,25 @@ hipError_t backward(AttendArgs a, const Plan &p, hipStream_t s) {
             hipLaunchKernelGGL((k_attend_dq<T, DP, 4 / sharing<T, DP>(), sharing<T, DP>()>), grid, dim3(kThreads), 0, s, a);
         else
             hipLaunchKernelGGL((k_attend_dq<T, DP, 4, 1>), grid, dim3(kThreads), 0, s, a);
-        if (a.splits > 1)
-            hipLaunchKernelGGL((k_attend_reduce<T>),
-                               dim3(static_cast<unsigned>(ceil_div(a.max_q * a.heads, 4)), z),
-                               dim3(kThreads), 0, s, a, 0);
     }
+    float *const part_kv = reinterpret_cast<float *>(a.ws + p.part_kv);
     if (a.max_k > 0) {
-        a.splits = p.dkv_splits;
-        a.per = p.dkv_per;
-        const dim3 grid(static_cast<unsigned>(p.k_tiles), static_cast<unsigned>(a.kv * a.splits), z);
+        AttendArgs b = a;
+        b.splits = p.dkv_splits;
+        b.per = p.dkv_per;
+        b.part = part_kv;
+        const dim3 grid(static_cast<unsigned>(p.k_tiles), static_cast<unsigned>(a.kv * b.splits), z);
         constexpr int kSides = sizeof(T) == 2 ? 2 : 1;
-        hipLaunchKernelGGL((k_attend_dkv<T, DP, kSides>), grid, dim3(kThreads * kSides), 0, s, a);
-        if (a.splits > 1)
-            hipLaunchKernelGGL((k_attend_reduce<T>),
-                               dim3(static_cast<unsigned>(ceil_div(a.max_k * a.kv, 4)), z),
-                               dim3(kThreads), 0, s, a, 1);
+        hipLaunchKernelGGL((k_attend_dkv<T, DP, kSides>), grid, dim3(kThreads * kSides), 0, s, b);
+    }
+    ReduceArgs r{p.per, p.dkv_per, part_kv, a.max_q > 0 && p.splits > 1, a.max_k > 0 && p.dkv_splits > 1};
+    if (r.dq || r.dkv) {
+        const int64_t fq = r.dq ? a.max_q * a.heads * (a.d / 4) : 0;
+        const int64_t fk = r.dkv ? a.max_k * a.kv * (a.d / 2) : 0;
+        hipLaunchKernelGGL((k_attend_reduce<T>),
+                           dim3(static_cast<unsigned>(ceil_div(fq > fk ? fq : fk, kThreads * kReduceFours)), z,
+                                static_cast<unsigned>(r.dq + r.dkv)),
+                           dim3(kThreads), 0, s, a, r);
     }
     return hipGetLastError();
 }
@@ -1008,6 +1031,7 @@ hipError_t launch_attend(AttendArgs a, bool backward, char *ws, hipStream_t s) {
     const Plan p = plan_for(a, backward);
     a.by_group = make_fastdiv(static_cast<uint32_t>(a.group));
     a.scale2 = a.scale * kLog2E;
+    a.ws = ws;
     a.stat = reinterpret_cast<float2 *>(ws + p.stat);
     a.part_stat = reinterpret_cast<float2 *>(ws + p.part_stat);
     a.part = reinterpret_cast<float *>(ws + p.part);

@@ -95,6 +95,7 @@ struct AttendArgs {
     FastDiv by_group;
     int32_t splits;
     int64_t per;           // states (or rows) per split
+    char *ws;
     float2 *stat;          // [n_q * heads] {lse log2(e), dout . out}
     float *part;           // partial sums of the splits
     float2 *part_stat;     // [splits, n_q * heads] {maximum, sum}
