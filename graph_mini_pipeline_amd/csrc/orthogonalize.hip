@@ -16,7 +16,8 @@
 //
 // Layout.  The matrix instructions want both operands with the summed index contiguous: X for A, the
 // symmetric A for A^2, and, since (Q X)^T = X^T Q, X^T and Q for the last product, which therefore
-// stores X and X^T.  The planes are padded with zeros to whole tiles, and zeros stay zeros.
+// stores X and X^T.  The planes are padded with zeros to multiples of 64, and zeros stay zeros; a tile
+// that reaches beyond them repeats their last row and stores nothing there.
 #include <math.h>
 
 #include "learn.hpp"
@@ -47,6 +48,7 @@ struct ProductArgs {
     f16 *c, *t;                  // the product, and its transpose (symmetric: the mirrored tiles)
     int64_t ld_c, ld_t, plane_c, plane_t, batch_c, batch_t;
     int64_t k;                   // summed length, a multiple of 64
+    int32_t rows_a, rows_b;      // padded rows of the operands: multiples of 64
     int32_t m_tiles, n_tiles;
     int32_t what;
     float ca, cb, cc;            // kPoly
@@ -70,174 +72,220 @@ struct PolyOf<2> {
     typedef double type;
 };
 
-template <int BM, int BN, int WM, int WN, int PL, typename TO>
-__global__ __launch_bounds__(WM *WN * 64) void k_newton_product(ProductArgs p) {
-    constexpr int T = WM * WN * 64;
+constexpr int kThreads = 256;      // four wavefronts, two by two quarters of a tile
+// Tiles on their way (even: LDS has two halves): as many as leave two workgroups per compute unit at
+// TILE = 128 their registers.
+template <int TILE>
+constexpr int depth() {
+    return TILE == 128 ? 2 : 4;
+}
+
+// One TILE x TILE tile of the product.  A wavefront's quarter is TM x TM matrix instructions of 32 x 32 a
+// summed sixteen; an operand piece that it reads from LDS is used TM times, so LDS keeps up from TM = 3
+// on (at TM = 2 it delivers just what the matrix units take).  The operands of the next sixteen are
+// read while those of the last multiply.  A tile of the planes takes longer to arrive than a turn's
+// products (some 2000 cycles against 512 at TILE = 128), so kDepth tiles are on their way at once, in
+// register sets of their own; the next one is put into the other half of LDS before a turn's last
+// products.
+template <int TILE, int PL, typename TO>
+__global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void k_newton_product(ProductArgs p) {
     constexpr int BK = PL == 1 ? 64 : 32;
     constexpr int CPR = BK / 8;                     // 16-byte pieces per row
+    constexpr int KK = BK / 16;
+    constexpr int TM = TILE / 64;
+    constexpr int kDepth = depth<TILE>();
+    constexpr int L = TILE * CPR / kThreads;        // pieces per thread, operand and plane
     // Small matrices are not bound by the products, and their sums are too short for the dropped one
     // to average out (1.2e-6 of a 5 x 1 update's norm without it, 1e-7 with it).
-    constexpr bool kAllFour = BM == 64;
+    constexpr bool kAllFour = TILE == 64;
     typedef typename PolyOf<PL>::type Poly;
-    constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
-    constexpr int LA = BM * CPR / T, LB = BN * CPR / T;   // pieces per thread and plane
-    __shared__ h8 lds[2][PL * (BM + BN) * CPR];
+    constexpr int kPlane = 2 * TILE * CPR;          // an A and a B tile
+    __shared__ h8 lds[2][PL * kPlane];
     const bool symmetric = p.what == kGram || p.what == kPoly;
+    // Workgroups b, b + 8, ... run on one XCD: each XCD takes a stretch of tiles next to each other, whose
+    // rows its L2 then holds.
+    constexpr unsigned kXcds = 8;
+    const unsigned whole = gridDim.x / kXcds * kXcds;
+    const int q0 = static_cast<int>(blockIdx.x < whole
+                                        ? blockIdx.x % kXcds * (whole / kXcds) + blockIdx.x / kXcds
+                                        : blockIdx.x);
     int tm, tn;
     if (symmetric) {
-        const int q = static_cast<int>(blockIdx.x);
-        tm = static_cast<int>((sqrtf(8.f * q + 1.f) - 1.f) * 0.5f);
-        while ((tm + 1) * (tm + 2) / 2 <= q) ++tm;
-        while (tm * (tm + 1) / 2 > q) --tm;
-        tn = q - tm * (tm + 1) / 2;
+        tm = static_cast<int>((sqrtf(8.f * q0 + 1.f) - 1.f) * 0.5f);
+        while ((tm + 1) * (tm + 2) / 2 <= q0) ++tm;
+        while (tm * (tm + 1) / 2 > q0) --tm;
+        tn = q0 - tm * (tm + 1) / 2;
     } else {
-        tm = static_cast<int>(blockIdx.x) / p.n_tiles;
-        tn = static_cast<int>(blockIdx.x) - tm * p.n_tiles;
+        // columns of four tiles, so that a stretch is about as wide as high
+        const int per = 4 * p.n_tiles, g = q0 / per, in = q0 - g * per;
+        const int high = p.m_tiles - 4 * g < 4 ? p.m_tiles - 4 * g : 4;
+        tn = in / high;
+        tm = 4 * g + in - tn * high;
     }
     const int64_t z = blockIdx.y;
     const int t = threadIdx.x, lane = lane_id(), w = t >> 6;
-    const int wm = w / WN, wn = w % WN;
-    const f16 *ga = p.a + z * p.batch_a + static_cast<int64_t>(tm) * BM * p.ld_a;
-    const f16 *gb = p.b + z * p.batch_b + static_cast<int64_t>(tn) * BN * p.ld_b;
-
-    h8 ra[PL][LA], rb[PL][LB];
-    auto load = [&](int64_t k0) {
+    const int wm = w >> 1, wn = w & 1;
+    const f16 *ga = p.a + z * p.batch_a;
+    const f16 *gb = p.b + z * p.batch_b;
+    // this thread's pieces: row and distance from the planes' start
+    uint32_t oa[L], ob[L];
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        const int e = i * kThreads + t, r = e / CPR, c = e % CPR;
+        const int ra = tm * TILE + r, rb = tn * TILE + r;
+        oa[i] = static_cast<uint32_t>(ra < p.rows_a ? ra : p.rows_a - 1) * static_cast<uint32_t>(p.ld_a) + c * 8;
+        ob[i] = static_cast<uint32_t>(rb < p.rows_b ? rb : p.rows_b - 1) * static_cast<uint32_t>(p.ld_b) + c * 8;
+    }
+    h8 ra[kDepth][PL][L], rb[kDepth][PL][L];
+    const int steps = static_cast<int>(p.k / BK);
+    // (past the end the last tile again: no branch, so that the waits count the loads exactly)
+    auto load = [&](int set, int s) {
+        const int64_t k0 = static_cast<int64_t>(s < steps ? s : steps - 1) * BK;
+#pragma unroll
+        for (int q = 0; q < PL; ++q)
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                ra[set][q][i] = *reinterpret_cast<const h8 *>(ga + q * p.plane_a + k0 + oa[i]);
+                rb[set][q][i] = *reinterpret_cast<const h8 *>(gb + q * p.plane_b + k0 + ob[i]);
+            }
+    };
+    auto store = [&](int set, int buf) {
 #pragma unroll
         for (int q = 0; q < PL; ++q) {
+            h8 *at = &lds[buf][q * kPlane];
 #pragma unroll
-            for (int i = 0; i < LA; ++i) {
-                const int e = i * T + t, r = e / CPR, c = e % CPR;
-                ra[q][i] = *reinterpret_cast<const h8 *>(ga + q * p.plane_a + r * p.ld_a + k0 + c * 8);
-            }
-#pragma unroll
-            for (int i = 0; i < LB; ++i) {
-                const int e = i * T + t, r = e / CPR, c = e % CPR;
-                rb[q][i] = *reinterpret_cast<const h8 *>(gb + q * p.plane_b + r * p.ld_b + k0 + c * 8);
+            for (int i = 0; i < L; ++i) {
+                const int e = i * kThreads + t, to = piece<CPR>(e / CPR, e % CPR);
+                at[to] = ra[set][q][i];
+                at[TILE * CPR + to] = rb[set][q][i];
             }
         }
     };
-    auto store = [&](int buf) {
-#pragma unroll
-        for (int q = 0; q < PL; ++q) {
-            h8 *at = &lds[buf][q * (BM + BN) * CPR];
-#pragma unroll
-            for (int i = 0; i < LA; ++i) {
-                const int e = i * T + t;
-                at[piece<CPR>(e / CPR, e % CPR)] = ra[q][i];
-            }
-#pragma unroll
-            for (int i = 0; i < LB; ++i) {
-                const int e = i * T + t;
-                at[BM * CPR + piece<CPR>(e / CPR, e % CPR)] = rb[q][i];
-            }
-        }
-    };
-    f16x acc[TM][TN];
+    f16x acc[TM][TM];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = f16x(0.f);
+        for (int j = 0; j < TM; ++j) acc[i][j] = f16x(0.f);
 
     const int row = lane & 31, half = lane >> 5;
-    const int steps = static_cast<int>(p.k / BK);
-    load(0);
-    store(0);
-    __syncthreads();
-    for (int s = 0; s < steps; ++s) {
-        if (s + 1 < steps) load(static_cast<int64_t>(s + 1) * BK);
-        const h8 *at = lds[s & 1];
+    h8 a[2][PL][TM], b[2][PL][TM];
+    auto read = [&](int buf, int kk) {
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk) {
-            h8 a[PL][TM], b[PL][TN];
+        for (int q = 0; q < PL; ++q) {
+            const h8 *pl = &lds[buf][q * kPlane];
 #pragma unroll
-            for (int q = 0; q < PL; ++q) {
-                const h8 *pl = at + q * (BM + BN) * CPR;
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-                    a[q][i] = pl[piece<CPR>((wm * TM + i) * 32 + row, kk * 2 + half)];
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    b[q][j] = pl[BM * CPR + piece<CPR>((wn * TN + j) * 32 + row, kk * 2 + half)];
+            for (int i = 0; i < TM; ++i) {
+                a[kk & 1][q][i] = pl[piece<CPR>((wm * TM + i) * 32 + row, kk * 2 + half)];
+                b[kk & 1][q][i] = pl[TILE * CPR + piece<CPR>((wn * TM + i) * 32 + row, kk * 2 + half)];
             }
+        }
+    };
+    // tile s, from LDS half s % 2; u = s % kDepth, whose register set is free
+    auto turn = [&](int u, int s) {
+        const int buf = u & 1;
+        load(u, s + kDepth);
+        read(buf, 0);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+            if (kk + 1 < KK) read(buf, kk + 1);
+            if (kk + 1 == KK) store((u + 1) % kDepth, buf ^ 1);
+            __builtin_amdgcn_sched_barrier(0);
+            const auto &x = a[kk & 1];
+            const auto &y = b[kk & 1];
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) {
+                for (int j = 0; j < TM; ++j) {
                     if (PL == 2) {
                         if (kAllFour)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[PL - 1][i], b[PL - 1][j], acc[i][j], 0, 0, 0);
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[0][i], b[PL - 1][j], acc[i][j], 0, 0, 0);
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[PL - 1][i], b[0][j], acc[i][j], 0, 0, 0);
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[PL - 1][i], y[PL - 1][j], acc[i][j], 0, 0, 0);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[0][i], y[PL - 1][j], acc[i][j], 0, 0, 0);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[PL - 1][i], y[0][j], acc[i][j], 0, 0, 0);
                     }
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[0][i], b[0][j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[0][i], y[0][j], acc[i][j], 0, 0, 0);
                 }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (s + 1 < steps) store((s + 1) & 1);
         __syncthreads();
+    };
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u) load(u, u);
+    store(0, 0);
+    __syncthreads();
+    int s = 0;
+    for (; s + kDepth <= steps; s += kDepth) {
+#pragma unroll
+        for (int u = 0; u < kDepth; ++u) turn(u, s + u);
     }
+#pragma unroll
+    for (int u = 0; u < kDepth - 1; ++u)
+        if (s + u < steps) turn(u, s + u);
 
-    // A lane holds column lane % 32 and rows 8 g + 4 (lane / 32) + 0..3 of each 32 x 32 accumulator.
-    const float first = p.first ? p.first[z] : 1.f;
-    const bool mirror = !symmetric || tm != tn;
+    // A lane holds column lane % 32 and rows 8 g + 4 (lane / 32) + 0..3 of each 32 x 32 accumulator:
+    // every(f) calls f(row, column, the four values) for what exists of the padded product.
+    const auto every = [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int64_t n = static_cast<int64_t>(tn) * BN + (wn * TN + j) * 32 + row;
+            for (int j = 0; j < TM; ++j) {
+                const int64_t n = static_cast<int64_t>(tn) * TILE + (wn * TM + j) * 32 + row;
+                const int64_t m0 = static_cast<int64_t>(tm) * TILE + (wm * TM + i) * 32 + 4 * half;
+                // a 32 x 32 accumulator exists or not as a whole
+                if (n >= p.rows_b || m0 >= p.rows_a) continue;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int64_t m = static_cast<int64_t>(tm) * BM + (wm * TM + i) * 32 + 8 * g + 4 * half;
-                vec<float, 4> v;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e];
-                if (p.what == kLast) {
-                    v *= kDown * kDown * first * p.scale;
-                    TO *out = static_cast<TO *>(p.out) + z * p.batch_out;
-                    if (n >= p.n) continue;
-                    if (p.out_rows) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (m + e < p.m) out[(m + e) * p.ld_out + n] = static_cast<TO>(v[e]);
-                    } else if (m + 4 <= p.m) {
-                        store_f32<TO, 4>(out + n * p.ld_out + m, v);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (m + e < p.m) out[n * p.ld_out + m + e] = static_cast<TO>(v[e]);
-                    }
-                    continue;
-                }
-                if (p.what == kGram) {
-                    v *= kDown * first * first;
-                } else if (p.what == kPoly) {
-                    // the product's operand is A itself; A[n][m..] = A[m..][n]
-                    const f16 *old = p.a + z * p.batch_a + n * p.ld_a + m;
-                    vec<Poly, 4> u = __builtin_convertvector(v, vec<Poly, 4>) * static_cast<Poly>(kDown * p.cc);
-#pragma unroll
-                    for (int q = 0; q < PL; ++q) {
-                        const vec<f16, 4> x = *reinterpret_cast<const vec<f16, 4> *>(old + q * p.plane_a);
-                        u += static_cast<Poly>(p.cb) * __builtin_convertvector(x, vec<Poly, 4>);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (m + e == n) u[e] += static_cast<Poly>(p.ca * kUp);
-                    v = __builtin_convertvector(u, vec<float, 4>);
-                } else {
-                    v *= kDown * first;
-                }
-#pragma unroll
-                for (int q = 0; q < PL; ++q) {
-                    const vec<f16, 4> x = __builtin_convertvector(v, vec<f16, 4>);
-                    f16 *c = p.c + z * p.batch_c + q * p.plane_c + m * p.ld_c + n;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) c[e * p.ld_c] = x[e];
-                    if (mirror)
-                        *reinterpret_cast<vec<f16, 4> *>(p.t + z * p.batch_t + q * p.plane_t +
-                                                         n * p.ld_t + m) = x;
-                    v -= __builtin_convertvector(x, vec<float, 4>);
-                }
+                for (int g = 0; g < 4; ++g)
+                    f(m0 + 8 * g, n,
+                      vec<float, 4>{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]});
             }
+    };
+    const float first = p.first ? p.first[z] : 1.f;
+    if (p.what == kLast) {
+        const float factor = kDown * kDown * first * p.scale;
+        TO *out = static_cast<TO *>(p.out) + z * p.batch_out;
+        every([&](int64_t m, int64_t n, vec<float, 4> v) {
+            v *= factor;
+            if (n >= p.n) return;
+            if (!p.out_rows && m + 4 <= p.m) {
+                store_f32<TO, 4>(out + n * p.ld_out + m, v);
+                return;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (m + e < p.m) out[p.out_rows ? (m + e) * p.ld_out + n : n * p.ld_out + m + e] = static_cast<TO>(v[e]);
+        });
+        return;
+    }
+    const bool mirror = !symmetric || tm != tn;
+    const auto keep = [&](int64_t m, int64_t n, vec<float, 4> v) {
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+            const vec<f16, 4> x = __builtin_convertvector(v, vec<f16, 4>);
+            f16 *c = p.c + z * p.batch_c + q * p.plane_c + m * p.ld_c + n;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[e * p.ld_c] = x[e];
+            if (mirror)
+                *reinterpret_cast<vec<f16, 4> *>(p.t + z * p.batch_t + q * p.plane_t + n * p.ld_t + m) = x;
+            v -= __builtin_convertvector(x, vec<float, 4>);
         }
+    };
+    if (p.what == kPoly) {
+        const f16 *old = p.a + z * p.batch_a;      // the product's operand is A itself, A[n][m..] = A[m..][n]
+        every([&](int64_t m, int64_t n, vec<float, 4> v) {
+            vec<Poly, 4> u = __builtin_convertvector(v, vec<Poly, 4>) * static_cast<Poly>(kDown * p.cc);
+#pragma unroll
+            for (int q = 0; q < PL; ++q) {
+                const vec<f16, 4> x = *reinterpret_cast<const vec<f16, 4> *>(old + q * p.plane_a + n * p.ld_a + m);
+                u += static_cast<Poly>(p.cb) * __builtin_convertvector(x, vec<Poly, 4>);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (m + e == n) u[e] += static_cast<Poly>(p.ca * kUp);
+            keep(m, n, __builtin_convertvector(u, vec<float, 4>));
+        });
+    } else {
+        const float factor = kDown * first * (p.what == kGram ? first : 1.f);
+        every([&](int64_t m, int64_t n, vec<float, 4> v) { keep(m, n, v * factor); });
+    }
 }
 
 // ---- the norm and the first X ---------------------------------------------------------------------
@@ -330,24 +378,38 @@ struct NewtonSpace {
     int64_t s, l;           // padded
     int64_t plane_x, plane_a;
     int32_t planes;
-    int32_t tile;
     size_t bytes;
 };
 
-// Tile edge: 128 keeps a compute unit's matrix units busy from one LDS read per two products; 64 where
-// 128 would leave most compute units without a tile.
-int32_t tile_for(int64_t rows, int64_t cols, int64_t batch) {
-    const int64_t s = rows < cols ? rows : cols, l = rows < cols ? cols : rows;
-    return batch * ((s + 127) / 128) * ((l + 127) / 128) >= 128 ? 128 : 64;
+// The tile edge of a product: the one whose tiles the compute units are through with first.  A tile's
+// time is its area over the rate at this edge, which is lower for a compute unit's only tile, whose
+// waits nothing covers.  Rates relative to an edge of 192, from squares of 1024 (one tile a unit) and
+// 4096: 192 costs a lone tile of 64 the time of 4.5, but is through with a 4096 square in 1.86 ms for 128's
+// 2.07 and 64's 2.89; a 1024 square takes 161 us by 64, 278 by 128, 477 by 192.
+int32_t tile_for(int64_t rows_a, int64_t rows_b, int64_t batch, bool symmetric) {
+    const int32_t edge[3] = {192, 128, 64};
+    const double many[3] = {1.0, 0.9, 0.64}, alone[3] = {1.0, 0.85, 0.42};
+    int32_t best = 64;
+    double least = 0;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t m = (rows_a + edge[i] - 1) / edge[i], n = (rows_b + edge[i] - 1) / edge[i];
+        const int64_t tiles = batch * (symmetric ? m * (m + 1) / 2 : m * n);
+        const double area = static_cast<double>(edge[i]) * edge[i];
+        const double time = fmax(static_cast<double>((tiles + 255) / 256) * area / many[i], area / alone[i]);
+        if (i == 0 || time < least) {
+            least = time;
+            best = edge[i];
+        }
+    }
+    return best;
 }
 
 NewtonSpace carve_newton(int64_t rows, int64_t cols, int64_t batch, int32_t type, char *base) {
     NewtonSpace n{};
     n.planes = type == GNN_F32 ? 2 : 1;
-    n.tile = tile_for(rows, cols, batch);
     const int64_t s = rows < cols ? rows : cols, l = rows < cols ? cols : rows;
-    n.s = (s + n.tile - 1) / n.tile * n.tile;
-    n.l = (l + n.tile - 1) / n.tile * n.tile;
+    n.s = (s + 63) / 64 * 64;
+    n.l = (l + 63) / 64 * 64;
     n.plane_x = n.s * n.l;
     n.plane_a = n.s * n.s;
     size_t off = 0;
@@ -370,17 +432,26 @@ NewtonSpace carve_newton(int64_t rows, int64_t cols, int64_t batch, int32_t type
     return n;
 }
 
-template <int PL, typename TO>
-hipError_t launch_product(const ProductArgs &p, int tile, int64_t batch, hipStream_t s) {
-    const bool symmetric = p.what == kGram || p.what == kPoly;
+template <int TILE, int PL, typename TO>
+hipError_t launch_tiles(ProductArgs p, int64_t batch, bool symmetric, hipStream_t s) {
+    p.m_tiles = (p.rows_a + TILE - 1) / TILE;
+    p.n_tiles = (p.rows_b + TILE - 1) / TILE;
     const int64_t tiles = symmetric ? static_cast<int64_t>(p.m_tiles) * (p.m_tiles + 1) / 2
                                     : static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(batch));
-    if (tile == 128)
-        hipLaunchKernelGGL((k_newton_product<128, 128, 2, 2, PL, TO>), grid, dim3(256), 0, s, p);
-    else
-        hipLaunchKernelGGL((k_newton_product<64, 64, 2, 2, PL, TO>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_newton_product<TILE, PL, TO>),
+                       dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(batch)), dim3(kThreads), 0,
+                       s, p);
     return hipGetLastError();
+}
+
+template <int PL, typename TO>
+hipError_t launch_product(const ProductArgs &p, int64_t batch, hipStream_t s) {
+    const bool symmetric = p.what == kGram || p.what == kPoly;
+    switch (tile_for(p.rows_a, p.rows_b, batch, symmetric)) {
+        case 192: return launch_tiles<192, PL, TO>(p, batch, symmetric, s);
+        case 128: return launch_tiles<128, PL, TO>(p, batch, symmetric, s);
+        default: return launch_tiles<64, PL, TO>(p, batch, symmetric, s);
+    }
 }
 
 template <int PL, typename T>
@@ -426,9 +497,9 @@ hipError_t run_newton(const NewtonArgs &a, hipStream_t s) {
         g.ld_c = g.ld_t = n.s;
         g.plane_c = g.plane_t = n.plane_a;
         g.batch_c = g.batch_t = ba;
-        g.m_tiles = g.n_tiles = static_cast<int32_t>(n.s / n.tile);
+        g.rows_a = g.rows_b = static_cast<int32_t>(n.s);
         g.first = first;
-        err = launch_product<PL, T>(g, n.tile, a.batch, s);
+        err = launch_product<PL, T>(g, a.batch, s);
         if (err != hipSuccess) return err;
         ProductArgs q = g;
         q.what = kPoly;
@@ -441,7 +512,7 @@ hipError_t run_newton(const NewtonArgs &a, hipStream_t s) {
         q.cb = a.coefs[1];
         q.cc = a.coefs[2];
         q.first = nullptr;
-        err = launch_product<PL, T>(q, n.tile, a.batch, s);
+        err = launch_product<PL, T>(q, a.batch, s);
         if (err != hipSuccess) return err;
         ProductArgs y{};
         y.what = last ? kLast : kApply;
@@ -459,8 +530,8 @@ hipError_t run_newton(const NewtonArgs &a, hipStream_t s) {
         y.batch_c = y.batch_t = bx;
         y.t = n.x;
         y.ld_t = n.l;
-        y.m_tiles = static_cast<int32_t>(n.l / n.tile);
-        y.n_tiles = static_cast<int32_t>(n.s / n.tile);
+        y.rows_a = static_cast<int32_t>(n.l);
+        y.rows_b = static_cast<int32_t>(n.s);
         y.first = first;
         y.out = a.out;
         y.ld_out = a.ld_out;
@@ -469,7 +540,7 @@ hipError_t run_newton(const NewtonArgs &a, hipStream_t s) {
         y.n = wide ? a.rows : a.cols;
         y.out_rows = wide ? 0 : 1;
         y.scale = a.scale;
-        err = launch_product<PL, T>(y, n.tile, a.batch, s);
+        err = launch_product<PL, T>(y, a.batch, s);
     }
     return err;
 }
