@@ -222,14 +222,15 @@ __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void k_newton_product
         if (s + u < steps) turn(u, s + u);
 
     // A lane holds column lane % 32 and rows 8 g + 4 (lane / 32) + 0..3 of each 32 x 32 accumulator:
-    // every(f) calls f(row, column, the four values) for what exists of the padded product.
+    // every(f) calls f(row, column, the four values) for what exists of the padded product.  A padded
+    // plane has at most 2^30 elements.
     const auto every = [&](auto f) {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TM; ++j) {
-                const int64_t n = static_cast<int64_t>(tn) * TILE + (wn * TM + j) * 32 + row;
-                const int64_t m0 = static_cast<int64_t>(tm) * TILE + (wm * TM + i) * 32 + 4 * half;
+                const int n = tn * TILE + (wn * TM + j) * 32 + row;
+                const int m0 = tm * TILE + (wm * TM + i) * 32 + 4 * half;
                 // a 32 x 32 accumulator exists or not as a whole
                 if (n >= p.rows_b || m0 >= p.rows_a) continue;
 #pragma unroll
@@ -242,39 +243,46 @@ __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void k_newton_product
     if (p.what == kLast) {
         const float factor = kDown * kDown * first * p.scale;
         TO *out = static_cast<TO *>(p.out) + z * p.batch_out;
-        every([&](int64_t m, int64_t n, vec<float, 4> v) {
+        const int rows = static_cast<int>(p.m), cols = static_cast<int>(p.n);
+        every([&](int m, int n, vec<float, 4> v) {
             v *= factor;
-            if (n >= p.n) return;
-            if (!p.out_rows && m + 4 <= p.m) {
+            if (n >= cols) return;
+            if (!p.out_rows && m + 4 <= rows) {
                 store_f32<TO, 4>(out + n * p.ld_out + m, v);
                 return;
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (m + e < p.m) out[p.out_rows ? (m + e) * p.ld_out + n : n * p.ld_out + m + e] = static_cast<TO>(v[e]);
+                if (m + e < rows) out[p.out_rows ? (m + e) * p.ld_out + n : n * p.ld_out + m + e] = static_cast<TO>(v[e]);
         });
         return;
     }
     const bool mirror = !symmetric || tm != tn;
-    const auto keep = [&](int64_t m, int64_t n, vec<float, 4> v) {
+    char *const pc = reinterpret_cast<char *>(p.c + z * p.batch_c);
+    char *const pt = reinterpret_cast<char *>(p.t + z * p.batch_t);
+    const uint32_t ld_c = static_cast<uint32_t>(p.ld_c), ld_t = static_cast<uint32_t>(p.ld_t);
+    const auto keep = [&](int m, int n, vec<float, 4> v) {
+        const uint32_t oc = 2 * (m * ld_c + n), ot = 2 * (n * ld_t + m);
 #pragma unroll
         for (int q = 0; q < PL; ++q) {
             const vec<f16, 4> x = __builtin_convertvector(v, vec<f16, 4>);
-            f16 *c = p.c + z * p.batch_c + q * p.plane_c + m * p.ld_c + n;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c[e * p.ld_c] = x[e];
-            if (mirror)
-                *reinterpret_cast<vec<f16, 4> *>(p.t + z * p.batch_t + q * p.plane_t + n * p.ld_t + m) = x;
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<f16 *>(pc + 2 * q * p.plane_c + (oc + 2 * e * ld_c)) = x[e];
+            if (mirror) *reinterpret_cast<vec<f16, 4> *>(pt + 2 * q * p.plane_t + ot) = x;
             v -= __builtin_convertvector(x, vec<float, 4>);
         }
     };
     if (p.what == kPoly) {
-        const f16 *old = p.a + z * p.batch_a;      // the product's operand is A itself, A[n][m..] = A[m..][n]
-        every([&](int64_t m, int64_t n, vec<float, 4> v) {
+        // the product's operand is A itself, A[n][m..] = A[m..][n]
+        const char *const old = reinterpret_cast<const char *>(p.a + z * p.batch_a);
+        const uint32_t ld_a = static_cast<uint32_t>(p.ld_a);
+        every([&](int m, int n, vec<float, 4> v) {
             vec<Poly, 4> u = __builtin_convertvector(v, vec<Poly, 4>) * static_cast<Poly>(kDown * p.cc);
 #pragma unroll
             for (int q = 0; q < PL; ++q) {
-                const vec<f16, 4> x = *reinterpret_cast<const vec<f16, 4> *>(old + q * p.plane_a + n * p.ld_a + m);
+                const vec<f16, 4> x =
+                    *reinterpret_cast<const vec<f16, 4> *>(old + 2 * q * p.plane_a + 2 * (n * ld_a + m));
                 u += static_cast<Poly>(p.cb) * __builtin_convertvector(x, vec<Poly, 4>);
             }
 #pragma unroll
@@ -284,7 +292,7 @@ __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void k_newton_product
         });
     } else {
         const float factor = kDown * first * (p.what == kGram ? first : 1.f);
-        every([&](int64_t m, int64_t n, vec<float, 4> v) { keep(m, n, v * factor); });
+        every([&](int m, int n, vec<float, 4> v) { keep(m, n, v * factor); });
     }
 }
 
@@ -330,6 +338,16 @@ __global__ __launch_bounds__(kNormThreads) void k_first_planes(PrepArgs p) {
     __shared__ f16 tile[PL][64][66];
     const int t = threadIdx.x, w = t >> 6;
     const int64_t z = blockIdx.z;
+    // the tile's values, every load made, of a place that exists, while the norm is put together
+    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64, c0 = static_cast<int64_t>(blockIdx.x) * 64;
+    const TI *g = static_cast<const TI *>(p.g) + z * p.batch_g;
+    const int64_t col = c0 + (t & 63) < p.cols ? c0 + (t & 63) : p.cols - 1;
+    TI raw[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int64_t r = r0 + w * 16 + i;
+        raw[i] = g[(r < p.rows ? r : p.rows - 1) * p.ld + col];
+    }
     const double s = wave_sum(t < p.blocks ? p.partial[z * p.blocks + t] : 0.0);
     if (lane_id() == 0) sm[w] = s;
     __syncthreads();
@@ -342,15 +360,12 @@ __global__ __launch_bounds__(kNormThreads) void k_first_planes(PrepArgs p) {
         if (!(norm <= 1.7e308)) rest = __builtin_nan("");
         p.first[z] = static_cast<float>(rest);
     }
-    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 64, c0 = static_cast<int64_t>(blockIdx.x) * 64;
-    const TI *g = static_cast<const TI *>(p.g) + z * p.batch_g;
     const int c = t & 63;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int r = w * 16 + i;
         float v = 0.f;
-        if (r0 + r < p.rows && c0 + c < p.cols)
-            v = ldexpf(static_cast<float>(g[(r0 + r) * p.ld + c0 + c]), 12 - e);
+        if (r0 + r < p.rows && c0 + c < p.cols) v = ldexpf(static_cast<float>(raw[i]), 12 - e);
 #pragma unroll
         for (int q = 0; q < PL; ++q) {
             const f16 x = static_cast<f16>(v);
@@ -385,18 +400,19 @@ struct NewtonSpace {
 // time is its area over the rate at this edge, which is lower for a compute unit's only tile, whose
 // waits nothing covers.  Rates relative to an edge of 192, from squares of 1024 (one tile a unit) and
 // 4096: 192 costs a lone tile of 64 the time of 4.5, but is through with a 4096 square in 1.86 ms for 128's
-// 2.07 and 64's 2.89; a 1024 square takes 161 us by 64, 278 by 128, 477 by 192.
-int32_t tile_for(int64_t rows_a, int64_t rows_b, int64_t batch, bool symmetric) {
+// 2.07 and 64's 2.89; a 1024 square takes 161 us by 64, 278 by 128, 477 by 192.  Two planes at 192 exceed
+// the registers.
+int32_t tile_for(int64_t rows_a, int64_t rows_b, int64_t batch, bool symmetric, int planes) {
     const int32_t edge[3] = {192, 128, 64};
     const double many[3] = {1.0, 0.9, 0.64}, alone[3] = {1.0, 0.85, 0.42};
     int32_t best = 64;
     double least = 0;
-    for (int i = 0; i < 3; ++i) {
+    for (int i = planes - 1; i < 3; ++i) {
         const int64_t m = (rows_a + edge[i] - 1) / edge[i], n = (rows_b + edge[i] - 1) / edge[i];
         const int64_t tiles = batch * (symmetric ? m * (m + 1) / 2 : m * n);
         const double area = static_cast<double>(edge[i]) * edge[i];
         const double time = fmax(static_cast<double>((tiles + 255) / 256) * area / many[i], area / alone[i]);
-        if (i == 0 || time < least) {
+        if (least == 0 || time < least) {
             least = time;
             best = edge[i];
         }
@@ -447,8 +463,8 @@ hipError_t launch_tiles(ProductArgs p, int64_t batch, bool symmetric, hipStream_
 template <int PL, typename TO>
 hipError_t launch_product(const ProductArgs &p, int64_t batch, hipStream_t s) {
     const bool symmetric = p.what == kGram || p.what == kPoly;
-    switch (tile_for(p.rows_a, p.rows_b, batch, symmetric)) {
-        case 192: return launch_tiles<192, PL, TO>(p, batch, symmetric, s);
+    switch (tile_for(p.rows_a, p.rows_b, batch, symmetric, PL)) {
+        case 192: return launch_tiles<PL == 1 ? 192 : 128, PL, TO>(p, batch, symmetric, s);
         case 128: return launch_tiles<128, PL, TO>(p, batch, symmetric, s);
         default: return launch_tiles<64, PL, TO>(p, batch, symmetric, s);
     }
