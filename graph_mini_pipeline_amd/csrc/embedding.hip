@@ -229,7 +229,8 @@ __global__ __launch_bounds__(256) void k_sort_scan(SortArgs a) {
 __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs a) {
     __shared__ uint32_t cnt[kSortWaves][kDigits];
     __shared__ uint32_t sums[2][kSortThreads / kDigits][kDigits];
-    __shared__ uint32_t base[kDigits];
+    __shared__ uint32_t base[kDigits], local[kDigits];
+    __shared__ uint32_t skey[kSortTile], spos[kSortTile];
     __shared__ uint32_t s4[4];
     const int t = threadIdx.x, w = t >> 6;
     for (int i = t; i < kSortWaves * kDigits; i += kSortThreads) (&cnt[0][0])[i] = 0;
@@ -277,12 +278,12 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs a) {
     rank_rounds<kSortRounds>(key, kSortRounds, a.shift, a.bits, cnt[w], rank);
     __syncthreads();
     before = total = 0;
+    uint32_t run = 0;
     if (t < kDigits) {
         for (int q = 0; q < kSortThreads / kDigits; ++q) {
             before += sums[0][q][t];
             total += sums[1][q][t];
         }
-        uint32_t run = 0;
         for (int q = 0; q < kSortWaves; ++q) {
             const uint32_t c = cnt[q][t];
             cnt[q][t] = run;
@@ -290,15 +291,33 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs a) {
         }
     }
     const uint32_t ex = scan_digits(total, s4);
-    if (t < kDigits) base[t] = ex + before;
+    const uint32_t in_tile = scan_digits(run, s4);
+    if (t < kDigits) {
+        base[t] = ex + before - in_tile;      // from a place in the sorted tile to the place in the list
+        local[t] = in_tile;
+    }
     __syncthreads();
+    // The tile is put in order in LDS first, so that a digit's keys leave it side by side: as single
+    // words they would each cost the memory a whole line (901120 positions: 21 us a digit, this
+    // way 18).
 #pragma unroll
     for (int j = 0; j < kSortRounds; ++j) {
-        if (i0 + j * 64 >= a.n) continue;
         const uint32_t g = (key[j] >> a.shift) & ((1u << a.bits) - 1u);
-        const uint32_t to = base[g] + cnt[w][g] + rank[j];
-        a.key_out[to] = key[j];
-        a.pos_out[to] = pos[j];
+        const uint32_t to = local[g] + cnt[w][g] + rank[j];
+        skey[to] = key[j];
+        spos[to] = pos[j];
+    }
+    __syncthreads();
+    const int64_t left = a.n - static_cast<int64_t>(blockIdx.x) * kSortTile;     // keys of this tile
+#pragma unroll
+    for (int j = 0; j < kSortRounds; ++j) {
+        const int i = j * kSortThreads + t;
+        const uint32_t k = skey[i];
+        // (past the end: the tile's last keys, which are no positions')
+        if (i >= left) continue;
+        const uint32_t to = base[(k >> a.shift) & ((1u << a.bits) - 1u)] + i;
+        a.key_out[to] = k;
+        a.pos_out[to] = spos[i];
     }
 }
 
