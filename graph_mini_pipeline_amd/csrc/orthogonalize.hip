@@ -138,28 +138,24 @@ __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void k_newton_product
     }
     h8 ra[kDepth][PL][L], rb[kDepth][PL][L];
     const int steps = static_cast<int>(p.k / BK);
-    // (past the end the last tile again: no branch, so that the waits count the loads exactly)
-    auto load = [&](int set, int s) {
+    // The pieces of a turn: plane, operand, and which of the thread's.  (Past the end the last tile is
+    // loaded again: no branch, so that the waits count the loads exactly.)
+    constexpr int kPieces = PL * 2 * L;
+    auto load = [&](int set, int s, int at) {
         const int64_t k0 = static_cast<int64_t>(s < steps ? s : steps - 1) * BK;
-#pragma unroll
-        for (int q = 0; q < PL; ++q)
-#pragma unroll
-            for (int i = 0; i < L; ++i) {
-                ra[set][q][i] = *reinterpret_cast<const h8 *>(ga + q * p.plane_a + k0 + oa[i]);
-                rb[set][q][i] = *reinterpret_cast<const h8 *>(gb + q * p.plane_b + k0 + ob[i]);
-            }
+        const int q = at / (2 * L), i = at % L;
+        if (at % (2 * L) < L)
+            ra[set][q][i] = *reinterpret_cast<const h8 *>(ga + q * p.plane_a + k0 + oa[i]);
+        else
+            rb[set][q][i] = *reinterpret_cast<const h8 *>(gb + q * p.plane_b + k0 + ob[i]);
     };
-    auto store = [&](int set, int buf) {
-#pragma unroll
-        for (int q = 0; q < PL; ++q) {
-            h8 *at = &lds[buf][q * kPlane];
-#pragma unroll
-            for (int i = 0; i < L; ++i) {
-                const int e = i * kThreads + t, to = piece<CPR>(e / CPR, e % CPR);
-                at[to] = ra[set][q][i];
-                at[TILE * CPR + to] = rb[set][q][i];
-            }
-        }
+    auto store = [&](int set, int buf, int at) {
+        const int q = at / (2 * L), i = at % L, e = i * kThreads + t;
+        h8 *to = &lds[buf][q * kPlane + piece<CPR>(e / CPR, e % CPR)];
+        if (at % (2 * L) < L)
+            *to = ra[set][q][i];
+        else
+            to[TILE * CPR] = rb[set][q][i];
     };
     f16x acc[TM][TM];
 #pragma unroll
@@ -169,48 +165,60 @@ __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void k_newton_product
 
     const int row = lane & 31, half = lane >> 5;
     h8 a[2][PL][TM], b[2][PL][TM];
-    auto read = [&](int buf, int kk) {
-#pragma unroll
-        for (int q = 0; q < PL; ++q) {
-            const h8 *pl = &lds[buf][q * kPlane];
-#pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                a[kk & 1][q][i] = pl[piece<CPR>((wm * TM + i) * 32 + row, kk * 2 + half)];
-                b[kk & 1][q][i] = pl[TILE * CPR + piece<CPR>((wn * TM + i) * 32 + row, kk * 2 + half)];
-            }
-        }
+    constexpr int kReads = PL * 2 * TM;
+    auto read = [&](int buf, int kk, int at) {
+        const int q = at / (2 * TM), i = at % TM;
+        const h8 *pl = &lds[buf][q * kPlane];
+        if (at % (2 * TM) < TM)
+            a[kk & 1][q][i] = pl[piece<CPR>((wm * TM + i) * 32 + row, kk * 2 + half)];
+        else
+            b[kk & 1][q][i] = pl[TILE * CPR + piece<CPR>((wn * TM + i) * 32 + row, kk * 2 + half)];
     };
-    // tile s, from LDS half s % 2; u = s % kDepth, whose register set is free
+    // Tile s, from LDS half s % 2; u = s % kDepth, whose register set is free.  Between any two products
+    // comes a share of the turn's other work (the next operands, the loads kDepth tiles ahead, the next
+    // tile's way into LDS): in a row, with no product under way, the loads alone take 670 cycles of a
+    // turn and the stores 600 beside the 1152 of its products (TILE = 192).
     auto turn = [&](int u, int s) {
         const int buf = u & 1;
-        load(u, s + kDepth);
-        read(buf, 0);
+#pragma unroll
+        for (int r = 0; r < kReads; ++r) read(buf, 0, r);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
-            if (kk + 1 < KK) read(buf, kk + 1);
-            if (kk + 1 == KK) store((u + 1) % kDepth, buf ^ 1);
-            __builtin_amdgcn_sched_barrier(0);
             const auto &x = a[kk & 1];
             const auto &y = b[kk & 1];
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TM; ++j) {
-                    if (PL == 2) {
-                        if (kAllFour)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[PL - 1][i], y[PL - 1][j], acc[i][j], 0, 0, 0);
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[0][i], y[PL - 1][j], acc[i][j], 0, 0, 0);
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[PL - 1][i], y[0][j], acc[i][j], 0, 0, 0);
-                    }
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[0][i], y[0][j], acc[i][j], 0, 0, 0);
+            for (int ij = 0; ij < TM * TM; ++ij) {
+                const int i = ij / TM, j = ij % TM;
+                if (PL == 2) {
+                    if (kAllFour)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[PL - 1][i], y[PL - 1][j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[0][i], y[PL - 1][j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[PL - 1][i], y[0][j], acc[i][j], 0, 0, 0);
                 }
-            __builtin_amdgcn_sched_barrier(0);
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[0][i], y[0][j], acc[i][j], 0, 0, 0);
+                if (kk + 1 < KK) {
+#pragma unroll
+                    for (int r = ij * kReads / (TM * TM); r < (ij + 1) * kReads / (TM * TM); ++r) read(buf, kk + 1, r);
+                }
+                constexpr int kSlots = KK * TM * TM;
+                const int slot = kk * TM * TM + ij;
+#pragma unroll
+                for (int r = slot * kPieces / kSlots; r < (slot + 1) * kPieces / kSlots; ++r) {
+                    load(u, s + kDepth, r);
+                    store((u + 1) % kDepth, buf ^ 1, r);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
         __syncthreads();
     };
 #pragma unroll
-    for (int u = 0; u < kDepth; ++u) load(u, u);
-    store(0, 0);
+    for (int u = 0; u < kDepth; ++u)
+#pragma unroll
+        for (int r = 0; r < kPieces; ++r) load(u, u, r);
+#pragma unroll
+    for (int r = 0; r < kPieces; ++r) store(0, 0, r);
     __syncthreads();
     int s = 0;
     for (; s + kDepth <= steps; s += kDepth) {
@@ -397,14 +405,13 @@ struct NewtonSpace {
 };
 
 // The tile edge of a product: the one whose tiles the compute units are through with first.  A tile's
-// time is its area over the rate at this edge, which is lower for a compute unit's only tile, whose
-// waits nothing covers.  Rates relative to an edge of 192, from squares of 1024 (one tile a unit) and
-// 4096: 192 costs a lone tile of 64 the time of 4.5, but is through with a 4096 square in 1.86 ms for 128's
-// 2.07 and 64's 2.89; a 1024 square takes 161 us by 64, 278 by 128, 477 by 192.  Two planes at 192 exceed
-// the registers.
+// time is its area over the rate at this edge, for a compute unit's only tile and for several.  Rates
+// relative to an edge of 192, from five steps on bf16 squares with one edge throughout: 4096 (several
+// tiles a unit) takes 1.65 ms by 192, 1.97 by 128, 2.89 by 64; 1024 (at most one) 364 us by 192, 228 by 128,
+// 145 by 64; 2048 530, 376 and 455 us.  Two planes at 192 exceed the registers.
 int32_t tile_for(int64_t rows_a, int64_t rows_b, int64_t batch, bool symmetric, int planes) {
     const int32_t edge[3] = {192, 128, 64};
-    const double many[3] = {1.0, 0.9, 0.64}, alone[3] = {1.0, 0.85, 0.42};
+    const double many[3] = {1.0, 0.85, 0.57}, alone[3] = {1.0, 0.9, 0.57};
     int32_t best = 64;
     double least = 0;
     for (int i = planes - 1; i < 3; ++i) {
