@@ -336,16 +336,13 @@ struct OneSort {
     uint32_t s4[4];
 };
 
-// mark: every named row's mark is set.  Every thread of the workgroup calls it.
+// The thread's keys, in the order that the sort takes them.
 template <int ROUNDS, int THREADS>
-__device__ __forceinline__ void sort_one(const SortArgs &a, OneSort<ROUNDS, THREADS> &m, bool mark) {
-    constexpr int kWaves = THREADS / 64;
-    const int t = threadIdx.x, w = t >> 6;
+__device__ __forceinline__ void load_keys(const SortArgs &a, uint32_t (&key)[ROUNDS]) {
     const int n = static_cast<int>(a.n);
     const int64_t n_act = load_count(a.d_n, a.n);
     const int rounds = (n + THREADS - 1) / THREADS;
-    const int i0 = w * 64 * rounds + lane_id();
-    uint32_t key[ROUNDS], pos[ROUNDS], rank[ROUNDS];
+    const int i0 = (static_cast<int>(threadIdx.x) >> 6) * 64 * rounds + lane_id();
 #pragma unroll
     for (int j = 0; j < ROUNDS; ++j)
         if (j < rounds) key[j] = static_cast<uint32_t>(a.ids[i0 + j * 64 < n ? i0 + j * 64 : n - 1]);
@@ -353,11 +350,22 @@ __device__ __forceinline__ void sort_one(const SortArgs &a, OneSort<ROUNDS, THRE
     for (int j = 0; j < ROUNDS; ++j) {
         if (j >= rounds) continue;
         const int i = i0 + j * 64;
-        pos[j] = static_cast<uint32_t>(i);
         // slots beyond n: after every position of the same key
         key[j] = i < n ? make_key(a, i, n_act, static_cast<int32_t>(key[j])) : a.num_rows;
-        if (mark && key[j] < a.num_rows) a.touched[key[j]] = 1;
     }
+}
+
+// Every thread of the workgroup calls it, with its keys.
+template <int ROUNDS, int THREADS>
+__device__ __forceinline__ void sort_one(const SortArgs &a, OneSort<ROUNDS, THREADS> &m,
+                                         uint32_t (&key)[ROUNDS]) {
+    constexpr int kWaves = THREADS / 64;
+    const int t = threadIdx.x, w = t >> 6;
+    const int rounds = (static_cast<int>(a.n) + THREADS - 1) / THREADS;
+    const int i0 = w * 64 * rounds + lane_id();
+    uint32_t pos[ROUNDS], rank[ROUNDS];
+#pragma unroll
+    for (int j = 0; j < ROUNDS; ++j) pos[j] = static_cast<uint32_t>(i0 + j * 64);
     for (int p = 0; p < a.passes; ++p) {
         const int shift = p * a.bits;
         for (int i = t; i < kWaves * kDigits; i += THREADS) (&m.cnt[0][0])[i] = 0;
@@ -402,12 +410,17 @@ __global__ __launch_bounds__(kOneThreads) void k_sort_one(SortArgs a) {
     __shared__ uint32_t sw[kOneThreads / 64];
     const int t = threadIdx.x;
     const int n = static_cast<int>(a.n);
+    uint32_t key[kSortRounds];
+    load_keys<kSortRounds, kOneThreads>(a, key);
     clear_marks(a);
     if (a.touched != nullptr) {
         __threadfence();        // before the marks
         __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kSortRounds; ++j)
+            if (j * kOneThreads < n && key[j] < a.num_rows) a.touched[key[j]] = 1;
     }
-    sort_one(a, m, a.touched != nullptr);
+    sort_one(a, m, key);
     for (int i = t; i < n; i += kOneThreads) {
         a.key_out[i] = m.key[i];
         a.pos_out[i] = m.pos[i];
@@ -703,14 +716,15 @@ __global__ __launch_bounds__(kSumThreads) void k_embedding_join(SumArgs a) {
 // ---- few positions --------------------------------------------------------------------------------
 //
 // Up to kFewMost positions the launches cost more than the work: one launch does it all.  Every
-// workgroup sorts all positions for itself and then takes its share: the runs that begin in its part
-// of the sorted list (short ones by a lane group each, long ones by all groups in turn) and, for a
-// written dense table, the unnamed rows in its part of the table.
+// workgroup clears, for a written dense table, the unnamed rows in its part of the table, sorts all
+// positions for itself, and takes the runs that begin in its part of the sorted list, short ones by a
+// lane group each, long ones by all groups in turn.
 constexpr int kFewThreads = 512;   // (workgroups of 1024 start up to 6 us apart, of 512 half that)
 constexpr int kFewRounds = 4;
 constexpr int kFewMost = kFewRounds * kFewThreads;
 constexpr int kFewShare = 16;      // sorted positions per workgroup
 constexpr int kFewRun = 32;        // longest run that one lane group takes
+constexpr int kFewRows = 512;      // table rows per workgroup at most: clears_all() is past 16 a position
 
 template <typename TI, typename TO, int VE>
 __global__ __launch_bounds__(kFewThreads) void k_embedding_few(SortArgs q, SumArgs a, int zero) {
@@ -719,9 +733,30 @@ __global__ __launch_bounds__(kFewThreads) void k_embedding_few(SortArgs q, SumAr
     __shared__ uint32_t rank_of[kFewShare];
     __shared__ uint32_t long_runs;       // one bit per position of the share
     __shared__ float sm[kFewThreads * VE];
+    __shared__ uint8_t named[kFewRows];
     const int t = threadIdx.x, n = static_cast<int>(q.n);
+    const int groups = kFewThreads / a.lanes, grp = t / a.lanes, lane = t & (a.lanes - 1);
     if (t == 0) long_runs = 0;
-    sort_one(q, m, false);
+    uint32_t keys[kFewRounds];
+    load_keys<kFewRounds, kFewThreads>(q, keys);
+    if (zero) {
+        const uint32_t share = (q.num_rows + gridDim.x - 1) / gridDim.x, r0 = blockIdx.x * share;
+        if (t < kFewRows) named[t] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kFewRounds; ++j)
+            if (j * kFewThreads < n && keys[j] - r0 < share) named[keys[j] - r0] = 1;
+        __syncthreads();
+        for (uint32_t r = grp; r < share && r0 + r < q.num_rows; r += groups) {
+            if (named[r]) continue;
+            TO *p = static_cast<TO *>(a.out) + static_cast<int64_t>(r0 + r) * a.ld_out;
+            for (int s = 0; s < a.slabs; ++s) {
+                const Cols c = lane_cols<VE>(s, a.lanes, lane, a.d);
+                if (c.on) store_f32<TO, VE>(p + c.at, vec<float, VE>(0.f));
+            }
+        }
+    }
+    sort_one(q, m, keys);
     const int lo = static_cast<int>(blockIdx.x) * kFewShare;
     const auto head = [&](int i) { return is_head(m.key[i], i > 0 ? m.key[i - 1] : 0u, i == 0, q.num_rows); };
     if (q.rows) {
@@ -742,7 +777,6 @@ __global__ __launch_bounds__(kFewThreads) void k_embedding_few(SortArgs q, SumAr
         }
         __syncthreads();
     }
-    const int groups = kFewThreads / a.lanes, grp = t / a.lanes, lane = t & (a.lanes - 1);
     const TI *dout = static_cast<const TI *>(a.dout);
     typedef typename loose<TI, VE>::type Raw;
     // the sum of positions i0, i0 + step, ... below end of the sorted list
@@ -796,21 +830,6 @@ __global__ __launch_bounds__(kFewThreads) void k_embedding_few(SortArgs q, SumAr
                     for (int e = 0; e < VE; ++e) acc[e] += sm[e * kFewThreads + g * a.lanes + lane];
                 put_row<TO, VE>(a, q.rows ? static_cast<int64_t>(rank_of[i - lo]) : m.key[i], c, acc);
             }
-        }
-    }
-    if (!zero) return;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * groups + grp; r < q.num_rows;
-         r += static_cast<int64_t>(gridDim.x) * groups) {
-        int from = 0, to = n;      // the first position whose key is at least r
-        while (from < to) {
-            const int mid = (from + to) / 2;
-            if (m.key[mid] < r) from = mid + 1; else to = mid;
-        }
-        if (from < n && m.key[from] == r) continue;
-        TO *p = static_cast<TO *>(a.out) + r * a.ld_out;
-        for (int s = 0; s < a.slabs; ++s) {
-            const Cols c = lane_cols<VE>(s, a.lanes, lane, a.d);
-            if (c.on) store_f32<TO, VE>(p + c.at, vec<float, VE>(0.f));
         }
     }
 }
@@ -910,6 +929,7 @@ hipError_t run_sums(const EmbedGradArgs &a, const GradSpace &g, const SortArgs &
         int64_t grid = (a.n + kFewShare - 1) / kFewShare;
         const int64_t clear = a.num_rows / 32 < 128 ? a.num_rows / 32 : 128;
         if (zero_untouched && grid < clear) grid = clear;     // more workgroups, for the unnamed rows
+        if (zero_untouched && grid * kFewRows < a.num_rows) grid = (a.num_rows + kFewRows - 1) / kFewRows;
         hipLaunchKernelGGL((k_embedding_few<TI, TO, VE>), dim3(static_cast<unsigned>(grid)),
                            dim3(kFewThreads), 0, s, sort, p,
                            zero_untouched ? 1 : 0);
