@@ -58,7 +58,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle without a Stream object around it (3 us of a short call)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -649,15 +650,17 @@ def _need_rows(t: torch.Tensor, name: str) -> int:
     kind = _type(t.dtype, name)
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a device tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or \
-            (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1) or \
+            (shape[0] > 1 and stride[0] < shape[1]):
         raise ValueError(f"{name}: must be a matrix with contiguous rows that do not overlap")
     return kind
 
 
 def _ld(t: torch.Tensor) -> int:
     """Elements from one row of a matrix to the next."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    shape = t.shape
+    return t.stride()[0] if shape[0] > 1 else shape[1]
 
 
 def gnn_embedding_lookup(table: torch.Tensor, ids: torch.Tensor, scale: float, out: torch.Tensor,
