@@ -23,7 +23,15 @@
 // the instruction's slots is the result's own, the same for both operands.
 //
 // fp32 runs on the fp32 matrix instructions; bf16 on the bf16 ones, with P and dS rounded to bf16
-// (2^-9, the size of the rounding of the results), everything else in fp32.
+// (a half step of 2^-8, the size of the rounding of the results), everything else in fp32.
+//
+// What bounds it.  For bf16 with many rows, LDS: an operand read is 1 KB for one matrix instruction of 32
+// cycles, four of them at once are the 128 bytes a cycle that a compute unit's LDS delivers, and the
+// exponentials and the tiles' way into LDS come on top.  4 sequences of up to 1024 queries of 16 heads
+// over 4, up to 2600 states of 128: forward 111 us (480 TFLOP/s), dq 118 us (670), dk and dv 230 us (460
+// by four products).  For single tokens, the reading of k and v: 16 sequences over up to 16384 states
+// of 4 x 128, 346 MB in 94 us (3.7 TB/s; a large copy reaches 4.9).  For fp32, the matrix
+// instructions, of which a 32 x 32 x 2 takes 64 cycles.
 #include <math.h>
 
 #include "learn.hpp"
@@ -665,9 +673,10 @@ __global__ __launch_bounds__(kThreads, WK == 1 && sizeof(T) == 2 ? 2 : 1) void k
 // dk and dv of 128 states, 32 a wavefront; splits > 1 shares the query rows among workgroups.  For bf16
 // (SIDES = 2) four wavefronts take dv and four more dk of the same states: S is computed twice, 40
 // products in place of 32, but each side's operands and sums leave room for two wavefronts per SIMD,
-// whose waits overlap (one side's 258 us for both became SIDES2_US at 4 x 1024 queries of 16 heads
-// over up to 2600 states).  For fp32, whose operands take twice the registers and whose products
-// take sixteen times as long, one wavefront does both.
+// whose waits overlap: 230 us in place of 258 at 4 x 1024 queries of 16 heads over up to 2600 states.
+// (A turn of the grid's 128 states takes some 2700 cycles, 2200 of them LDS reads.)  For fp32, whose
+// operands take twice the registers and whose products take sixteen times as long, one wavefront
+// does both.
 template <typename T, int DP, int SIDES>
 __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArgs a) {
     constexpr int BR = 32, DB = DP / 32;

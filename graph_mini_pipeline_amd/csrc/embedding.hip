@@ -1,7 +1,8 @@
 // Embedding lookup with scaling, and its gradient by sorted ids.
 //
 // Lookup: out[i, :] = scale * table[ids[i], :], one rounding to the output's type.  Memory-bound: a
-// thread holds kLookUnroll independent 16-byte row pieces in flight.
+// thread holds kLookUnroll independent 16-byte row pieces in flight.  1081344 rows of 100 fp32 to bf16:
+// 135 us, 4.8 TB/s of rows and results, what a large copy reaches; 16384 x 768 bf16 8 us on the device.
 //
 // Gradient: G[t, :] = scale * sum over the positions i with ids[i] = t of dout[i, :], for a dense
 // table or for the distinct ids only.  The (id, position) pairs are sorted by id, stably, so that
@@ -14,6 +15,12 @@
 //   - those are joined in chunk order: a run of two chunks by a lane group, a longer one, which the
 //     first pass lists, by a workgroup.
 // No atomic touches a sum, so results do not depend on timing.
+//
+// What bounds it: the reading of dout, in rows that lie apart.  131072 x 1024 bf16 over 50257 rows: sums 107
+// us of 146 (4.3 TB/s of dout and the fp32 table), two digits of the sort 31, joining 10.  901120 x 100 fp32
+// over 400000 nodes: sums 154 of 263 (rows of 400 bytes fetch 512), three digits 69, ids 12, joining 22.
+// (Finishing a run of two chunks by the group that began it saves partial sums but makes the chunks'
+// walks uneven: 139 + 10 us for 107 + 17 at the first shape, and was left.)
 #include "learn.hpp"
 
 namespace gnnmb {

@@ -50,6 +50,15 @@ KERNEL_SOURCES = {
     "k_hash_probe": "csrc/probe.hip",
     "k_fill": "csrc/relabel.hip",
     "k_sage_update": "csrc/sage.hip",
+    "k_embedding": "csrc/embedding.hip",
+    "k_sort": "csrc/embedding.hip",
+    "k_count_heads": "csrc/embedding.hip",
+    "k_emit_heads": "csrc/embedding.hip",
+    "k_zero_rows": "csrc/embedding.hip",
+    "k_attend": "csrc/attention.hip",
+    "k_newton": "csrc/orthogonalize.hip",
+    "k_norm_squares": "csrc/orthogonalize.hip",
+    "k_first_planes": "csrc/orthogonalize.hip",
 }
 
 
