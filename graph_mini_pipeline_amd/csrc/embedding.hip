@@ -125,8 +125,7 @@ struct SortArgs {
     uint8_t *touched;       // [num_rows] 1: some id names the row; cleared by the first count, marked
     int64_t touched_words;  // by the first placement; NULL: none
     uint32_t *long_runs;    // their number is cleared by the first count
-    // run heads (one-tile sort of the rows form)
-    int32_t rows;
+    // run heads (the rows form)
     int32_t *uniq;
     int64_t *d_n_uniq;
     int64_t row_cap;
@@ -362,22 +361,29 @@ __device__ __forceinline__ void load_keys(const SortArgs &a, uint32_t (&key)[ROU
     }
 }
 
-// Every thread of the workgroup calls it, with its keys.
+// The thread's positions, of the keys that load_keys() gives it.
 template <int ROUNDS, int THREADS>
-__device__ __forceinline__ void sort_one(const SortArgs &a, OneSort<ROUNDS, THREADS> &m,
-                                         uint32_t (&key)[ROUNDS]) {
-    constexpr int kWaves = THREADS / 64;
-    const int t = threadIdx.x, w = t >> 6;
-    const int rounds = (static_cast<int>(a.n) + THREADS - 1) / THREADS;
-    const int i0 = w * 64 * rounds + lane_id();
-    uint32_t pos[ROUNDS], rank[ROUNDS];
+__device__ __forceinline__ void own_positions(int64_t n, uint32_t (&pos)[ROUNDS]) {
+    const int rounds = (static_cast<int>(n) + THREADS - 1) / THREADS;
+    const int i0 = (static_cast<int>(threadIdx.x) >> 6) * 64 * rounds + lane_id();
 #pragma unroll
     for (int j = 0; j < ROUNDS; ++j) pos[j] = static_cast<uint32_t>(i0 + j * 64);
-    for (int p = 0; p < a.passes; ++p) {
-        const int shift = p * a.bits;
+}
+
+// Every thread of the workgroup calls it, with its keys and their positions.
+template <int ROUNDS, int THREADS>
+__device__ __forceinline__ void sort_one(int n, int passes, int bits, OneSort<ROUNDS, THREADS> &m,
+                                         uint32_t (&key)[ROUNDS], uint32_t (&pos)[ROUNDS]) {
+    constexpr int kWaves = THREADS / 64;
+    const int t = threadIdx.x, w = t >> 6;
+    const int rounds = (n + THREADS - 1) / THREADS;
+    const int i0 = w * 64 * rounds + lane_id();
+    uint32_t rank[ROUNDS];
+    for (int p = 0; p < passes; ++p) {
+        const int shift = p * bits;
         for (int i = t; i < kWaves * kDigits; i += THREADS) (&m.cnt[0][0])[i] = 0;
         __syncthreads();
-        rank_rounds<ROUNDS>(key, rounds, shift, a.bits, m.cnt[w], rank);
+        rank_rounds<ROUNDS>(key, rounds, shift, bits, m.cnt[w], rank);
         __syncthreads();
         uint32_t total = 0;
         if (t < kDigits) {
@@ -396,13 +402,13 @@ __device__ __forceinline__ void sort_one(const SortArgs &a, OneSort<ROUNDS, THRE
 #pragma unroll
         for (int j = 0; j < ROUNDS; ++j) {
             if (j >= rounds) continue;
-            const uint32_t g = (key[j] >> shift) & ((1u << a.bits) - 1u);
+            const uint32_t g = (key[j] >> shift) & ((1u << bits) - 1u);
             const uint32_t to = m.base[g] + m.cnt[w][g] + rank[j];
             m.key[to] = key[j];
             m.pos[to] = static_cast<uint16_t>(pos[j]);
         }
         __syncthreads();
-        if (p + 1 == a.passes) break;
+        if (p + 1 == passes) break;
 #pragma unroll
         for (int j = 0; j < ROUNDS; ++j) {
             if (j >= rounds) continue;
@@ -420,19 +426,13 @@ __global__ __launch_bounds__(kOneThreads) void k_sort_one(SortArgs a) {
     uint32_t key[kSortRounds];
     load_keys<kSortRounds, kOneThreads>(a, key);
     clear_marks(a);
-    if (a.touched != nullptr) {
-        __threadfence();        // before the marks
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kSortRounds; ++j)
-            if (j * kOneThreads < n && key[j] < a.num_rows) a.touched[key[j]] = 1;
-    }
-    sort_one(a, m, key);
+    uint32_t pos[kSortRounds];
+    own_positions<kSortRounds, kOneThreads>(a.n, pos);
+    sort_one(n, a.passes, a.bits, m, key, pos);
     for (int i = t; i < n; i += kOneThreads) {
         a.key_out[i] = m.key[i];
         a.pos_out[i] = m.pos[i];
     }
-    if (!a.rows) return;
     uint32_t carry = 0;
     for (int r0 = 0; r0 < n; r0 += kOneThreads) {
         const int i = r0 + t;
@@ -657,8 +657,30 @@ __global__ __launch_bounds__(kSumThreads) void k_embedding_sums(SumArgs a) {
     }
 }
 
+// The sum over a workgroup's lane groups of their acc, in the groups' order, for the first group; a
+// thread adds the groups' values of one column.  Every thread of the workgroup calls it.
+template <int VE, int THREADS>
+__device__ __forceinline__ void join_groups(vec<float, VE> &acc, float *sm, int lanes) {
+    const int t = threadIdx.x;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < VE; ++e) sm[e * THREADS + t] = acc[e];
+    __syncthreads();
+    for (int i = t; i < lanes * VE; i += THREADS) {
+        float *p = sm + i / lanes * THREADS + (i & (lanes - 1));
+        float x = p[0];
+#pragma unroll 8
+        for (int g = lanes; g < THREADS; g += lanes) x += p[g];
+        p[0] = x;
+    }
+    __syncthreads();
+    if (t < lanes)
+#pragma unroll
+        for (int e = 0; e < VE; ++e) acc[e] = sm[e * THREADS + t];
+}
+
 // Joins the partial sums: a lane group takes a chunk's last run where it ends in the next chunk, and
-// the workgroups of the grid's last row take the listed longer runs, whose partial sums their lane
+// the workgroups past sum_blocks take the listed longer runs, whose partial sums their lane
 // groups add in turn, and then each other's sums in the groups' order.
 template <typename TO, int VE>
 __global__ __launch_bounds__(kSumThreads) void k_embedding_join(SumArgs a) {
@@ -706,103 +728,111 @@ __global__ __launch_bounds__(kSumThreads) void k_embedding_join(SumArgs a) {
             for (int64_t q = chunk + 1 + grp; q <= last; q += groups)
                 acc += load_f32<float, VE>(p + 2 * q * a.d);
         }
-#pragma unroll
-        for (int e = 0; e < VE; ++e) sm[e * kSumThreads + threadIdx.x] = acc[e];
-        __syncthreads();
-        if (grp == 0) {
-            for (int q = 1; q < groups; ++q)
-#pragma unroll
-                for (int e = 0; e < VE; ++e) acc[e] += sm[e * kSumThreads + q * a.lanes + lane];
-            // the run's rank is that of the next chunk's first run
+        join_groups<VE, kSumThreads>(acc, sm, a.lanes);
+        // the run's rank is that of the next chunk's first run
+        if (grp == 0)
             put_row<TO, VE>(a, a.chunk_rank ? static_cast<int64_t>(a.chunk_rank[chunk + 1]) : cur, c, acc);
-        }
-        __syncthreads();
     }
 }
 
 // ---- few positions --------------------------------------------------------------------------------
 //
-// Up to kFewMost positions the launches cost more than the work: one launch does it all.  Every
-// workgroup clears, for a written dense table, the unnamed rows in its part of the table, sorts all
-// positions for itself, and takes the runs that begin in its part of the sorted list, short ones by a
-// lane group each, long ones by all groups in turn.
+// With few positions the launches cost more than the work: one
+// launch does it all.
+//
+// The distinct ids: every workgroup sorts all positions for itself, and takes the runs that begin in
+// its part of the sorted list.
+//
+// A dense table: a workgroup owns the rows r with r mod 2^shift = blockIdx.x, so that neighbouring
+// frequent ids go to different ones.  It picks its positions from the list of ids, which all read, in
+// their order, clears its unnamed rows where the table is written, and sorts its own positions only,
+// by the rest of the id.  1024 x 64 fp32 over 10000 rows: 7.8 us a call, most of it the launch.
+//
+// Both: a lane group adds a short run, all groups together, one after the other, the long ones.
 constexpr int kFewThreads = 512;   // (workgroups of 1024 start up to 6 us apart, of 512 half that)
 constexpr int kFewRounds = 4;
 constexpr int kFewMost = kFewRounds * kFewThreads;
 constexpr int kFewShare = 16;      // sorted positions per workgroup
 constexpr int kFewRun = 32;        // longest run that one lane group takes
-constexpr int kFewRows = 512;      // table rows per workgroup at most: clears_all() is past 16 a position
+// Dense tables of up to kBucketMid positions, and of up to kBucketMost where a row of dout has at most
+// kBucketBytes bytes, go by buckets (all ids of a zipf law: 8192 x 104 bf16 over 50000 rows 23 us for the
+// sort's 44, 16384 x 256 over 20000 37 for 44, but 16384 x 400 over 3000 53 for 45: the most frequent
+// row's many positions belong to one workgroup).
+constexpr int kBucketMid = 16 * kFewThreads, kBucketMost = 32 * kFewThreads;
+constexpr int64_t kBucketBytes = 512;
+constexpr int kBucketWide = 256;   // workgroups
+constexpr int kBucketRows = 16 * kBucketMost / 64;  // of a workgroup: clears_all() is past 16 a position
+
+// The sum of positions pos[i0], pos[i0 + step], ... below pos[end].
+template <typename TI, int VE>
+__device__ __forceinline__ vec<float, VE> sum_run(const SumArgs &a, const uint16_t *pos, int i0, int end,
+                                                  int step, const Cols &c) {
+    typedef typename loose<TI, VE>::type Raw;
+    const TI *dout = static_cast<const TI *>(a.dout);
+    vec<float, VE> acc(0.f);
+    for (int i = i0; i < end; i += kSumUnroll * step) {
+        Raw v[kSumUnroll];
+#pragma unroll
+        for (int u = 0; u < kSumUnroll; ++u) {
+            const int at = i + u * step < end ? i + u * step : i;
+            v[u] = *reinterpret_cast<const Raw *>(dout + static_cast<int64_t>(pos[at]) * a.ld_dout +
+                                                  (c.on ? c.at : 0));
+        }
+#pragma unroll
+        for (int u = 0; u < kSumUnroll; ++u)
+            if (i + u * step < end) acc += __builtin_convertvector(v[u], vec<float, VE>);
+    }
+    return acc;
+}
+
+// The run that begins at sorted position i and is longer than kFewRun, by the whole workgroup.
+template <typename TI, typename TO, int VE>
+__device__ __forceinline__ void sum_long(const SumArgs &a, const uint32_t *key, const uint16_t *pos,
+                                         int i, int n, int64_t row, int slab, float *sm) {
+    const int groups = kFewThreads / a.lanes, grp = threadIdx.x / a.lanes;
+    int end = i + kFewRun + 1, over = n;     // the first position of another key
+    while (end < over) {
+        const int mid = (end + over) / 2;
+        if (key[mid] == key[i]) end = mid + 1; else over = mid;
+    }
+    const Cols c = lane_cols<VE>(slab, a.lanes, threadIdx.x & (a.lanes - 1), a.d);
+    vec<float, VE> acc = sum_run<TI, VE>(a, pos, i + grp, end, groups, c);
+    join_groups<VE, kFewThreads>(acc, sm, a.lanes);
+    if (grp == 0) put_row<TO, VE>(a, row, c, acc);
+}
 
 template <typename TI, typename TO, int VE>
-__global__ __launch_bounds__(kFewThreads) void k_embedding_few(SortArgs q, SumArgs a, int zero) {
+__global__ __launch_bounds__(kFewThreads) void k_embedding_few(SortArgs q, SumArgs a) {
     __shared__ OneSort<kFewRounds, kFewThreads> m;
     __shared__ uint32_t sw[kFewThreads / 64];
     __shared__ uint32_t rank_of[kFewShare];
     __shared__ uint32_t long_runs;       // one bit per position of the share
     __shared__ float sm[kFewThreads * VE];
-    __shared__ uint8_t named[kFewRows];
     const int t = threadIdx.x, n = static_cast<int>(q.n);
     const int groups = kFewThreads / a.lanes, grp = t / a.lanes, lane = t & (a.lanes - 1);
     if (t == 0) long_runs = 0;
-    uint32_t keys[kFewRounds];
+    uint32_t keys[kFewRounds], pos[kFewRounds];
     load_keys<kFewRounds, kFewThreads>(q, keys);
-    if (zero) {
-        const uint32_t share = (q.num_rows + gridDim.x - 1) / gridDim.x, r0 = blockIdx.x * share;
-        if (t < kFewRows) named[t] = 0;
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kFewRounds; ++j)
-            if (j * kFewThreads < n && keys[j] - r0 < share) named[keys[j] - r0] = 1;
-        __syncthreads();
-        for (uint32_t r = grp; r < share && r0 + r < q.num_rows; r += groups) {
-            if (named[r]) continue;
-            TO *p = static_cast<TO *>(a.out) + static_cast<int64_t>(r0 + r) * a.ld_out;
-            for (int s = 0; s < a.slabs; ++s) {
-                const Cols c = lane_cols<VE>(s, a.lanes, lane, a.d);
-                if (c.on) store_f32<TO, VE>(p + c.at, vec<float, VE>(0.f));
-            }
-        }
-    }
-    sort_one(q, m, keys);
+    own_positions<kFewRounds, kFewThreads>(q.n, pos);
+    sort_one(n, q.passes, q.bits, m, keys, pos);
     const int lo = static_cast<int>(blockIdx.x) * kFewShare;
     const auto head = [&](int i) { return is_head(m.key[i], i > 0 ? m.key[i - 1] : 0u, i == 0, q.num_rows); };
-    if (q.rows) {
-        // ranks of the runs; the first workgroup writes the list
-        uint32_t carry = 0;
-        for (int r0 = 0; r0 < n; r0 += kFewThreads) {
-            const int i = r0 + t;
-            const uint32_t h = i < n && head(i);
-            uint32_t total;
-            const uint32_t at = carry + block_exclusive_scan<uint32_t, kFewThreads>(h, &total, sw);
-            if (i >= lo && i < lo + kFewShare) rank_of[i - lo] = at;
-            if (blockIdx.x == 0 && h && at < q.row_cap) q.uniq[at] = static_cast<int32_t>(m.key[i]);
-            carry += total;
-        }
-        if (blockIdx.x == 0 && t == 0) {
-            *q.d_n_uniq = carry;
-            if (carry > q.row_cap) set_status(q.status, GNN_ERR_CAPACITY);
-        }
-        __syncthreads();
+    // ranks of the runs; the first workgroup writes the list
+    uint32_t carry = 0;
+    for (int r0 = 0; r0 < n; r0 += kFewThreads) {
+        const int i = r0 + t;
+        const uint32_t h = i < n && head(i);
+        uint32_t total;
+        const uint32_t at = carry + block_exclusive_scan<uint32_t, kFewThreads>(h, &total, sw);
+        if (i >= lo && i < lo + kFewShare) rank_of[i - lo] = at;
+        if (blockIdx.x == 0 && h && at < q.row_cap) q.uniq[at] = static_cast<int32_t>(m.key[i]);
+        carry += total;
     }
-    const TI *dout = static_cast<const TI *>(a.dout);
-    typedef typename loose<TI, VE>::type Raw;
-    // the sum of positions i0, i0 + step, ... below end of the sorted list
-    const auto sum = [&](int i0, int end, int step, const Cols &c) {
-        vec<float, VE> acc(0.f);
-        for (int i = i0; i < end; i += kSumUnroll * step) {
-            Raw v[kSumUnroll];
-#pragma unroll
-            for (int u = 0; u < kSumUnroll; ++u) {
-                const int at = i + u * step < end ? i + u * step : i;
-                v[u] = *reinterpret_cast<const Raw *>(dout + static_cast<int64_t>(m.pos[at]) * a.ld_dout +
-                                                      (c.on ? c.at : 0));
-            }
-#pragma unroll
-            for (int u = 0; u < kSumUnroll; ++u)
-                if (i + u * step < end) acc += __builtin_convertvector(v[u], vec<float, VE>);
-        }
-        return acc;
-    };
+    if (blockIdx.x == 0 && t == 0) {
+        *q.d_n_uniq = carry;
+        if (carry > q.row_cap) set_status(q.status, GNN_ERR_CAPACITY);
+    }
+    __syncthreads();
     const int hi = lo + kFewShare < n ? lo + kFewShare : n;
     for (int item = grp; item < (hi - lo) * a.slabs; item += groups) {
         const int i = lo + item / a.slabs;
@@ -814,30 +844,102 @@ __global__ __launch_bounds__(kFewThreads) void k_embedding_few(SortArgs q, SumAr
         int end = i + 1;
         while (end < n && m.key[end] == m.key[i]) ++end;
         const Cols c = lane_cols<VE>(item % a.slabs, a.lanes, lane, a.d);
-        put_row<TO, VE>(a, q.rows ? static_cast<int64_t>(rank_of[i - lo]) : m.key[i], c, sum(i, end, 1, c));
+        put_row<TO, VE>(a, rank_of[i - lo], c, sum_run<TI, VE>(a, m.pos, i, end, 1, c));
     }
     __syncthreads();
-    for (uint32_t left = long_runs; left != 0; left &= left - 1) {      // whole workgroup
+    for (uint32_t left = long_runs; left != 0; left &= left - 1) {
         const int i = lo + __ffs(static_cast<int>(left)) - 1;
-        int end = i + kFewRun + 1, over = n;     // the first position of another key
-        while (end < over) {
-            const int mid = (end + over) / 2;
-            if (m.key[mid] == m.key[i]) end = mid + 1; else over = mid;
-        }
-        for (int slab = 0; slab < a.slabs; ++slab) {
-            const Cols c = lane_cols<VE>(slab, a.lanes, lane, a.d);
-            vec<float, VE> acc = sum(i + grp, end, groups, c);
-            __syncthreads();
+        for (int slab = 0; slab < a.slabs; ++slab)
+            sum_long<TI, TO, VE>(a, m.key, m.pos, i, n, rank_of[i - lo], slab, sm);
+    }
+}
+
+template <typename TI, typename TO, int VE, int ROUNDS>
+__global__ __launch_bounds__(kFewThreads) void k_embedding_buckets(SortArgs q, SumArgs a, int shift,
+                                                                   int zero) {
+    constexpr int kWaves = kFewThreads / 64, kMost = ROUNDS * kFewThreads;
+    __shared__ OneSort<ROUNDS, kFewThreads> m;
+    __shared__ uint16_t runs[kMost];     // where runs begin: short ones from the front, long ones from the back
+    __shared__ uint32_t found[kWaves], count[2];
+    __shared__ float sm[kFewThreads * VE];
+    __shared__ uint8_t named[kBucketRows];
+    const int t = threadIdx.x, w = t >> 6;
+    const int groups = kFewThreads / a.lanes, grp = t / a.lanes, lane = t & (a.lanes - 1);
+    const int slab = blockIdx.y;
+    const Cols c = lane_cols<VE>(slab, a.lanes, lane, a.d);
+    const uint32_t b = blockIdx.x, low = (1u << shift) - 1u;
+    const uint64_t below = (1ull << lane_id()) - 1ull;
+    const int rounds = (static_cast<int>(q.n) + kFewThreads - 1) / kFewThreads;
+    uint32_t keys[ROUNDS], pos[ROUNDS];
+    load_keys<ROUNDS, kFewThreads>(q, keys);
+    own_positions<ROUNDS, kFewThreads>(q.n, pos);
+    if (t < 2) count[t] = 0;
+    if (zero)
+        for (int i = t; i < kBucketRows; i += kFewThreads) named[i] = 0;
+    uint32_t total = 0;
 #pragma unroll
-            for (int e = 0; e < VE; ++e) sm[e * kFewThreads + t] = acc[e];
-            __syncthreads();
-            if (grp == 0) {
-                for (int g = 1; g < groups; ++g)
+    for (int j = 0; j < ROUNDS; ++j)
+        if (j < rounds) total += __popcll(__ballot(keys[j] < q.num_rows && (keys[j] & low) == b));
+    if (lane_id() == 0) found[w] = total;
+    __syncthreads();
+    uint32_t at = 0;
+    int n = 0;                           // this workgroup's positions
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) acc[e] += sm[e * kFewThreads + g * a.lanes + lane];
-                put_row<TO, VE>(a, q.rows ? static_cast<int64_t>(rank_of[i - lo]) : m.key[i], c, acc);
-            }
+    for (int i = 0; i < kWaves; ++i) {
+        if (i < w) at += found[i];
+        n += static_cast<int>(found[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < ROUNDS; ++j) {
+        if (j >= rounds) continue;
+        const bool mine = keys[j] < q.num_rows && (keys[j] & low) == b;
+        const uint64_t all = __ballot(mine);
+        if (mine) {
+            const uint32_t to = at + __popcll(all & below);
+            m.key[to] = keys[j] >> shift;
+            m.pos[to] = static_cast<uint16_t>(pos[j]);
+            if (zero) named[keys[j] >> shift] = 1;
         }
+        at += __popcll(all);
+    }
+    __syncthreads();
+    if (zero)
+        for (uint32_t r = grp; (r << shift) + b < q.num_rows; r += groups) {
+            if (named[r] || !c.on) continue;
+            store_f32<TO, VE>(static_cast<TO *>(a.out) +
+                                  static_cast<int64_t>((r << shift) + b) * a.ld_out + c.at,
+                              vec<float, VE>(0.f));
+        }
+    if (n == 0) return;
+    const int mine = (n + kFewThreads - 1) / kFewThreads, i0 = w * 64 * mine + lane_id();
+#pragma unroll
+    for (int j = 0; j < ROUNDS; ++j) {
+        if (j >= mine) continue;
+        const int i = i0 + j * 64;
+        keys[j] = i < n ? m.key[i] : ~0u;        // after every position of the same digits
+        pos[j] = i < n ? m.pos[i] : 0u;
+    }
+    __syncthreads();
+    sort_one(n, q.passes, q.bits, m, keys, pos);
+    for (int i = t; i < n; i += kFewThreads) {
+        if (i > 0 && m.key[i] == m.key[i - 1]) continue;
+        if (i + kFewRun < n && m.key[i + kFewRun] == m.key[i])
+            runs[kMost - 1 - atomicAdd(&count[1], 1u)] = static_cast<uint16_t>(i);
+        else
+            runs[atomicAdd(&count[0], 1u)] = static_cast<uint16_t>(i);
+    }
+    __syncthreads();
+    for (int r = grp; r < static_cast<int>(count[0]); r += groups) {
+        const int i = runs[r];
+        int end = i + 1;
+        while (end < n && m.key[end] == m.key[i]) ++end;
+        put_row<TO, VE>(a, (static_cast<int64_t>(m.key[i]) << shift) + b, c,
+                        sum_run<TI, VE>(a, m.pos, i, end, 1, c));
+    }
+    for (uint32_t r = 0; r < count[1]; ++r) {
+        const int i = runs[kMost - 1 - r];
+        sum_long<TI, TO, VE>(a, m.key, m.pos, i, n, (static_cast<int64_t>(m.key[i]) << shift) + b, slab,
+                             sm);
     }
 }
 
@@ -868,7 +970,7 @@ struct GradSpace {
 };
 
 // Chunk length: 64 positions, so that the partial sums of a chunk's two ends cost at most a
-// sixteenth of its rows of fp32, or shorter where that leaves fewer than kMinGroups lane groups.
+// sixteenth of its rows of fp32, or shorter where that leaves too few lane groups.
 int32_t chunk_for(int64_t n) {
     int64_t c = 64;
     while (c > kChunkMin && n / c < 2048) c /= 2;
@@ -932,14 +1034,31 @@ hipError_t run_sums(const EmbedGradArgs &a, const GradSpace &g, const SortArgs &
     p.lanes = 1;
     while (p.lanes < cpr && p.lanes < 64) p.lanes *= 2;
     p.slabs = static_cast<int32_t>((cpr + p.lanes - 1) / p.lanes);
+    if (key == nullptr && a.rows) {
+        hipLaunchKernelGGL((k_embedding_few<TI, TO, VE>),
+                           dim3(static_cast<unsigned>((a.n + kFewShare - 1) / kFewShare)),
+                           dim3(kFewThreads), 0, s, sort, p);
+        return hipGetLastError();
+    }
     if (key == nullptr) {
-        int64_t grid = (a.n + kFewShare - 1) / kFewShare;
-        const int64_t clear = a.num_rows / 32 < 128 ? a.num_rows / 32 : 128;
-        if (zero_untouched && grid < clear) grid = clear;     // more workgroups, for the unnamed rows
-        if (zero_untouched && grid * kFewRows < a.num_rows) grid = (a.num_rows + kFewRows - 1) / kFewRows;
-        hipLaunchKernelGGL((k_embedding_few<TI, TO, VE>), dim3(static_cast<unsigned>(grid)),
-                           dim3(kFewThreads), 0, s, sort, p,
-                           zero_untouched ? 1 : 0);
+        int shift = 6;
+        while (p.slabs << shift < kBucketWide && ((a.n * p.lanes) >> shift) > kFewThreads) ++shift;
+        SortArgs q = sort;
+        int nb = 1;
+        while ((static_cast<uint64_t>(a.num_rows - 1) >> shift >> nb) != 0) ++nb;
+        q.passes = (nb + kSortBits - 1) / kSortBits;
+        q.bits = (nb + q.passes - 1) / q.passes;
+        const dim3 grid(1u << shift, static_cast<unsigned>(p.slabs)), block(kFewThreads);
+        const int zero = zero_untouched ? 1 : 0;
+        if (a.n <= kFewMost)
+            hipLaunchKernelGGL((k_embedding_buckets<TI, TO, VE, kFewRounds>), grid, block, 0, s, q, p,
+                               shift, zero);
+        else if (a.n <= kBucketMid)
+            hipLaunchKernelGGL((k_embedding_buckets<TI, TO, VE, kBucketMid / kFewThreads>), grid, block,
+                               0, s, q, p, shift, zero);
+        else
+            hipLaunchKernelGGL((k_embedding_buckets<TI, TO, VE, kBucketMost / kFewThreads>), grid, block, 0, s, q, p,
+                               shift, zero);
         return hipGetLastError();
     }
     const int per = kSumThreads / p.lanes;
@@ -1016,7 +1135,6 @@ hipError_t launch_embedding_grad(const EmbedGradArgs &a, hipStream_t s) {
     while ((static_cast<uint64_t>(a.num_rows) >> nb) != 0) ++nb;
     q.passes = (nb + kSortBits - 1) / kSortBits;
     q.bits = (nb + q.passes - 1) / q.passes;
-    q.rows = a.rows;
     q.uniq = a.uniq;
     q.d_n_uniq = a.d_n_uniq;
     q.row_cap = a.row_cap;
@@ -1024,7 +1142,9 @@ hipError_t launch_embedding_grad(const EmbedGradArgs &a, hipStream_t s) {
     q.chunk = g.chunk;
     const uint32_t *key, *pos;
     q.long_runs = g.long_runs;
-    if (a.n > 0 && a.n <= kFewMost) {
+    const int64_t row = a.d * (a.dout_type == GNN_F32 ? 4 : 2);
+    const int64_t few = a.rows ? kFewMost : row <= kBucketBytes ? kBucketMost : kBucketMid;
+    if (a.n > 0 && a.n <= few) {
         key = pos = nullptr;        // sorted by the kernel that adds
     } else if (a.n <= kOneTile) {
         q.key_out = g.key[0];

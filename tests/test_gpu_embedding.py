@@ -146,6 +146,31 @@ def test_grad_dense(n, rows, d, kind, pad, dt, gt):
         assert not bad.any() and not got.isnan().any(), (accumulate, int(bad.sum()))
 
 
+BUCKETS = [(2048, 1, 9, "one", -1), (2049, 65, 5, "uniform", 0), (5000, 3, 1030, "skewed", -1),
+           (8192, 20_000, 260, "skewed", 1), (12_000, 191_999, 31, "uniform", -1),
+           (12_000, 192_000, 31, "uniform", -1), (16_384, 262_143, 128, "skewed", -1),
+           (16_384, 1, 7, "one", -1), (16_384, 2_000_003, 8, "skewed", 0), (16_385, 5000, 64, "skewed", -1)]
+
+
+@pytest.mark.parametrize("n,rows,d,kind,pad", BUCKETS)
+@pytest.mark.parametrize("dt,gt", [(F32, F32), (F32, BF16), (BF16, F32), (BF16, BF16)])
+def test_grad_dense_of_some_thousand_positions(n, rows, d, kind, pad, dt, gt):
+    test_grad_dense(n, rows, d, kind, pad, dt, gt)
+    # the same bits every time, and ids out of range and positions past the count have no part in them
+    ids, dout = make_ids(kind, n, rows, n), padded(n, d, 1, dt, seed=n)
+    first, again = torch.empty(rows, d, dtype=gt, device="cuda"), torch.empty(rows, d, dtype=gt, device="cuda")
+    ids[n // 3] = pad
+    d_n = torch.tensor([n - 5], device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gm.gnn_embedding_grad(ids.cuda(), dout, 1.0, first, ws_for(n, rows, d), pad_id=pad, d_n=d_n)
+    ids[n // 3] = rows
+    dout[n // 3], dout[n - 5:] = math.nan, math.nan
+    gm.gnn_embedding_grad(ids.cuda(), dout, 1.0, again, ws_for(n, rows, d), pad_id=pad, d_n=d_n,
+                          d_status=status)
+    assert torch.equal(first, again) and not first.isnan().any()
+    assert status.item() == gm.GNN_ERR_OUT_OF_RANGE
+
+
 @pytest.mark.parametrize("n,rows,d,kind,pad", GRADS)
 def test_grad_rows(n, rows, d, kind, pad):
     ids = make_ids(kind, n, rows, n)
