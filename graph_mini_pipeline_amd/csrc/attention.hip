@@ -23,7 +23,8 @@
 // the instruction's slots is the result's own, the same for both operands.
 //
 // fp32 runs on the fp32 matrix instructions; bf16 on the bf16 ones, with P and dS rounded to bf16
-// (a half step of 2^-8, the size of the rounding of the results), everything else in fp32.
+// (a half step of 2^-8, the size of the rounding of the results; short sums of the gradients: as two
+// bf16, 2^-16), everything else in fp32.
 //
 // What bounds it.  For bf16 with many rows, LDS: an operand read is 1 KB for one matrix instruction of 32
 // cycles, four of them at once are the 128 bytes a cycle that a compute unit's LDS delivers, and the
@@ -135,14 +136,19 @@ struct Turned<bf16, DP> {
         return V{__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at),
                  __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(at + 2 * kRow))};
     }
-    Piece<bf16> b;      // p's half that the current steps multiply
+    Piece<bf16> b, low; // p's half that the current steps multiply, and what bf16 leaves of it
+    template <bool LOW>
     __device__ __forceinline__ void use(f32x16 (&acc)[DB], const V &v, int s, const f32x16 &p) {
         if (s % DB == 0) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) b[e] = static_cast<bf16>(p[8 * (s / DB) + e]);
+#pragma unroll
+            for (int e = 0; LOW && e < 8; ++e)
+                low[e] = static_cast<bf16>(p[8 * (s / DB) + e] - static_cast<float>(b[e]));
         }
         const vec<short, 8> a = __builtin_shufflevector(v.lo, v.hi, 0, 1, 2, 3, 4, 5, 6, 7);
         mma(acc[s % DB], __builtin_bit_cast(Piece<bf16>, a), b);
+        if (LOW) mma(acc[s % DB], __builtin_bit_cast(Piece<bf16>, a), low);
     }
 };
 
@@ -162,6 +168,7 @@ struct Turned<float, DP> {
         for (int db = 0; db < DB; ++db) v.a[db] = at[32 * db];
         return v;
     }
+    template <bool LOW>
     __device__ __forceinline__ void use(f32x16 (&acc)[DB], const V &v, int s, const f32x16 &p) {
 #pragma unroll
         for (int db = 0; db < DB; ++db)
@@ -402,7 +409,7 @@ __global__ __launch_bounds__(kThreads, WK == 1 ? 2 : 1) void k_attend(AttendArgs
         Tu tu;
         stream<Tu::kRing, KB * Tu::kSteps>(turned, column, [&](int st, const typename Tu::V &v) {
             const int b = st / Tu::kSteps, t = st % Tu::kSteps;
-            tu.use(o, v, t, x[b]);
+            tu.template use<false>(o, v, t, x[b]);
             if (b + 1 < KB) {                         // the next block's weights, meanwhile
 #pragma unroll
                 for (int i = t * 16 / Tu::kSteps; i < (t + 1) * 16 / Tu::kSteps; ++i) weigh(b + 1, i);
@@ -546,7 +553,10 @@ __global__ __launch_bounds__(kThreads) void k_attend_stat(AttendArgs a) {
     }
 }
 
-template <typename T, int DP, int WQ, int WK>
+// Dq of tiles of rows, as the forward kernel's.  LOW (bf16): dS is multiplied as two bf16, and where a
+// sequence's states fit one turn, D, which comes from the rounded out, is put right by what the row of dS
+// adds up to, which is zero; dk's kernel, which follows, reads it.
+template <typename T, int DP, int WQ, int WK, bool LOW>
 __global__ __launch_bounds__(kThreads, WK == 1 && sizeof(T) == 2 ? 2 : 1) void k_attend_dq(AttendArgs a) {
     constexpr int KW = 32, BK = KW * WK, BQ = 32 * WQ, DB = DP / 32;
     typedef Tile<T, DP> Tl;
@@ -606,16 +616,26 @@ __global__ __launch_bounds__(kThreads, WK == 1 && sizeof(T) == 2 ? 2 : 1) void k
             }
         });
         prime<Tu::kRing, Tu::kSteps>(turned, column);
+        f32x16 weight = x;
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] *= dp[i] - st.y;
         if (k1 > ke) {        // the last turn: states past the end
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                if (k0 + wk * KW + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= ke) x[i] = 0.f;
+                if (k0 + wk * KW + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= ke) x[i] = weight[i] = 0.f;
+        }
+        if (LOW && s.nk <= KW) {
+            float over = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) over += x[i];
+            over += __shfl_xor(over, 32, 64);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] -= over * weight[i];
+            if (wk == 0 && lane < 32 && r < rows) a.stat[stat_at(a, me.pos, me.head)].y = st.y + over;
         }
         Tu tu;
         stream<Tu::kRing, Tu::kSteps>(turned, column,
-                                      [&](int i, const typename Tu::V &v) { tu.use(dq, v, i, x); });
+                                      [&](int i, const typename Tu::V &v) { tu.template use<LOW>(dq, v, i, x); });
         if (k1 < ke) put(next, k1);
     };
     if (kb < ke) {
@@ -677,7 +697,7 @@ __global__ __launch_bounds__(kThreads, WK == 1 && sizeof(T) == 2 ? 2 : 1) void k
 // (A turn of the grid's 128 states takes some 2700 cycles, 2200 of them LDS reads.)  For fp32, whose
 // operands take twice the registers and whose products take sixteen times as long, one wavefront
 // does both.
-template <typename T, int DP, int SIDES>
+template <typename T, int DP, int SIDES, bool LOW>
 __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArgs a) {
     constexpr int BR = 32, DB = DP / 32;
     typedef Tile<T, DP> Tl;
@@ -791,7 +811,7 @@ __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArg
 #pragma unroll
             for (int j = 0; j < 16; ++j) weigh(j);
             stream<Tu::kRing, Tu::kSteps>(turned, column,
-                                          [&](int i, const typename Tu::V &u) { tu.use(dv, u, i, p); });
+                                          [&](int i, const typename Tu::V &u) { tu.template use<LOW>(dv, u, i, p); });
         } else {
             Both pairs[kR];
             prime<kR, 2 * KK>(pairs, both);
@@ -817,11 +837,11 @@ __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArg
             }
             stream<Tu::kRing, kSteps>(turned, column, [&](int i, const typename Tu::V &u) {
                 if (i < kFirst) {
-                    tu.use(dv, u, i, p);
+                    tu.template use<LOW>(dv, u, i, p);
 #pragma unroll
                     for (int j = i * 16 / Tu::kSteps; j < (i + 1) * 16 / Tu::kSteps; ++j) differ(j);
                 } else {
-                    tu.use(dk, u, i - kFirst, ds);
+                    tu.template use<LOW>(dk, u, i - kFirst, ds);
                 }
             });
         }
@@ -985,7 +1005,13 @@ hipError_t forward(AttendArgs a, const Plan &p, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <typename T, int DP>
+// The bf16 that P and dS are rounded to leaves the gradients sqrt(2) times the error of their own
+// rounding where the sums are long, and more where they are short (over 3 to 66 states 1.5 to 2 times):
+// there, where either has fewer than kLongSums terms, P and dS are multiplied as two bf16, which at
+// 4 x 1024 queries of 16 heads over up to 2600 states would take 579 us in place of 423.
+constexpr int64_t kLongSums = 512;
+
+template <typename T, int DP, bool LOW>
 hipError_t backward(AttendArgs a, const Plan &p, hipStream_t s) {
     const unsigned z = static_cast<unsigned>(a.n_seq);
     if (a.n_q > 0)
@@ -997,9 +1023,9 @@ hipError_t backward(AttendArgs a, const Plan &p, hipStream_t s) {
         a.per = p.per;
         const dim3 grid(static_cast<unsigned>(p.q_tiles), static_cast<unsigned>(a.kv * a.splits), z);
         if (p.few)
-            hipLaunchKernelGGL((k_attend_dq<T, DP, 4 / sharing<T, DP>(), sharing<T, DP>()>), grid, dim3(kThreads), 0, s, a);
+            hipLaunchKernelGGL((k_attend_dq<T, DP, 4 / sharing<T, DP>(), sharing<T, DP>(), LOW>), grid, dim3(kThreads), 0, s, a);
         else
-            hipLaunchKernelGGL((k_attend_dq<T, DP, 4, 1>), grid, dim3(kThreads), 0, s, a);
+            hipLaunchKernelGGL((k_attend_dq<T, DP, 4, 1, LOW>), grid, dim3(kThreads), 0, s, a);
     }
     float *const part_kv = reinterpret_cast<float *>(a.ws + p.part_kv);
     if (a.max_k > 0) {
@@ -1009,7 +1035,7 @@ hipError_t backward(AttendArgs a, const Plan &p, hipStream_t s) {
         b.part = part_kv;
         const dim3 grid(static_cast<unsigned>(p.k_tiles), static_cast<unsigned>(a.kv * b.splits), z);
         constexpr int kSides = sizeof(T) == 2 ? 2 : 1;
-        hipLaunchKernelGGL((k_attend_dkv<T, DP, kSides>), grid, dim3(kThreads * kSides), 0, s, b);
+        hipLaunchKernelGGL((k_attend_dkv<T, DP, kSides, LOW>), grid, dim3(kThreads * kSides), 0, s, b);
     }
     ReduceArgs r{p.per, p.dkv_per, part_kv, a.max_q > 0 && p.splits > 1, a.max_k > 0 && p.dkv_splits > 1};
     if (r.dq || r.dkv) {
@@ -1021,6 +1047,13 @@ hipError_t backward(AttendArgs a, const Plan &p, hipStream_t s) {
                            dim3(kThreads), 0, s, a, r);
     }
     return hipGetLastError();
+}
+
+template <typename T, int DP>
+hipError_t backward(const AttendArgs &a, const Plan &p, hipStream_t s) {
+    if (sizeof(T) == 2 && (a.max_q * a.group < kLongSums || a.max_k < kLongSums))
+        return backward<T, DP, sizeof(T) == 2>(a, p, s);
+    return backward<T, DP, false>(a, p, s);
 }
 
 template <typename T>
