@@ -8,11 +8,12 @@
 //
 // Numbers.  The products run on the 16-bit matrix instructions with fp32 accumulation.  X, A and Q
 // are stored in fp16, times 2^12: the singular values stay below 3 (newton_in_range), so that
-// every entry fits, and entries down to 2^-26 keep fp16's 11 bits.  For a bf16 update one fp16 plane carries
-// eight times the precision of the result's type; the fp32 update takes two planes, x = hi + lo (22
-// bits), and three matrix products, hi hi + hi lo + lo hi (all four for small matrices); the dropped
-// product is below 2^-22 of a term.  The first X is G times a power of two, so nothing is rounded that need not be, and the rest
-// of 1 / (|G|_F + eps) multiplies the first A and the first Q X.
+// every entry fits, and entries down to 2^-26 keep fp16's 11 bits.  For a bf16 update one fp16 plane
+// carries eight times the precision of the result's type; the fp32 update, and some long matrices, take two
+// planes, x = hi + lo (22 bits), and three matrix products, hi hi + hi lo + lo hi (all four for small
+// matrices); the dropped product is below 2^-22 of a term.  The first X is G times a power of two, so
+// nothing is rounded that need not be, and the rest of 1 / (|G|_F + eps) multiplies the first A and the
+// first Q X.
 //
 // Layout.  The matrix instructions want both operands with the summed index contiguous: X for A, the
 // symmetric A for A^2, and, since (Q X)^T = X^T Q, X^T and Q for the last product, which therefore
@@ -433,9 +434,20 @@ int32_t tile_for(int64_t rows_a, int64_t rows_b, int64_t batch, bool symmetric, 
     return best;
 }
 
+// One plane for a bf16 update, unless the matrix is long and of some 200 rows: there A is nearly a
+// multiple of I, most of its eigenvalues being alike, and the rounding of Q's diagonal, the same in all
+// of it, scales the whole result.  With one plane the result is off, in units of its own rounding, by 1.41
+// at 6 x 223 columns, 1.53 at 11 x 223 and 1.45 at 16 x 256, and by 1.1 to 1.3 at fewer than 6 squares and
+// with fewer than 160 or more than 320 rows, where the steps pass by other values; with two by 1.0, in
+// twice the time (2 x 2368 x 223: 257 us for 130).
+int32_t planes_for(int64_t rows, int64_t cols, int32_t type) {
+    const int64_t s = rows < cols ? rows : cols, l = rows < cols ? cols : rows;
+    return type == GNN_F32 || (l >= 6 * s && s >= 160 && s <= 320) ? 2 : 1;
+}
+
 NewtonSpace carve_newton(int64_t rows, int64_t cols, int64_t batch, int32_t type, char *base) {
     NewtonSpace n{};
-    n.planes = type == GNN_F32 ? 2 : 1;
+    n.planes = planes_for(rows, cols, type);
     const int64_t s = rows < cols ? rows : cols, l = rows < cols ? cols : rows;
     n.s = (s + 63) / 64 * 64;
     n.l = (l + 63) / 64 * 64;
@@ -611,7 +623,8 @@ bool newton_in_range(const float *coefs, int steps) {
 }
 
 hipError_t launch_newton(const NewtonArgs &a, hipStream_t s) {
-    return a.type == GNN_F32 ? run_newton<2, float>(a, s) : run_newton<1, bf16>(a, s);
+    if (a.type == GNN_F32) return run_newton<2, float>(a, s);
+    return planes_for(a.rows, a.cols, a.type) == 2 ? run_newton<2, bf16>(a, s) : run_newton<1, bf16>(a, s);
 }
 
 }  // namespace gnnmb

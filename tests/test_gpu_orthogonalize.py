@@ -94,6 +94,19 @@ def test_number_of_steps_and_scale(steps, dtype):
     check(g, run(g, steps=steps, scale=0.2), steps=steps, scale=0.2)
 
 
+@pytest.mark.parametrize("m,n", [(1600, 223), (223, 2400), (960, 160), (320, 1920)])
+def test_long_matrices_keep_their_size(m, n):
+    """Their eigenvalues are alike, so that rounded factors would scale the result: with 22 bits by some
+    2^-21 a step, which the steps' slopes (below 4 each) can make 2^-11 at most; the rounding of the
+    result is of either sign."""
+    k = n // 8 if n < m else m // 8
+    strong = gaussian(m, k, seed=m) @ gaussian(k, n, seed=n)
+    g = (strong / math.sqrt(k) + gaussian(m, n, seed=m + n)).to(BF16)
+    got, want = run(g).double().cpu(), steps64(g, 5)
+    assert abs(float((got * want).sum() / want.square().sum()) - 1) < 1e-4
+    check(g, run(g))
+
+
 def test_low_rank_and_strong_directions():
     a, b = gaussian(200, 4, seed=1), gaussian(4, 333, seed=2)
     g = a @ b + 1e-3 * gaussian(200, 333, seed=3)
