@@ -693,8 +693,9 @@ __global__ __launch_bounds__(kThreads, WK == 1 && sizeof(T) == 2 ? 2 : 1) void k
 // dk and dv of 128 states, 32 a wavefront; splits > 1 shares the query rows among workgroups.  For bf16
 // (SIDES = 2) four wavefronts take dv and four more dk of the same states: S is computed twice, 40
 // products in place of 32, but each side's operands and sums leave room for two wavefronts per SIMD,
-// whose waits overlap: 230 us in place of 258 at 4 x 1024 queries of 16 heads over up to 2600 states.
-// (A turn of the grid's 128 states takes some 2700 cycles, 2200 of them LDS reads.)  For fp32, whose
+// whose waits overlap: the training step at 4 x 1024 queries of 16 heads over up to 2600 states takes
+// 421 us in place of 466, this kernel 227 of it.  (A turn takes some 2700 cycles, 2200 of them LDS
+// reads.)  For fp32, whose
 // operands take twice the registers and whose products take sixteen times as long, one wavefront
 // does both.
 template <typename T, int DP, int SIDES, bool LOW>
