@@ -34,6 +34,7 @@
 // of 4 x 128, 346 MB in 94 us (3.7 TB/s; a large copy reaches 4.9).  For fp32, the matrix
 // instructions, of which a 32 x 32 x 2 takes 64 cycles.
 #include <math.h>
+#include <type_traits>
 
 #include "learn.hpp"
 
@@ -553,11 +554,24 @@ __global__ __launch_bounds__(kThreads) void k_attend_stat(AttendArgs a) {
     }
 }
 
-// Dq of tiles of rows, as the forward kernel's.  LOW (bf16): dS is multiplied as two bf16, and where a
-// sequence's states fit one turn, D, which comes from the rounded out, is put right by what the row of dS
-// adds up to, which is zero; dk's kernel, which follows, reads it.
+// Over a single state the weight is 1 whatever q and k are: dS is zero.  P (dP - D) would leave the
+// difference of two sums of the same products in other orders, rounding alone, so what dS is multiplied
+// by last is zero there (a dS that is not finite still shows).
+__device__ __forceinline__ float ds_factor(const AttendArgs &a, const Seq &s) {
+    return s.nk == 1 ? 0.f : a.scale;
+}
+
+// Workgroups of k_attend_dq on a compute unit: two where their tiles and registers (256) allow.
+template <typename T, int DP, int WK>
+constexpr int dq_groups() {
+    return (WK == 1 && sizeof(T) == 2) || sizeof(T) * DP * (WK == 1 ? 1 : 2) <= 256 ? 2 : 1;
+}
+
+// Dq of tiles of rows, as the forward kernel's.  Where a sequence's states fit one turn, D, which comes
+// from the rounded out and another order of its sum, is put right by what the row of dS adds up to,
+// which is zero; dk's kernel, which follows, reads it.  LOW (bf16): dS is multiplied as two bf16.
 template <typename T, int DP, int WQ, int WK, bool LOW>
-__global__ __launch_bounds__(kThreads, WK == 1 && sizeof(T) == 2 ? 2 : 1) void k_attend_dq(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, (dq_groups<T, DP, WK>())) void k_attend_dq(AttendArgs a) {
     constexpr int KW = 32, BK = KW * WK, BQ = 32 * WQ, DB = DP / 32;
     typedef Tile<T, DP> Tl;
     typedef Turned<T, DP> Tu;
@@ -594,10 +608,11 @@ __global__ __launch_bounds__(kThreads, WK == 1 && sizeof(T) == 2 ? 2 : 1) void k
         sv.put(Tl{pair + kPair / 2}, ke - at, a.d);
         __syncthreads();
     };
-    const auto turn = [&](Piece<T> *pair, Piece<T> *next, int64_t k0) {
+    // (one_turn is a constant: what the short sequences need would cost the others registers)
+    const auto turn = [&](auto one_turn, Piece<T> *pair, Piece<T> *next, int64_t k0) {
         const Tl tk{pair}, tv{pair + kPair / 2};
         const int64_t k1 = k0 + BK;
-        if (k1 < ke) load(k1);
+        if (!one_turn.value && k1 < ke) load(k1);
         constexpr int KK = RowPieces<T, DP>::KK, kR = row_ring<T>();
         f32x16 x(0.f), dp(0.f);
         Piece<T> ring[kR];
@@ -616,35 +631,40 @@ __global__ __launch_bounds__(kThreads, WK == 1 && sizeof(T) == 2 ? 2 : 1) void k
             }
         });
         prime<Tu::kRing, Tu::kSteps>(turned, column);
-        f32x16 weight = x;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] *= dp[i] - st.y;
-        if (k1 > ke) {        // the last turn: states past the end
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (k0 + wk * KW + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= ke) x[i] = weight[i] = 0.f;
-        }
-        if (LOW && s.nk <= KW) {
+        const auto past = [&](int i) {        // (in the last turn) a state past the end
+            return k0 + wk * KW + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) >= ke;
+        };
+        dp -= st.y;
+        if (one_turn.value) {
             float over = 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) over += x[i];
+            for (int i = 0; i < 16; ++i) over += past(i) ? 0.f : x[i] * dp[i];
             over += __shfl_xor(over, 32, 64);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] -= over * weight[i];
+            dp -= over;       // (D + over, as one number, is rounded again)
             if (wk == 0 && lane < 32 && r < rows) a.stat[stat_at(a, me.pos, me.head)].y = st.y + over;
+        }
+        x *= dp;
+        if (k1 > ke) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (past(i)) x[i] = 0.f;
         }
         Tu tu;
         stream<Tu::kRing, Tu::kSteps>(turned, column,
                                       [&](int i, const typename Tu::V &v) { tu.template use<LOW>(dq, v, i, x); });
-        if (k1 < ke) put(next, k1);
+        if (!one_turn.value && k1 < ke) put(next, k1);
     };
     if (kb < ke) {
         load(kb);
         put(smem, kb);
     }
-    for (int64_t k0 = kb; k0 < ke; k0 += 2 * BK) {
-        turn(smem, smem + kPair, k0);
-        if (k0 + BK < ke) turn(smem + kPair, smem, k0 + BK);
+    if (kb < ke && s.nk <= KW) {
+        turn(std::true_type{}, smem, smem + kPair, kb);
+    } else {
+        for (int64_t k0 = kb; k0 < ke; k0 += 2 * BK) {
+            turn(std::false_type{}, smem, smem + kPair, k0);
+            if (k0 + BK < ke) turn(std::false_type{}, smem + kPair, smem, k0 + BK);
+        }
     }
     if (WK > 1) {
         constexpr int kRow = DP + 4;
@@ -675,13 +695,14 @@ __global__ __launch_bounds__(kThreads, WK == 1 && sizeof(T) == 2 ? 2 : 1) void k
         }
     }
     if (r >= rows) return;
+    const float factor = ds_factor(a, s);
     T *out = static_cast<T *>(a.dq) + me.pos * a.ld_dq + me.head * a.d;
     float *part = a.part + (static_cast<int64_t>(split) * a.n_q * a.heads + line) * a.d;
 #pragma unroll
     for (int i = 0; i < DB; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const f32x4 v = f32x4{dq[i][4 * j], dq[i][4 * j + 1], dq[i][4 * j + 2], dq[i][4 * j + 3]} * a.scale;
+            const f32x4 v = f32x4{dq[i][4 * j], dq[i][4 * j + 1], dq[i][4 * j + 2], dq[i][4 * j + 3]} * factor;
             const int d0 = 32 * i + 8 * j + 4 * (lane >> 5);
             if (a.splits > 1)
                 put4<float>(part, d0, a.d, v);
@@ -874,7 +895,7 @@ __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArg
                     put4<T>(to, d0, a.d, x);
             }
     };
-    if (do_k) write(dk, a.scale, static_cast<T *>(a.dk) + kr * a.ld_dk + hk * a.d, part);
+    if (do_k) write(dk, ds_factor(a, s), static_cast<T *>(a.dk) + kr * a.ld_dk + hk * a.d, part);
     if (do_v) write(dv, 1.f, static_cast<T *>(a.dv) + kr * a.ld_dv + hk * a.d, part + a.d);
 }
 

@@ -1,0 +1,73 @@
+"""Gradients of gnn_cross_attention over few states, where P (dP - D) is a small difference of large
+numbers.  Helpers and notation as in test_gpu_attention.py; u = 2^-24."""
+import math
+
+import pytest
+import torch
+
+from tests.test_gpu_attention import BF16, F32, U, Call, indptr
+
+pytestmark = pytest.mark.gpu
+
+gm = pytest.importorskip("graph_mini_pipeline_amd")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("nq,heads,kv,d", [([1], 1, 1, 8), ([5, 2, 9], 4, 2, 64), ([1, 1, 1, 1], 8, 2, 40),
+                                           ([300, 130, 40], 8, 8, 128), ([33] * 40, 8, 8, 72)])
+def test_a_single_state_has_no_gradient_of_its_score(nq, heads, kv, d, dtype):
+    """P is 1 whatever q and k are: dq and dk are zero, not roundings of dP - D."""
+    c = Call(nq, [1] * len(nq), heads, kv, d, dtype, seed=d)
+    got = c.run()
+    c.check(got)
+    assert torch.all(got["dq"] == 0) and torch.all(got["dk"] == 0)
+    assert torch.any(got["dv"] != 0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_single_state_beside_others(dtype):
+    """By length, and by a count that leaves one state."""
+    c = Call([4, 7, 3, 6], [1, 90, 30, 0], 4, 2, 32, dtype, count=[1, 90, 1, 0], seed=41)
+    got = c.run()
+    c.check(got)
+    q, k = indptr(c.nq).tolist(), indptr(c.nk).tolist()
+    for b in (0, 2):
+        assert torch.all(got["dq"][q[b]:q[b + 1]] == 0) and torch.all(got["dk"][k[b]:k[b + 1]] == 0)
+    assert torch.any(got["dq"][q[1]:q[2]] != 0) and torch.any(got["dk"][k[1]:k[2]] != 0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_single_state_still_shows_what_is_not_finite(dtype):
+    c = Call([3], [1], 2, 1, 16, dtype, seed=43)
+    c.dout[1, 0, 3] = math.nan
+    got = c.run()
+    assert torch.isnan(got["dq"][1, 0]).all() and torch.isnan(got["dk"]).all()
+    assert torch.all(got["dq"][0] == 0) and torch.all(got["dq"][1, 1] == 0)
+
+
+@pytest.mark.parametrize("nk", [2, 3, 17, 31, 32])
+@pytest.mark.parametrize("nq", [3, 70])
+def test_scores_gradients_add_up_to_zero(nq, nk):
+    """Where all states have one k, dq = scale k sum_j dS_j = 0.  v is the same up to 2^-12, so dS is far
+    smaller than dP and D, whose own roundings (of d products) must drop out of the sum: what may be
+    left of it is (n + 8) u of the terms' sizes, twice (the sum, and its correction's), and what the
+    weights' sum is off 1 of the correction."""
+    d = 64
+    c = Call([nq, nq], [nk, nk], 2, 1, d, F32, seed=nk)
+    c.k[:] = c.k[:1]
+    c.v = 1 + 2.0 ** -12 * c.v
+    got = c.run()
+    c.check(got)
+    scale = c.scale
+    for b in range(2):
+        q = c.q[b * nq:(b + 1) * nq].double()
+        g = c.dout[b * nq:(b + 1) * nq].double()
+        k, v = c.k[b * nk:(b + 1) * nk, 0].double(), c.v[b * nk:(b + 1) * nk, 0].double()
+        dp = g @ v.T                                     # [nq, heads, nk]
+        ds = (dp - dp.mean(2, keepdim=True)).abs().sum(2) / nk
+        dp_err = (d + 1) * U * (g.abs() @ v.abs().T).amax(2)
+        e = (d + 6) * U * scale * (q.abs() @ k[0].abs())
+        eta = 4 * e + (2 * nk + 16) * U
+        bound = 2 * (nk + 8) * U * (ds + 2 * dp_err) + eta * 3 * dp_err
+        tol = 1.1 * scale * bound[:, :, None] * k[0].abs() + 2.0 ** -126
+        assert torch.all(got["dq"][b * nq:(b + 1) * nq].double().abs() <= tol)
