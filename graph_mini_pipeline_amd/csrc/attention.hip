@@ -350,11 +350,11 @@ __global__ __launch_bounds__(kThreads, WK == 1 ? 2 : 1) void k_attend(AttendArgs
     const auto k_row = [&](int i) { return static_cast<uint32_t>(i) * static_cast<uint32_t>(a.ld_k); };
     const auto v_row = [&](int i) { return static_cast<uint32_t>(i) * static_cast<uint32_t>(a.ld_v); };
     Stage<T, DP, BK> sk, sv;
-    const auto load = [&](int64_t at) {
+    const auto load = [&](int64_t at) __attribute__((always_inline)) {
         sk.load(kp + at * a.ld_k, ke - at, a.d, k_row);
         sv.load(vp + at * a.ld_v, ke - at, a.d, v_row);
     };
-    const auto put = [&](Piece<T> *pair, int64_t at) {
+    const auto put = [&](Piece<T> *pair, int64_t at) __attribute__((always_inline)) {
         sk.put(Tl{pair}, ke - at, a.d);
         sv.put(Tl{pair + kPair / 2}, ke - at, a.d);
         __syncthreads();
@@ -554,6 +554,17 @@ __global__ __launch_bounds__(kThreads) void k_attend_stat(AttendArgs a) {
     }
 }
 
+// The bf16 that P and dS are rounded to leaves the gradients sqrt(2) times the error of their own
+// rounding where the sums are long, and more where they are short (over 3 to 66 states 1.5 to 2 times):
+// of a sequence with fewer than kLongSums rows or states, P and dS are multiplied as two bf16, which at
+// 4 x 1024 queries of 16 heads over up to 2600 states would take 579 us in place of 423.  The rule goes by the
+// sequence's own lengths, so their precision does not depend on what else is in the call.
+constexpr int64_t kLongSums = 512;
+template <typename T>
+__device__ __forceinline__ bool short_sums(const Seq &s, int64_t rows) {
+    return sizeof(T) == 2 && (s.nk < kLongSums || rows < kLongSums);
+}
+
 // Over a single state the weight is 1 whatever q and k are: dS is zero.  P (dP - D) would leave the
 // difference of two sums of the same products in other orders, rounding alone, so what dS is multiplied
 // by last is zero there (a dS that is not finite still shows).
@@ -569,8 +580,8 @@ constexpr int dq_groups() {
 
 // Dq of tiles of rows, as the forward kernel's.  Where a sequence's states fit one turn, D, which comes
 // from the rounded out and another order of its sum, is put right by what the row of dS adds up to,
-// which is zero; dk's kernel, which follows, reads it.  LOW (bf16): dS is multiplied as two bf16.
-template <typename T, int DP, int WQ, int WK, bool LOW>
+// which is zero; dk's kernel, which follows, reads it.
+template <typename T, int DP, int WQ, int WK>
 __global__ __launch_bounds__(kThreads, (dq_groups<T, DP, WK>())) void k_attend_dq(AttendArgs a) {
     constexpr int KW = 32, BK = KW * WK, BQ = 32 * WQ, DB = DP / 32;
     typedef Tile<T, DP> Tl;
@@ -599,17 +610,17 @@ __global__ __launch_bounds__(kThreads, (dq_groups<T, DP, WK>())) void k_attend_d
     const auto k_row = [&](int i) { return static_cast<uint32_t>(i) * static_cast<uint32_t>(a.ld_k); };
     const auto v_row = [&](int i) { return static_cast<uint32_t>(i) * static_cast<uint32_t>(a.ld_v); };
     Stage<T, DP, BK> sk, sv;
-    const auto load = [&](int64_t at) {
+    const auto load = [&](int64_t at) __attribute__((always_inline)) {
         sk.load(kp + at * a.ld_k, ke - at, a.d, k_row);
         sv.load(vp + at * a.ld_v, ke - at, a.d, v_row);
     };
-    const auto put = [&](Piece<T> *pair, int64_t at) {
+    const auto put = [&](Piece<T> *pair, int64_t at) __attribute__((always_inline)) {
         sk.put(Tl{pair}, ke - at, a.d);
         sv.put(Tl{pair + kPair / 2}, ke - at, a.d);
         __syncthreads();
     };
-    // (one_turn is a constant: what the short sequences need would cost the others registers)
-    const auto turn = [&](auto one_turn, Piece<T> *pair, Piece<T> *next, int64_t k0) {
+    // (one_turn and low are constants: what the short sequences need would cost the others registers)
+    const auto turn = [&](auto one_turn, auto low, Piece<T> *pair, Piece<T> *next, int64_t k0) __attribute__((always_inline)) {
         const Tl tk{pair}, tv{pair + kPair / 2};
         const int64_t k1 = k0 + BK;
         if (!one_turn.value && k1 < ke) load(k1);
@@ -651,21 +662,26 @@ __global__ __launch_bounds__(kThreads, (dq_groups<T, DP, WK>())) void k_attend_d
         }
         Tu tu;
         stream<Tu::kRing, Tu::kSteps>(turned, column,
-                                      [&](int i, const typename Tu::V &v) { tu.template use<LOW>(dq, v, i, x); });
+                                      [&](int i, const typename Tu::V &v) { tu.template use<low.value>(dq, v, i, x); });
         if (!one_turn.value && k1 < ke) put(next, k1);
     };
     if (kb < ke) {
         load(kb);
         put(smem, kb);
     }
-    if (kb < ke && s.nk <= KW) {
-        turn(std::true_type{}, smem, smem + kPair, kb);
-    } else {
+    typedef std::bool_constant<sizeof(T) == 2> Low;
+    const auto turns = [&](auto low) __attribute__((always_inline)) {
         for (int64_t k0 = kb; k0 < ke; k0 += 2 * BK) {
-            turn(std::false_type{}, smem, smem + kPair, k0);
-            if (k0 + BK < ke) turn(std::false_type{}, smem + kPair, smem, k0 + BK);
+            turn(std::false_type{}, low, smem, smem + kPair, k0);
+            if (k0 + BK < ke) turn(std::false_type{}, low, smem + kPair, smem, k0 + BK);
         }
-    }
+    };
+    if (kb < ke && s.nk <= KW)
+        turn(std::true_type{}, Low{}, smem, smem + kPair, kb);
+    else if (short_sums<T>(s, rows))
+        turns(Low{});
+    else
+        turns(std::false_type{});
     if (WK > 1) {
         constexpr int kRow = DP + 4;
         static_assert((WK - 1) * WQ * 32 * kRow * 4 <= static_cast<int>(sizeof(smem)), "join area");
@@ -719,7 +735,7 @@ __global__ __launch_bounds__(kThreads, (dq_groups<T, DP, WK>())) void k_attend_d
 // reads.)  For fp32, whose
 // operands take twice the registers and whose products take sixteen times as long, one wavefront
 // does both.
-template <typename T, int DP, int SIDES, bool LOW>
+template <typename T, int DP, int SIDES>
 __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArgs a) {
     constexpr int BR = 32, DB = DP / 32;
     typedef Tile<T, DP> Tl;
@@ -765,7 +781,7 @@ __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArg
     // dv's side, which has less to do, brings the tiles
     Stage<T, DP, BR> sq, sg;
     float2 st;
-    const auto load = [&](int64_t r0) {
+    const auto load = [&](int64_t r0) __attribute__((always_inline)) {
         if (!do_v) return;
         // the tile's first query row, and the rows' distances from its first head of the group
         const uint32_t p0 = fast_div(static_cast<uint32_t>(r0), a.by_group);
@@ -780,7 +796,7 @@ __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArg
         const int64_t r = r0 + (threadIdx.x & (BR - 1));
         st = stat[r < re ? r : re - 1];
     };
-    const auto put = [&](int pair, int64_t r0) {
+    const auto put = [&](int pair, int64_t r0) __attribute__((always_inline)) {
         if (do_v) {
             // rows past the end are row 0 again, without weights (zeros would make NaN of states that
             // are not finite)
@@ -793,7 +809,7 @@ __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArg
         }
         __syncthreads();
     };
-    const auto turn = [&](int pair, int64_t r0) {
+    const auto turn = [&](auto low, int pair, int64_t r0) __attribute__((always_inline)) {
         const Tl tq{smem + pair * kPair}, tg{smem + pair * kPair + kPair / 2};
         const int64_t r1 = r0 + BR;
         if (r1 < re) load(r1);
@@ -833,7 +849,7 @@ __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArg
 #pragma unroll
             for (int j = 0; j < 16; ++j) weigh(j);
             stream<Tu::kRing, Tu::kSteps>(turned, column,
-                                          [&](int i, const typename Tu::V &u) { tu.template use<LOW>(dv, u, i, p); });
+                                          [&](int i, const typename Tu::V &u) { tu.template use<low.value>(dv, u, i, p); });
         } else {
             Both pairs[kR];
             prime<kR, 2 * KK>(pairs, both);
@@ -859,11 +875,11 @@ __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArg
             }
             stream<Tu::kRing, kSteps>(turned, column, [&](int i, const typename Tu::V &u) {
                 if (i < kFirst) {
-                    tu.template use<LOW>(dv, u, i, p);
+                    tu.template use<low.value>(dv, u, i, p);
 #pragma unroll
                     for (int j = i * 16 / Tu::kSteps; j < (i + 1) * 16 / Tu::kSteps; ++j) differ(j);
                 } else {
-                    tu.template use<LOW>(dk, u, i - kFirst, ds);
+                    tu.template use<low.value>(dk, u, i - kFirst, ds);
                 }
             });
         }
@@ -873,10 +889,16 @@ __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArg
         load(rb);
         put(0, rb);
     }
-    for (int64_t r0 = rb; r0 < re; r0 += 2 * BR) {
-        turn(0, r0);
-        if (r0 + BR < re) turn(1, r0 + BR);
-    }
+    const auto turns = [&](auto low) __attribute__((always_inline)) {
+        for (int64_t r0 = rb; r0 < re; r0 += 2 * BR) {
+            turn(low, 0, r0);
+            if (r0 + BR < re) turn(low, 1, r0 + BR);
+        }
+    };
+    if (short_sums<T>(s, rows))
+        turns(std::bool_constant<sizeof(T) == 2>{});
+    else
+        turns(std::false_type{});
     if (key >= s.span) return;
     // a state past the count has no gradient
     const int64_t line = kr * a.kv + hk, all = a.n_k * a.kv;
@@ -1027,13 +1049,7 @@ hipError_t forward(AttendArgs a, const Plan &p, hipStream_t s) {
     return hipGetLastError();
 }
 
-// The bf16 that P and dS are rounded to leaves the gradients sqrt(2) times the error of their own
-// rounding where the sums are long, and more where they are short (over 3 to 66 states 1.5 to 2 times):
-// there, where either has fewer than kLongSums terms, P and dS are multiplied as two bf16, which at
-// 4 x 1024 queries of 16 heads over up to 2600 states would take 579 us in place of 423.
-constexpr int64_t kLongSums = 512;
-
-template <typename T, int DP, bool LOW>
+template <typename T, int DP>
 hipError_t backward(AttendArgs a, const Plan &p, hipStream_t s) {
     const unsigned z = static_cast<unsigned>(a.n_seq);
     if (a.n_q > 0)
@@ -1045,9 +1061,9 @@ hipError_t backward(AttendArgs a, const Plan &p, hipStream_t s) {
         a.per = p.per;
         const dim3 grid(static_cast<unsigned>(p.q_tiles), static_cast<unsigned>(a.kv * a.splits), z);
         if (p.few)
-            hipLaunchKernelGGL((k_attend_dq<T, DP, 4 / sharing<T, DP>(), sharing<T, DP>(), LOW>), grid, dim3(kThreads), 0, s, a);
+            hipLaunchKernelGGL((k_attend_dq<T, DP, 4 / sharing<T, DP>(), sharing<T, DP>()>), grid, dim3(kThreads), 0, s, a);
         else
-            hipLaunchKernelGGL((k_attend_dq<T, DP, 4, 1, LOW>), grid, dim3(kThreads), 0, s, a);
+            hipLaunchKernelGGL((k_attend_dq<T, DP, 4, 1>), grid, dim3(kThreads), 0, s, a);
     }
     float *const part_kv = reinterpret_cast<float *>(a.ws + p.part_kv);
     if (a.max_k > 0) {
@@ -1057,7 +1073,7 @@ hipError_t backward(AttendArgs a, const Plan &p, hipStream_t s) {
         b.part = part_kv;
         const dim3 grid(static_cast<unsigned>(p.k_tiles), static_cast<unsigned>(a.kv * b.splits), z);
         constexpr int kSides = sizeof(T) == 2 ? 2 : 1;
-        hipLaunchKernelGGL((k_attend_dkv<T, DP, kSides, LOW>), grid, dim3(kThreads * kSides), 0, s, b);
+        hipLaunchKernelGGL((k_attend_dkv<T, DP, kSides>), grid, dim3(kThreads * kSides), 0, s, b);
     }
     ReduceArgs r{p.per, p.dkv_per, part_kv, a.max_q > 0 && p.splits > 1, a.max_k > 0 && p.dkv_splits > 1};
     if (r.dq || r.dkv) {
@@ -1069,13 +1085,6 @@ hipError_t backward(AttendArgs a, const Plan &p, hipStream_t s) {
                            dim3(kThreads), 0, s, a, r);
     }
     return hipGetLastError();
-}
-
-template <typename T, int DP>
-hipError_t backward(const AttendArgs &a, const Plan &p, hipStream_t s) {
-    if (sizeof(T) == 2 && (a.max_q * a.group < kLongSums || a.max_k < kLongSums))
-        return backward<T, DP, sizeof(T) == 2>(a, p, s);
-    return backward<T, DP, false>(a, p, s);
 }
 
 template <typename T>

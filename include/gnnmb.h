@@ -567,7 +567,9 @@ gnn_status gnn_embedding_grad_rows(const int32_t *ids, const int64_t *d_n, int64
  *   hold.
  *   q, out: [n_q, ld] with heads * head_dim elements a row; k, v: [n_k, ld] with kv_heads * head_dim;
  *   type GNN_F32 or GNN_BF16 (products and sums in fp32; for GNN_BF16 the weights exp(S - lse) are
- *   rounded to bf16 before they multiply v).  lse: float [n_q, heads], may be NULL for
+ *   rounded to bf16 before they multiply v; in the backward pass they and the gradients of S are taken as
+ *   one bf16, or as two for a sequence with fewer than 512 states or 512 queries times heads /
+ *   kv_heads).  lse: float [n_q, heads], may be NULL for
  *   gnn_cross_attention.  max_q, max_k: host bounds on a sequence's queries and state rows.
  *   Rows that belong to no sequence are left as they are.
  * gnn_cross_attention_backward: with out and lse of the forward call and dout [n_q, ld_dout], writes

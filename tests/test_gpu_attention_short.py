@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_attention import BF16, F32, U, Call, indptr
+from tests.test_gpu_attention import BF16, F32, U, Call, formulas, indptr
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +71,60 @@ def test_scores_gradients_add_up_to_zero(nq, nk):
         bound = 2 * (nk + 8) * U * (ds + 2 * dp_err) + eta * 3 * dp_err
         tol = 1.1 * scale * bound[:, :, None] * k[0].abs() + 2.0 ** -126
         assert torch.all(got["dq"][b * nq:(b + 1) * nq].double().abs() <= tol)
+
+
+def short_formulas(q, k, v, dout, scale):
+    """{name: (value, bound before the last rounding)} of one sequence's gradients in bf16 where P and dS
+    are multiplied as two bf16 (2^-8 of 2^-8 off): as formulas(), with D from the stored out, or over
+    up to 32 states from P dP itself."""
+    n, d = k.shape
+    m = q.shape[0]
+    forward = formulas(q, k, v, None, scale, 2.0 ** -8)
+    out, out_err = forward["out"]
+    lse_err = forward["lse"][1][:, None]
+    s = scale * (q @ k.T)
+    size = abs(scale) * (q.abs() @ k.abs().T)
+    p = torch.softmax(s, 1)
+    r = 2.0 ** -16
+    eta = 2 * (d + 6) * U * size.amax(1, keepdim=True) + (n + 8) * U + lse_err
+    dp, dp_err = dout @ v.T, (d + 1) * U * (dout.abs() @ v.abs().T)
+    dd = (p * dp).sum(1, keepdim=True)
+    ds = p * (dp - dd)
+    dd_err = (dout.abs() * (out_err + out.abs() * (2.0 ** -8 + U))).sum(1, keepdim=True) + \
+        (d + 1) * U * (dout * out).abs().sum(1, keepdim=True)
+    if n <= 32:
+        dd_err = (p * dp_err).sum(1, keepdim=True) + U * dd.abs() + \
+            (eta + (n + 2) * U) * (ds.abs().sum(1, keepdim=True) + dd_err)
+    ds_err = (eta + r + 3 * U) * ds.abs() + p * (dp_err + dd_err) + 2.0 ** -126
+    p_err = (eta + r) * p + 2.0 ** -126
+    a = abs(scale)
+    return {"dq": (scale * ds @ k, 1.1 * a * (ds_err @ k.abs() + (n + 2) * U * (ds.abs() @ k.abs()))),
+            "dk": (scale * ds.T @ q, 1.1 * a * (ds_err.T @ q.abs() + (m + 2) * U * (ds.abs().T @ q.abs()))),
+            "dv": (p.T @ dout, 1.1 * (p_err.T @ dout.abs() + (m + 2) * U * (p.T @ dout.abs())))}
+
+
+@pytest.mark.parametrize("d", [32, 80, 128])
+@pytest.mark.parametrize("nq,nk,heads,kv,max_k", [
+    ([3, 40, 600, 9, 300], [5, 60, 700, 300, 31], 4, 2, None),      # beside a long sequence
+    ([300] * 40, [31, 2, 17, 32, 7] * 8, 4, 2, 10_000),             # under a loose bound
+    ([130] * 20 + [700], [45, 3, 66, 32, 12] * 4 + [520], 32, 16, None)])
+def test_precision_goes_by_the_sequence_itself(nq, nk, heads, kv, max_k, d):
+    """The gradients of a sequence of few rows or states carry two bf16 of P and dS, whatever else is in
+    the call and however loose its bounds are."""
+    c = Call(nq, nk, heads, kv, d, BF16, seed=d)
+    got = c.run(max_k=max_k)
+    c.check(got)
+    group, scale = heads // kv, float(torch.tensor(c.scale, dtype=F32))
+    q, k = indptr(nq).tolist(), indptr(nk).tolist()
+    for b in range(len(nq)):
+        if nk[b] >= 512 and nq[b] * group >= 512:
+            continue
+        i, j = slice(q[b], q[b + 1]), slice(k[b], k[b + 1])
+        for h in range(kv):
+            rows = lambda t: t[i, h * group:(h + 1) * group].double().reshape(-1, d)
+            ref = short_formulas(rows(c.q), c.k[j, h].double(), c.v[j, h].double(), rows(c.dout), scale)
+            for name, (want, bound) in ref.items():
+                have = rows(got[name]) if name == "dq" else got[name][j, h].double()
+                tol = bound + 2.0 ** -8 * (want.abs() + bound)
+                bad = ~((have - want).abs() <= tol)
+                assert not bad.any(), (b, h, name, int(bad.sum()), float((have - want).abs().max()))
