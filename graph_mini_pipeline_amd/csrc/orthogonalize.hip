@@ -8,10 +8,15 @@
 //
 // Numbers.  The products run on the 16-bit matrix instructions with fp32 accumulation.  X, A and Q
 // are stored in fp16, times 2^12: the singular values stay below 3 (newton_in_range), so that
-// every entry fits, and entries down to 2^-26 keep fp16's 11 bits.  For a bf16 update one fp16 plane
-// carries eight times the precision of the result's type; the fp32 update, and some long matrices, take two
-// planes, x = hi + lo (22 bits), and three matrix products, hi hi + hi lo + lo hi (all four for small
-// matrices); the dropped product is below 2^-22 of a term.  The first X is G times a power of two, so
+// every entry fits, and entries down to 2^-26 keep fp16's 11 bits.  A bf16 update takes one fp16 plane, eight
+// times the precision of its own entries (directions below 2^-9 of the strongest are as much its own
+// rounding as the update), and what the plane leaves of the diagonals of A and Q, in fp32.  Those are
+// often alike, and one rounding common to all of them scales the whole result, by up to half a step of
+// bf16 (400 x 4000 orthonormal rows: 1.8e-3 of it; the diagonals' rest brings the error from 1.9 times the
+// result's own rounding to 1.05, and is 1.14 at most over Gaussian, orthonormal and low-rank updates of
+// 3 to 700 rows); the other entries' roundings are of either sign.  The fp32 update takes two planes,
+// x = hi + lo (22 bits), and three matrix products, hi hi + hi lo + lo hi (all four for small matrices);
+// the dropped product is below 2^-22 of a term.  The first X is G times a power of two, so
 // nothing is rounded that need not be, and the rest of 1 / (|G|_F + eps) multiplies the first A and the
 // first Q X.
 //
@@ -21,9 +26,9 @@
 // that reaches beyond them repeats their last row and stores nothing there.
 //
 // What bounds it.  Large squares: LDS reads and the tiles' way into it next to the matrix units: five
-// steps of 4096 x 4096 bf16 in 1.57 ms, 870 TFLOP/s of the needed operations (a library product reaches
+// steps of 4096 x 4096 bf16 in 1.62 ms, 850 TFLOP/s of the needed operations (a library product reaches
 // 1050 to 1150 at this size).  Two planes: 2 x 2571 x 1030 fp32 720 us, three products for one.  Small ones:
-// the chain of three products a step; 256 x 256 fp32 takes 116 us in 17 launches of about 7 us each, of
+// the chain of three products a step; 256 x 256 fp32 takes 114 us in 17 launches of about 7 us each, of
 // which 2.6 are the launch's own, 0.7 the first load and 0.9 the stores.
 #include <math.h>
 
@@ -60,6 +65,10 @@ struct ProductArgs {
     int32_t what;
     float ca, cb, cc;            // kPoly
     const float *first;          // [batch] factor of X in the first step, NULL: 1
+    // one plane: [batch][ld_rest] what the planes leave of the diagonals (times 2^12): of A, written by
+    // kGram and read by kPoly, and of Q, written by kPoly and read by the last product
+    float *rest_a, *rest_q;
+    int64_t ld_rest;
     // kLast
     void *out;
     int64_t ld_out, batch_out;
@@ -221,9 +230,11 @@ __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void k_newton_product
         __syncthreads();
     };
 #pragma unroll
-    for (int u = 0; u < kDepth; ++u)
+    for (int u = 0; u < kDepth; ++u) {
 #pragma unroll
         for (int r = 0; r < kPieces; ++r) load(u, u, r);
+        __builtin_amdgcn_sched_barrier(0);      // in this order: the first tile is waited for alone
+    }
 #pragma unroll
     for (int r = 0; r < kPieces; ++r) store(0, 0, r);
     __syncthreads();
@@ -255,6 +266,30 @@ __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void k_newton_product
             }
     };
     const float first = p.first ? p.first[z] : 1.f;
+    float *rest_a = nullptr, *rest_q = nullptr;
+    if constexpr (PL == 1) {
+        rest_a = p.rest_a + z * p.ld_rest;
+        rest_q = p.rest_q + z * p.ld_rest;
+        if (!symmetric) {
+            // X^T Q (a holds X^T): what Q's plane leaves of its diagonal, times X itself.  All loads before any
+            // store.
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                const int n = tn * TILE + (wn * TM + j) * 32 + row;
+                if (n >= p.rows_b) continue;
+                const float rest = rest_q[n];
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const int m0 = tm * TILE + (wm * TM + i) * 32 + 4 * half;
+                    if (m0 >= p.rows_a) continue;
+                    const f16 *x = ga + m0 * p.ld_a + n;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        acc[i][j][e] += rest * static_cast<float>(x[(8 * (e >> 2) + (e & 3)) * p.ld_a]);
+                }
+            }
+        }
+    }
     if (p.what == kLast) {
         const float factor = kDown * kDown * first * p.scale;
         TO *out = static_cast<TO *>(p.out) + z * p.batch_out;
@@ -276,7 +311,7 @@ __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void k_newton_product
     char *const pc = reinterpret_cast<char *>(p.c + z * p.batch_c);
     char *const pt = reinterpret_cast<char *>(p.t + z * p.batch_t);
     const uint32_t ld_c = static_cast<uint32_t>(p.ld_c), ld_t = static_cast<uint32_t>(p.ld_t);
-    const auto keep = [&](int m, int n, vec<float, 4> v) {
+    const auto keep = [&](int m, int n, vec<float, 4> v, float *rest) {
         const uint32_t oc = 2 * (m * ld_c + n), ot = 2 * (n * ld_t + m);
 #pragma unroll
         for (int q = 0; q < PL; ++q) {
@@ -287,12 +322,32 @@ __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void k_newton_product
             if (mirror) *reinterpret_cast<vec<f16, 4> *>(pt + 2 * q * p.plane_t + ot) = x;
             v -= __builtin_convertvector(x, vec<float, 4>);
         }
+        if (PL == 1 && rest != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (m + e == n) rest[n] = v[e];
+        }
     };
     if (p.what == kPoly) {
         // the product's operand is A itself, A[n][m..] = A[m..][n]
         const char *const old = reinterpret_cast<const char *>(p.a + z * p.batch_a);
         const uint32_t ld_a = static_cast<uint32_t>(p.ld_a);
         every([&](int m, int n, vec<float, 4> v) {
+            if constexpr (PL == 1) {
+                // (A + R)^2 = A^2 + R A + A R + R^2, R being the diagonal's rest
+                const vec<f16, 4> x = *reinterpret_cast<const vec<f16, 4> *>(old + 2 * (n * ld_a + m));
+                const float rn = rest_a[n];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float rm = rest_a[m + e], y = static_cast<float>(x[e]);
+                    v[e] += (rm + rn) * y;
+                    if (m + e == n) v[e] += rn * rn;
+                    v[e] = v[e] * (kDown * p.cc) + p.cb * y;
+                    if (m + e == n) v[e] += p.cb * rn + p.ca * kUp;
+                }
+                keep(m, n, v, rest_q);
+                return;
+            }
             vec<Poly, 4> u = __builtin_convertvector(v, vec<Poly, 4>) * static_cast<Poly>(kDown * p.cc);
 #pragma unroll
             for (int q = 0; q < PL; ++q) {
@@ -303,11 +358,12 @@ __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void k_newton_product
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (m + e == n) u[e] += static_cast<Poly>(p.ca * kUp);
-            keep(m, n, __builtin_convertvector(u, vec<float, 4>));
+            keep(m, n, __builtin_convertvector(u, vec<float, 4>), nullptr);
         });
     } else {
         const float factor = kDown * first * (p.what == kGram ? first : 1.f);
-        every([&](int m, int n, vec<float, 4> v) { keep(m, n, v * factor); });
+        float *const rest = p.what == kGram ? rest_a : nullptr;
+        every([&](int m, int n, vec<float, 4> v) { keep(m, n, v * factor, rest); });
     }
 }
 
@@ -403,7 +459,7 @@ __global__ __launch_bounds__(kNormThreads) void k_first_planes(PrepArgs p) {
 
 struct NewtonSpace {
     f16 *x, *xt[2], *a, *q;
-    float *first;
+    float *first, *rest_a, *rest_q;      // (rests: [batch][s])
     double *partial;
     int64_t s, l;           // padded
     int64_t plane_x, plane_a;
@@ -434,20 +490,9 @@ int32_t tile_for(int64_t rows_a, int64_t rows_b, int64_t batch, bool symmetric, 
     return best;
 }
 
-// One plane for a bf16 update, unless the matrix is long and of some 200 rows: there A is nearly a
-// multiple of I, most of its eigenvalues being alike, and the rounding of Q's diagonal, the same in all
-// of it, scales the whole result.  With one plane the result is off, in units of its own rounding, by 1.41
-// at 6 x 223 columns, 1.53 at 11 x 223 and 1.45 at 16 x 256, and by 1.1 to 1.3 at fewer than 6 squares and
-// with fewer than 160 or more than 320 rows, where the steps pass by other values; with two by 1.0, in
-// twice the time (2 x 2368 x 223: 257 us for 130).
-int32_t planes_for(int64_t rows, int64_t cols, int32_t type) {
-    const int64_t s = rows < cols ? rows : cols, l = rows < cols ? cols : rows;
-    return type == GNN_F32 || (l >= 6 * s && s >= 160 && s <= 320) ? 2 : 1;
-}
-
 NewtonSpace carve_newton(int64_t rows, int64_t cols, int64_t batch, int32_t type, char *base) {
     NewtonSpace n{};
-    n.planes = planes_for(rows, cols, type);
+    n.planes = type == GNN_F32 ? 2 : 1;
     const int64_t s = rows < cols ? rows : cols, l = rows < cols ? cols : rows;
     n.s = (s + 63) / 64 * 64;
     n.l = (l + 63) / 64 * 64;
@@ -469,6 +514,9 @@ NewtonSpace carve_newton(int64_t rows, int64_t cols, int64_t batch, int32_t type
     n.q = reinterpret_cast<f16 *>(take(a));
     n.partial = reinterpret_cast<double *>(take(static_cast<size_t>(batch) * kNormBlocks * 8));
     n.first = reinterpret_cast<float *>(take(static_cast<size_t>(batch) * 4));
+    const size_t rest = n.planes == 1 ? static_cast<size_t>(batch * n.s) * 4 : 0;
+    n.rest_a = reinterpret_cast<float *>(take(rest));
+    n.rest_q = reinterpret_cast<float *>(take(rest));
     n.bytes = off;
     return n;
 }
@@ -540,6 +588,9 @@ hipError_t run_newton(const NewtonArgs &a, hipStream_t s) {
         g.batch_c = g.batch_t = ba;
         g.rows_a = g.rows_b = static_cast<int32_t>(n.s);
         g.first = first;
+        g.rest_a = n.rest_a;
+        g.rest_q = n.rest_q;
+        g.ld_rest = n.s;
         err = launch_product<PL, T>(g, a.batch, s);
         if (err != hipSuccess) return err;
         ProductArgs q = g;
@@ -574,6 +625,9 @@ hipError_t run_newton(const NewtonArgs &a, hipStream_t s) {
         y.rows_a = static_cast<int32_t>(n.l);
         y.rows_b = static_cast<int32_t>(n.s);
         y.first = first;
+        y.rest_a = n.rest_a;
+        y.rest_q = n.rest_q;
+        y.ld_rest = n.s;
         y.out = a.out;
         y.ld_out = a.ld_out;
         y.batch_out = a.batch_out;
@@ -623,8 +677,7 @@ bool newton_in_range(const float *coefs, int steps) {
 }
 
 hipError_t launch_newton(const NewtonArgs &a, hipStream_t s) {
-    if (a.type == GNN_F32) return run_newton<2, float>(a, s);
-    return planes_for(a.rows, a.cols, a.type) == 2 ? run_newton<2, bf16>(a, s) : run_newton<1, bf16>(a, s);
+    return a.type == GNN_F32 ? run_newton<2, float>(a, s) : run_newton<1, bf16>(a, s);
 }
 
 }  // namespace gnnmb

@@ -620,7 +620,9 @@ gnn_status gnn_cross_attention_backward(const gnn_attention *x, const gnn_attent
  * in five steps.  coefs: host [3].
  *   g, out: device, batch matrices [rows, ld] with stride elements from one to the next, of type
  *     GNN_F32 or GNN_BF16; out may be g.  Sums are fp32; the products carry 22 bits of X for
- *     GNN_F32 and 11 for GNN_BF16.  A zero update gives zeros; one that is not finite gives NaN.
+ *     GNN_F32 and 11 for GNN_BF16 (24 on the diagonals of A and of the factor of X): of a bf16 update the
+ *     directions below 2^-9 of the strongest are its own rounding, and what those are taken to is off by
+ *     some 2%.  A zero update gives zeros; one that is not finite gives NaN.
  *     Entries are kept relative to max(1, eps / |G|_F): precision falls where |G|_F < eps / 256.
  *   ws: ws_bytes >= gnn_orthogonalize_workspace_size(batch, rows, cols, type).
  * Errors: GNN_ERR_INVALID_ARG; GNN_ERR_CAPACITY (ws too small); GNN_ERR_UNSUPPORTED for another
