@@ -331,7 +331,7 @@ __global__ __launch_bounds__(kThreads, WK == 1 ? 2 : 1) void k_attend(AttendArgs
     __shared__ Piece<T> smem[2 * kPair];
     const Seq s = sequence(a, blockIdx.z);
     const int hk = static_cast<int>(blockIdx.y) / a.splits, split = static_cast<int>(blockIdx.y) % a.splits;
-    const int64_t rows = s.nq * a.group, r0 = static_cast<int64_t>(blockIdx.x) * BQ;
+    const int64_t rows = s.nq * a.group, r0 = (a.first_block + blockIdx.x) * BQ;
     if (r0 >= rows || split >= parts_of(s.nk, a.per)) return;      // whole workgroup
     int64_t kb, ke;
     part_range(s.nk, a.per, split, BK, kb, ke);
@@ -534,7 +534,7 @@ __device__ __forceinline__ int64_t stat_at(const AttendArgs &a, int64_t pos, int
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_attend_stat(AttendArgs a) {
     // eight lanes a row, 16 columns a lane
-    const int64_t line = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x >> 3);
+    const int64_t line = (a.first_block + blockIdx.x) * 32 + (threadIdx.x >> 3);
     if (line >= a.n_q * a.heads) return;
     const int64_t pos = line / a.heads, head = line - pos * a.heads;
     const T *o = static_cast<const T *>(a.out) + pos * a.ld_out + head * a.d;
@@ -590,7 +590,7 @@ __global__ __launch_bounds__(kThreads, (dq_groups<T, DP, WK>())) void k_attend_d
     __shared__ Piece<T> smem[2 * kPair];
     const Seq s = sequence(a, blockIdx.z);
     const int hk = static_cast<int>(blockIdx.y) / a.splits, split = static_cast<int>(blockIdx.y) % a.splits;
-    const int64_t rows = s.nq * a.group, r0 = static_cast<int64_t>(blockIdx.x) * BQ;
+    const int64_t rows = s.nq * a.group, r0 = (a.first_block + blockIdx.x) * BQ;
     if (r0 >= rows || split >= parts_of(s.nk, a.per)) return;      // whole workgroup
     int64_t kb, ke;
     part_range(s.nk, a.per, split, BK, kb, ke);
@@ -746,7 +746,7 @@ __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArg
     __shared__ Piece<T> own[SIDES == 2 ? Tl::pieces(128) : 1];     // the states' v rows (dk's side)
     const Seq s = sequence(a, blockIdx.z);
     const int hk = static_cast<int>(blockIdx.y) / a.splits, split = static_cast<int>(blockIdx.y) % a.splits;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * 128;
+    const int64_t c0 = (a.first_block + blockIdx.x) * 128;
     const int64_t rows = s.nq * a.group;
     if (c0 >= s.span || split >= parts_of(rows, a.per)) return;      // whole workgroup
     int64_t rb, re;
@@ -1031,50 +1031,61 @@ Plan plan_for(const AttendArgs &a, bool backward) {
     return p;
 }
 
+#define TRY_LAUNCH(call)                       \
+    do {                                       \
+        const hipError_t err = (call);         \
+        if (err != hipSuccess) return err;     \
+    } while (0)
+
 template <typename T, int DP>
 hipError_t forward(AttendArgs a, const Plan &p, hipStream_t s) {
     a.splits = p.splits;
     a.per = p.per;
-    const dim3 grid(static_cast<unsigned>(p.q_tiles), static_cast<unsigned>(a.kv * p.splits),
-                    static_cast<unsigned>(a.n_seq));
-    if (p.few)
-        hipLaunchKernelGGL((k_attend<T, DP, 4 / sharing<T, DP>(), sharing<T, DP>()>), grid, dim3(kThreads), 0, s, a);
-    else
-        hipLaunchKernelGGL((k_attend<T, DP, 4, 1>), grid, dim3(kThreads), 0, s, a);
+    const unsigned y = static_cast<unsigned>(a.kv * p.splits), z = static_cast<unsigned>(a.n_seq);
+    TRY_LAUNCH(launch_pieces(p.q_tiles, kThreads, [&](int64_t first, unsigned x) {
+        a.first_block = first;
+        if (p.few)
+            hipLaunchKernelGGL((k_attend<T, DP, 4 / sharing<T, DP>(), sharing<T, DP>()>), dim3(x, y, z),
+                               dim3(kThreads), 0, s, a);
+        else
+            hipLaunchKernelGGL((k_attend<T, DP, 4, 1>), dim3(x, y, z), dim3(kThreads), 0, s, a);
+    }));
+    // (a call with splits has few tiles, and so few rows)
     if (p.splits > 1)
         hipLaunchKernelGGL((k_attend_combine<T>),
-                           dim3(static_cast<unsigned>(ceil_div(a.max_q * a.heads, 4)),
-                                static_cast<unsigned>(a.n_seq)),
-                           dim3(kThreads), 0, s, a);
+                           dim3(static_cast<unsigned>(ceil_div(a.max_q * a.heads, 4)), z), dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }
 
+// Each kernel reads what the one before left: none is enqueued after one that failed.
 template <typename T, int DP>
 hipError_t backward(AttendArgs a, const Plan &p, hipStream_t s) {
     const unsigned z = static_cast<unsigned>(a.n_seq);
-    if (a.n_q > 0)
-        hipLaunchKernelGGL((k_attend_stat<T>),
-                           dim3(static_cast<unsigned>(ceil_div(a.n_q * a.heads, 32))),
-                           dim3(kThreads), 0, s, a);
-    if (a.max_q > 0) {
-        a.splits = p.splits;
-        a.per = p.per;
-        const dim3 grid(static_cast<unsigned>(p.q_tiles), static_cast<unsigned>(a.kv * a.splits), z);
+    TRY_LAUNCH(launch_pieces(ceil_div(a.n_q * a.heads, 32), kThreads, [&](int64_t first, unsigned x) {
+        a.first_block = first;
+        hipLaunchKernelGGL((k_attend_stat<T>), dim3(x), dim3(kThreads), 0, s, a);
+    }));
+    a.splits = p.splits;
+    a.per = p.per;
+    TRY_LAUNCH(launch_pieces(p.q_tiles, kThreads, [&](int64_t first, unsigned x) {
+        a.first_block = first;
+        const dim3 grid(x, static_cast<unsigned>(a.kv * a.splits), z);
         if (p.few)
             hipLaunchKernelGGL((k_attend_dq<T, DP, 4 / sharing<T, DP>(), sharing<T, DP>()>), grid, dim3(kThreads), 0, s, a);
         else
             hipLaunchKernelGGL((k_attend_dq<T, DP, 4, 1>), grid, dim3(kThreads), 0, s, a);
-    }
+    }));
     float *const part_kv = reinterpret_cast<float *>(a.ws + p.part_kv);
-    if (a.max_k > 0) {
-        AttendArgs b = a;
-        b.splits = p.dkv_splits;
-        b.per = p.dkv_per;
-        b.part = part_kv;
-        const dim3 grid(static_cast<unsigned>(p.k_tiles), static_cast<unsigned>(a.kv * b.splits), z);
-        constexpr int kSides = sizeof(T) == 2 ? 2 : 1;
-        hipLaunchKernelGGL((k_attend_dkv<T, DP, kSides>), grid, dim3(kThreads * kSides), 0, s, b);
-    }
+    AttendArgs b = a;
+    b.splits = p.dkv_splits;
+    b.per = p.dkv_per;
+    b.part = part_kv;
+    constexpr int kSides = sizeof(T) == 2 ? 2 : 1;
+    TRY_LAUNCH(launch_pieces(p.k_tiles, kThreads * kSides, [&](int64_t first, unsigned x) {
+        b.first_block = first;
+        hipLaunchKernelGGL((k_attend_dkv<T, DP, kSides>), dim3(x, static_cast<unsigned>(a.kv * b.splits), z),
+                           dim3(kThreads * kSides), 0, s, b);
+    }));
     ReduceArgs r{p.per, p.dkv_per, part_kv, a.max_q > 0 && p.splits > 1, a.max_k > 0 && p.dkv_splits > 1};
     if (r.dq || r.dkv) {
         const int64_t fq = r.dq ? a.max_q * a.heads * (a.d / 4) : 0;

@@ -33,7 +33,7 @@ constexpr int kLookUnroll = 4;
 template <typename TI, typename TO, int VE>
 __global__ __launch_bounds__(kLookThreads) void k_embedding_lookup(LookupArgs a) {
     const int64_t n = load_count(a.d_n, a.n);
-    const int64_t base = static_cast<int64_t>(blockIdx.x) * (kLookThreads * kLookUnroll);
+    const int64_t base = (a.first_block + blockIdx.x) * (kLookThreads * kLookUnroll);
     const int64_t row0 = base / a.cpr;
     if (row0 >= n) return;
     const uint32_t rem = static_cast<uint32_t>(base - row0 * a.cpr);
@@ -73,10 +73,10 @@ hipError_t run_lookup(LookupArgs a, hipStream_t s) {
     a.cpr = static_cast<uint32_t>((a.d + VE - 1) / VE);
     a.by_cpr = make_fastdiv(a.cpr);
     const int64_t per = kLookThreads * kLookUnroll;
-    const int64_t grid = (a.n * a.cpr + per - 1) / per;
-    hipLaunchKernelGGL((k_embedding_lookup<TI, TO, VE>), dim3(static_cast<unsigned>(grid)),
-                       dim3(kLookThreads), 0, s, a);
-    return hipGetLastError();
+    return launch_pieces((a.n * a.cpr + per - 1) / per, kLookThreads, [&](int64_t first, unsigned blocks) {
+        a.first_block = first;
+        hipLaunchKernelGGL((k_embedding_lookup<TI, TO, VE>), dim3(blocks), dim3(kLookThreads), 0, s, a);
+    });
 }
 
 template <typename TI, typename TO>

@@ -29,6 +29,19 @@ __device__ __forceinline__ void store_f32(T *p, vec<float, N> v) {
     *reinterpret_cast<typename loose<T, N>::type *>(p) = __builtin_convertvector(v, vec<T, N>);
 }
 
+// A grid has fewer than 2^32 threads a dimension: launch(first, blocks) enqueues `blocks` workgroups of
+// `threads` from the first on, in as many pieces as that takes (one, but for calls of gigabytes).
+template <typename F>
+hipError_t launch_pieces(int64_t blocks, int threads, F launch) {
+    const int64_t most = (int64_t(1) << 31) / threads;
+    for (int64_t first = 0; first < blocks; first += most) {
+        launch(first, static_cast<unsigned>(blocks - first < most ? blocks - first : most));
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+}
+
 // ---- embedding ----------------------------------------------------------------------------------
 
 struct LookupArgs {
@@ -45,6 +58,7 @@ struct LookupArgs {
     int32_t *status;
     uint32_t cpr;       // vectors per row (set by the launcher, with its divisor)
     FastDiv by_cpr;
+    int64_t first_block;
 };
 hipError_t launch_embedding_lookup(LookupArgs a, hipStream_t s);
 
@@ -93,6 +107,7 @@ struct AttendArgs {
     int64_t ld_dq, ld_dk, ld_dv;
     // set by the launcher
     FastDiv by_group;
+    int64_t first_block;
     int32_t splits;
     int64_t per;           // states (or rows) per split
     char *ws;
