@@ -56,10 +56,16 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without a Stream object around it (3 us of a short call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        # the current stream's handle without a Stream object around it (3 us of a short call)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+        device = torch.cuda.current_device()      # initialises the device, or says why it cannot
+        if _raw_stream is not None:
+            return ctypes.c_void_p(_raw_stream(device))
+        stream = torch.cuda.current_stream(device)
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
