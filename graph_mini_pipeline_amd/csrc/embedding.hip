@@ -54,8 +54,9 @@ __global__ __launch_bounds__(kLookThreads) void k_embedding_lookup(LookupArgs a)
         if (col[u] > a.d - VE) col[u] = a.d - VE;
         const int32_t id = a.ids[row[u] < n ? row[u] : n - 1];
         const bool good = id >= 0 && id < a.num_rows;
-        live[u] = good && id != a.pad_id;
-        if (!good && row[u] < n) set_status(a.status, GNN_ERR_OUT_OF_RANGE);
+        const bool pad = id >= 0 && id == a.pad_id;      // (which may lie outside the table)
+        live[u] = good && !pad;
+        if (!good && !pad && row[u] < n) set_status(a.status, GNN_ERR_OUT_OF_RANGE);
         v[u] = *reinterpret_cast<const typename loose<TI, VE>::type *>(
             table + static_cast<int64_t>(good ? id : 0) * a.ld + col[u]);
     }
@@ -136,12 +137,12 @@ struct SortArgs {
 
 // The key of position i, which holds id.
 __device__ __forceinline__ uint32_t make_key(const SortArgs &a, int64_t i, int64_t n_act, int32_t id) {
-    if (i >= n_act) return a.num_rows;
+    if (i >= n_act || (id >= 0 && id == a.pad_id)) return a.num_rows;
     if (id < 0 || static_cast<uint32_t>(id) >= a.num_rows) {
         set_status(a.status, GNN_ERR_OUT_OF_RANGE);
         return a.num_rows;
     }
-    return id == a.pad_id ? a.num_rows : static_cast<uint32_t>(id);
+    return static_cast<uint32_t>(id);
 }
 
 // Clears the marks and the number of long runs; the grid's threads share the work.

@@ -511,11 +511,11 @@ gnn_status gnn_minibatch(const gnn_graph *g, const gnn_feature_store *fs, const 
 /*
  * Embedding lookup with scaling (learned node or token vectors; the gather of a table that is
  * trained): out[i, 0..d) = scale * table[ids[i], 0..d), i < n, computed in fp32 and rounded once to
- * out's type.  ids[i] = pad_id (pad_id >= 0; -1: none) gives a zero row.
+ * out's type.  ids[i] = pad_id (pad_id >= 0, in the table or not; -1: none) gives a zero row.
  *   table: device [num_rows, ld], out: device [n, ld_out], types GNN_F32 or GNN_BF16 (any pair);
  *   rows may start at any multiple of their element; out must not overlap table.
  *   n and d_n as in gnn_gather_features: rows at or past *d_n are left as they are.
- * Device errors: GNN_ERR_OUT_OF_RANGE (an id outside [0, num_rows); its row is zero), written to
+ * Device errors: GNN_ERR_OUT_OF_RANGE (another id outside [0, num_rows); its row is zero), written to
  * *d_status if not NULL.
  * Errors: GNN_ERR_INVALID_ARG; GNN_ERR_UNSUPPORTED for another type, n or num_rows over 2^31 - 1,
  * d over 2^24 or n * d over 2^40.
@@ -537,7 +537,7 @@ gnn_status gnn_embedding_lookup(const void *table, int32_t table_type, int64_t n
  *     grad[p, 0..d) the row of uniq[p]; nothing is written at or past U or uniq_cap.
  *   dout: device [n, ld_dout]; types GNN_F32 or GNN_BF16 (any pair).  grad must not overlap dout.
  *   ws: ws_bytes >= gnn_embedding_grad_workspace_size(n, num_rows, d).
- * Device errors (in *d_status if not NULL): GNN_ERR_OUT_OF_RANGE (an id outside [0, num_rows), which
+ * Device errors (in *d_status if not NULL): GNN_ERR_OUT_OF_RANGE (another id outside [0, num_rows), which
  * then adds nothing), GNN_ERR_CAPACITY (U > uniq_cap; *d_n_uniq still holds U).
  * Errors: as gnn_embedding_lookup; GNN_ERR_CAPACITY when ws is too small.
  */
