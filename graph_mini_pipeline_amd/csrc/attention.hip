@@ -798,10 +798,10 @@ __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArg
     };
     const auto put = [&](int pair, int64_t r0) __attribute__((always_inline)) {
         if (do_v) {
-            // rows past the end are row 0 again, without weights (zeros would make NaN of states that
-            // are not finite)
+            // rows past the end are row 0's q again, without weights (zeros would make NaN of states
+            // that are not finite), and zeros of dout (row 0's would make NaN of its infinities)
             sq.put(Tl{smem + pair * kPair}, BR, a.d);
-            sg.put(Tl{smem + pair * kPair + kPair / 2}, BR, a.d);
+            sg.put(Tl{smem + pair * kPair + kPair / 2}, re - r0, a.d);
             if (threadIdx.x < BR) {
                 sstat[pair][0][threadIdx.x] = r0 + threadIdx.x < re ? st.x : INFINITY;
                 sstat[pair][1][threadIdx.x] = st.y;

@@ -574,7 +574,7 @@ gnn_status gnn_embedding_grad_rows(const int32_t *ids, const int64_t *d_n, int64
  *   Rows that belong to no sequence are left as they are.
  * gnn_cross_attention_backward: with out and lse of the forward call and dout [n_q, ld_dout], writes
  * dq, dk, dv of the same shapes (dk and dv zero for states that do not count), each summed in fp32
- * in a fixed order and rounded once.  No output may overlap an input or another output.
+ * in a fixed order and rounded once.  What is not finite in dout makes what it enters not finite.  No output may overlap an input or another output.
  *   ws: ws_bytes >= gnn_cross_attention_workspace_size(x, backward); x->type, heads, kv_heads,
  *   head_dim, n_seq, n_q, n_k, max_q and max_k decide it.
  * Device errors (in *d_status if not NULL): GNN_ERR_OUT_OF_RANGE (an indptr that decreases or

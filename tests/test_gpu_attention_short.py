@@ -128,3 +128,21 @@ def test_precision_goes_by_the_sequence_itself(nq, nk, heads, kv, max_k, d):
                 tol = bound + 2.0 ** -8 * (want.abs() + bound)
                 bad = ~((have - want).abs() <= tol)
                 assert not bad.any(), (b, h, name, int(bad.sum()), float((have - want).abs().max()))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("nq", [1, 5, 33, 64, 70])
+def test_infinite_gradients_of_the_output(nq, dtype):
+    """dv = P^T dout is infinite where a row of dout is, with the number of rows inside a tile or not, and
+    finite in its other columns; the row is the first of a tile.  (bf16: P is the sum of two, of which the
+    lower may be zero or negative, and zero times infinity is NaN.)"""
+    c = Call([nq], [40], 1, 1, 16, dtype, seed=nq)
+    for row in (0, 32, 64):
+        if row < nq:
+            c.dout[row, 0, 3], c.dout[row, 0, 5] = math.inf, -math.inf
+    got = c.run()
+    if dtype == F32:
+        assert torch.all(got["dv"][:, 0, 3] == math.inf) and torch.all(got["dv"][:, 0, 5] == -math.inf)
+    assert not torch.isfinite(got["dv"][:, 0, [3, 5]]).any()
+    rest = [x for x in range(16) if x not in (3, 5)]
+    assert torch.isfinite(got["dv"][:, 0, rest]).all()
