@@ -984,7 +984,7 @@ constexpr int64_t kMaxSplits = 64;        // one lane each in the combining kern
 // The plan of a call, from its host-side sizes alone.
 struct Plan {
     bool few;                 // tiles of few rows, the wavefronts share the states
-    int64_t q_tiles, k_tiles;
+    int64_t q_tiles, k_tiles; // at least one: what is wrong with the indptrs or bounds is reported by the kernels
     int splits, dkv_splits;   // of the states (forward, dq) and of the rows (dk, dv)
     int64_t per, dkv_per;     // their lengths
     size_t stat, part_stat, part, part_kv, bytes;      // byte offsets
@@ -1014,6 +1014,8 @@ Plan plan_for(const AttendArgs &a, bool backward) {
     p.k_tiles = ceil_div(a.max_k, 128);
     pick_splits(side * p.q_tiles, a.max_k, p.few ? 128 : 256, p.splits, p.per);
     pick_splits(side * p.k_tiles, rows, 128, p.dkv_splits, p.dkv_per);
+    if (p.q_tiles < 1) p.q_tiles = 1;
+    if (p.k_tiles < 1) p.k_tiles = 1;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -1111,7 +1113,7 @@ hipError_t run(const AttendArgs &a, const Plan &p, bool back, hipStream_t s) {
 size_t attend_bytes(const AttendArgs &a, bool backward) { return plan_for(a, backward).bytes; }
 
 hipError_t launch_attend(AttendArgs a, bool backward, char *ws, hipStream_t s) {
-    if (a.n_seq == 0 || (!backward && a.max_q == 0)) return hipSuccess;
+    if (a.n_seq == 0) return hipSuccess;
     const Plan p = plan_for(a, backward);
     a.by_group = make_fastdiv(static_cast<uint32_t>(a.group));
     a.scale2 = a.scale * kLog2E;
