@@ -1648,6 +1648,8 @@ gnn_status gnn_minibatch(const gnn_graph *g, const gnn_feature_store *fs, const 
 
 namespace {
 bool known_type(int32_t t) { return t == GNN_F32 || t == GNN_BF16; }
+// The kernels' counters, doubles and vectors in a workspace lie at multiples of 256 from its start.
+bool workspace(const void *ws) { return ws && reinterpret_cast<uintptr_t>(ws) % 16 == 0; }
 // Bounds of the kernels' grids: rows * columns, and the columns of one row.
 constexpr int64_t kEmbedMax = int64_t(1) << 40;
 constexpr int64_t kEmbedMaxCols = int64_t(1) << 24;
@@ -1664,7 +1666,7 @@ gnn_status embedding_grad(EmbedGradArgs a, void *ws, size_t ws_bytes, gnn_stream
     if (!known_type(a.dout_type) || !known_type(a.out_type)) return GNN_ERR_UNSUPPORTED;
     if (a.ld_dout < a.d || a.ld_out < a.d || a.pad_id < -1) return GNN_ERR_INVALID_ARG;
     if (a.n > 0 && (!a.ids || !a.dout)) return GNN_ERR_INVALID_ARG;
-    if (!ws) return GNN_ERR_INVALID_ARG;
+    if (!workspace(ws)) return GNN_ERR_INVALID_ARG;
     if (ws_bytes < embedding_grad_bytes(a.n, a.num_rows, a.d)) return GNN_ERR_CAPACITY;
     if (fault(kFaultLaunch)) return GNN_ERR_HIP;
     a.ws = static_cast<char *>(ws);
@@ -1838,7 +1840,7 @@ gnn_status gnn_cross_attention_workspace_size(const gnn_attention *x, int32_t ba
 gnn_status gnn_cross_attention(const gnn_attention *x, void *ws, size_t ws_bytes, gnn_stream stream) {
     AttendArgs a;
     GNN_TRY(attend_args(x, &a));
-    if (!ws) return GNN_ERR_INVALID_ARG;
+    if (!workspace(ws)) return GNN_ERR_INVALID_ARG;
     if (ws_bytes < attend_bytes(a, false)) return GNN_ERR_CAPACITY;
     if (fault(kFaultLaunch)) return GNN_ERR_HIP;
     GNN_TRY_HIP(launch_attend(a, false, static_cast<char *>(ws), static_cast<hipStream_t>(stream)));
@@ -1849,7 +1851,7 @@ gnn_status gnn_cross_attention_backward(const gnn_attention *x, const gnn_attent
                                         size_t ws_bytes, gnn_stream stream) {
     AttendArgs a;
     GNN_TRY(attend_args(x, &a));
-    if (!g || !ws) return GNN_ERR_INVALID_ARG;
+    if (!g || !workspace(ws)) return GNN_ERR_INVALID_ARG;
     const int64_t wq = static_cast<int64_t>(x->heads) * x->head_dim;
     const int64_t wk = static_cast<int64_t>(x->kv_heads) * x->head_dim;
     if (g->ld_dout < wq || g->ld_dq < wq || g->ld_dk < wk || g->ld_dv < wk) return GNN_ERR_INVALID_ARG;
@@ -1900,7 +1902,7 @@ gnn_status gnn_orthogonalize(const void *g, int32_t type, int64_t batch, int64_t
     if (steps < 1 || !(eps >= 0) || ld_g < cols || ld_out < cols) return GNN_ERR_INVALID_ARG;
     if (batch > 1 && (stride_g < (rows - 1) * ld_g + cols || stride_out < (rows - 1) * ld_out + cols))
         return GNN_ERR_INVALID_ARG;
-    if (!ws || (batch > 0 && (!g || !out))) return GNN_ERR_INVALID_ARG;
+    if (!workspace(ws) || (batch > 0 && (!g || !out))) return GNN_ERR_INVALID_ARG;
     NewtonArgs a{};
     const float quintic[3] = {3.4445f, -4.7750f, 2.0315f};
     for (int i = 0; i < 3; ++i) a.coefs[i] = coefs ? coefs[i] : quintic[i];

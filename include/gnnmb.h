@@ -536,7 +536,7 @@ gnn_status gnn_embedding_lookup(const void *table, int32_t table_type, int64_t n
  *     (device int64) their number U, uniq[0..U) (device int32) the ids, ascending, and
  *     grad[p, 0..d) the row of uniq[p]; nothing is written at or past U or uniq_cap.
  *   dout: device [n, ld_dout]; types GNN_F32 or GNN_BF16 (any pair).  grad must not overlap dout.
- *   ws: ws_bytes >= gnn_embedding_grad_workspace_size(n, num_rows, d).
+ *   ws: 16-byte aligned, ws_bytes >= gnn_embedding_grad_workspace_size(n, num_rows, d).
  * Device errors (in *d_status if not NULL): GNN_ERR_OUT_OF_RANGE (another id outside [0, num_rows), which
  * then adds nothing), GNN_ERR_CAPACITY (U > uniq_cap; *d_n_uniq still holds U).
  * Errors: as gnn_embedding_lookup; GNN_ERR_CAPACITY when ws is too small.
@@ -574,9 +574,10 @@ gnn_status gnn_embedding_grad_rows(const int32_t *ids, const int64_t *d_n, int64
  *   Rows that belong to no sequence are left as they are.
  * gnn_cross_attention_backward: with out and lse of the forward call and dout [n_q, ld_dout], writes
  * dq, dk, dv of the same shapes (dk and dv zero for states that do not count), each summed in fp32
- * in a fixed order and rounded once.  What is not finite in dout makes what it enters not finite.  No output may overlap an input or another output.
- *   ws: ws_bytes >= gnn_cross_attention_workspace_size(x, backward); x->type, heads, kv_heads,
- *   head_dim, n_seq, n_q, n_k, max_q and max_k decide it.
+ * in a fixed order and rounded once.  What is not finite in dout makes what it enters not finite.
+ * No output may overlap an input or another output.
+ *   ws: 16-byte aligned, ws_bytes >= gnn_cross_attention_workspace_size(x, backward); x->type, heads,
+ *   kv_heads, head_dim, n_seq, n_q, n_k, max_q and max_k decide it.
  * Device errors (in *d_status if not NULL): GNN_ERR_OUT_OF_RANGE (an indptr that decreases or
  * leaves [0, n]; it is clamped), GNN_ERR_CAPACITY (a sequence longer than max_q or max_k; the rows
  * beyond are left out).
@@ -624,7 +625,7 @@ gnn_status gnn_cross_attention_backward(const gnn_attention *x, const gnn_attent
  *     directions below 2^-9 of the strongest are its own rounding, and what those are taken to is off by
  *     some 2%.  A zero update gives zeros; one that is not finite gives NaN.
  *     Entries are kept relative to max(1, eps / |G|_F): precision falls where |G|_F < eps / 256.
- *   ws: ws_bytes >= gnn_orthogonalize_workspace_size(batch, rows, cols, type).
+ *   ws: 16-byte aligned, ws_bytes >= gnn_orthogonalize_workspace_size(batch, rows, cols, type).
  * Errors: GNN_ERR_INVALID_ARG; GNN_ERR_CAPACITY (ws too small); GNN_ERR_UNSUPPORTED for another
  * type, rows or cols over 32768, batch over 65535, steps over 16, or coefficients that can drive
  * a singular value of at most 1 beyond 3 or have |c[0] + c[1] s^2 + c[2] s^4| beyond 15.
