@@ -173,11 +173,17 @@ __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void k_newton_product
         else
             to[TILE * CPR] = rb[set][q][i];
     };
-    f16x acc[TM][TM];
+    // Two planes: what hi lo, lo hi and lo lo add is some 2^-12 of the sum, and is summed apart, so that the
+    // sum itself is rounded once a product of sixteen and not three times (long sums: 4 x 3290 x 138 fp32 is
+    // off by 1.8e-6 so, 3.0e-6 otherwise).
+    f16x acc[TM][TM], small[PL == 2 ? TM : 1][PL == 2 ? TM : 1];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TM; ++j) acc[i][j] = f16x(0.f);
+        for (int j = 0; j < TM; ++j) {
+            acc[i][j] = f16x(0.f);
+            if (PL == 2) small[i][j] = f16x(0.f);
+        }
 
     const int row = lane & 31, half = lane >> 5;
     h8 a[2][PL][TM], b[2][PL][TM];
@@ -208,9 +214,9 @@ __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void k_newton_product
                 const int i = ij / TM, j = ij % TM;
                 if (PL == 2) {
                     if (kAllFour)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[PL - 1][i], y[PL - 1][j], acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[0][i], y[PL - 1][j], acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[PL - 1][i], y[0][j], acc[i][j], 0, 0, 0);
+                        small[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[PL - 1][i], y[PL - 1][j], small[i][j], 0, 0, 0);
+                    small[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[0][i], y[PL - 1][j], small[i][j], 0, 0, 0);
+                    small[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[PL - 1][i], y[0][j], small[i][j], 0, 0, 0);
                 }
                 acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[0][i], y[0][j], acc[i][j], 0, 0, 0);
                 if (kk + 1 < KK) {
@@ -246,6 +252,12 @@ __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void k_newton_product
 #pragma unroll
     for (int u = 0; u < kDepth - 1; ++u)
         if (s + u < steps) turn(u, s + u);
+    if (PL == 2) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TM; ++j) acc[i][j] += small[i][j];
+    }
 
     // A lane holds column lane % 32 and rows 8 g + 4 (lane / 32) + 0..3 of each 32 x 32 accumulator:
     // every(f) calls f(row, column, the four values) for what exists of the padded product.  A padded
