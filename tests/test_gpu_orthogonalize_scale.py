@@ -75,3 +75,19 @@ def test_square_multiples_of_the_identity_and_constant_updates():
         g = g.to(BF16).cuda()
         y, want = run(g).double().cpu(), steps64(g, 5)
         assert float((y - want).abs().max()) <= 2 * 2.0 ** -7 * float(want.abs().max())
+
+
+@pytest.mark.parametrize("b,m,n", [(4, 3290, 138), (3, 2529, 167), (7, 144, 2562)])
+def test_long_sums_in_fp32(b, m, n):
+    """A's diagonal is a sum of k squares: k / 16 additions of a sum of sixteen, each rounded by up to 2^-24
+    of the sum so far, by 2.5e-8 of it in the root mean square over the mantissas, 2.5e-8 (k / 48)^(1/2) of
+    the whole in all.  A step's Q moves by up to 1.8 of that (where s^2 = 1.4), and the later steps'
+    slopes carry it on by up to 5, so 9 at most and, for the other terms' part, 12 here; the planes add some
+    2e-7."""
+    k = max(m, n)
+    tol = 12 * 2.5e-8 * (k / 48) ** 0.5 + 2e-7
+    g = torch.stack([gaussian(m, min(m, n) // 8, seed=i) @ gaussian(min(m, n) // 8, n, seed=9 + i) /
+                     math.sqrt(min(m, n) // 8) + gaussian(m, n, seed=20 + i) for i in range(b)])
+    for x, y in zip(g, run(g)):
+        want = steps64(x, 5)
+        assert float((y.double().cpu() - want).norm() / want.norm()) <= tol
