@@ -94,7 +94,8 @@ hipError_t pick_lookup(const LookupArgs &a, hipStream_t s) {
 // Least-significant-digit radix sort of (key, position) by digits of at most 8 bits, stable.  A
 // workgroup takes a tile of keys, 8 per thread; a wavefront's keys lie next to each other, 64 a
 // round, so the order (wavefront, round, lane) is the order of the positions.  Lanes with the same
-// digit find each other by one ballot per bit of the digit.  Up to 8192 keys are sorted by one
+// digit find each other by one ballot per bit of the digit.  Up to 8192 keys (of the distinct ids: a dense
+// table of so few positions goes by buckets) are sorted by one
 // workgroup of 16 wavefronts in LDS in one launch.  Beyond that, each digit takes two launches over
 // tiles of 4096 keys: digit counts of every tile, then the placement, where every tile sums the
 // counts of the tiles before it (beyond kSumTiles tiles a third launch does that once for all).
@@ -426,7 +427,7 @@ __global__ __launch_bounds__(kOneThreads) void k_sort_one(SortArgs a) {
     const int n = static_cast<int>(a.n);
     uint32_t key[kSortRounds];
     load_keys<kSortRounds, kOneThreads>(a, key);
-    clear_marks(a);
+    if (t == 0) *a.long_runs = 0;
     uint32_t pos[kSortRounds];
     own_positions<kSortRounds, kOneThreads>(a.n, pos);
     sort_one(n, a.passes, a.bits, m, key, pos);
