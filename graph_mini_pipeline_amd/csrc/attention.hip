@@ -29,7 +29,7 @@
 // What bounds it.  For bf16 with many rows, LDS: an operand read is 1 KB for one matrix instruction of 32
 // cycles, four of them at once are the 128 bytes a cycle that a compute unit's LDS delivers, and the
 // exponentials and the tiles' way into LDS come on top.  4 sequences of up to 1024 queries of 16 heads
-// over 4, up to 2600 states of 128: forward 111 us (480 TFLOP/s), dq 118 us (670), dk and dv 230 us (460
+// over 4, up to 2600 states of 128: forward 109 us (490 TFLOP/s), dq 109 us (730), dk and dv 208 us (510
 // by four products).  For single tokens, the reading of k and v: 16 sequences over up to 16384 states
 // of 4 x 128, 346 MB in 94 us (3.7 TB/s; a large copy reaches 4.9).  For fp32, the matrix
 // instructions, of which a 32 x 32 x 2 takes 64 cycles.
@@ -428,7 +428,8 @@ __global__ __launch_bounds__(kThreads, WK == 1 ? 2 : 1) void k_attend(AttendArgs
     }
     sum += __shfl_xor(sum, 32, 64);
     if (WK > 1) {
-        // join the wavefronts' sums: [WK - 1][32 rows][DP + 2] floats in the tiles' memory
+        // join the wavefronts' sums: [WK - 1][32 rows][DP + 4] floats in the tiles' memory (DP sums, the
+        // maximum and the weights' sum)
         constexpr int kRow = DP + 4;
         static_assert((WK - 1) * WQ * 32 * kRow * 4 <= static_cast<int>(sizeof(smem)), "join area");
         float *join = reinterpret_cast<float *>(smem) + (wq * (WK - 1) * 32 + (lane & 31)) * kRow;
@@ -557,7 +558,7 @@ __global__ __launch_bounds__(kThreads) void k_attend_stat(AttendArgs a) {
 // The bf16 that P and dS are rounded to leaves the gradients sqrt(2) times the error of their own
 // rounding where the sums are long, and more where they are short (over 3 to 66 states 1.5 to 2 times):
 // of a sequence with fewer than kLongSums rows or states, P and dS are multiplied as two bf16, which at
-// 4 x 1024 queries of 16 heads over up to 2600 states would take 579 us in place of 423.  The rule goes by the
+// 4 x 1024 queries of 16 heads over up to 2600 states took 579 us in place of 423.  The rule goes by the
 // sequence's own lengths, so their precision does not depend on what else is in the call.
 constexpr int64_t kLongSums = 512;
 template <typename T>
@@ -731,10 +732,9 @@ __global__ __launch_bounds__(kThreads, (dq_groups<T, DP, WK>())) void k_attend_d
 // (SIDES = 2) four wavefronts take dv and four more dk of the same states: S is computed twice, 40
 // products in place of 32, but each side's operands and sums leave room for two wavefronts per SIMD,
 // whose waits overlap: the training step at 4 x 1024 queries of 16 heads over up to 2600 states takes
-// 421 us in place of 466, this kernel 227 of it.  (A turn takes some 2700 cycles, 2200 of them LDS
-// reads.)  For fp32, whose
-// operands take twice the registers and whose products take sixteen times as long, one wavefront
-// does both.
+// 405 us (with one wavefront for both it took 466 where this took 421), this kernel 208 of it.  (At
+// 227 us a turn took some 2700 cycles, 2200 of them LDS reads.)  For fp32, whose operands take twice the registers and whose
+// products take sixteen times as long, one wavefront does both.
 template <typename T, int DP, int SIDES>
 __global__ __launch_bounds__(kThreads *SIDES, SIDES) void k_attend_dkv(AttendArgs a) {
     constexpr int BR = 32, DB = DP / 32;

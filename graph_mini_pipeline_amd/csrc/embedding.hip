@@ -264,7 +264,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs a) {
             if (a.touched && key[j] < a.num_rows) a.touched[key[j]] = 1;
         }
     }
-    // counts of the tiles before this one and of all tiles, four threads per digit
+    // counts of the tiles before this one and of all tiles, kSortThreads / kDigits threads per digit
     const int dg = t & (kDigits - 1), part = t / kDigits;
     uint32_t before = 0, total = 0;
     if (a.scanned) {
@@ -748,7 +748,9 @@ __global__ __launch_bounds__(kSumThreads) void k_embedding_join(SumArgs a) {
 // A dense table: a workgroup owns the rows r with r mod 2^shift = blockIdx.x, so that neighbouring
 // frequent ids go to different ones.  It picks its positions from the list of ids, which all read, in
 // their order, clears its unnamed rows where the table is written, and sorts its own positions only,
-// by the rest of the id.  1024 x 64 fp32 over 10000 rows: 7.8 us a call, most of it the launch.
+// by the rest of the id.  1024 x 64 fp32 over 10000 rows: 7.6 us a call
+// among others (10 under a profiler): the kernel's loading, picking, clearing, sorting and adding, which wait
+// for each other behind barriers; a launch's own share is some 2.6.
 //
 // Both: a lane group adds a short run, all groups together, one after the other, the long ones.
 constexpr int kFewThreads = 512;   // (workgroups of 1024 start up to 6 us apart, of 512 half that)

@@ -27,7 +27,7 @@
 //
 // What bounds it.  Large squares: LDS reads and the tiles' way into it next to the matrix units: five
 // steps of 4096 x 4096 bf16 in 1.62 ms, 850 TFLOP/s of the needed operations (a library product reaches
-// 1050 to 1150 at this size).  Two planes: 2 x 2571 x 1030 fp32 720 us, three products for one.  Small ones:
+// 1050 to 1150 at this size).  Two planes: 2 x 2571 x 1030 fp32 710 us, three products for one.  Small ones:
 // the chain of three products a step; 256 x 256 fp32 takes 119 us in 17 launches of about 7 us each, of
 // which 2.6 are the launch's own, 0.7 the first load and 0.9 the stores.
 #include <math.h>
