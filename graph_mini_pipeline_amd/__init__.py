@@ -32,6 +32,9 @@ __all__ = [
     "gnn_embedding_lookup", "gnn_embedding_grad", "gnn_embedding_grad_rows",
     "gnn_embedding_grad_workspace_size", "gnn_orthogonalize", "gnn_orthogonalize_workspace_size",
     "gnn_cross_attention", "gnn_cross_attention_backward", "gnn_cross_attention_workspace_size",
+    "gnn_layer_norm", "gnn_layer_norm_backward", "gnn_layer_norm_workspace_size",
+    "gnn_linear", "gnn_linear_backward", "gnn_linear_workspace_size",
+    "gnn_gated_linear", "gnn_gated_linear_backward", "gnn_gated_linear_workspace_size",
     "gnn_read_device_status", "gnn_timer_create", "gnn_timer_destroy", "gnn_timer_reset",
     "gnn_timer_elapsed", "gnn_copy_probe", "gnn_copy_probe_host", "gnn_hash_probe", "lib",
 ]
@@ -881,6 +884,237 @@ def gnn_orthogonalize(g: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, step
                                 out.data_ptr(), old, ostride, ws.data_ptr(),
                                 ws.numel() * ws.element_size(), _stream(stream)),
         "gnn_orthogonalize")
+
+
+def _matrix(t: torch.Tensor, dtype, rows: int, cols: int, name: str):
+    """(pointer, row stride) of a [>= rows, cols] device matrix of this type; (None, 0) of None."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] < rows or shape[1] != cols or (cols > 1 and stride[1] != 1) or \
+            (shape[0] > 1 and stride[0] < cols):
+        raise ValueError(f"{name}: must be [{rows}, {cols}] with contiguous rows that do not overlap")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else cols
+
+
+def _vector(t: torch.Tensor, dtype, n: int, name: str):
+    """The pointer of a contiguous device tensor of n elements; None of None."""
+    if t is None:
+        return None
+    _need(t, dtype, name)
+    if t.numel() != n:
+        raise ValueError(f"{name}: [{n}]")
+    return t.data_ptr()
+
+
+def _space(ws: torch.Tensor):
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws: must be a contiguous device tensor")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _rows_of(x: torch.Tensor):
+    if x.dim() != 2:
+        raise ValueError("x: must be a matrix")
+    return x.shape
+
+
+def _norm(x, weight, bias, eps, mean, rstd, d_n) -> _abi.gnn_norm:
+    n, d = _rows_of(x)
+    kind = _type(x.dtype, "x")
+    px, ld_x = _matrix(x, x.dtype, n, d, "x")
+    param = weight if weight is not None else bias
+    pt = x.dtype if param is None else param.dtype
+    a = _abi.gnn_norm(kind, kind, _type(pt, "weight"), eps, n, d)
+    a.x, a.ld_x = px, ld_x
+    a.d_n = _vector(d_n, torch.int64, 1, "d_n")
+    a.weight, a.bias = _vector(weight, pt, d, "weight"), _vector(bias, pt, d, "bias")
+    a.mean = _vector(mean, torch.float32, n, "mean")
+    a.rstd = _vector(rstd, torch.float32, n, "rstd")
+    return a
+
+
+def gnn_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor],
+                   eps: float, out: torch.Tensor, mean: Optional[torch.Tensor] = None,
+                   rstd: Optional[torch.Tensor] = None, d_n: Optional[torch.Tensor] = None,
+                   stream=None) -> None:
+    """out = (x - mean) * rstd * weight + bias over the rows of x [n, d], mean and rstd (float32 [n])
+    those of each row, rstd = 1 / sqrt(variance + eps).  x, out and weight with bias: float32 or
+    bfloat16 each; None for weight: ones, for bias: zeros."""
+    a = _norm(x, weight, bias, eps, mean, rstd, d_n)
+    a.out_type = _type(out.dtype, "out")
+    a.out, a.ld_out = _matrix(out, out.dtype, a.n, a.d, "out")
+    _ok(lib().gnn_layer_norm(ctypes.byref(a), _stream(stream)), "gnn_layer_norm")
+
+
+def gnn_layer_norm_workspace_size(n: int, d: int) -> int:
+    b = ctypes.c_size_t(0)
+    _ok(lib().gnn_layer_norm_workspace_size(n, d, ctypes.byref(b)), "gnn_layer_norm_workspace_size")
+    return int(b.value)
+
+
+def gnn_layer_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
+                            rstd: torch.Tensor, dout: torch.Tensor, dx: Optional[torch.Tensor],
+                            ws: torch.Tensor, dweight: Optional[torch.Tensor] = None,
+                            dbias: Optional[torch.Tensor] = None,
+                            residual_grad: Optional[torch.Tensor] = None,
+                            d_n: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dx, dweight and dbias (those that are not None) of gnn_layer_norm from its mean and rstd and the
+    gradient dout of out; residual_grad, the gradient that reaches x past the norm, is added to dx."""
+    n, d = _rows_of(x)
+    param = next((t for t in (weight, dweight, dbias) if t is not None), None)
+    a = _norm(x, weight, None, 0.0, mean, rstd, d_n)
+    if param is not None:
+        a.param_type = _type(param.dtype, "dweight")
+    a.out_type = _type(dout.dtype, "dout")
+    g = _abi.gnn_norm_grad()
+    g.dout, g.ld_dout = _matrix(dout, dout.dtype, n, d, "dout")
+    g.residual_grad, g.ld_residual_grad = _matrix(residual_grad, x.dtype, n, d, "residual_grad")
+    g.dx, g.ld_dx = _matrix(dx, x.dtype, n, d, "dx")
+    if param is not None:
+        g.dweight = _vector(dweight, param.dtype, d, "dweight")
+        g.dbias = _vector(dbias, param.dtype, d, "dbias")
+    p, size = _space(ws)
+    _ok(lib().gnn_layer_norm_backward(ctypes.byref(a), ctypes.byref(g), p, size, _stream(stream)),
+        "gnn_layer_norm_backward")
+
+
+#: The activations of the dense layers, by name.
+ACTIVATIONS = {"none": _abi.GNN_ACT_NONE, "relu": _abi.GNN_ACT_RELU, "gelu": _abi.GNN_ACT_GELU,
+               "gelu_tanh": _abi.GNN_ACT_GELU_TANH, "silu": _abi.GNN_ACT_SILU,
+               "sigmoid": _abi.GNN_ACT_SIGMOID}
+
+
+def _activation(name: str) -> int:
+    a = ACTIVATIONS.get(name)
+    if a is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    return a
+
+
+def _layer(layer, x, w, activation, d_n):
+    """The parts that gnn_dense and gnn_gated share; w: any of the layer's weights."""
+    n, d_in = _rows_of(x)
+    if w.dim() != 2:
+        raise ValueError("weights: must be matrices")
+    a = layer(_type(x.dtype, "x"), _activation(activation), n, d_in, w.shape[1])
+    a.x, a.ld_x = _matrix(x, x.dtype, n, d_in, "x")
+    a.d_n = _vector(d_n, torch.int64, 1, "d_n")
+    return a
+
+
+def _same_stride(first, second, names: str):
+    """One row stride of two matrices, either of which may be missing."""
+    (p, ld), (q, ld2) = first, second
+    if p is not None and q is not None and ld != ld2:
+        raise ValueError(f"{names}: must have one row stride")
+    return p, q, ld if p is not None else ld2
+
+
+def _layer_size(layer, call, n, d_in, d_out, dtype, backward):
+    a = layer(_type(dtype, "dtype"), _abi.GNN_ACT_NONE, n, d_in, d_out)
+    b = ctypes.c_size_t(0)
+    _ok(getattr(lib(), call)(ctypes.byref(a), 1 if backward else 0, ctypes.byref(b)), call)
+    return int(b.value)
+
+
+def gnn_linear_workspace_size(n: int, d_in: int, d_out: int, dtype, backward: bool = False) -> int:
+    return _layer_size(_abi.gnn_dense, "gnn_linear_workspace_size", n, d_in, d_out, dtype, backward)
+
+
+def gnn_linear(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
+               bias: Optional[torch.Tensor] = None, activation: str = "none",
+               residual: Optional[torch.Tensor] = None, pre: Optional[torch.Tensor] = None,
+               d_n: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out = act(x w + bias) + residual; pre, if given, receives x w + bias for the backward pass.
+    x: [n, d_in], w: [d_in, d_out], the others [n, d_out] and [d_out], one type, float32 or bfloat16."""
+    a = _layer(_abi.gnn_dense, x, w, activation, d_n)
+    n, d_out, dt = a.n, a.d_out, x.dtype
+    a.w, a.ld_w = _matrix(w, dt, a.d_in, d_out, "w")
+    a.bias = _vector(bias, dt, d_out, "bias")
+    a.residual, a.ld_residual = _matrix(residual, dt, n, d_out, "residual")
+    a.out, a.ld_out = _matrix(out, dt, n, d_out, "out")
+    a.pre, a.ld_pre = _matrix(pre, dt, n, d_out, "pre")
+    p, size = _space(ws)
+    _ok(lib().gnn_linear(ctypes.byref(a), p, size, _stream(stream)), "gnn_linear")
+
+
+def gnn_linear_backward(x: torch.Tensor, w: torch.Tensor, dout: torch.Tensor, ws: torch.Tensor,
+                        activation: str = "none", pre: Optional[torch.Tensor] = None,
+                        dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                        dbias: Optional[torch.Tensor] = None, d_n: Optional[torch.Tensor] = None,
+                        stream=None) -> None:
+    """Those of dx, dw and dbias that are given, from the gradient dout of gnn_linear's out and, where
+    there is an activation, its pre.  (The residual's gradient is dout.)"""
+    a = _layer(_abi.gnn_dense, x, w, activation, d_n)
+    n, d_in, d_out, dt = a.n, a.d_in, a.d_out, x.dtype
+    a.w, a.ld_w = _matrix(w, dt, d_in, d_out, "w")
+    a.pre, a.ld_pre = _matrix(pre, dt, n, d_out, "pre")
+    g = _abi.gnn_dense_grad()
+    g.dout, g.ld_dout = _matrix(dout, dt, n, d_out, "dout")
+    g.dx, g.ld_dx = _matrix(dx, dt, n, d_in, "dx")
+    g.dw, g.ld_dw = _matrix(dw, dt, d_in, d_out, "dw")
+    g.dbias = _vector(dbias, dt, d_out, "dbias")
+    p, size = _space(ws)
+    _ok(lib().gnn_linear_backward(ctypes.byref(a), ctypes.byref(g), p, size, _stream(stream)),
+        "gnn_linear_backward")
+
+
+def gnn_gated_linear_workspace_size(n: int, d_in: int, d_out: int, dtype, backward: bool = False) -> int:
+    return _layer_size(_abi.gnn_gated, "gnn_gated_linear_workspace_size", n, d_in, d_out, dtype, backward)
+
+
+def gnn_gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, out: torch.Tensor,
+                     ws: torch.Tensor, bias_gate: Optional[torch.Tensor] = None,
+                     bias_up: Optional[torch.Tensor] = None, activation: str = "silu",
+                     gate: Optional[torch.Tensor] = None, up: Optional[torch.Tensor] = None,
+                     d_n: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out = act(x w_gate + bias_gate) * (x w_up + bias_up); gate and up, if given, receive the two sums for
+    the backward pass.  x: [n, d_in], weights: [d_in, d_out] of one row stride (halves of one matrix, for
+    instance), the others [n, d_out] and [d_out], one type, float32 or bfloat16."""
+    a = _layer(_abi.gnn_gated, x, w_gate, activation, d_n)
+    n, d_in, d_out, dt = a.n, a.d_in, a.d_out, x.dtype
+    a.w_gate, a.w_up, a.ld_w = _same_stride(_matrix(w_gate, dt, d_in, d_out, "w_gate"),
+                                            _matrix(w_up, dt, d_in, d_out, "w_up"), "w_gate, w_up")
+    a.bias_gate, a.bias_up = _vector(bias_gate, dt, d_out, "bias_gate"), _vector(bias_up, dt, d_out, "bias_up")
+    a.out, a.ld_out = _matrix(out, dt, n, d_out, "out")
+    a.gate, a.up, a.ld_pre = _same_stride(_matrix(gate, dt, n, d_out, "gate"),
+                                          _matrix(up, dt, n, d_out, "up"), "gate, up")
+    p, size = _space(ws)
+    _ok(lib().gnn_gated_linear(ctypes.byref(a), p, size, _stream(stream)), "gnn_gated_linear")
+
+
+def gnn_gated_linear_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                              gate: torch.Tensor, up: torch.Tensor, dout: torch.Tensor,
+                              ws: torch.Tensor, activation: str = "silu",
+                              dx: Optional[torch.Tensor] = None, dw_gate: Optional[torch.Tensor] = None,
+                              dw_up: Optional[torch.Tensor] = None,
+                              dbias_gate: Optional[torch.Tensor] = None,
+                              dbias_up: Optional[torch.Tensor] = None,
+                              d_n: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Those of dx, dw_gate, dw_up, dbias_gate and dbias_up that are given, from the gradient dout of
+    gnn_gated_linear's out and its gate and up.  dw_gate and dw_up have one row stride, like gate and up."""
+    a = _layer(_abi.gnn_gated, x, w_gate, activation, d_n)
+    n, d_in, d_out, dt = a.n, a.d_in, a.d_out, x.dtype
+    a.w_gate, a.w_up, a.ld_w = _same_stride(_matrix(w_gate, dt, d_in, d_out, "w_gate"),
+                                            _matrix(w_up, dt, d_in, d_out, "w_up"), "w_gate, w_up")
+    a.gate, a.up, a.ld_pre = _same_stride(_matrix(gate, dt, n, d_out, "gate"),
+                                          _matrix(up, dt, n, d_out, "up"), "gate, up")
+    g = _abi.gnn_gated_grad()
+    g.dout, g.ld_dout = _matrix(dout, dt, n, d_out, "dout")
+    g.dx, g.ld_dx = _matrix(dx, dt, n, d_in, "dx")
+    g.dw_gate, g.dw_up, g.ld_dw = _same_stride(_matrix(dw_gate, dt, d_in, d_out, "dw_gate"),
+                                               _matrix(dw_up, dt, d_in, d_out, "dw_up"),
+                                               "dw_gate, dw_up")
+    g.dbias_gate = _vector(dbias_gate, dt, d_out, "dbias_gate")
+    g.dbias_up = _vector(dbias_up, dt, d_out, "dbias_up")
+    p, size = _space(ws)
+    _ok(lib().gnn_gated_linear_backward(ctypes.byref(a), ctypes.byref(g), p, size, _stream(stream)),
+        "gnn_gated_linear_backward")
 
 
 def gnn_copy_probe(src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:

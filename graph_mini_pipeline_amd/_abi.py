@@ -26,6 +26,12 @@ GNN_NOALLOC_SCRATCH_BYTES = (24 << 20) + (64 << 10)
 GNN_DYN_AUTO = 1
 GNN_F32 = 0
 GNN_BF16 = 1
+GNN_ACT_NONE = 0
+GNN_ACT_RELU = 1
+GNN_ACT_GELU = 2
+GNN_ACT_GELU_TANH = 3
+GNN_ACT_SILU = 4
+GNN_ACT_SIGMOID = 5
 
 GNN_OK = 0
 GNN_ERR_INVALID_ARG = -1
@@ -93,6 +99,41 @@ class gnn_attention_grad(ctypes.Structure):
                 ("ld_dk", i64), ("ld_dv", i64)]
 
 
+class gnn_norm(ctypes.Structure):
+    _fields_ = [("x_type", i32), ("out_type", i32), ("param_type", i32), ("eps", f32), ("n", i64),
+                ("d", i64), ("d_n", vp), ("x", vp), ("ld_x", i64), ("weight", vp), ("bias", vp),
+                ("out", vp), ("ld_out", i64), ("mean", vp), ("rstd", vp)]
+
+
+class gnn_norm_grad(ctypes.Structure):
+    _fields_ = [("dout", vp), ("ld_dout", i64), ("residual_grad", vp), ("ld_residual_grad", i64),
+                ("dx", vp), ("ld_dx", i64), ("dweight", vp), ("dbias", vp)]
+
+
+class gnn_dense(ctypes.Structure):
+    _fields_ = [("type", i32), ("activation", i32), ("n", i64), ("d_in", i64), ("d_out", i64),
+                ("d_n", vp), ("x", vp), ("ld_x", i64), ("w", vp), ("ld_w", i64), ("bias", vp),
+                ("residual", vp), ("ld_residual", i64), ("out", vp), ("ld_out", i64), ("pre", vp),
+                ("ld_pre", i64)]
+
+
+class gnn_dense_grad(ctypes.Structure):
+    _fields_ = [("dout", vp), ("ld_dout", i64), ("dx", vp), ("ld_dx", i64), ("dw", vp), ("ld_dw", i64),
+                ("dbias", vp)]
+
+
+class gnn_gated(ctypes.Structure):
+    _fields_ = [("type", i32), ("activation", i32), ("n", i64), ("d_in", i64), ("d_out", i64),
+                ("d_n", vp), ("x", vp), ("ld_x", i64), ("w_gate", vp), ("w_up", vp), ("ld_w", i64),
+                ("bias_gate", vp), ("bias_up", vp), ("out", vp), ("ld_out", i64), ("gate", vp),
+                ("up", vp), ("ld_pre", i64)]
+
+
+class gnn_gated_grad(ctypes.Structure):
+    _fields_ = [("dout", vp), ("ld_dout", i64), ("dx", vp), ("ld_dx", i64), ("dw_gate", vp),
+                ("dw_up", vp), ("ld_dw", i64), ("dbias_gate", vp), ("dbias_up", vp)]
+
+
 P = ctypes.POINTER
 
 # name -> (restype, argtypes); every entry point the header declares
@@ -140,6 +181,15 @@ SIGNATURES = {
     "gnn_orthogonalize_workspace_size": (i32, [i64, i64, i64, i32, P(size_t)]),
     "gnn_orthogonalize": (i32, [vp, i32, i64, i64, i64, i64, i64, i32, P(f32), f32, f32, vp, i64, i64,
                                 vp, size_t, vp]),
+    "gnn_layer_norm": (i32, [P(gnn_norm), vp]),
+    "gnn_layer_norm_workspace_size": (i32, [i64, i64, P(size_t)]),
+    "gnn_layer_norm_backward": (i32, [P(gnn_norm), P(gnn_norm_grad), vp, size_t, vp]),
+    "gnn_linear_workspace_size": (i32, [P(gnn_dense), i32, P(size_t)]),
+    "gnn_linear": (i32, [P(gnn_dense), vp, size_t, vp]),
+    "gnn_linear_backward": (i32, [P(gnn_dense), P(gnn_dense_grad), vp, size_t, vp]),
+    "gnn_gated_linear_workspace_size": (i32, [P(gnn_gated), i32, P(size_t)]),
+    "gnn_gated_linear": (i32, [P(gnn_gated), vp, size_t, vp]),
+    "gnn_gated_linear_backward": (i32, [P(gnn_gated), P(gnn_gated_grad), vp, size_t, vp]),
     "gnn_read_device_status": (i32, [vp, vp, P(i32)]),
     "gnn_timer_create": (i32, [i32, P(vp)]),
     "gnn_timer_destroy": (i32, [vp]),

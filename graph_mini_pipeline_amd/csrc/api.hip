@@ -1928,6 +1928,251 @@ gnn_status gnn_orthogonalize(const void *g, int32_t type, int64_t batch, int64_t
     return GNN_OK;
 }
 
+// ---- layer norm -----------------------------------------------------------------------------------
+
+namespace {
+constexpr int64_t kNormMaxCols = 16384;      // a row is held in a workgroup's registers
+
+gnn_status check_norm_sizes(int64_t n, int64_t d) {
+    if (n < 0 || d < 1) return GNN_ERR_INVALID_ARG;
+    if (n > kInt32Max || d > kNormMaxCols) return GNN_ERR_UNSUPPORTED;
+    return GNN_OK;
+}
+
+gnn_status norm_args(const gnn_norm *x, NormArgs *a) {
+    if (!x) return GNN_ERR_INVALID_ARG;
+    GNN_TRY(check_norm_sizes(x->n, x->d));
+    if (!known_type(x->x_type) || !known_type(x->out_type) || !known_type(x->param_type))
+        return GNN_ERR_UNSUPPORTED;
+    if (!(x->eps >= 0) || x->ld_x < x->d || (x->n > 0 && !x->x)) return GNN_ERR_INVALID_ARG;
+    *a = NormArgs{};
+    a->x = x->x;
+    a->x_type = x->x_type;
+    a->out_type = x->out_type;
+    a->param_type = x->param_type;
+    a->ld_x = x->ld_x;
+    a->d_n = x->d_n;
+    a->n = x->n;
+    a->d = x->d;
+    a->weight = x->weight;
+    a->eps = x->eps;
+    a->mean = x->mean;
+    a->rstd = x->rstd;
+    return GNN_OK;
+}
+}  // namespace
+
+gnn_status gnn_layer_norm(const gnn_norm *x, gnn_stream stream) {
+    NormArgs a;
+    GNN_TRY(norm_args(x, &a));
+    if (x->ld_out < x->d || (x->n > 0 && !x->out)) return GNN_ERR_INVALID_ARG;
+    if (fault(kFaultLaunch)) return GNN_ERR_HIP;
+    a.bias = x->bias;
+    a.out = x->out;
+    a.ld_out = x->ld_out;
+    GNN_TRY_HIP(launch_norm(a, static_cast<hipStream_t>(stream)));
+    return GNN_OK;
+}
+
+gnn_status gnn_layer_norm_workspace_size(int64_t n, int64_t d, size_t *out_bytes) {
+    if (!out_bytes) return GNN_ERR_INVALID_ARG;
+    GNN_TRY(check_norm_sizes(n, d));
+    *out_bytes = norm_bytes(n, d);
+    return GNN_OK;
+}
+
+gnn_status gnn_layer_norm_backward(const gnn_norm *x, const gnn_norm_grad *g, void *ws, size_t ws_bytes,
+                                   gnn_stream stream) {
+    NormArgs a;
+    GNN_TRY(norm_args(x, &a));
+    if (!g || !workspace(ws) || g->ld_dout < x->d) return GNN_ERR_INVALID_ARG;
+    if ((g->dx && g->ld_dx < x->d) || (g->residual_grad && g->ld_residual_grad < x->d))
+        return GNN_ERR_INVALID_ARG;
+    if (x->n > 0 && (!x->mean || !x->rstd || !g->dout)) return GNN_ERR_INVALID_ARG;
+    if (ws_bytes < norm_bytes(x->n, x->d)) return GNN_ERR_CAPACITY;
+    if (fault(kFaultLaunch)) return GNN_ERR_HIP;
+    a.dout = g->dout;
+    a.ld_dout = g->ld_dout;
+    a.dres = g->residual_grad;
+    a.ld_dres = g->ld_residual_grad;
+    a.dx = g->dx;
+    a.ld_dx = g->ld_dx;
+    a.dweight = g->dweight;
+    a.dbias = g->dbias;
+    a.ws = static_cast<char *>(ws);
+    GNN_TRY_HIP(launch_norm_backward(a, static_cast<hipStream_t>(stream)));
+    return GNN_OK;
+}
+
+// ---- dense layers ---------------------------------------------------------------------------------
+
+extern "C++" {
+namespace {
+constexpr int64_t kDenseMaxRows = int64_t(1) << 30;
+// The lines of a tile lie fewer than 2^32 bytes apart (the gradient of a pair's sums has both in a row).
+constexpr int64_t kDenseMaxCols = int64_t(1) << 20;
+constexpr int64_t kDenseMaxLd = int64_t(1) << 21;
+
+gnn_status dense_sizes(int32_t type, int32_t activation, int64_t n, int64_t d_in, int64_t d_out, DenseArgs *a) {
+    if (n < 0 || d_in < 1 || d_out < 1) return GNN_ERR_INVALID_ARG;
+    if (!known_type(type) || activation < GNN_ACT_NONE || activation > GNN_ACT_SIGMOID || n > kDenseMaxRows ||
+        d_in > kDenseMaxCols || d_out > kDenseMaxCols)
+        return GNN_ERR_UNSUPPORTED;
+    *a = DenseArgs{};
+    a->type = type;
+    a->act = activation;
+    a->n = n;
+    a->d_in = d_in;
+    a->d_out = d_out;
+    return GNN_OK;
+}
+
+// A row stride of at least `wide` elements that the kernels take.
+gnn_status check_ld(int64_t ld, int64_t wide) {
+    if (ld < wide) return GNN_ERR_INVALID_ARG;
+    return ld > kDenseMaxLd ? GNN_ERR_UNSUPPORTED : GNN_OK;
+}
+
+template <typename Layer>
+gnn_status dense_inputs(const Layer *x, DenseArgs *a) {
+    GNN_TRY(check_ld(x->ld_x, x->d_in));
+    GNN_TRY(check_ld(x->ld_w, x->d_out));
+    if (x->n > 0 && !x->x) return GNN_ERR_INVALID_ARG;
+    a->d_n = x->d_n;
+    a->x = x->x;
+    a->ld_x = x->ld_x;
+    a->ld_w = x->ld_w;
+    return GNN_OK;
+}
+
+gnn_status linear_sizes(const gnn_dense *x, DenseArgs *a) {
+    if (!x) return GNN_ERR_INVALID_ARG;
+    return dense_sizes(x->type, x->activation, x->n, x->d_in, x->d_out, a);
+}
+
+gnn_status gated_sizes(const gnn_gated *x, DenseArgs *a) {
+    if (!x) return GNN_ERR_INVALID_ARG;
+    GNN_TRY(dense_sizes(x->type, x->activation, x->n, x->d_in, x->d_out, a));
+    a->pair = 1;
+    return GNN_OK;
+}
+
+// What the forward calls share once their own arguments are in place.
+template <typename Layer>
+gnn_status dense_forward(const Layer *x, DenseArgs *a, void *ws, size_t ws_bytes, gnn_stream stream) {
+    GNN_TRY(check_ld(x->ld_out, x->d_out));
+    if (a->pre[0] || a->pre[1]) GNN_TRY(check_ld(x->ld_pre, x->d_out));
+    if (x->n > 0 && !x->out) return GNN_ERR_INVALID_ARG;
+    if (!workspace(ws)) return GNN_ERR_INVALID_ARG;
+    if (ws_bytes < dense_bytes(*a, false)) return GNN_ERR_CAPACITY;
+    if (fault(kFaultLaunch)) return GNN_ERR_HIP;
+    a->out = x->out;
+    a->ld_out = x->ld_out;
+    a->ld_pre = x->ld_pre;
+    a->ws = static_cast<char *>(ws);
+    GNN_TRY_HIP(launch_dense(*a, static_cast<hipStream_t>(stream)));
+    return GNN_OK;
+}
+
+template <typename Layer, typename Grad>
+gnn_status dense_backward(const Layer *x, const Grad *g, DenseArgs *a, void *ws, size_t ws_bytes, gnn_stream stream) {
+    GNN_TRY(check_ld(g->ld_dout, x->d_out));
+    if (a->pair || a->act != GNN_ACT_NONE) GNN_TRY(check_ld(x->ld_pre, x->d_out));
+    if (g->dx) GNN_TRY(check_ld(g->ld_dx, x->d_in));
+    if (a->dw[0] || a->dw[1]) GNN_TRY(check_ld(g->ld_dw, x->d_out));
+    if (x->n > 0 && !g->dout) return GNN_ERR_INVALID_ARG;
+    if (!workspace(ws)) return GNN_ERR_INVALID_ARG;
+    if (ws_bytes < dense_bytes(*a, true)) return GNN_ERR_CAPACITY;
+    if (fault(kFaultLaunch)) return GNN_ERR_HIP;
+    a->dout = g->dout;
+    a->ld_dout = g->ld_dout;
+    a->dx = g->dx;
+    a->ld_dx = g->ld_dx;
+    a->ld_dw = g->ld_dw;
+    a->ld_pre = x->ld_pre;
+    a->ws = static_cast<char *>(ws);
+    GNN_TRY_HIP(launch_dense_backward(*a, static_cast<hipStream_t>(stream)));
+    return GNN_OK;
+}
+}  // namespace
+}  // extern "C++"
+
+gnn_status gnn_linear_workspace_size(const gnn_dense *x, int32_t backward, size_t *out_bytes) {
+    if (!out_bytes) return GNN_ERR_INVALID_ARG;
+    DenseArgs a;
+    GNN_TRY(linear_sizes(x, &a));
+    *out_bytes = dense_bytes(a, backward != 0);
+    return GNN_OK;
+}
+
+gnn_status gnn_linear(const gnn_dense *x, void *ws, size_t ws_bytes, gnn_stream stream) {
+    DenseArgs a;
+    GNN_TRY(linear_sizes(x, &a));
+    GNN_TRY(dense_inputs(x, &a));
+    if (!x->w) return GNN_ERR_INVALID_ARG;
+    if (x->residual) GNN_TRY(check_ld(x->ld_residual, x->d_out));
+    a.w[0] = x->w;
+    a.bias[0] = x->bias;
+    a.res = x->residual;
+    a.ld_res = x->ld_residual;
+    a.pre[0] = x->pre;
+    return dense_forward(x, &a, ws, ws_bytes, stream);
+}
+
+gnn_status gnn_linear_backward(const gnn_dense *x, const gnn_dense_grad *g, void *ws, size_t ws_bytes,
+                               gnn_stream stream) {
+    DenseArgs a;
+    GNN_TRY(linear_sizes(x, &a));
+    GNN_TRY(dense_inputs(x, &a));
+    if (!g || (g->dx && !x->w)) return GNN_ERR_INVALID_ARG;
+    if (x->n > 0 && x->activation != GNN_ACT_NONE && !x->pre) return GNN_ERR_INVALID_ARG;
+    a.w[0] = x->w;
+    a.pre[0] = x->pre;
+    a.dw[0] = g->dw;
+    a.dbias[0] = g->dbias;
+    return dense_backward(x, g, &a, ws, ws_bytes, stream);
+}
+
+gnn_status gnn_gated_linear_workspace_size(const gnn_gated *x, int32_t backward, size_t *out_bytes) {
+    if (!out_bytes) return GNN_ERR_INVALID_ARG;
+    DenseArgs a;
+    GNN_TRY(gated_sizes(x, &a));
+    *out_bytes = dense_bytes(a, backward != 0);
+    return GNN_OK;
+}
+
+gnn_status gnn_gated_linear(const gnn_gated *x, void *ws, size_t ws_bytes, gnn_stream stream) {
+    DenseArgs a;
+    GNN_TRY(gated_sizes(x, &a));
+    GNN_TRY(dense_inputs(x, &a));
+    if (!x->w_gate || !x->w_up) return GNN_ERR_INVALID_ARG;
+    a.w[0] = x->w_gate;
+    a.w[1] = x->w_up;
+    a.bias[0] = x->bias_gate;
+    a.bias[1] = x->bias_up;
+    a.pre[0] = x->gate;
+    a.pre[1] = x->up;
+    return dense_forward(x, &a, ws, ws_bytes, stream);
+}
+
+gnn_status gnn_gated_linear_backward(const gnn_gated *x, const gnn_gated_grad *g, void *ws, size_t ws_bytes,
+                                     gnn_stream stream) {
+    DenseArgs a;
+    GNN_TRY(gated_sizes(x, &a));
+    GNN_TRY(dense_inputs(x, &a));
+    if (!g || (g->dx && (!x->w_gate || !x->w_up))) return GNN_ERR_INVALID_ARG;
+    if (x->n > 0 && (!x->gate || !x->up)) return GNN_ERR_INVALID_ARG;
+    a.w[0] = x->w_gate;
+    a.w[1] = x->w_up;
+    a.pre[0] = x->gate;
+    a.pre[1] = x->up;
+    a.dw[0] = g->dw_gate;
+    a.dw[1] = g->dw_up;
+    a.dbias[0] = g->dbias_gate;
+    a.dbias[1] = g->dbias_up;
+    return dense_backward(x, g, &a, ws, ws_bytes, stream);
+}
+
 gnn_status gnn_read_device_status(const void *ws, gnn_stream stream, gnn_status *out) {
     if (!ws || !out) return GNN_ERR_INVALID_ARG;
     hipStream_t s = static_cast<hipStream_t>(stream);

@@ -1,5 +1,5 @@
 // Launchers of the learned side of the path (embedding lookup and gradient, cross attention,
-// orthogonalised updates), and the element types they share.  Internal; not part of the ABI.
+// orthogonalised updates, layer norm, dense layers), and the element types they share.  Internal; not part of the ABI.
 #pragma once
 
 #include "common.hpp"
@@ -135,5 +135,68 @@ size_t newton_bytes(int64_t rows, int64_t cols, int64_t batch, int32_t type);
 // Whether the values of these steps fit the planes they are kept in.
 bool newton_in_range(const float *coefs, int steps);
 hipError_t launch_newton(const NewtonArgs &a, hipStream_t s);
+
+// out[c] = the sum of `parts` rows of sums [parts][ld], c < cols, for out0 and, `second` columns further,
+// out1 (each may be NULL); added in fp32 in a fixed order.
+hipError_t launch_column_sums(const float *sums, int64_t ld, int parts, int64_t cols, int64_t second, int type, void *out0,
+                              void *out1, hipStream_t s);
+
+// ---- layer norm -------------------------------------------------------------------------------------
+
+struct NormArgs {
+    const void *x;
+    int32_t x_type, out_type, param_type;
+    int64_t ld_x;
+    const int64_t *d_n;
+    int64_t n, d;
+    const void *weight, *bias;             // may be NULL: ones, zeros
+    float eps;
+    void *out;
+    int64_t ld_out;
+    float *mean, *rstd;                    // [n]; forward: may be NULL
+    // backward
+    const void *dout, *dres;               // of out's and of x's type; dres may be NULL
+    int64_t ld_dout, ld_dres;
+    void *dx;                              // x's type, may be NULL
+    int64_t ld_dx;
+    void *dweight, *dbias;                 // of the parameters' type, may be NULL
+    char *ws;
+};
+size_t norm_bytes(int64_t n, int64_t d);
+hipError_t launch_norm(const NormArgs &a, hipStream_t s);
+hipError_t launch_norm_backward(const NormArgs &a, hipStream_t s);
+
+// ---- dense layers -----------------------------------------------------------------------------------
+
+// One layer, or the gated pair of them (pair = 1: index 0 is the gate, 1 the other projection).
+struct DenseArgs {
+    int32_t type, act, pair;
+    int64_t n, d_in, d_out;
+    const int64_t *d_n;
+    const void *x;
+    int64_t ld_x;
+    const void *w[2];
+    int64_t ld_w;
+    const void *bias[2];
+    const void *res;
+    int64_t ld_res;
+    void *out;
+    int64_t ld_out;
+    void *pre[2];                          // backward: read
+    int64_t ld_pre;
+    // backward
+    const void *dout;
+    int64_t ld_dout;
+    void *dx;                              // any of the gradients may be NULL
+    int64_t ld_dx;
+    void *dw[2];
+    int64_t ld_dw;
+    void *dbias[2];
+    char *ws;
+};
+// Bytes of workspace for type, pair, n, d_in, d_out, whatever the activation and the rows' alignment.
+size_t dense_bytes(const DenseArgs &a, bool backward);
+hipError_t launch_dense(const DenseArgs &a, hipStream_t s);
+hipError_t launch_dense_backward(const DenseArgs &a, hipStream_t s);
 
 }  // namespace gnnmb

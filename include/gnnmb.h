@@ -61,6 +61,15 @@ typedef void *gnn_stream; /* hipStream_t */
 #define GNN_F32 0
 #define GNN_BF16 1
 
+/* Activations of the calls that take one: gelu is z Phi(z) with the normal distribution's Phi, gelu_tanh
+ * z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))), silu z / (1 + e^-z). */
+#define GNN_ACT_NONE 0
+#define GNN_ACT_RELU 1
+#define GNN_ACT_GELU 2
+#define GNN_ACT_GELU_TANH 3
+#define GNN_ACT_SILU 4
+#define GNN_ACT_SIGMOID 5
+
 /* Flags for gnn_options.flags. */
 #define GNN_SYNC 1u /* synchronise the stream at the end of the call and return the device status */
 /* How gnn_minibatch relabels the sub-batches of a super-batch (results are identical; at most one
@@ -636,6 +645,148 @@ gnn_status gnn_orthogonalize(const void *g, int32_t type, int64_t batch, int64_t
                              int64_t ld_g, int64_t stride_g, int32_t steps, const float *coefs,
                              float eps, float scale, void *out, int64_t ld_out, int64_t stride_out,
                              void *ws, size_t ws_bytes, gnn_stream stream);
+
+/*
+ * Layer norm of the rows of x: with m = sum x / d, v = sum (x - m)^2 / d and r = 1 / sqrt(v + eps),
+ *   out[i, j] = (x[i, j] - m_i) r_i weight[j] + bias[j],  mean[i] = m_i,  rstd[i] = r_i.
+ * gnn_layer_norm_backward: with mean and rstd of the forward call and dout [n, ld_dout],
+ *   g = dout weight,  h = (x - m) r,
+ *   dx = r (g - sum g / d - h sum (g h) / d) + residual_grad,
+ *   dweight = sum over rows of dout h,  dbias = sum over rows of dout,
+ * all sums in fp32 in an order that the sizes alone decide, each result rounded once.
+ *   x, dx, residual_grad: [n, ld] of x_type; out, dout: [n, ld] of out_type; weight, bias, dweight, dbias:
+ *     [d] of param_type; types GNN_F32 or GNN_BF16; mean, rstd: float [n].  Rows may start at any multiple
+ *     of their element.  weight (ones), bias (zeros) and residual_grad (zeros) may be NULL; mean and rstd
+ *     may be NULL for gnn_layer_norm, which may also write out over x where the types and row strides
+ *     are the same; gnn_layer_norm_backward reads neither bias nor out, writes those of dx, dweight and dbias that
+ *     are not NULL, and dx over residual_grad if that is the same array.  No other output may overlap an
+ *     input or another output.
+ *   n and d_n as in gnn_gather_features: rows at or past *d_n are left as they are, and add nothing.
+ *   ws: 16-byte aligned, ws_bytes >= gnn_layer_norm_workspace_size(n, d).
+ * Errors: GNN_ERR_INVALID_ARG; GNN_ERR_CAPACITY (ws too small); GNN_ERR_UNSUPPORTED for another type, n over
+ * 2^31 - 1 or d over 16384.
+ */
+typedef struct gnn_norm {
+    int32_t x_type, out_type, param_type;
+    float eps;
+    int64_t n, d;
+    const int64_t *d_n;
+    const void *x;
+    int64_t ld_x;
+    const void *weight, *bias;
+    void *out;
+    int64_t ld_out;
+    float *mean, *rstd;
+} gnn_norm;
+
+typedef struct gnn_norm_grad {
+    const void *dout;
+    int64_t ld_dout;
+    const void *residual_grad;
+    int64_t ld_residual_grad;
+    void *dx;
+    int64_t ld_dx;
+    void *dweight, *dbias;
+} gnn_norm_grad;
+
+gnn_status gnn_layer_norm(const gnn_norm *x, gnn_stream stream);
+gnn_status gnn_layer_norm_workspace_size(int64_t n, int64_t d, size_t *out_bytes);
+gnn_status gnn_layer_norm_backward(const gnn_norm *x, const gnn_norm_grad *g, void *ws, size_t ws_bytes,
+                                   gnn_stream stream);
+
+/*
+ * A dense layer: pre = x w + bias, out = act(pre) + residual, with x [n, ld_x] (d_in columns), w [d_in,
+ * ld_w] (d_out columns: the layout of gnn_sage_update's W), out, pre and residual [n, ld] (d_out), bias
+ * [d_out], all of one type, GNN_F32 or GNN_BF16; activation: GNN_ACT_*.  Rows may start at any multiple of their
+ * element (rows at multiples of 16 bytes are faster).  bias, residual and pre may be NULL; out may be
+ * residual itself.  Sums are fp32; out and pre are rounded once, each from the fp32 sums.
+ * gnn_linear_backward: with dout [n, ld_dout] and pre of the forward call (not read for GNN_ACT_NONE),
+ *   dpre = dout act'(pre),  dx = dpre w^T,  dw = x^T dpre,  dbias = sum over rows of dpre;
+ * those of dx [n, ld_dx], dw [d_in, ld_dw] and dbias that are not NULL are written (the residual's gradient
+ *   is dout).  act' of relu is 0 at 0.  For GNN_BF16 with an activation, dpre is multiplied as one bf16, or as
+ *   two where fewer than 512 terms are summed; every sum is fp32, in an order that the sizes alone decide.
+ *   bias, residual and out of x are not read.
+ *   n and d_n as in gnn_gather_features: rows at or past *d_n are left as they are, and add nothing.
+ *   No output may overlap an input or another output, but for out and residual.
+ *   ws: 16-byte aligned, ws_bytes >= gnn_linear_workspace_size(x, backward); x->type, n, d_in and d_out
+ *   decide it.
+ * Errors: GNN_ERR_INVALID_ARG; GNN_ERR_CAPACITY (ws too small); GNN_ERR_UNSUPPORTED for another type or
+ * activation, n over 2^30, d_in or d_out over 2^20, or rows over 2^21 elements apart.
+ */
+typedef struct gnn_dense {
+    int32_t type, activation;
+    int64_t n, d_in, d_out;
+    const int64_t *d_n;
+    const void *x;
+    int64_t ld_x;
+    const void *w;
+    int64_t ld_w;
+    const void *bias;
+    const void *residual;
+    int64_t ld_residual;
+    void *out;
+    int64_t ld_out;
+    void *pre;
+    int64_t ld_pre;
+} gnn_dense;
+
+typedef struct gnn_dense_grad {
+    const void *dout;
+    int64_t ld_dout;
+    void *dx;
+    int64_t ld_dx;
+    void *dw;
+    int64_t ld_dw;
+    void *dbias;
+} gnn_dense_grad;
+
+gnn_status gnn_linear_workspace_size(const gnn_dense *x, int32_t backward, size_t *out_bytes);
+gnn_status gnn_linear(const gnn_dense *x, void *ws, size_t ws_bytes, gnn_stream stream);
+gnn_status gnn_linear_backward(const gnn_dense *x, const gnn_dense_grad *g, void *ws, size_t ws_bytes,
+                               gnn_stream stream);
+
+/*
+ * The gated pair of projections of a feed-forward block, in one kernel:
+ *   gate = x w_gate + bias_gate,  up = x w_up + bias_up,  out = act(gate) up,
+ * shapes, types and strides as in gnn_linear; w_gate and w_up have one row stride (the halves of one
+ * [d_in, 2 d_out] matrix, or matrices of their own), and so have gate and up, of which either may be NULL.
+ * out is rounded once, from the fp32 sums.
+ * gnn_gated_linear_backward: with dout and gate and up of the forward call,
+ *   dgate = dout up act'(gate),  dup = dout act(gate),  dx = dgate w_gate^T + dup w_up^T,
+ *   dw_gate = x^T dgate,  dw_up = x^T dup,  dbias_gate, dbias_up = the sums of their rows;
+ * those that are not NULL are written; numbers as in gnn_linear_backward (for dx, the terms of both products
+ * count).  bias_gate, bias_up and out of x are not read.
+ *   d_n, overlaps, ws and errors as in gnn_linear.
+ */
+typedef struct gnn_gated {
+    int32_t type, activation;
+    int64_t n, d_in, d_out;
+    const int64_t *d_n;
+    const void *x;
+    int64_t ld_x;
+    const void *w_gate, *w_up;
+    int64_t ld_w;
+    const void *bias_gate, *bias_up;
+    void *out;
+    int64_t ld_out;
+    void *gate, *up;
+    int64_t ld_pre;
+} gnn_gated;
+
+typedef struct gnn_gated_grad {
+    const void *dout;
+    int64_t ld_dout;
+    void *dx;
+    int64_t ld_dx;
+    void *dw_gate, *dw_up;
+    int64_t ld_dw;
+    void *dbias_gate, *dbias_up;
+} gnn_gated_grad;
+
+gnn_status gnn_gated_linear_workspace_size(const gnn_gated *x, int32_t backward, size_t *out_bytes);
+gnn_status gnn_gated_linear(const gnn_gated *x, void *ws, size_t ws_bytes, gnn_stream stream);
+gnn_status gnn_gated_linear_backward(const gnn_gated *x, const gnn_gated_grad *g, void *ws, size_t ws_bytes,
+                                     gnn_stream stream);
 
 /*
  * Device status word of a workspace: synchronises `stream`, returns the first device error
