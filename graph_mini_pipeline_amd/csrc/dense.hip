@@ -19,25 +19,26 @@ namespace gnnmb {
 
 namespace {
 
-// out[c] = the sum of `parts` rows of sums; a workgroup takes 32 columns, 8 rows at a time.
+// out[c] = the sum of `parts` rows of sums; a workgroup takes 32 columns, 32 rows at a time.
+constexpr int kColumnHigh = 32;
 template <typename T>
-__global__ __launch_bounds__(256) void k_column_sums(const float *sums, int64_t ld, int parts, int64_t cols, int64_t second,
-                                                     void *out0, void *out1) {
+__global__ __launch_bounds__(32 * kColumnHigh) void k_column_sums(const float *sums, int64_t ld, int parts, int64_t cols,
+                                                                  int64_t second, void *out0, void *out1) {
     const int x = threadIdx.x % 32, y = threadIdx.x / 32;
     const int64_t c = blockIdx.x * 32ll + x;
     T *out = static_cast<T *>(blockIdx.y ? out1 : out0);
     if (out == nullptr) return;
     float s = 0.f;
     if (c < cols) {
-#pragma unroll 4
-        for (int i = y; i < parts; i += 8) s += sums[i * ld + blockIdx.y * second + c];
+#pragma unroll 8
+        for (int i = y; i < parts; i += kColumnHigh) s += sums[i * ld + blockIdx.y * second + c];
     }
-    __shared__ float lds[8][33];
+    __shared__ float lds[kColumnHigh][33];
     lds[y][x] = s;
     __syncthreads();
     if (y == 0 && c < cols) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += lds[i][x];
+        for (int i = 1; i < kColumnHigh; ++i) s += lds[i][x];
         out[c] = static_cast<T>(s);
     }
 }
@@ -326,9 +327,9 @@ hipError_t launch_column_sums(const float *sums, int64_t ld, int parts, int64_t 
                               void *out1, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>((cols + 31) / 32), 2);
     if (type == GNN_BF16)
-        k_column_sums<bf16><<<grid, 256, 0, s>>>(sums, ld, parts, cols, second, out0, out1);
+        k_column_sums<bf16><<<grid, 32 * kColumnHigh, 0, s>>>(sums, ld, parts, cols, second, out0, out1);
     else
-        k_column_sums<float><<<grid, 256, 0, s>>>(sums, ld, parts, cols, second, out0, out1);
+        k_column_sums<float><<<grid, 32 * kColumnHigh, 0, s>>>(sums, ld, parts, cols, second, out0, out1);
     return hipGetLastError();
 }
 

@@ -17,38 +17,53 @@ namespace gnnmb {
 
 namespace {
 
-constexpr int V = 8;
 constexpr int kNormThreads = 256;
 
-template <typename T>
-__device__ __forceinline__ vec<float, V> load_piece(const T *p, int64_t left) {
-    if (left >= V) return load_f32<T, V>(p);
-    vec<float, V> v(0.f);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (i < left) v[i] = static_cast<float>(p[i]);
-    return v;
-}
-
-template <typename T>
-__device__ __forceinline__ void store_piece(T *p, int64_t left, vec<float, V> v) {
-    if (left >= V) {
-        store_f32<T, V>(p, v);
-        return;
+// Piece j of lane l of G: V elements, the row's last ones where it would reach past its end.  Those that
+// an earlier piece holds too (the first `twice`) count once in sums; computed and stored they are the same.
+template <int G, int V>
+struct Piece {
+    int c;           // first column
+    int twice;       // V or more: the piece is a copy altogether
+    __device__ __forceinline__ Piece(int j, int l, int cols) {
+        const int at = (j * G + l) * V;
+        c = at < cols - V ? at : cols - V;
+        twice = at - c;
     }
+    // The sum of the elements that count; `ragged` (uniform): some piece of the row counts in part.
+    __device__ __forceinline__ float sum(vec<float, V> v, bool ragged) const {
+        if (ragged) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (i < left) p[i] = static_cast<T>(v[i]);
+            for (int i = 0; i < V; ++i) v[i] = i >= twice ? v[i] : 0.f;
+        }
+        float s = v[0];
+        if constexpr (V == 8) s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        return twice < V ? s : 0.f;
+    }
+};
+
+template <int V, typename T>
+__device__ __forceinline__ vec<T, V> load_raw(const T *p) {
+    return *reinterpret_cast<const typename loose<T, V>::type *>(p);
 }
 
-__device__ __forceinline__ vec<float, V> load_param(const void *p, int32_t type, int64_t c, int64_t left, float otherwise) {
+// Forgets what has been computed of v: what a later pass needs of it is computed again from the piece as
+// it was loaded (half the registers for bf16), not kept.
+template <typename T, int V>
+__device__ __forceinline__ void again(vec<T, V> &v) {
+    if constexpr (sizeof(T) * V == 16) {
+        typedef vec<uint32_t, 4> Words;
+        Words x = __builtin_bit_cast(Words, v);
+        asm volatile("" : "+v"(x));
+        v = __builtin_bit_cast(vec<T, V>, x);
+    }
+}
+
+template <int V>
+__device__ __forceinline__ vec<float, V> load_param(const void *p, int32_t type, int c, float otherwise) {
     if (p == nullptr) return vec<float, V>(otherwise);
-    return type == GNN_BF16 ? load_piece(static_cast<const bf16 *>(p) + c, left)
-                            : load_piece(static_cast<const float *>(p) + c, left);
-}
-
-__device__ __forceinline__ float sum_of(vec<float, V> v) {
-    return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    return type == GNN_BF16 ? load_f32<bf16, V>(static_cast<const bf16 *>(p) + c)
+                            : load_f32<float, V>(static_cast<const float *>(p) + c);
 }
 
 // The sums of N values over the G threads of a row, in all of them.  G over 64: `lds` has N floats a
@@ -76,113 +91,138 @@ __device__ __forceinline__ void sum_row(float (&v)[N], float *lds) {
     }
 }
 
-// G threads a row of up to G * V * CH elements.
-template <typename TX, typename TO, int G, int CH>
+// Which of the workgroup's rows this thread works on: one for a wavefront of lane groups of 64 or more.
+template <int G>
+__device__ __forceinline__ int group_of() {
+    const int g = static_cast<int>(threadIdx.x) / G;
+    return G >= 64 ? __builtin_amdgcn_readfirstlane(g) : g;
+}
+
+// G threads a row of up to G * V * CH elements, R rows at a time; the parameters stay in registers.
+template <typename TX, typename TO, int G, int CH, int R, int V>
 __global__ __launch_bounds__(G > kNormThreads ? G : kNormThreads) void k_norm(NormArgs p) {
     constexpr int kThreads = G > kNormThreads ? G : kNormThreads, kRows = kThreads / G;
-    __shared__ float lds[2][G > 64 ? G / 64 : 1];
+    typedef vec<float, V> Wide;
+    __shared__ float lds[2][(G > 64 ? G / 64 : 1) * R];
     const int64_t n = load_count(p.d_n, p.n);
-    const int l = threadIdx.x % G;
+    const int l = threadIdx.x % G, cols = static_cast<int>(p.d);
+    const bool ragged = cols % V != 0;
     const float d = static_cast<float>(p.d);      // divided by: equal elements have their own value as mean
-    for (int64_t m = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G; m < n; m += static_cast<int64_t>(gridDim.x) * kRows) {
-        const TX *row = static_cast<const TX *>(p.x) + m * p.ld_x;
-        vec<float, V> x[CH];
-        float s[1] = {0.f};
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+    Wide w[CH], b[CH];
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const int64_t c = (j * G + l) * V;
-            x[j] = load_piece(row + c, p.d - c);
+    for (int j = 0; j < CH; ++j) {
+        const Piece<G, V> at(j, l, cols);
+        w[j] = load_param<V>(p.weight, p.param_type, at.c, 1.f);
+        b[j] = load_param<V>(p.bias, p.param_type, at.c, 0.f);
+    }
+    // (a workgroup that is one lane group leaves the loop as a whole)
+    for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRows + group_of<G>(); m0 < n; m0 += step * R) {
+        vec<TX, V> raw[R][CH];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            // past the end the first row again, which is not stored
+            const int64_t m = m0 + r * step < n ? m0 + r * step : m0;
+            const TX *row = static_cast<const TX *>(p.x) + m * p.ld_x;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) raw[r][j] = load_raw<V>(row + Piece<G, V>(j, l, cols).c);
         }
+        float s[R], mean[R];
 #pragma unroll
-        for (int j = 0; j < CH; ++j) s[0] += sum_of(x[j]);
+        for (int r = 0; r < R; ++r) {
+            s[r] = 0.f;
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+                s[r] += Piece<G, V>(j, l, cols).sum(__builtin_convertvector(raw[r][j], Wide), ragged);
+        }
         sum_row<G>(s, lds[0]);
-        const float mean = s[0] / d;
-        s[0] = 0.f;
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const int64_t left = p.d - (j * G + l) * V;
-            x[j] -= mean;
-            if (left < V) {
+        for (int r = 0; r < R; ++r) {
+            mean[r] = s[r] / d;
+            s[r] = 0.f;
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (i >= left) x[j][i] = 0.f;
+            for (int j = 0; j < CH; ++j) {
+                again(raw[r][j]);
+                const Wide x = __builtin_convertvector(raw[r][j], Wide) - mean[r];
+                s[r] += Piece<G, V>(j, l, cols).sum(x * x, ragged);
             }
-            s[0] += sum_of(x[j] * x[j]);
         }
         sum_row<G>(s, lds[1]);
-        const float rstd = 1.f / sqrtf(s[0] / d + p.eps);
-        if (l == 0) {
-            if (p.mean) p.mean[m] = mean;
-            if (p.rstd) p.rstd[m] = rstd;
-        }
-        TO *out = static_cast<TO *>(p.out) + m * p.ld_out;
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            const int64_t c = (j * G + l) * V, left = p.d - c;
-            if (left <= 0) break;
-            const vec<float, V> w = load_param(p.weight, p.param_type, c, left, 1.f);
-            const vec<float, V> b = load_param(p.bias, p.param_type, c, left, 0.f);
-            store_piece(out + c, left, x[j] * rstd * w + b);
+        for (int r = 0; r < R; ++r) {
+            const int64_t m = m0 + r * step;
+            if (m >= n) break;
+            const float rstd = 1.f / sqrtf(s[r] / d + p.eps);
+            if (l == 0) {
+                if (p.mean) p.mean[m] = mean[r];
+                if (p.rstd) p.rstd[m] = rstd;
+            }
+            TO *out = static_cast<TO *>(p.out) + m * p.ld_out;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                const Piece<G, V> at(j, l, cols);
+                again(raw[r][j]);
+                if (at.twice < V)
+                    store_f32<TO, V>(out + at.c, (__builtin_convertvector(raw[r][j], Wide) - mean[r]) * rstd * w[j] + b[j]);
+            }
         }
     }
 }
 
-template <typename TX, typename TO, int G, int CH>
+template <typename TX, typename TO, int G, int CH, int R, int V>
 __global__ __launch_bounds__(G > kNormThreads ? G : kNormThreads) void k_norm_backward(NormArgs p, float *sums) {
     constexpr int kThreads = G > kNormThreads ? G : kNormThreads, kRows = kThreads / G;
-    constexpr int R = G > 512 ? 1 : 2;   // rows that a lane group loads at a time (128 registers a lane at G = 1024)
+    typedef vec<float, V> Wide;
     __shared__ float lds[2][(G > 64 ? G / 64 : 1) * 2 * R];
     const int64_t n = load_count(p.d_n, p.n);
-    const int l = threadIdx.x % G;
+    const int l = threadIdx.x % G, cols = static_cast<int>(p.d);
+    const bool ragged = cols % V != 0;
     const float inv_d = 1.f / static_cast<float>(p.d);
-    vec<float, V> w[CH], dw[CH], db[CH];
+    Wide w[CH], dw[CH], db[CH];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-        const int64_t c = (j * G + l) * V;
-        w[j] = load_param(p.weight, p.param_type, c, p.d - c, 1.f);
-        dw[j] = db[j] = vec<float, V>(0.f);
+        w[j] = load_param<V>(p.weight, p.param_type, Piece<G, V>(j, l, cols).c, 1.f);
+        dw[j] = db[j] = Wide(0.f);
     }
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
     int turn = 0;
-    // (a workgroup that is one lane group leaves the loop as a whole)
-    for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / G; m0 < n; m0 += step * R, turn ^= 1) {
-        vec<float, V> x[R][CH], g[R][CH];
-        float s[2 * R], rstd[R];
+    for (int64_t m0 = static_cast<int64_t>(blockIdx.x) * kRows + group_of<G>(); m0 < n; m0 += step * R, turn ^= 1) {
+        vec<TX, V> x[R][CH], dres[R][CH];
+        vec<TO, V> dy[R][CH];
+        float s[2 * R], mean[R], rstd[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            // past the end the last row again, which then counts for nothing
-            const bool there = m0 + r * step < n;
-            const int64_t m = there ? m0 + r * step : m0;
+            // past the end the first row again, which then counts for nothing
+            const int64_t m = m0 + r * step < n ? m0 + r * step : m0;
             const TX *row = static_cast<const TX *>(p.x) + m * p.ld_x;
-            const TO *dy = static_cast<const TO *>(p.dout) + m * p.ld_dout;
+            const TO *from = static_cast<const TO *>(p.dout) + m * p.ld_dout;
+            mean[r] = p.mean[m];
+            rstd[r] = p.rstd[m];
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                const int64_t c = (j * G + l) * V;
-                x[r][j] = load_piece(row + c, p.d - c);
-                g[r][j] = load_piece(dy + c, p.d - c);
+                const int c = Piece<G, V>(j, l, cols).c;
+                x[r][j] = load_raw<V>(row + c);
+                dy[r][j] = load_raw<V>(from + c);
+                if (p.dres) dres[r][j] = load_raw<V>(static_cast<const TX *>(p.dres) + m * p.ld_dres + c);
             }
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const bool there = m0 + r * step < n;
-            const int64_t m = there ? m0 + r * step : m0;
-            const float mean = p.mean[m];
-            rstd[r] = p.rstd[m];
-            float sg = 0.f, sgh = 0.f;
+            const bool there = r == 0 || m0 + r * step < n;
+            s[2 * r] = s[2 * r + 1] = 0.f;
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                const vec<float, V> h = (x[r][j] - mean) * rstd[r];
+                const Piece<G, V> at(j, l, cols);
+                const Wide h = (__builtin_convertvector(x[r][j], Wide) - mean[r]) * rstd[r];
+                const Wide g = __builtin_convertvector(dy[r][j], Wide);
                 if (there) {
-                    dw[j] += g[r][j] * h;
-                    db[j] += g[r][j];
+                    dw[j] += g * h;
+                    db[j] += g;
                 }
-                x[r][j] = h;
-                g[r][j] *= w[j];
-                sg += sum_of(g[r][j]);
-                sgh += sum_of(g[r][j] * h);
+                const Wide gw = g * w[j];
+                s[2 * r] += at.sum(gw, ragged);
+                s[2 * r + 1] += at.sum(gw * h, ragged);
             }
-            s[2 * r] = sg;
-            s[2 * r + 1] = sgh;
         }
         if (p.dx == nullptr) continue;
         sum_row<G>(s, lds[turn]);
@@ -192,40 +232,45 @@ __global__ __launch_bounds__(G > kNormThreads ? G : kNormThreads) void k_norm_ba
             if (m >= n) break;
             const float sg = s[2 * r] * inv_d, sgh = s[2 * r + 1] * inv_d;
             TX *dx = static_cast<TX *>(p.dx) + m * p.ld_dx;
-            const TX *dres = p.dres ? static_cast<const TX *>(p.dres) + m * p.ld_dres : nullptr;
 #pragma unroll
             for (int j = 0; j < CH; ++j) {
-                const int64_t c = (j * G + l) * V, left = p.d - c;
-                if (left <= 0) break;
-                vec<float, V> v = (g[r][j] - sg - x[r][j] * sgh) * rstd[r];
-                if (dres) v += load_piece(dres + c, left);
-                store_piece(dx + c, left, v);
+                const Piece<G, V> at(j, l, cols);
+                if (at.twice >= V) continue;
+                again(x[r][j]);
+                again(dy[r][j]);
+                const Wide h = (__builtin_convertvector(x[r][j], Wide) - mean[r]) * rstd[r];
+                Wide v = (__builtin_convertvector(dy[r][j], Wide) * w[j] - sg - h * sgh) * rstd[r];
+                if (p.dres) v += __builtin_convertvector(dres[r][j], Wide);
+                store_f32<TX, V>(dx + at.c, v);
             }
         }
     }
     if (sums == nullptr) return;
-    // the groups' sums, joined; part b: [dweight, dbias] of d columns each
+    // the groups' sums, joined: [dweight, dbias] of the workgroup
     float *to = sums + static_cast<int64_t>(blockIdx.x) * 2 * p.d;
     if (kRows == 1) {
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int64_t c = (j * G + l) * V, left = p.d - c;
-            if (left <= 0) break;
-            store_piece(to + c, left, dw[j]);
-            store_piece(to + p.d + c, left, db[j]);
+            const Piece<G, V> at(j, l, cols);
+            if (at.twice >= V) continue;
+            store_f32<float, V>(to + at.c, dw[j]);
+            store_f32<float, V>(to + p.d + at.c, db[j]);
         }
         return;
     }
-    __shared__ float joined[kRows > 1 ? kRows * G * V * CH : 1];
     constexpr int kWide = G * V * CH;
+    __shared__ float joined[kRows > 1 ? kRows * kWide : 1];
     for (int half = 0; half < 2; ++half) {
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
+        for (int j = 0; j < CH; ++j) {
+            const Piece<G, V> at(j, l, cols);
 #pragma unroll
-            for (int i = 0; i < V; ++i) joined[threadIdx.x / G * kWide + (j * G + l) * V + i] = half ? db[j][i] : dw[j][i];
+            for (int i = 0; i < V; ++i)
+                if (at.twice < V) joined[threadIdx.x / G * kWide + at.c + i] = half ? db[j][i] : dw[j][i];
+        }
         __syncthreads();
-        for (int c = threadIdx.x; c < p.d; c += kThreads) {
+        for (int c = threadIdx.x; c < cols; c += kThreads) {
             float v = 0.f;
             for (int r = 0; r < kRows; ++r) v += joined[r * kWide + c];
             to[half * p.d + c] = v;
@@ -233,71 +278,48 @@ __global__ __launch_bounds__(G > kNormThreads ? G : kNormThreads) void k_norm_ba
     }
 }
 
-// Threads a row, and pieces a thread: f(G, CH).
+// Threads a row, pieces a thread and rows at a time, and elements a piece, by the row's width: f(G, CH, R, V).
 template <typename F>
-hipError_t by_forward_width(int64_t d, F f) {
+hipError_t by_width(int64_t d, F f) {
     using std::integral_constant;
-    const integral_constant<int, 8> g8{};
-    const integral_constant<int, 16> g16{};
-    const integral_constant<int, 32> g32{};
-    const integral_constant<int, 64> g64{};
-    const integral_constant<int, 256> g256{};
-    const integral_constant<int, 1> c1{};
-    const integral_constant<int, 2> c2{};
-    const integral_constant<int, 4> c4{};
-    const integral_constant<int, 8> c8{};
-    if (d <= 8 * V) return f(g8, c1);
-    if (d <= 16 * V) return f(g16, c1);
-    if (d <= 32 * V) return f(g32, c1);
-    if (d <= 64 * V) return f(g64, c1);
-    if (d <= 128 * V) return f(g64, c2);
-    if (d <= 256 * V) return f(g64, c4);
-    if (d <= 512 * V) return f(g64, c8);
-    if (d <= 1024 * V) return f(g256, c4);
-    return f(g256, c8);
+    const integral_constant<int, 1> one{};
+    const integral_constant<int, 2> two{};
+    const integral_constant<int, 8> eight{};
+    if (d < 8) return f(eight, one, two, one);
+    if (d <= 64) return f(eight, one, two, eight);
+    if (d <= 128) return f(integral_constant<int, 16>{}, one, two, eight);
+    if (d <= 256) return f(integral_constant<int, 32>{}, one, two, eight);
+    if (d <= 512) return f(integral_constant<int, 64>{}, one, two, eight);
+    if (d <= 1024) return f(integral_constant<int, 64>{}, two, two, eight);
+    if (d <= 2048) return f(integral_constant<int, 256>{}, one, two, eight);
+    if (d <= 4096) return f(integral_constant<int, 256>{}, two, two, eight);
+    if (d <= 8192) return f(integral_constant<int, 512>{}, two, two, eight);
+    return f(integral_constant<int, 1024>{}, two, one, eight);      // 128 registers a lane
 }
 
-// Fewer pieces a thread: it keeps the sums of dw and db beside x and dy.
-template <typename F>
-hipError_t by_backward_width(int64_t d, F f) {
-    using std::integral_constant;
-    const integral_constant<int, 8> g8{};
-    const integral_constant<int, 16> g16{};
-    const integral_constant<int, 32> g32{};
-    const integral_constant<int, 64> g64{};
-    const integral_constant<int, 256> g256{};
-    const integral_constant<int, 512> g512{};
-    const integral_constant<int, 1024> g1024{};
-    const integral_constant<int, 1> c1{};
-    const integral_constant<int, 2> c2{};
-    if (d <= 8 * V) return f(g8, c1);
-    if (d <= 16 * V) return f(g16, c1);
-    if (d <= 32 * V) return f(g32, c1);
-    if (d <= 64 * V) return f(g64, c1);
-    if (d <= 128 * V) return f(g64, c2);
-    if (d <= 256 * V) return f(g256, c1);
-    if (d <= 512 * V) return f(g256, c2);
-    if (d <= 1024 * V) return f(g512, c2);
-    return f(g1024, c2);
-}
-
-// Workgroups of the backward pass: as many as keep memory busy, and no more than their partial sums are
-// worth (two a compute unit for wide rows: 512 x 2 x 4096 sums take 3% of the time of 32768 rows).
-int64_t backward_blocks(int64_t n, int64_t d) {
-    const int64_t rows = d <= 128 * V ? kNormThreads / (d <= 8 * V ? 8 : d <= 16 * V ? 16 : d <= 32 * V ? 32 : 64) : 1;
-    int64_t blocks = (n + rows * 2 - 1) / (rows * 2);
-    const int64_t most = d > 128 * V ? 512 : 1024;
+int64_t row_blocks(int64_t n, int g, int r, int64_t most) {
+    const int rows = g < kNormThreads ? kNormThreads / g : 1;
+    int64_t blocks = (n + rows * r - 1) / (rows * r);
     if (blocks > most) blocks = most;
     return blocks < 1 ? 1 : blocks;
 }
 
+// Workgroups of the backward pass: as many as keep memory busy, and no more than their partial sums are
+// worth.
+int64_t backward_blocks(int64_t n, int64_t d) {
+    int64_t blocks = 0;
+    (void)by_width(d, [&](auto g, auto, auto r, auto) {
+        blocks = row_blocks(n, g, r, d > 1024 ? 512 : 1024);
+        return hipSuccess;
+    });
+    return blocks;
+}
+
 template <typename TX, typename TO>
 hipError_t norm(const NormArgs &a, hipStream_t s) {
-    return by_forward_width(a.d, [&](auto g, auto ch) {
-        constexpr int G = g, CH = ch, kThreads = G > kNormThreads ? G : kNormThreads;
-        int64_t blocks = (a.n + kThreads / G - 1) / (kThreads / G);
-        if (blocks > 1 << 20) blocks = 1 << 20;
-        k_norm<TX, TO, G, CH><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a);
+    return by_width(a.d, [&](auto g, auto ch, auto r, auto v) {
+        constexpr int G = g, CH = ch, R = r, V = v, kThreads = G > kNormThreads ? G : kNormThreads;
+        k_norm<TX, TO, G, CH, R, V><<<static_cast<unsigned>(row_blocks(a.n, G, R, 2048)), kThreads, 0, s>>>(a);
         return hipGetLastError();
     });
 }
@@ -306,9 +328,9 @@ template <typename TX, typename TO>
 hipError_t norm_backward(const NormArgs &a, hipStream_t s) {
     const int64_t blocks = backward_blocks(a.n, a.d);
     float *sums = a.dweight || a.dbias ? reinterpret_cast<float *>(a.ws) : nullptr;
-    const hipError_t err = by_backward_width(a.d, [&](auto g, auto ch) {
-        constexpr int G = g, CH = ch, kThreads = G > kNormThreads ? G : kNormThreads;
-        k_norm_backward<TX, TO, G, CH><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a, sums);
+    const hipError_t err = by_width(a.d, [&](auto g, auto ch, auto r, auto v) {
+        constexpr int G = g, CH = ch, R = r, V = v, kThreads = G > kNormThreads ? G : kNormThreads;
+        k_norm_backward<TX, TO, G, CH, R, V><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a, sums);
         return hipGetLastError();
     });
     if (err != hipSuccess || sums == nullptr) return err;
