@@ -19,163 +19,213 @@ namespace gnnmb {
 
 namespace {
 
-// out[c] = the sum of `parts` rows of sums; a workgroup takes 32 columns, 32 rows at a time.
-constexpr int kColumnHigh = 32;
-template <typename T>
-__global__ __launch_bounds__(32 * kColumnHigh) void k_column_sums(const float *sums, int64_t ld, int parts, int64_t cols,
-                                                                  int64_t second, void *out0, void *out1) {
-    const int x = threadIdx.x % 32, y = threadIdx.x / 32;
-    const int64_t c = blockIdx.x * 32ll + x;
-    T *out = static_cast<T *>(blockIdx.y ? out1 : out0);
-    if (out == nullptr) return;
-    float s = 0.f;
-    if (c < cols) {
-#pragma unroll 8
-        for (int i = y; i < parts; i += kColumnHigh) s += sums[i * ld + blockIdx.y * second + c];
-    }
-    __shared__ float lds[kColumnHigh][33];
-    lds[y][x] = s;
-    __syncthreads();
-    if (y == 0 && c < cols) {
-#pragma unroll
-        for (int i = 1; i < kColumnHigh; ++i) s += lds[i][x];
-        out[c] = static_cast<T>(s);
-    }
-}
-
 constexpr int kCus = 256;
 
-// ---- splits of a summed length, joined -----------------------------------------------------------------
+int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
-template <typename T, bool PAIR>
-__global__ __launch_bounds__(256) void k_product_join(ProductArgs p, int rows_are_n, int wide_log2) {
-    const int64_t rows = rows_are_n ? load_count(p.d_n, p.rows) : p.rows;
-    const int wide = 1 << wide_log2;
-    const int z = blockIdx.y;
-    const int64_t n = ((static_cast<int64_t>(blockIdx.z) << wide_log2) + (threadIdx.x & (wide - 1))) * 4;
-    if (n >= p.cols) return;
-    const int64_t step = gridDim.x * static_cast<int64_t>(256 >> wide_log2);
-    const int64_t products = PAIR ? 2 : p.products;
-    for (int64_t m = blockIdx.x * static_cast<int64_t>(256 >> wide_log2) + (threadIdx.x >> wide_log2); m < rows; m += step) {
-        vec<float, 4> v(0.f), u(0.f);
-        const float *from = p.part + (z * p.rows + m) * p.ld_part + n;
-#pragma unroll 4
-        for (int s = 0; s < p.splits; ++s) {
-            v += *reinterpret_cast<const vec<float, 4> *>(from);
-            if (PAIR) u += *reinterpret_cast<const vec<float, 4> *>(from + p.rows * p.ld_part);
-            from += products * p.rows * p.ld_part;
-        }
-        finish<T, 4, PAIR>(p.e, z, m, n, p.cols - n, v, u);
-    }
+constexpr int kColumnThreads = 1024;
+
+__global__ __launch_bounds__(kColumnThreads) void k_column_sums(ColumnArgs p) {
+    __shared__ float lds[kColumnThreads / 32 * 33];
+    column_sums<kColumnThreads>(p, blockIdx.x, lds);
 }
 
-template <typename T>
-hipError_t launch_join(const ProductArgs &a, bool rows_are_n, bool pair, hipStream_t s) {
-    int wide = 0;
-    while (wide < 8 && (4 << wide) < a.cols) ++wide;
-    const int64_t high = 256 >> wide, groups = (a.cols + (4 << wide) - 1) / (4 << wide);
-    int64_t blocks = (a.rows + high - 1) / high;
-    if (blocks > 4096) blocks = 4096;
-    const dim3 grid(static_cast<unsigned>(blocks), pair ? 1 : a.products, static_cast<unsigned>(groups));
-    if (pair)
-        k_product_join<T, true><<<grid, 256, 0, s>>>(a, rows_are_n, wide);
+// ---- parts of a summed length, joined ------------------------------------------------------------------
+
+// A workgroup takes 256 / L groups of four columns; L threads of each take every L-th part.
+template <typename T, bool PAIR>
+__device__ __forceinline__ void join_parts(const ProductArgs &p, int64_t rows, int lanes_log2, uint32_t block,
+                                           vec<float, 4> *lds) {
+    const uint32_t t = threadIdx.x, wide = 256u >> lanes_log2, lanes = 1u << lanes_log2;
+    const uint32_t groups = static_cast<uint32_t>(p.ld_part >> 2), height = static_cast<uint32_t>(p.rows);
+    const uint32_t e = block * wide + (t & (wide - 1)), lane = t >> (8 - lanes_log2);
+    const uint32_t line = e / groups, z = line / height;
+    const int64_t m = line - z * height, n = (e - line * groups) * 4;
+    const bool there = z < (PAIR ? 1u : static_cast<uint32_t>(p.products)) && m < rows;
+    const int64_t plane = static_cast<int64_t>(p.rows) * p.ld_part, products = PAIR ? 2 : p.products;
+    vec<float, 4> v(0.f), u(0.f);
+    if (there) {
+        const float *from = p.part + (lane * products + z) * plane + m * p.ld_part + n;
+        const int64_t step = lanes * products * plane;
+#pragma unroll 4
+        for (int s = lane; s < p.splits; s += lanes, from += step) {
+            v += *reinterpret_cast<const vec<float, 4> *>(from);
+            if (PAIR) u += *reinterpret_cast<const vec<float, 4> *>(from + plane);
+        }
+    }
+    if (lanes > 1) {
+        lds[t] = v;
+        if (PAIR) lds[256 + t] = u;
+        __syncthreads();
+        if (lane == 0) {
+            for (uint32_t i = 1; i < lanes; ++i) {
+                v += lds[i * wide + t];
+                if (PAIR) u += lds[256 + i * wide + t];
+            }
+        }
+    }
+    if (there && lane == 0) finish<T, 4, PAIR>(p.e, static_cast<int>(z), m, n, p.cols - n, v, u);
+}
+
+struct JoinArgs {
+    ProductArgs p[2];
+    int32_t lanes_log2[2];
+    uint32_t blocks0;            // workgroups of p[0]
+};
+
+// FORWARD: p[0] alone, its rows counted by d_n.  Otherwise p[0] is of dW, p[1] of dx.
+template <typename T, bool FORWARD, bool PAIR>
+__global__ __launch_bounds__(256) void k_product_join(JoinArgs a) {
+    __shared__ vec<float, 4> lds[PAIR ? 512 : 256];
+    if (FORWARD || blockIdx.x < a.blocks0)
+        join_parts<T, PAIR>(a.p[0], FORWARD ? load_count(a.p[0].d_n, a.p[0].rows) : a.p[0].rows, a.lanes_log2[0], blockIdx.x, lds);
     else
-        k_product_join<T, false><<<grid, 256, 0, s>>>(a, rows_are_n, wide);
-    return hipGetLastError();
+        join_parts<T, PAIR>(a.p[1], load_count(a.p[1].d_n, a.p[1].rows), a.lanes_log2[1], blockIdx.x - a.blocks0, lds);
+}
+
+// Threads a group of columns, and workgroups: eight threads for many parts where that fills the card.
+uint32_t join_blocks(const ProductArgs &a, bool pair, int32_t *lanes_log2) {
+    const int64_t groups = (pair ? 1 : a.products) * a.rows * (a.ld_part >> 2);
+    *lanes_log2 = a.splits >= 8 && groups < 512 * kCus ? 3 : 0;
+    const int64_t wide = 256 >> *lanes_log2;
+    return static_cast<uint32_t>((groups + wide - 1) / wide);
 }
 
 // ---- planning ------------------------------------------------------------------------------------------
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Whether the product's operands can go into LDS directly: whole 16-byte pieces everywhere.
-bool direct_fits(const ProductArgs &a, int form, bool pair, int size) {
-    const int64_t elems = 16 / size;
+// The largest unit (16, 4 or 2 bytes) that all operands' lines are multiples of, as the way of their tiles
+// into LDS.
+int way_of(const ProductArgs &a, int form, bool pair, int size) {
     const int segs = a.segs > a.short_segs ? a.segs : a.short_segs;
-    bool fits = a.ld_a % elems == 0 && a.ld_b % elems == 0;
+    uint64_t bits = static_cast<uint64_t>((a.ld_a | a.ld_b) * size);
     for (int i = 0; i < segs; ++i) {
-        fits = fits && aligned16(a.a[i]);
-        for (int z = 0; z < (pair ? 2 : a.products); ++z) fits = fits && aligned16(a.b[z][i]);
+        bits |= reinterpret_cast<uintptr_t>(a.a[i]);
+        for (int z = 0; z < (pair ? 2 : a.products); ++z) bits |= reinterpret_cast<uintptr_t>(a.b[z][i]);
     }
-    if (form == kGradW) fits = fits && a.rows % elems == 0;
-    if (form != kGradX) fits = fits && a.cols % elems == 0;
-    return fits;
+    if (form == kGradW) bits |= static_cast<uint64_t>(a.rows * size);
+    if (form != kGradX) bits |= static_cast<uint64_t>(a.cols * size);
+    return bits % 16 == 0 ? kByPiece : bits % 4 == 0 ? kByWord : kThrough;
 }
 
-struct Tiling {
-    int tile;
-    int64_t splits;
+// A product to be planned.
+struct Shape {
+    int form;
+    int64_t rows, cols, k;
+    int segs, products;
 };
 
-// The tile and the number of parts of the summed length with the least time by a model: each compute unit
-// works off its share of the workgroups, a workgroup takes `step` us for 128 bytes of the summed length
-// when it has the unit to itself with as many others as fit (and at least `alone`), and a split sum goes
-// through memory once more.
-Tiling choose_tiling(int form, int type, bool pair, bool direct, int64_t rows, int64_t cols, int64_t k, int segs, int products) {
-    const bool bf = type == GNN_BF16;
-    const int64_t bk = bf ? 64 : 32;
-    const int64_t steps = (k + bk - 1) / bk * segs;
-    Tiling best{kTile128, 1};
+// What a workgroup takes, in us: its share of a compute unit that is full of such, for 128 bytes of the summed length
+// (step) and besides, for the first loads and the epilogue (busy); and the same where it has the unit to itself (alone,
+// fixed).  Measured on products of 1024 to 8192 rows and columns and on single rows.
+struct TileCost {
+    double step, busy, alone, fixed;
+};
+constexpr TileCost kCostBf16[4] = {{1.65, 8, 1.4, 8}, {0.62, 5, 0.62, 5}, {0.24, 1, 0.26, 2}, {0.24, 1.6, 0.27, 2}};
+constexpr TileCost kCostF32[4] = {{0, 0, 0, 0}, {2.05, 5, 2.0, 4}, {0.56, 1.8, 0.58, 1.2}, {0.56, 1.8, 0.6, 1.2}};
+
+// Parts of a sum are written and read again, at 3 TB/s, by a launch of its own.
+constexpr double kJoinLaunch = 2.5;
+double join_us(int64_t parts, double elements) { return kJoinLaunch + static_cast<double>(parts) * elements * (8e-6 / 3.0); }
+
+constexpr int kSplitChoices = 12;
+constexpr int64_t kSplits[kSplitChoices] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+
+// What a product costs in so many parts.
+struct Split {
+    double groups, each;       // workgroups, steps of each
+    double chain, work;        // us: of one workgroup, of all of them on one compute unit
+    double join;
+    bool sensible;
+};
+
+Split split_cost(const Shape &s, int type, int tile, bool pair, int64_t parts) {
+    const TileCost &c = type == GNN_BF16 ? kCostBf16[tile] : kCostF32[tile];
+    const int bk = type == GNN_BF16 ? 64 : 32;
+    const int64_t tr = tile_rows(tile), tc = tile_cols(tile, pair);
+    const int64_t tiles = ((s.rows + tr - 1) / tr) * ((s.cols + tc - 1) / tc) * s.products;
+    const int64_t steps = (s.k + bk - 1) / bk * s.segs;
+    const double elements = static_cast<double>(s.rows) * s.cols * s.products * (pair ? 2 : 1);
+    Split r;
+    r.sensible = parts == 1 || (parts <= steps && tiles * parts <= 8 * kCus && elements < 1e9);
+    r.groups = static_cast<double>(tiles * parts);
+    r.each = static_cast<double>((steps + parts - 1) / parts);
+    r.chain = r.each * c.alone + c.fixed;
+    r.work = r.groups * (r.each * c.step + c.busy);
+    r.join = parts > 1 ? join_us(parts, elements) : 0.0;
+    return r;
+}
+
+struct ForwardPlan {
+    int tile;
+    bool pair;         // one workgroup has both sums
+    int64_t parts;
+    bool joined;
+};
+
+ForwardPlan plan_forward(const DenseArgs &a) {
+    ForwardPlan best{};
     double least = 1e30;
-    for (int tile = kTile256; tile <= kTile32; ++tile) {
-        if (tile == kTile256 && (!bf || !direct)) continue;
-        if (tile == kTile32 && (form == kGradW || rows > 64)) continue;
-        // few rows: a gated pair is taken as two products whose parts are joined
-        const bool paired = pair && tile != kTile32;
-        const int64_t tr = tile_rows(tile), tc = tile_cols(tile, paired);
-        const int64_t tiles = ((rows + tr - 1) / tr) * ((cols + tc - 1) / tc) * (tile == kTile32 && pair ? 2 : products);
-        const double step = tile == kTile256 ? 1.9 : tile == kTile128 ? (bf ? 0.65 : 2.0) : (bf ? 0.5 : 0.6);
-        const double alone = tile == kTile256 ? 1.9 : tile == kTile128 ? (bf ? 0.8 : 2.0) : 0.6;
-        for (int64_t splits = 1; splits <= 64 && splits <= (steps > 0 ? steps : 1); splits += splits < 8 ? 1 : splits / 4) {
-            const bool joined = splits > 1 || (tile == kTile32 && pair);
-            const int64_t each = (steps + splits - 1) / splits;
-            const int64_t load = (tiles * splits + kCus - 1) / kCus;
-            double us = load * (each * step + 1.0);
-            const double one = each * alone + 2.0;
-            if (us < one) us = one;
-            if (joined) us += 4.0 + splits * products * (pair ? 2 : 1) * rows * cols * 8e-6 / 3.0;
+    for (int tile = a.type == GNN_BF16 ? kTile256 : kTile128; tile <= kTile32; ++tile) {
+        if (tile == kTile32 && a.n > 64) continue;
+        const TileCost &c = a.type == GNN_BF16 ? kCostBf16[tile] : kCostF32[tile];
+        // small tiles take a gated pair as two products, whose sums are joined
+        const bool pair = a.pair && tile <= kTile128, apart = a.pair && !pair;
+        for (const int64_t parts : kSplits) {
+            const Split s = split_cost({kForward, a.n, a.d_out, a.d_in, 1, apart ? 2 : 1}, a.type, tile, pair, parts);
+            if (!s.sensible) break;
+            // the last round of workgroups may leave compute units idle
+            const double rounds = static_cast<double>((static_cast<int64_t>(s.groups) + kCus - 1) / kCus);
+            double us = rounds <= 1 ? s.chain : rounds * (s.each * c.step + c.busy);
+            if (us < s.chain) us = s.chain;
+            us += apart && parts == 1 ? join_us(1, 2.0 * static_cast<double>(a.n) * a.d_out) : s.join;
             if (us < least) {
                 least = us;
-                best = {tile, splits};
+                best = {tile, pair, parts, parts > 1 || apart};
             }
         }
     }
     return best;
 }
 
-int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+struct GradientPlan {
+    int tile;
+    int64_t w_parts, x_parts;
+};
 
-// Floats of the parts that a product's plan needs.
-int64_t part_floats(const Tiling &t, bool pair, int64_t rows, int64_t cols, int products) {
-    const bool joined = t.splits > 1 || (t.tile == kTile32 && pair);
-    return joined ? t.splits * (pair ? 2 : products) * rows * round_up(cols, 4) : 0;
-}
-
-// Whatever the operands' alignment.
-int64_t most_part_floats(int form, int type, bool pair, int64_t rows, int64_t cols, int64_t k, int segs, int products) {
-    int64_t most = 0;
-    for (int direct = 0; direct < 2; ++direct) {
-        const int64_t f = part_floats(choose_tiling(form, type, pair, direct, rows, cols, k, segs, products), pair, rows, cols, products);
-        most = f > most ? f : most;
+// Both products' workgroups run in one launch: their parts are chosen together.
+GradientPlan plan_gradients(const Shape &w, const Shape &x, int type) {
+    GradientPlan best{};
+    double least = 1e30;
+    for (int tile = type == GNN_BF16 ? kTile256 : kTile128; tile <= kTile64; ++tile) {
+        Split sx[kSplitChoices];
+        for (int i = 0; i < kSplitChoices; ++i) sx[i] = split_cost(x, type, tile, false, kSplits[i]);
+        for (const int64_t w_parts : kSplits) {
+            const Split sw = split_cost(w, type, tile, false, w_parts);
+            if (!sw.sensible) break;
+            for (int i = 0; i < kSplitChoices && sx[i].sensible; ++i) {
+                const double chain = sw.chain > sx[i].chain ? sw.chain : sx[i].chain;
+                const double shorter = sw.chain > sx[i].chain ? sx[i].chain : sw.chain;
+                double us = (sw.work + sx[i].work) / kCus;
+                if (sw.groups + sx[i].groups > kCus) us += 0.25 * shorter;      // of the last ones
+                if (us < chain) us = chain;
+                us += sw.join + sx[i].join - (sw.join > 0 && sx[i].join > 0 ? kJoinLaunch : 0.0);
+                if (us < least) {
+                    least = us;
+                    best = {tile, w_parts, kSplits[i]};
+                }
+            }
+        }
     }
-    return most;
+    return best;
 }
 
-// What a product needs beside its operands: where parts of its sum go (ws).
-hipError_t product(ProductArgs a, int form, int type, bool pair, char *ws, hipStream_t s) {
-    const bool direct = direct_fits(a, form, pair, type == GNN_BF16 ? 2 : 4);
-    const Tiling t = choose_tiling(form, type, pair, direct, a.rows, a.cols, a.k, a.segs, a.products);
-    const bool joined = t.splits > 1 || (t.tile == kTile32 && pair);
-    a.splits = static_cast<int32_t>(t.splits);
-    a.part = joined ? reinterpret_cast<float *>(ws) : nullptr;
-    a.ld_part = round_up(a.cols, 4);
-    ProductArgs b = a;
-    if (t.tile == kTile32 && pair) b.products = 2;
-    const ProductPlan plan{form, t.tile, pair && t.tile != kTile32, direct};
-    const hipError_t err = type == GNN_BF16 ? launch_product_bf16(b, plan, s) : launch_product_f32(b, plan, s);
-    if (err != hipSuccess || !joined) return err;
-    return type == GNN_BF16 ? launch_join<bf16>(a, form != kGradW, pair, s) : launch_join<float>(a, form != kGradW, pair, s);
-}
+// Floats of the parts of a product.
+int64_t part_floats(int64_t parts, const Shape &s) { return parts * s.products * s.rows * round_up(s.cols, 4); }
+
+// Only pieces fill the largest tile.
+int filled_tile(int tile, int load) { return tile == kTile256 && load != kByPiece ? kTile128 : tile; }
 
 // ---- the gradient of the sums ----------------------------------------------------------------------------
 
@@ -196,48 +246,54 @@ constexpr int kSlopeWide = 32, kSlopeHigh = 8;     // threads of a workgroup
 constexpr int kSlopeBlocks = 2048;                 // workgroups at most, unless the columns alone need more
 constexpr int kSlopeRows = 4;                      // rows that a thread loads at a time
 
-template <typename T, bool PAIR>
+// Each thread takes 16 bytes of a line; what it loads stays as it was loaded until its row's turn.  A line's last
+// columns are taken by a piece that overlaps the one before: what both compute is the same, and counts in one's
+// sums.  (SINGLE: lines shorter than a piece, element by element.)
+template <typename T, bool PAIR, bool SINGLE>
 __global__ __launch_bounds__(kSlopeWide * kSlopeHigh) void k_slopes(SlopeArgs p) {
-    constexpr int V = 16 / static_cast<int>(sizeof(T));
+    constexpr int V = SINGLE ? 1 : 16 / static_cast<int>(sizeof(T));
     constexpr bool kFast = sizeof(T) == 2;
+    typedef vec<float, V> Wide;
+    typedef vec<T, V> Raw;
+    typedef typename loose<T, V>::type Loose;
     const int64_t n = load_count(p.d_n, p.n);
     const bool planes = kFast && (p.planes_wide || n < kShortSum);
     const int x = threadIdx.x % kSlopeWide, y = threadIdx.x / kSlopeWide;
-    const int64_t c = (static_cast<int64_t>(blockIdx.x) * kSlopeWide + x) * V, left = p.cols - c;
-    vec<float, V> sum0(0.f), sum1(0.f);
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * kSlopeWide + x) * V;
+    const int64_t c = at < p.cols - V ? at : p.cols - V;
+    const bool there = at < p.cols;
+    Wide sum0(0.f), sum1(0.f);
     const int64_t step = static_cast<int64_t>(gridDim.y) * kSlopeHigh;
-    const auto keep = [&](int64_t at, vec<float, V> v) {
-        T *to = static_cast<T *>(p.dz) + at;
-        const vec<T, V> r = __builtin_convertvector(v, vec<T, V>);
-        // dz is the library's own and its lines are padded
-        *reinterpret_cast<vec<T, V> *>(to) = r;
-        if (planes) {
-            v -= __builtin_convertvector(r, vec<float, V>);
-            *reinterpret_cast<vec<T, V> *>(static_cast<T *>(p.rest) + at) = __builtin_convertvector(v, vec<T, V>);
-        }
+    const auto load = [](const void *from, int64_t e) { return *reinterpret_cast<const Loose *>(static_cast<const T *>(from) + e); };
+    const auto keep = [&](int64_t e, Wide v) {
+        const Raw r = __builtin_convertvector(v, Raw);
+        *reinterpret_cast<Loose *>(static_cast<T *>(p.dz) + e) = r;
+        if (planes) *reinterpret_cast<Loose *>(static_cast<T *>(p.rest) + e) = __builtin_convertvector(v - __builtin_convertvector(r, Wide), Raw);
     };
-    if (left > 0) {
+    if (there) {
         for (int64_t m0 = static_cast<int64_t>(blockIdx.y) * kSlopeHigh + y; m0 < n; m0 += step * kSlopeRows) {
-            vec<float, V> d[kSlopeRows], a[kSlopeRows], b[kSlopeRows];
+            Raw d[kSlopeRows], a[kSlopeRows], b[kSlopeRows];
 #pragma unroll
             for (int i = 0; i < kSlopeRows; ++i) {
-                const int64_t m = m0 + i * step;
-                if (m >= n) break;
-                d[i] = load_some<T, V>(static_cast<const T *>(p.dout) + m * p.ld_dout + c, left);
-                if (p.store) a[i] = load_some<T, V>(static_cast<const T *>(p.pre[0]) + m * p.ld_pre + c, left);
-                if (PAIR) b[i] = load_some<T, V>(static_cast<const T *>(p.pre[1]) + m * p.ld_pre + c, left);
+                // past the end the first row again, which then counts for nothing
+                const int64_t m = m0 + i * step < n ? m0 + i * step : m0;
+                d[i] = load(p.dout, m * p.ld_dout + c);
+                if (p.store) a[i] = load(p.pre[0], m * p.ld_pre + c);
+                if (PAIR) b[i] = load(p.pre[1], m * p.ld_pre + c);
             }
 #pragma unroll
             for (int i = 0; i < kSlopeRows; ++i) {
                 const int64_t m = m0 + i * step;
                 if (m >= n) break;
-                vec<float, V> g = d[i];
+                const Wide dy = __builtin_convertvector(d[i], Wide);
+                Wide g = dy;
                 if (p.store) {
-                    const vec<float, V> slope = activate_slope<kFast, V>(p.act, a[i]);
-                    g = PAIR ? g * b[i] * slope : g * slope;
+                    Wide z = __builtin_convertvector(a[i], Wide);
+                    const Wide slope = activate_slope<kFast, V>(p.act, z);
+                    g = PAIR ? dy * __builtin_convertvector(b[i], Wide) * slope : dy * slope;
                     keep(m * p.ld_dz + c, g);
                     if (PAIR) {
-                        const vec<float, V> u = d[i] * a[i];
+                        const Wide u = dy * z;
                         keep(m * p.ld_dz + p.second + c, u);
                         sum1 += u;
                     }
@@ -247,18 +303,19 @@ __global__ __launch_bounds__(kSlopeWide * kSlopeHigh) void k_slopes(SlopeArgs p)
         }
     }
     if (p.sums == nullptr) return;
-    __shared__ float lds[kSlopeHigh][(PAIR ? 2 : 1) * V][kSlopeWide + 1];
+    constexpr int kSums = (PAIR ? 2 : 1) * V;
+    __shared__ float lds[kSlopeHigh][kSums][kSlopeWide + 1];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         lds[y][i][x] = sum0[i];
         if (PAIR) lds[y][V + i][x] = sum1[i];
     }
     __syncthreads();
-    for (int e = y; e < (PAIR ? 2 : 1) * V; e += kSlopeHigh) {
+    for (int e = y; e < kSums; e += kSlopeHigh) {
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < kSlopeHigh; ++i) s += lds[i][e][x];
-        if (e % V < left) p.sums[blockIdx.y * p.ld_sums + (e >= V ? p.second : 0) + c + e % V] = s;
+        if (there) p.sums[blockIdx.y * p.ld_sums + (e >= V ? p.second : 0) + c + e % V] = s;
     }
 }
 
@@ -273,51 +330,53 @@ int slope_parts(int64_t n, int64_t cols, int type) {
 
 // ---- workspace -----------------------------------------------------------------------------------------
 
+// What the backward pass keeps in its workspace.  dz has whole 128-byte lines; of its second plane only what a
+// short sum reads is there.
 struct DenseSpace {
-    char *dz, *rest, *sums, *part;
+    char *dz, *rest, *sums, *w_part, *x_part;
     int64_t ld_dz, second;
     bool wide;               // two planes of every row: dx sums few terms
+    Shape w, x;
+    GradientPlan plan;
     size_t bytes;
 };
 
-// dz has whole 128-byte lines; of its second plane only what a short sum reads is there.
 DenseSpace carve_dense(const DenseArgs &a, char *ws) {
-    DenseSpace w{};
+    DenseSpace s{};
     const int mats = a.pair ? 2 : 1;
-    const int64_t size = a.type == GNN_BF16 ? 2 : 4;
-    w.second = round_up(a.d_out, 128 / size);
-    w.ld_dz = w.second * mats;
-    w.wide = a.type == GNN_BF16 && a.d_out * mats < kShortSum;
+    const bool bf = a.type == GNN_BF16;
+    const int64_t size = bf ? 2 : 4;
+    s.second = round_up(a.d_out, 128 / size);
+    s.ld_dz = s.second * mats;
+    s.wide = bf && a.d_out * mats < kShortSum;
+    s.w = {kGradW, a.d_in, a.d_out, a.n, 1, mats};
+    s.x = {kGradX, a.n, a.d_in, a.d_out, s.wide ? 2 * mats : mats, 1};
+    s.plan = plan_gradients(s.w, s.x, a.type);
     size_t at = 0;
     const auto take = [&](char **p, int64_t bytes) {
         *p = ws + at;
         at += static_cast<size_t>(round_up(bytes < 1 ? 1 : bytes, 256));
     };
-    take(&w.dz, a.n * w.ld_dz * size);
-    const int64_t rest_rows = a.type != GNN_BF16 ? 0 : w.wide || a.n < kShortSum ? a.n : kShortSum;
-    take(&w.rest, rest_rows * w.ld_dz * size);
-    take(&w.sums, static_cast<int64_t>(slope_parts(a.n, a.d_out, a.type)) * w.ld_dz * 4);
-    int64_t floats = 0;
-    for (int i = 1; i <= 2; ++i) {     // one plane or two, one weight's gradient or two
-        const int64_t dx = most_part_floats(kGradX, a.type, false, a.n, a.d_in, a.d_out, i * mats, 1);
-        const int64_t dw = most_part_floats(kGradW, a.type, false, a.d_in, a.d_out, a.n, 1, i < mats ? i : mats);
-        floats = dx > floats ? dx : floats;
-        floats = dw > floats ? dw : floats;
-    }
-    take(&w.part, 4 * floats);
-    w.bytes = at;
-    return w;
+    take(&s.dz, a.n * s.ld_dz * size);
+    take(&s.rest, !bf ? 0 : (s.wide || a.n < kShortSum ? a.n : kShortSum) * s.ld_dz * size);
+    take(&s.sums, static_cast<int64_t>(slope_parts(a.n, a.d_out, a.type)) * s.ld_dz * 4);
+    take(&s.w_part, s.plan.w_parts > 1 ? 4 * part_floats(s.plan.w_parts, s.w) : 0);
+    take(&s.x_part, s.plan.x_parts > 1 ? 4 * part_floats(s.plan.x_parts, s.x) : 0);
+    s.bytes = at;
+    return s;
 }
 
-template <typename T>
-hipError_t launch_slopes(const SlopeArgs &a, bool pair, hipStream_t s) {
-    const int64_t wide = kSlopeWide * 16 / static_cast<int64_t>(sizeof(T));
+template <typename T, bool PAIR>
+hipError_t launch_slopes(const SlopeArgs &a, hipStream_t s) {
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
+    const bool single = a.cols < V;
+    const int64_t wide = kSlopeWide * (single ? 1 : V);
     const dim3 grid(static_cast<unsigned>((a.cols + wide - 1) / wide),
                     slope_parts(a.n, a.cols, sizeof(T) == 2 ? GNN_BF16 : GNN_F32));
-    if (pair)
-        k_slopes<T, true><<<grid, kSlopeWide * kSlopeHigh, 0, s>>>(a);
+    if (single)
+        k_slopes<T, PAIR, true><<<grid, kSlopeWide * kSlopeHigh, 0, s>>>(a);
     else
-        k_slopes<T, false><<<grid, kSlopeWide * kSlopeHigh, 0, s>>>(a);
+        k_slopes<T, PAIR, false><<<grid, kSlopeWide * kSlopeHigh, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -325,22 +384,23 @@ hipError_t launch_slopes(const SlopeArgs &a, bool pair, hipStream_t s) {
 
 hipError_t launch_column_sums(const float *sums, int64_t ld, int parts, int64_t cols, int64_t second, int type, void *out0,
                               void *out1, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>((cols + 31) / 32), 2);
-    if (type == GNN_BF16)
-        k_column_sums<bf16><<<grid, 32 * kColumnHigh, 0, s>>>(sums, ld, parts, cols, second, out0, out1);
-    else
-        k_column_sums<float><<<grid, 32 * kColumnHigh, 0, s>>>(sums, ld, parts, cols, second, out0, out1);
+    const ColumnArgs c{sums, ld, parts, cols, second, type, {out0, out1}, static_cast<uint32_t>((cols + 31) / 32)};
+    k_column_sums<<<2 * c.blocks, kColumnThreads, 0, s>>>(c);
     return hipGetLastError();
 }
 
 size_t dense_bytes(const DenseArgs &a, bool backward) {
     if (backward) return carve_dense(a, nullptr).bytes;
-    return static_cast<size_t>(4 * most_part_floats(kForward, a.type, a.pair, a.n, a.d_out, a.d_in, 1, 1)) + 256;
+    const ForwardPlan p = plan_forward(a);
+    return 256 + (p.joined ? static_cast<size_t>(4 * part_floats(p.parts, {kForward, a.n, a.d_out, a.d_in, 1, a.pair ? 2 : 1})) : 0);
 }
 
 hipError_t launch_dense(const DenseArgs &a, hipStream_t s) {
     if (a.n == 0) return hipSuccess;
-    ProductArgs p{};
+    const bool bf = a.type == GNN_BF16;
+    const ForwardPlan plan = plan_forward(a);
+    JoinArgs j{};
+    ProductArgs &p = j.p[0];
     p.a[0] = a.x;
     p.ld_a = a.ld_x;
     p.ld_b = a.ld_w;
@@ -350,6 +410,9 @@ hipError_t launch_dense(const DenseArgs &a, hipStream_t s) {
     p.d_n = a.d_n;
     p.segs = p.short_segs = 1;
     p.products = 1;
+    p.splits = static_cast<int32_t>(plan.parts);
+    p.part = plan.joined ? reinterpret_cast<float *>(a.ws) : nullptr;
+    p.ld_part = round_up(a.d_out, 4);
     p.e.act = a.act;
     p.e.res = a.res;
     p.e.ld_res = a.ld_res;
@@ -361,16 +424,33 @@ hipError_t launch_dense(const DenseArgs &a, hipStream_t s) {
         p.e.bias[z] = a.bias[z];
         p.e.pre[z] = a.pre[z];
     }
-    return product(p, kForward, a.type, a.pair, a.ws, s);
+    const int load = way_of(p, kForward, a.pair, bf ? 2 : 4);
+    ProductArgs q = p;
+    if (a.pair && !plan.pair) q.products = 2;
+    const int tile = filled_tile(plan.tile, load);
+    const hipError_t err = bf ? launch_product_bf16(q, tile, plan.pair, load, s) : launch_product_f32(q, tile, plan.pair, load, s);
+    if (err != hipSuccess || !plan.joined) return err;
+    const uint32_t blocks = join_blocks(p, a.pair, &j.lanes_log2[0]);
+    if (bf && a.pair)
+        k_product_join<bf16, true, true><<<blocks, 256, 0, s>>>(j);
+    else if (bf)
+        k_product_join<bf16, true, false><<<blocks, 256, 0, s>>>(j);
+    else if (a.pair)
+        k_product_join<float, true, true><<<blocks, 256, 0, s>>>(j);
+    else
+        k_product_join<float, true, false><<<blocks, 256, 0, s>>>(j);
+    return hipGetLastError();
 }
 
 hipError_t launch_dense_backward(const DenseArgs &a, hipStream_t s) {
     const int mats = a.pair ? 2 : 1;
     const bool bf = a.type == GNN_BF16, own = a.pair || a.act != GNN_ACT_NONE;      // dz is not dout itself
     const DenseSpace w = carve_dense(a, a.ws);
-    const bool summed = a.dbias[0] || a.dbias[1];
+    const bool summed = a.dbias[0] || a.dbias[1], weights = a.dw[0] || a.dw[1], inputs = a.dx && a.n > 0;
     const int64_t size = bf ? 2 : 4;
-    if (summed || (own && (a.dx || a.dw[0] || a.dw[1]))) {
+    if (!summed && !weights && !inputs) return hipSuccess;
+    ColumnArgs c{};
+    if (summed || own) {
         SlopeArgs p{};
         p.dout = a.dout;
         p.ld_dout = a.ld_dout;
@@ -389,63 +469,67 @@ hipError_t launch_dense_backward(const DenseArgs &a, hipStream_t s) {
         p.second = w.second;
         p.sums = summed ? reinterpret_cast<float *>(w.sums) : nullptr;
         p.ld_sums = w.ld_dz;
-        hipError_t err = bf ? launch_slopes<bf16>(p, a.pair, s) : launch_slopes<float>(p, a.pair, s);
+        const hipError_t err = a.pair ? (bf ? launch_slopes<bf16, true>(p, s) : launch_slopes<float, true>(p, s))
+                                      : (bf ? launch_slopes<bf16, false>(p, s) : launch_slopes<float, false>(p, s));
         if (err != hipSuccess) return err;
-        if (summed) {
-            err = launch_column_sums(p.sums, p.ld_sums, slope_parts(a.n, a.d_out, a.type), a.d_out, w.second, a.type,
-                                     a.dbias[0], a.dbias[1], s);
-            if (err != hipSuccess) return err;
-        }
+        if (summed)
+            c = ColumnArgs{p.sums, p.ld_sums, slope_parts(a.n, a.d_out, a.type), a.d_out, w.second, a.type,
+                           {a.dbias[0], a.dbias[1]}, static_cast<uint32_t>((a.d_out + 31) / 32)};
     }
     // Planes and projections of dz: index 2 plane + projection.
     const void *dz[4];
     for (int i = 0; i < 4; ++i)
         dz[i] = own ? (i < 2 ? w.dz : w.rest) + (i & 1) * w.second * size : static_cast<const char *>(a.dout);
     const int64_t ld_dz = own ? w.ld_dz : a.ld_dout;
-    ProductArgs p{};
-    p.d_n = a.d_n;
-    p.e.act = GNN_ACT_NONE;
-    if (a.dx && a.n > 0) {
-        ProductArgs q = p;
-        q.rows = a.n;
-        q.cols = a.d_in;
-        q.k = a.d_out;
-        q.ld_a = ld_dz;
-        q.ld_b = a.ld_w;
-        q.segs = q.short_segs = mats;
-        if (own && w.wide) q.segs = q.short_segs = 2 * mats;
-        for (int i = 0; i < q.segs; ++i) {
-            q.a[i] = a.pair ? dz[i] : dz[2 * i];
-            q.b[0][i] = a.w[a.pair ? i & 1 : 0];
-        }
-        q.products = 1;
-        q.e.out[0] = a.dx;
-        q.e.ld_out = a.ld_dx;
-        const hipError_t err = product(q, kGradX, a.type, false, w.part, s);
-        if (err != hipSuccess) return err;
+    JoinArgs j{};
+    ProductArgs &pw = j.p[0], &px = j.p[1];
+    const auto sized = [&](ProductArgs &q, const Shape &shape, int64_t parts, char *part) {
+        q.rows = shape.rows;
+        q.cols = shape.cols;
+        q.k = shape.k;
+        q.d_n = a.d_n;
+        q.splits = static_cast<int32_t>(parts);
+        q.part = parts > 1 ? reinterpret_cast<float *>(part) : nullptr;
+        q.ld_part = round_up(q.cols, 4);
+        q.e.act = GNN_ACT_NONE;
+    };
+    sized(pw, w.w, w.plan.w_parts, w.w_part);
+    pw.ld_a = a.ld_x;
+    pw.ld_b = ld_dz;
+    pw.segs = 1;
+    pw.short_segs = own && bf ? 2 : 1;
+    pw.a[0] = pw.a[1] = a.x;
+    pw.e.ld_out = a.ld_dw;
+    for (int z = 0; z < mats; ++z) {
+        if (!a.dw[z]) continue;
+        pw.b[pw.products][0] = dz[z];
+        pw.b[pw.products][1] = dz[2 + z];
+        pw.e.out[pw.products++] = a.dw[z];
     }
-    if (a.dw[0] || a.dw[1]) {
-        ProductArgs q = p;
-        q.rows = a.d_in;
-        q.cols = a.d_out;
-        q.k = a.n;
-        q.ld_a = a.ld_x;
-        q.ld_b = ld_dz;
-        q.segs = 1;
-        q.short_segs = own && bf ? 2 : 1;
-        q.a[0] = q.a[1] = a.x;
-        q.products = 0;
-        q.e.ld_out = a.ld_dw;
-        for (int z = 0; z < mats; ++z) {
-            if (!a.dw[z]) continue;
-            q.b[q.products][0] = dz[z];
-            q.b[q.products][1] = dz[2 + z];
-            q.e.out[q.products++] = a.dw[z];
-        }
-        const hipError_t err = product(q, kGradW, a.type, false, w.part, s);
-        if (err != hipSuccess) return err;
+    sized(px, w.x, w.plan.x_parts, w.x_part);
+    px.ld_a = ld_dz;
+    px.ld_b = a.ld_w;
+    px.segs = px.short_segs = own && w.wide ? 2 * mats : mats;
+    for (int i = 0; i < px.segs; ++i) {
+        px.a[i] = a.pair ? dz[i] : dz[2 * i];
+        px.b[0][i] = a.w[a.pair ? i & 1 : 0];
     }
-    return hipSuccess;
+    px.products = inputs ? 1 : 0;
+    px.e.out[0] = a.dx;
+    px.e.ld_out = a.ld_dx;
+    const int way_w = weights ? way_of(pw, kGradW, false, size) : kByPiece;
+    const int way_x = inputs ? way_of(px, kGradX, false, size) : kByPiece;
+    const int load = way_w > way_x ? way_w : way_x, tile = filled_tile(w.plan.tile, load);
+    hipError_t err = bf ? launch_gradients_bf16(pw, px, c, tile, load, s) : launch_gradients_f32(pw, px, c, tile, load, s);
+    if (err != hipSuccess) return err;
+    j.blocks0 = pw.part && weights ? join_blocks(pw, false, &j.lanes_log2[0]) : 0;
+    const uint32_t blocks = j.blocks0 + (px.part && inputs ? join_blocks(px, false, &j.lanes_log2[1]) : 0);
+    if (blocks == 0) return hipSuccess;
+    if (bf)
+        k_product_join<bf16, false, false><<<blocks, 256, 0, s>>>(j);
+    else
+        k_product_join<float, false, false><<<blocks, 256, 0, s>>>(j);
+    return hipGetLastError();
 }
 
 }  // namespace gnnmb

@@ -18,18 +18,19 @@
 // Contiguous operands lie in rows of eight 16-byte pieces; strided ones as in memory, one line of the
 // tile's width per summed index, and the matrix instruction's operand is turned on the way out of LDS
 // (ds_read_b64_tr_b16; fp32 takes single words).  Pieces are permuted within their line so that what one
-// LDS read touches spreads over the banks: lds_piece below.  Where both operands start at multiples of 16
-// bytes and their lines are whole pieces, tiles go from memory into LDS directly (kDirect); otherwise
-// through registers.  A tile that the summed length cuts is filled with zeros, element by element where
-// it must be.
+// LDS read touches spreads over the banks: lds_piece below.  Tiles go from memory into LDS directly, by
+// pieces where both operands' lines start at multiples of 16 bytes and are whole pieces (kByPiece), by words
+// where they are multiples of 4 bytes, fp32 always (kByWord); other bf16 operands go through registers
+// (kThrough).  A tile that the summed length cuts is filled with zeros, element by element where it must be.
 #pragma once
 
 #include "learn.hpp"
 
 namespace gnnmb {
 
-// Order of the operands' elements, see above.
+// Order of the operands' elements, and the way of a tile into LDS, see above.
 enum : int32_t { kForward, kGradX, kGradW };
+enum : int32_t { kByPiece, kByWord, kThrough };
 
 // What becomes of a sum z = A B (of both sums g, u of a gated layer).
 struct Epilogue {
@@ -229,7 +230,7 @@ __device__ __forceinline__ int dealt(int r) {
 //  - Contiguous: one read takes the same piece of 32 lines, in the order of dealt; eight lanes of it cover
 //    128 bytes, sixteen 256 (the parity of the line gives the half).
 //  - Strided bf16: sixteen lanes read 4 lines of the summed index and, of each, two pieces: next to each
-//    other for A, one apart for B; 32 lanes four pieces in a row.
+//    other for A, one apart for B; 32 lanes four pieces in a row.  (Lines of eight pieces: 128 bytes.)
 //  - Strided fp32: 32 lanes read 128 bytes of one line, the others of the line four below.
 template <typename T, bool CONTIGUOUS, bool B, int CPR>
 __device__ __forceinline__ int lds_piece(int r, int c) {
@@ -238,25 +239,33 @@ __device__ __forceinline__ int lds_piece(int r, int c) {
         return c ^ low ^ ((B ? r >> 2 : r >> 3) & 1);
     }
     if (sizeof(T) == 4) return c ^ ((r >> 2) & 1) * 8;
-    if (CPR == 8) return c ^ ((r & 1) | (r & 2) << 1);
+    if (CPR == 8) return c ^ (B ? (r & 1) | (r & 2) << 1 : (r & 3) * 2);
     return c ^ ((r & 1) * 4 | ((r >> 1) & 1) * 11);
 }
 
-// A load from memory into LDS: 16 bytes of each lane, from base + offset, to 16 bytes times the lane
-// from `lds` on (both uniform).  It writes no register; vmcnt counts it, but the compiler does not (of the
-// builtin it knows, and waits for all of them before every read of LDS that it cannot tell apart).
+// A load from memory into LDS: 16 bytes (or a word) of each lane, from base + offset, to as many bytes times
+// the lane from `lds` on (both uniform).  It writes no register; vmcnt counts it, but the compiler does not
+// (of the builtin it knows, and waits for all of them before every read of LDS that it cannot tell apart).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"      // that m0 is reserved
+template <bool WORD>
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t offset, const void *base) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :
-                 : "s"(lds), "v"(offset), "s"(base)
-                 : "memory", "m0");
+    if (WORD)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                     :
+                     : "s"(lds), "v"(offset), "s"(base)
+                     : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :
+                     : "s"(lds), "v"(offset), "s"(base)
+                     : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
 template <int PENDING>
 __device__ __forceinline__ void wait_and_meet() {
+    static_assert(PENDING < 64, "vmcnt counts 63 loads");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(PENDING) : "memory");
 }
 
@@ -287,7 +296,7 @@ struct Step<float> {
 
 // TILE lines of one operand for a product tile: what the threads load of it and where a wavefront reads.
 // SUB: column stretches of their own (two for the pair of a gated layer), TILE / SUB wide each.
-template <typename T, bool CONTIGUOUS, bool B, int TILE, int SUB, int THREADS>
+template <typename T, bool CONTIGUOUS, bool B, int TILE, int SUB, int THREADS, int LOAD>
 struct TileOf {
     static constexpr int kElems = Step<T>::kElems;
     static constexpr int kWide = TILE / SUB;
@@ -297,6 +306,8 @@ struct TileOf {
     static constexpr int kLinesPerPass = THREADS / kCpr;
     static_assert(kPieces % SUB == 0 && kPieces > 0, "a pass of the threads lies in one stretch");
     static_assert(CONTIGUOUS ? kLinesPerPass % 32 == 0 : kLinesPerPass % 8 == 0, "lds_piece repeats from pass to pass");
+    static constexpr bool kWord = LOAD == kByWord;
+    static constexpr int kLoads = kWord ? 4 * kPieces : kPieces;      // per thread
 
     // Line and memory piece of this thread's piece i (within its stretch).
     static __device__ __forceinline__ int line(int i, int t) { return (i % (kPieces / SUB)) * kLinesPerPass + t / kCpr; }
@@ -304,72 +315,95 @@ struct TileOf {
         return lds_piece<T, CONTIGUOUS, B, kCpr>(t / kCpr, t % kCpr);
     }
 
-    // Byte offsets of the thread's loads from the operand's start (strided: from the summed index's line).
-    // Lines or columns beyond `limit` repeat the last ones; what they give is not stored.
-    static constexpr int kOffsets = CONTIGUOUS ? kPieces : 1;
+    // Byte offsets of the thread's loads from the tile's place in the operand (strided: from the summed index's
+    // line; the second stretch has those of the first).  Lines or columns beyond `limit` repeat the last ones; what
+    // they give is not stored.
+    static constexpr int kOffsets = kWord ? 1 : kPieces / SUB;
     uint32_t offset[kOffsets];
     int64_t first;          // contiguous: first line of the tile
     int64_t limit;
-    int shift;              // strided: elements by which a piece at the lines' end is moved
+    uint32_t line_bytes;    // kByWord
+    uint32_t last;          // kByWord: the last line or element of the tile that exists
+    int shift;              // kThrough, strided: elements by which a piece at the lines' end is moved
 
     __device__ __forceinline__ void init(int64_t first_, int64_t limit_, int64_t ld, int t) {
         first = first_;
         limit = limit_;
         shift = 0;
-        if (CONTIGUOUS) {
+        if (kWord) {
+            line_bytes = static_cast<uint32_t>(ld) * static_cast<uint32_t>(sizeof(T));
+            const int64_t left = limit - first - (CONTIGUOUS ? 1 : 4 / static_cast<int>(sizeof(T)));
+            last = static_cast<uint32_t>(left < TILE ? left : TILE);
+        } else if (CONTIGUOUS) {
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
+            for (int i = 0; i < kOffsets; ++i) {
                 int64_t r = line(i, t);
                 if (first + r >= limit) r = limit - 1 - first;
                 offset[i] = static_cast<uint32_t>(r * ld + piece(t) * kElems) * static_cast<uint32_t>(sizeof(T));
             }
         } else {
             int64_t c = first + piece(t) * kElems;
-            const int64_t last = limit < kElems ? 0 : limit - kElems;
-            if (c > last) {
-                if (c < limit) shift = static_cast<int>(c - last);
-                c = last;
+            const int64_t last_piece = limit < kElems ? 0 : limit - kElems;
+            if (c > last_piece) {
+                if (c < limit) shift = static_cast<int>(c - last_piece);
+                c = last_piece;
             }
-            offset[0] = static_cast<uint32_t>(c + t / kCpr * ld) * static_cast<uint32_t>(sizeof(T));
+#pragma unroll
+            for (int i = 0; i < kOffsets; ++i)
+                offset[i] = static_cast<uint32_t>(c + line(i, t) * ld) * static_cast<uint32_t>(sizeof(T));
         }
     }
-    // Start of the loads of piece i for summed index k0.
-    __device__ __forceinline__ const char *base(const void *p, int64_t ld, int i, int64_t k0) const {
-        const int64_t e = CONTIGUOUS ? first * ld + k0 : (k0 + (i % (kPieces / SUB)) * kLinesPerPass) * ld;
+    // Where the tile's loads start for summed index k0, and how far it is to the next tile's.
+    __device__ __forceinline__ const char *base(const void *p, int64_t ld, int64_t k0) const {
+        const int64_t e = CONTIGUOUS ? first * ld + k0 : (kWord ? first : 0) + k0 * ld;
         return static_cast<const char *>(p) + e * static_cast<int64_t>(sizeof(T));
     }
-    __device__ __forceinline__ uint32_t at(int i) const { return offset[CONTIGUOUS ? i : 0]; }
+    static __device__ __forceinline__ int64_t advance(int64_t ld) {
+        return CONTIGUOUS ? 128 : 128 / static_cast<int>(sizeof(T)) * ld * static_cast<int>(sizeof(T));
+    }
+    // The thread's offset of load i.
+    __device__ __forceinline__ uint32_t at(int i, int t) const {
+        if (!kWord) return offset[i % kOffsets];
+        constexpr int kLines = THREADS / 4 / kCpr;         // lines per load of all threads
+        const int r = (i % (kLoads / SUB)) * kLines + t / 4 / kCpr;
+        const uint32_t c = lds_piece<T, CONTIGUOUS, B, kCpr>(r, t / 4 % kCpr) * 16 + t % 4 * 4;     // bytes
+        const uint32_t end = CONTIGUOUS ? 0 : last * static_cast<uint32_t>(sizeof(T));
+        if (CONTIGUOUS) return (static_cast<uint32_t>(r) < last ? r : last) * line_bytes + c;
+        return r * line_bytes + (c < end ? c : end);
+    }
+    // Bytes of LDS that one load of all threads fills.
+    static constexpr int kLoadBytes = THREADS * (kWord ? 4 : 16);
 
-    // One piece, with zeros where the summed length k or the limit ends.
+    // Piece i of a tile that the summed length k cuts: what of it exists, shifted to its place, zeros past k.  (Columns
+    // past the limit hold anything.)
     __device__ __forceinline__ u4 cut(const void *from, int64_t ld, int i, int64_t k0, int64_t k, int t) const {
         const T *p = static_cast<const T *>(from);
-        int64_t there;
-        if (CONTIGUOUS) {
-            int64_t r = first + line(i, t);
-            if (r >= limit) r = limit - 1;
-            const int64_t c = k0 + piece(t) * kElems;
-            p += r * ld + c;
-            there = k - c;
+        const int64_t r = CONTIGUOUS ? first + line(i, t) : k0 + line(i, t);
+        const int64_t c = (CONTIGUOUS ? k0 : first) + piece(t) * kElems;
+        const int64_t lines = CONTIGUOUS ? limit : k, across = CONTIGUOUS ? k : limit;
+        p += (r < lines ? r : lines - 1) * ld;
+        int64_t over = c + kElems - across;                 // elements that do not exist
+        if (over < 0) over = 0;
+        u4 v;
+        if (across >= kElems) {
+            v = __builtin_bit_cast(u4, *reinterpret_cast<const typename loose<T, kElems>::type *>(
+                                           p + (over > 0 ? across - kElems : c)));
         } else {
-            const int64_t r = k0 + line(i, t), c = first + piece(t) * kElems;
-            p += r * ld + c;
-            there = r < k ? limit - c : 0;
-        }
-        vec<T, kElems> v(static_cast<T>(0.f));
-        if (there >= kElems) {
-            v = *reinterpret_cast<const typename loose<T, kElems>::type *>(p);
-        } else {
+            vec<T, kElems> w(static_cast<T>(0.f));
 #pragma unroll
             for (int e = 0; e < kElems; ++e)
-                if (e < there) v[e] = p[e];
+                if (e < across) w[e] = p[e];
+            v = __builtin_bit_cast(u4, w);
+            over -= kElems - across;                        // the piece starts at 0, or past the end
         }
-        return __builtin_bit_cast(u4, v);
+        if (over > 0) v = shifted(v, static_cast<int>(over < kElems ? over : 0));
+        if (over >= kElems || (!CONTIGUOUS && r >= k)) v = u4(0);
+        return v;
     }
-    // A piece that was loaded `shift` elements too early, put right.
-    __device__ __forceinline__ u4 shifted(u4 v) const {
-        if (shift == 0) return v;
-        unsigned __int128 x = __builtin_bit_cast(unsigned __int128, v);
-        return __builtin_bit_cast(u4, x >> (shift * 8 * static_cast<int>(sizeof(T))));
+    // A piece that was loaded `by` elements too early, put right.
+    static __device__ __forceinline__ u4 shifted(u4 v, int by) {
+        const unsigned __int128 x = __builtin_bit_cast(unsigned __int128, v);
+        return __builtin_bit_cast(u4, x >> (by * 8 * static_cast<int>(sizeof(T))));
     }
 
     // Where in LDS a lane's 16 bytes of 32 lines `frag` lie for step 0 of a tile, in bytes.
@@ -413,18 +447,23 @@ struct TileOf {
 
 // ---- the product ------------------------------------------------------------------------------------
 
-template <typename T, int FORM, int TR, int TC, int WR, int WC, int NB, int WAVES, bool PAIR, bool DIRECT>
-__global__ __launch_bounds__(WR * WC * 64, WAVES) void k_product(ProductArgs p) {
+// One tile of the product in `lds` (NB buffers of 128 (TR + TC) bytes); q: which tile of which part.
+template <typename T, int FORM, int TR, int TC, int WR, int WC, int NB, bool PAIR, int LOAD>
+__device__ __forceinline__ void product_tile(const ProductArgs &p, int64_t q, char *lds) {
     constexpr int kThreads = WR * WC * 64;
     constexpr int kBk = 128 / static_cast<int>(sizeof(T));
     constexpr int FR = TR / WR / 32, FC = TC / WC / 32;       // 32 x 32 sums of a wavefront
     static_assert(FR > 0 && FC > 0 && (!PAIR || FC % 2 == 0), "a wavefront holds both sums of a pair");
-    static_assert(DIRECT || NB == 2, "through registers: one tile under way");
-    typedef TileOf<T, FORM != kGradW, false, TR, 1, kThreads> A;
-    typedef TileOf<T, FORM == kGradX, true, TC, PAIR ? 2 : 1, kThreads> B;
-    constexpr int kPieces = A::kPieces + B::kPieces;
+    constexpr bool kDirect = LOAD != kThrough;
+    static_assert(kDirect || NB == 2, "through registers: one tile under way");
+    // A wavefront of one 32 x 32 sum in bf16 multiplies 32 cycles a step, where LDS takes over 100 to answer: it has
+    // the operands of a whole tile in registers and reads the next one's before it multiplies.  Others have those of a
+    // step (fp32, 256 cycles a step: 64 x 64 tiles of 2048 squares 143 us by steps, 150 by whole tiles).
+    constexpr bool kWhole = FR * FC == 1 && sizeof(T) == 2;
+    typedef TileOf<T, FORM != kGradW, false, TR, 1, kThreads, LOAD> A;
+    typedef TileOf<T, FORM == kGradX, true, TC, PAIR ? 2 : 1, kThreads, LOAD> B;
+    constexpr int kLoads = A::kLoads + B::kLoads;
     constexpr int kBuffer = A::kBytes + B::kBytes;
-    __shared__ __align__(1024) char lds[NB * kBuffer];
     lds_char *const shared = (lds_char *)lds;
 
     // The tile, and the part of the summed length, of this workgroup.  Workgroups b, b + 8, ... run on one
@@ -432,7 +471,6 @@ __global__ __launch_bounds__(WR * WC * 64, WAVES) void k_product(ProductArgs p) 
     // in columns of eight, so that a stretch is about as high as wide.
     constexpr int64_t kXcds = 8, kHigh = 8;
     const int64_t tiles = p.r_tiles * p.c_tiles;
-    int64_t q = p.first_tile + blockIdx.x;
     const int64_t outer = q / tiles;                        // split, product
     q -= outer * tiles;
     const int64_t whole = tiles / kXcds * kXcds;
@@ -465,63 +503,90 @@ __global__ __launch_bounds__(WR * WC * 64, WAVES) void k_product(ProductArgs p) 
         steps64 = steps64 - lo < share ? steps64 - lo : share;
     }
     const int steps = static_cast<int>(steps64);
-    // segment and summed index of the next tile to load
+    // Segment and summed index of the next tile to load, and where its loads start (scalars: a look at the
+    // arguments for every tile costs 0.1 us of waiting).
     int seg = seg_tiles > 0 ? static_cast<int>(lo / seg_tiles) : 0;
     int64_t k0 = (lo - seg * seg_tiles) * kBk;
+    const int64_t step_a = A::advance(p.ld_a), step_b = B::advance(p.ld_b);
+    const char *from_a, *from_b0, *from_b1;
+    const auto place = [&] {
+        from_a = ta.base(p.a[seg], p.ld_a, k0);
+        from_b0 = tb.base(p.b[z][seg], p.ld_b, k0);
+        from_b1 = PAIR ? tb.base(p.b[1][seg], p.ld_b, k0) : from_b0;
+    };
+    place();
 
     // A tile narrower than a piece is always taken element by element.
-    const bool narrow = !DIRECT && ((FORM == kGradW && p.rows < A::kElems) || (FORM != kGradX && p.cols < B::kElems));
-    u4 ra[DIRECT ? 1 : A::kPieces], rb[DIRECT ? 1 : B::kPieces];
+    const bool narrow = !kDirect && ((FORM == kGradW && p.rows < A::kElems) || (FORM != kGradX && p.cols < B::kElems));
+    u4 ra[kDirect ? 1 : A::kPieces], rb[kDirect ? 1 : B::kPieces];
     bool staged = false;       // the tile that was last issued waits in ra and rb
     const uint32_t lds0 = static_cast<uint32_t>((uintptr_t)shared);
     auto issue = [&](int buf) {
-        const void *pa = p.a[seg];
-        const void *pb0 = p.b[z][seg], *pb1 = PAIR ? p.b[1][seg] : nullptr;
         if (k0 + kBk <= k && !narrow) {
-            if (DIRECT) {
-                const uint32_t to = lds0 + buf * kBuffer + w * 1024;
+            if (kDirect) {
+                const uint32_t to = lds0 + buf * kBuffer + w * (64 * (A::kWord ? 4 : 16));
 #pragma unroll
-                for (int i = 0; i < A::kPieces; ++i)
-                    load_to_lds(to + i * kThreads * 16, ta.at(i), ta.base(pa, p.ld_a, i, k0));
+                for (int i = 0; i < A::kLoads; ++i) load_to_lds<A::kWord>(to + i * A::kLoadBytes, ta.at(i, t), from_a);
 #pragma unroll
-                for (int i = 0; i < B::kPieces; ++i)
-                    load_to_lds(to + A::kBytes + i * kThreads * 16, tb.at(i),
-                                tb.base(PAIR && i >= B::kPieces / 2 ? pb1 : pb0, p.ld_b, i, k0));
+                for (int i = 0; i < B::kLoads; ++i)
+                    load_to_lds<B::kWord>(to + A::kBytes + i * B::kLoadBytes, tb.at(i, t),
+                                          PAIR && i >= B::kLoads / 2 ? from_b1 : from_b0);
             } else {
                 staged = true;
 #pragma unroll
                 for (int i = 0; i < A::kPieces; ++i)
-                    ra[i] = __builtin_bit_cast(u4, *reinterpret_cast<const typename loose<T, A::kElems>::type *>(
-                                                       ta.base(pa, p.ld_a, i, k0) + ta.at(i)));
+                    ra[i] = __builtin_bit_cast(u4, *reinterpret_cast<const typename loose<T, A::kElems>::type *>(from_a + ta.at(i, t)));
 #pragma unroll
                 for (int i = 0; i < B::kPieces; ++i)
                     rb[i] = __builtin_bit_cast(u4, *reinterpret_cast<const typename loose<T, B::kElems>::type *>(
-                                                       tb.base(PAIR && i >= B::kPieces / 2 ? pb1 : pb0, p.ld_b, i, k0) + tb.at(i)));
+                                                       (PAIR && i >= B::kPieces / 2 ? from_b1 : from_b0) + tb.at(i, t)));
             }
         } else {
             staged = false;
+            const void *pa = p.a[seg], *pb0 = p.b[z][seg], *pb1 = PAIR ? p.b[1][seg] : pb0;
             u4 *to = reinterpret_cast<u4 *>(lds + buf * kBuffer) + t;
-            for (int i = 0; i < A::kPieces; ++i) to[i * kThreads] = ta.cut(pa, p.ld_a, i, k0, k, t);
+            // pieces under way together (beside the largest tile's sums there are registers for two)
+            constexpr int kA = FR * FC > 4 ? 2 : A::kPieces, kB = FR * FC > 4 ? 2 : B::kPieces;
+#pragma unroll 1
+            for (int at = 0; at < A::kPieces; at += kA) {
+                u4 v[kA];
+#pragma unroll
+                for (int i = 0; i < kA; ++i) v[i] = ta.cut(pa, p.ld_a, at + i, k0, k, t);
+#pragma unroll
+                for (int i = 0; i < kA; ++i) to[(at + i) * kThreads] = v[i];
+            }
             to += A::kBytes / 16;
-            for (int i = 0; i < B::kPieces; ++i)
-                to[i * kThreads] = tb.cut(PAIR && i >= B::kPieces / 2 ? pb1 : pb0, p.ld_b, i, k0, k, t);
+#pragma unroll 1
+            for (int at = 0; at < B::kPieces; at += kB) {
+                u4 v[kB];
+                const void *const pb = PAIR && at >= B::kPieces / 2 ? pb1 : pb0;
+                const void *const pe = PAIR && at + kB > B::kPieces / 2 ? pb1 : pb0;     // of the batch's second half
+#pragma unroll
+                for (int i = 0; i < kB; ++i) v[i] = tb.cut(i < kB / 2 || kB < B::kPieces ? pb : pe, p.ld_b, at + i, k0, k, t);
+#pragma unroll
+                for (int i = 0; i < kB; ++i) to[(at + i) * kThreads] = v[i];
+            }
         }
         k0 += kBk;
-        if (k0 >= k) {
+        from_a += step_a;
+        from_b0 += step_b;
+        if (PAIR) from_b1 += step_b;
+        if (k0 >= k && seg + 1 < segs) {
             k0 = 0;
             ++seg;
+            place();
         }
     };
     // Through registers: the tile that was last issued goes into LDS.
-    const bool turned = !DIRECT && (p.rows % A::kElems != 0 || p.cols % B::kElems != 0);
+    const bool turned = !kDirect && (p.rows % A::kElems != 0 || p.cols % B::kElems != 0);
     auto commit = [&](int buf) {
-        if (DIRECT || !staged) return;
+        if (kDirect || !staged) return;
         u4 *to = reinterpret_cast<u4 *>(lds + buf * kBuffer) + t;
         if (turned) {
 #pragma unroll
-            for (int i = 0; i < A::kPieces; ++i) ra[i] = ta.shifted(ra[i]);
+            for (int i = 0; i < A::kPieces; ++i) ra[i] = A::shifted(ra[i], ta.shift);
 #pragma unroll
-            for (int i = 0; i < B::kPieces; ++i) rb[i] = tb.shifted(rb[i]);
+            for (int i = 0; i < B::kPieces; ++i) rb[i] = B::shifted(rb[i], tb.shift);
         }
 #pragma unroll
         for (int i = 0; i < A::kPieces; ++i) to[i * kThreads] = ra[i];
@@ -541,36 +606,48 @@ __global__ __launch_bounds__(WR * WC * 64, WAVES) void k_product(ProductArgs p) 
     for (int j = 0; j < FC; ++j)
         at_b[j] = A::kBytes + (PAIR ? (j & 1) * (B::kBytes / 2) + B::read_base(wc * (FC / 2) + j / 2, lane)
                                     : B::read_base(wc * FC + j, lane));
-    u4 fa[2][FR], fb[2][FC];
-    auto read = [&](int buf, int step, int at) {
+    constexpr int kSets = kWhole ? 8 : 2;      // kWhole: 4 set + step; otherwise the parity of the step
+    u4 fa[kSets][FR], fb[kSets][FC];
+    auto read = [&](int set, int buf, int step, int at) {
         const lds_char *from = shared + buf * kBuffer;
         if (at < FR)
-            fa[step & 1][at] = A::read(from, at_a[at], step);
+            fa[set][at] = A::read(from, at_a[at], step);
         else
-            fb[step & 1][at - FR] = B::read(from, at_b[at - FR], step);
+            fb[set][at - FR] = B::read(from, at_b[at - FR], step);
     };
     constexpr int kReads = FR + FC, kProducts = FR * FC;
-    // The products of a step, and between them the reads of the next.
-    auto multiply = [&](int step, bool next, int buf, int next_step) {
+    // The products of a step, and between them the reads of the next.  (With a tile's loads between them as well, each
+    // after one instruction, tiles of 128 and 64 ran 10% slower, and tiles of 256 out of registers.)
+    auto multiply = [&](int set, bool next, int buf, int next_step) {
 #pragma unroll
         for (int ij = 0; ij < kProducts; ++ij) {
             const int i = ij / FC, j = ij % FC;
-            acc[i][j] = Step<T>::mul(fb[step & 1][j], fa[step & 1][i], acc[i][j]);
+            acc[i][j] = Step<T>::mul(fb[set][j], fa[set][i], acc[i][j]);
             if (next) {
 #pragma unroll
-                for (int r = ij * kReads / kProducts; r < (ij + 1) * kReads / kProducts; ++r) read(buf, next_step, r);
+                for (int r = ij * kReads / kProducts; r < (ij + 1) * kReads / kProducts; ++r)
+                    read(next_step & 1, buf, next_step, r);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
     };
+    // The next tile (of `left` that follow the one in hand, in buffer buf) has to be there, and buf has been read.
+    auto turn = [&](int buf, int next, int left) {
+        commit(next);
+        if (NB > 2 && left >= NB - 1)
+            wait_and_meet<(NB - 2) * kLoads>();
+        else
+            wait_and_meet<0>();
+        if (left >= (kDirect ? NB : 2)) issue(buf);
+    };
 
     if (steps > 0) {
-        if (DIRECT) {
+        if (kDirect) {
 #pragma unroll
             for (int j = 0; j < NB - 1; ++j)
                 if (j < steps) issue(j);
             if (steps >= NB - 1)
-                wait_and_meet<(NB - 2) * kPieces>();
+                wait_and_meet<(NB - 2) * kLoads>();
             else
                 wait_and_meet<0>();
             if (NB - 1 < steps) issue(NB - 1);
@@ -580,30 +657,46 @@ __global__ __launch_bounds__(WR * WC * 64, WAVES) void k_product(ProductArgs p) 
             wait_and_meet<0>();
             if (steps > 1) issue(1);
         }
+        int buf = 0, left = steps - 1;
+        if constexpr (kWhole) {
+            const auto read_all = [&](int set, int from) {
 #pragma unroll
-        for (int r = 0; r < kReads; ++r) read(0, 0, r);
-        int buf = 0;
-        for (int s = 0; s + 1 < steps; ++s) {
-            const int next = buf + 1 == NB ? 0 : buf + 1;
+                for (int step = 0; step < 4; ++step)
 #pragma unroll
-            for (int step = 0; step < 3; ++step) multiply(step, true, buf, step + 1);
-            // Tile s is read; the next one has to be there.
-            commit(next);
-            if (NB > 2 && s + NB <= steps)
-                wait_and_meet<(NB - 2) * kPieces>();
-            else
-                wait_and_meet<0>();
-            if (DIRECT) {
-                if (s + NB < steps) issue(buf);
-            } else {
-                if (s + 2 < steps) issue(buf);
+                    for (int r = 0; r < kReads; ++r) read(4 * set + step, from, step, r);
+            };
+            const auto tile = [&](int set) {
+                if (left > 0) {
+                    const int next = buf + 1 == NB ? 0 : buf + 1;
+                    turn(buf, next, left);
+                    read_all(set ^ 1, next);
+                    buf = next;
+                }
+#pragma unroll
+                for (int step = 0; step < 4; ++step) multiply(4 * set + step, false, 0, 0);
+            };
+            read_all(0, 0);
+            while (true) {
+                tile(0);
+                if (--left < 0) break;
+                tile(1);
+                if (--left < 0) break;
             }
-            multiply(3, true, next, 0);
-            buf = next;
-        }
+        } else {
 #pragma unroll
-        for (int step = 0; step < 3; ++step) multiply(step, true, buf, step + 1);
-        multiply(3, false, 0, 0);
+            for (int r = 0; r < kReads; ++r) read(0, 0, 0, r);
+            for (; left > 0; --left) {
+                const int next = buf + 1 == NB ? 0 : buf + 1;
+#pragma unroll
+                for (int step = 0; step < 3; ++step) multiply(step & 1, true, buf, step + 1);
+                turn(buf, next, left);
+                multiply(1, true, next, 0);
+                buf = next;
+            }
+#pragma unroll
+            for (int step = 0; step < 3; ++step) multiply(step & 1, true, buf, step + 1);
+            multiply(1, false, 0, 0);
+        }
     }
 
     // A lane holds row lane % 32 of each 32 x 32 sum, and its columns 16 (lane / 32) + 0..15.
@@ -627,45 +720,167 @@ __global__ __launch_bounds__(WR * WC * 64, WAVES) void k_product(ProductArgs p) 
     }
 }
 
-// ---- launching --------------------------------------------------------------------------------------
-
-// Tile shapes of the kernel: 256 x 256 by eight wavefronts (bf16 only), 128 x 128 by four, 32 x 128 for
-// few rows.
-enum : int32_t { kTile256, kTile128, kTile32 };
-
-struct ProductPlan {
-    int32_t form, tile, pair, direct;
+// out[c] = the sum of `parts` rows of sums; a workgroup takes 32 columns, a row for every 32 threads at a time.
+struct ColumnArgs {
+    const float *sums;             // [parts][ld]
+    int64_t ld;
+    int32_t parts;
+    int64_t cols, second;          // out[1] is of the columns from `second` on
+    int32_t type;
+    void *out[2];                  // may be NULL
+    uint32_t blocks;               // workgroups of each of the two (0: nothing to do)
 };
 
-inline int tile_rows(int tile) { return tile == kTile256 ? 256 : tile == kTile128 ? 128 : 32; }
-inline int tile_cols(int tile, bool pair) { return (tile == kTile256 ? 256 : 128) / (pair ? 2 : 1); }
+template <int THREADS>
+__device__ __forceinline__ void column_sums(const ColumnArgs &p, uint32_t block, float *lds) {
+    constexpr int kHigh = THREADS / 32;
+    const int z = block >= p.blocks ? 1 : 0;
+    void *const out = p.out[z];
+    if (out == nullptr) return;      // whole workgroup
+    const int x = threadIdx.x % 32, y = threadIdx.x / 32;
+    const int64_t c = (block - z * p.blocks) * 32ll + x;
+    float s = 0.f;
+    if (c < p.cols) {
+        const float *from = p.sums + z * p.second + c;
+#pragma unroll 8
+        for (int i = y; i < p.parts; i += kHigh) s += from[i * p.ld];
+    }
+    lds[y * 33 + x] = s;
+    __syncthreads();
+    if (y == 0 && c < p.cols) {
+#pragma unroll
+        for (int i = 1; i < kHigh; ++i) s += lds[i * 33 + x];
+        if (p.type == GNN_BF16)
+            static_cast<bf16 *>(out)[c] = static_cast<bf16>(s);
+        else
+            static_cast<float *>(out)[c] = s;
+    }
+}
 
-hipError_t launch_product_bf16(ProductArgs a, const ProductPlan &p, hipStream_t s);
-hipError_t launch_product_f32(ProductArgs a, const ProductPlan &p, hipStream_t s);
+// Wavefronts, buffers of LDS (by the type's bytes) and wavefronts a SIMD of each tile shape.
+struct Tile256 {          // bf16 only, by pieces only
+    static constexpr int kRows = 256, kCols = 256, kWr = 2, kWc = 4;
+    static constexpr int buffers(int, int) { return 2; }
+    static constexpr int waves(int) { return 2; }
+};
+struct Tile128 {          // bf16: one workgroup a compute unit (large bf16 products take Tile256)
+    static constexpr int kRows = 128, kCols = 128, kWr = 2, kWc = 2;
+    static constexpr int buffers(int size, int load) { return size == 4 || load == kThrough ? 2 : load == kByWord ? 3 : 4; }
+    static constexpr int waves(int size) { return size == 2 ? 1 : 2; }
+};
+struct Tile64 {
+    static constexpr int kRows = 64, kCols = 64, kWr = 2, kWc = 2;
+    static constexpr int buffers(int, int load) { return load == kThrough ? 2 : 4; }
+    static constexpr int waves(int) { return 2; }
+};
+struct Tile32 {           // few rows
+    static constexpr int kRows = 32, kCols = 128, kWr = 1, kWc = 4;
+    static constexpr int buffers(int, int load) { return load == kThrough ? 2 : 4; }
+    static constexpr int waves(int) { return 2; }
+};
 
-template <typename T, int FORM, int TR, int TC, int WR, int WC, int NB, int WAVES, bool PAIR, bool DIRECT>
-hipError_t launch_tile(ProductArgs &a, hipStream_t s) {
-    a.r_tiles = (a.rows + TR - 1) / TR;
-    const int64_t wide = PAIR ? TC / 2 : TC;
-    a.c_tiles = (a.cols + wide - 1) / wide;
-    return launch_pieces(a.r_tiles * a.c_tiles * a.products * a.splits, WR * WC * 64, [&](int64_t first, unsigned blocks) {
+template <typename T, typename TILE, bool PAIR, int LOAD>
+__global__ __launch_bounds__(TILE::kWr * TILE::kWc * 64, TILE::waves(sizeof(T))) void k_product(ProductArgs p) {
+    constexpr int NB = TILE::buffers(sizeof(T), LOAD);
+    __shared__ __align__(1024) char lds[NB * (TILE::kRows + TILE::kCols) * 128];
+    product_tile<T, kForward, TILE::kRows, TILE::kCols, TILE::kWr, TILE::kWc, NB, PAIR, LOAD>(p, p.first_tile + blockIdx.x, lds);
+}
+
+// Both gradients of a layer, and the sums of the bias's: w_tiles workgroups of dW, x_tiles of dx (those whose summed
+// length is longer come first, so that none of them is left at the end), and the last ones add columns.
+template <typename T, typename TILE, int LOAD>
+__global__ __launch_bounds__(TILE::kWr * TILE::kWc * 64, TILE::waves(sizeof(T))) void k_gradients(
+    ProductArgs w, ProductArgs x, ColumnArgs c, int64_t w_tiles, int64_t x_tiles, bool x_first) {
+    constexpr int NB = TILE::buffers(sizeof(T), LOAD);
+    __shared__ __align__(1024) char lds[NB * (TILE::kRows + TILE::kCols) * 128];
+    const int64_t q = w.first_tile + blockIdx.x, all = w_tiles + x_tiles;
+    const int64_t qw = x_first ? q - x_tiles : q, qx = x_first ? q : q - w_tiles;
+    if (q >= all)
+        column_sums<TILE::kWr * TILE::kWc * 64>(c, static_cast<uint32_t>(q - all), reinterpret_cast<float *>(lds));
+    else if (x_first ? qw >= 0 : qx < 0)
+        product_tile<T, kGradW, TILE::kRows, TILE::kCols, TILE::kWr, TILE::kWc, NB, false, LOAD>(w, qw, lds);
+    else
+        product_tile<T, kGradX, TILE::kRows, TILE::kCols, TILE::kWr, TILE::kWc, NB, false, LOAD>(x, qx, lds);
+}
+
+// ---- launching --------------------------------------------------------------------------------------
+
+enum : int32_t { kTile256, kTile128, kTile64, kTile32 };
+
+inline int tile_rows(int tile) { return tile == kTile256 ? 256 : tile == kTile128 ? 128 : tile == kTile64 ? 64 : 32; }
+inline int tile_cols(int tile, bool pair) {
+    return (tile == kTile256 ? 256 : tile == kTile64 ? 64 : 128) / (pair ? 2 : 1);
+}
+
+// pair: the two products' sums meet in one workgroup (kTile256 and kTile128); load: kByPiece, kByWord or kThrough.
+hipError_t launch_product_bf16(ProductArgs a, int tile, bool pair, int load, hipStream_t s);
+hipError_t launch_product_f32(ProductArgs a, int tile, bool pair, int load, hipStream_t s);
+// Either of w and x may have no products.
+hipError_t launch_gradients_bf16(ProductArgs w, ProductArgs x, const ColumnArgs &c, int tile, int load, hipStream_t s);
+hipError_t launch_gradients_f32(ProductArgs w, ProductArgs x, const ColumnArgs &c, int tile, int load, hipStream_t s);
+
+inline int64_t set_tiles(ProductArgs &a, int tile, bool pair) {
+    a.r_tiles = (a.rows + tile_rows(tile) - 1) / tile_rows(tile);
+    a.c_tiles = (a.cols + tile_cols(tile, pair) - 1) / tile_cols(tile, pair);
+    return a.r_tiles * a.c_tiles * a.products * a.splits;
+}
+
+template <typename T, typename TILE, bool PAIR, int LOAD>
+hipError_t launch_tiles(ProductArgs &a, int64_t tiles, hipStream_t s) {
+    constexpr int kThreads = TILE::kWr * TILE::kWc * 64;
+    return launch_pieces(tiles, kThreads, [&](int64_t first, unsigned blocks) {
         a.first_tile = first;
-        k_product<T, FORM, TR, TC, WR, WC, NB, WAVES, PAIR, DIRECT><<<blocks, WR * WC * 64, 0, s>>>(a);
+        k_product<T, TILE, PAIR, LOAD><<<blocks, kThreads, 0, s>>>(a);
     });
 }
 
-template <typename T, int FORM, bool PAIR>
-hipError_t launch_form(ProductArgs &a, const ProductPlan &p, hipStream_t s) {
+template <typename T, typename TILE, bool PAIR>
+hipError_t launch_by(ProductArgs &a, int load, int64_t tiles, hipStream_t s) {
+    if (load == kByPiece) return launch_tiles<T, TILE, PAIR, kByPiece>(a, tiles, s);
+    if (sizeof(T) == 4 || load == kByWord) return launch_tiles<T, TILE, PAIR, kByWord>(a, tiles, s);
+    if constexpr (sizeof(T) == 2) return launch_tiles<T, TILE, PAIR, kThrough>(a, tiles, s);
+    return hipErrorInvalidValue;
+}
+
+template <typename T>
+hipError_t launch_product(ProductArgs a, int tile, bool pair, int load, hipStream_t s) {
+    const int64_t tiles = set_tiles(a, tile, pair);
     if constexpr (sizeof(T) == 2) {
-        if (p.tile == kTile256 && p.direct) return launch_tile<T, FORM, 256, 256, 2, 4, 2, 2, PAIR, true>(a, s);
+        if (tile == kTile256)
+            return pair ? launch_tiles<T, Tile256, true, kByPiece>(a, tiles, s) : launch_tiles<T, Tile256, false, kByPiece>(a, tiles, s);
     }
-    if constexpr (FORM != kGradW && !PAIR) {
-        if (p.tile == kTile32)
-            return p.direct ? launch_tile<T, FORM, 32, 128, 1, 4, 4, 2, false, true>(a, s)
-                            : launch_tile<T, FORM, 32, 128, 1, 4, 2, 2, false, false>(a, s);
+    if (tile == kTile32) return launch_by<T, Tile32, false>(a, load, tiles, s);
+    if (tile == kTile64) return launch_by<T, Tile64, false>(a, load, tiles, s);
+    return pair ? launch_by<T, Tile128, true>(a, load, tiles, s) : launch_by<T, Tile128, false>(a, load, tiles, s);
+}
+
+template <typename T, typename TILE, int LOAD>
+hipError_t launch_both(ProductArgs &w, ProductArgs &x, const ColumnArgs &c, int64_t w_tiles, int64_t x_tiles, hipStream_t s) {
+    constexpr int kThreads = TILE::kWr * TILE::kWc * 64;
+    const bool x_first = x.k * x.segs * w.splits > w.k * w.segs * x.splits;
+    return launch_pieces(w_tiles + x_tiles + 2 * c.blocks, kThreads, [&](int64_t first, unsigned blocks) {
+        w.first_tile = first;
+        k_gradients<T, TILE, LOAD><<<blocks, kThreads, 0, s>>>(w, x, c, w_tiles, x_tiles, x_first);
+    });
+}
+
+template <typename T, typename TILE>
+hipError_t launch_both_by(ProductArgs &w, ProductArgs &x, const ColumnArgs &c, int load, int64_t w_tiles, int64_t x_tiles,
+                          hipStream_t s) {
+    if (load == kByPiece) return launch_both<T, TILE, kByPiece>(w, x, c, w_tiles, x_tiles, s);
+    if (sizeof(T) == 4 || load == kByWord) return launch_both<T, TILE, kByWord>(w, x, c, w_tiles, x_tiles, s);
+    if constexpr (sizeof(T) == 2) return launch_both<T, TILE, kThrough>(w, x, c, w_tiles, x_tiles, s);
+    return hipErrorInvalidValue;
+}
+
+template <typename T>
+hipError_t launch_gradients(ProductArgs w, ProductArgs x, const ColumnArgs &c, int tile, int load, hipStream_t s) {
+    const int64_t w_tiles = set_tiles(w, tile, false), x_tiles = set_tiles(x, tile, false);
+    if constexpr (sizeof(T) == 2) {
+        if (tile == kTile256) return launch_both<T, Tile256, kByPiece>(w, x, c, w_tiles, x_tiles, s);
     }
-    return p.direct ? launch_tile<T, FORM, 128, 128, 2, 2, 2, 2, PAIR, true>(a, s)
-                    : launch_tile<T, FORM, 128, 128, 2, 2, 2, 2, PAIR, false>(a, s);
+    if (tile == kTile64) return launch_both_by<T, Tile64>(w, x, c, load, w_tiles, x_tiles, s);
+    return launch_both_by<T, Tile128>(w, x, c, load, w_tiles, x_tiles, s);
 }
 
 }  // namespace gnnmb
