@@ -886,14 +886,30 @@ def gnn_orthogonalize(g: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, step
         "gnn_orthogonalize")
 
 
-def _matrix(t: torch.Tensor, dtype, rows: int, cols: int, name: str):
-    """(pointer, row stride) of a [>= rows, cols] device matrix of this type; (None, 0) of None."""
+def _on(t: torch.Tensor, device: int, name: str) -> None:
+    """Refuses a tensor that is on another device than the call (-1: the host)."""
+    if t.get_device() < 0:
+        raise ValueError(f"{name}: must be a device tensor")
+    raise ValueError(f"{name}: is on device {t.get_device()}, the call on device {device}")
+
+
+def _device_of(x: torch.Tensor, stream) -> int:
+    """The device that a call on x runs on: the stream's (a handle's is the current one)."""
+    device = stream.device_index if isinstance(stream, torch.cuda.Stream) else torch.cuda.current_device() \
+        if x.is_cuda else -1
+    if device < 0 or x.get_device() != device:
+        _on(x, device, "x")
+    return device
+
+
+def _matrix(t: Optional[torch.Tensor], dtype, rows: int, cols: int, name: str, device: int):
+    """(pointer, row stride) of a [>= rows, cols] matrix of this type on the device; (None, 0) of None."""
     if t is None:
         return None, 0
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a device tensor")
+    if t.get_device() != device:
+        _on(t, device, name)
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[0] < rows or shape[1] != cols or (cols > 1 and stride[1] != 1) or \
             (shape[0] > 1 and stride[0] < cols):
@@ -901,41 +917,32 @@ def _matrix(t: torch.Tensor, dtype, rows: int, cols: int, name: str):
     return t.data_ptr(), stride[0] if shape[0] > 1 else cols
 
 
-def _vector(t: torch.Tensor, dtype, n: int, name: str):
-    """The pointer of a contiguous device tensor of n elements; None of None."""
+def _vector(t: Optional[torch.Tensor], dtype, n: int, name: str, device: int):
+    """The pointer of a contiguous tensor of n elements on the device; None of None."""
     if t is None:
         return None
-    _need(t, dtype, name)
+    if t.dtype is not dtype or not t.is_contiguous():
+        _need(t, dtype, name)
+    if t.get_device() != device:
+        _on(t, device, name)
     if t.numel() != n:
         raise ValueError(f"{name}: [{n}]")
     return t.data_ptr()
 
 
-def _space(ws: torch.Tensor):
-    if not ws.is_cuda or not ws.is_contiguous():
+def _space(ws: torch.Tensor, device: int):
+    if ws.get_device() != device:
+        _on(ws, device, "ws")
+    if not ws.is_contiguous():
         raise ValueError("ws: must be a contiguous device tensor")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _rows_of(x: torch.Tensor):
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x: must be a matrix")
-    return x.shape
-
-
-def _norm(x, weight, bias, eps, mean, rstd, d_n) -> _abi.gnn_norm:
-    n, d = _rows_of(x)
-    kind = _type(x.dtype, "x")
-    px, ld_x = _matrix(x, x.dtype, n, d, "x")
-    param = weight if weight is not None else bias
-    pt = x.dtype if param is None else param.dtype
-    a = _abi.gnn_norm(kind, kind, _type(pt, "weight"), eps, n, d)
-    a.x, a.ld_x = px, ld_x
-    a.d_n = _vector(d_n, torch.int64, 1, "d_n")
-    a.weight, a.bias = _vector(weight, pt, d, "weight"), _vector(bias, pt, d, "bias")
-    a.mean = _vector(mean, torch.float32, n, "mean")
-    a.rstd = _vector(rstd, torch.float32, n, "rstd")
-    return a
+    return shape
 
 
 def gnn_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor],
@@ -945,9 +952,16 @@ def gnn_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Option
     """out = (x - mean) * rstd * weight + bias over the rows of x [n, d], mean and rstd (float32 [n])
     those of each row, rstd = 1 / sqrt(variance + eps).  x, out and weight with bias: float32 or
     bfloat16 each; None for weight: ones, for bias: zeros."""
-    a = _norm(x, weight, bias, eps, mean, rstd, d_n)
-    a.out_type = _type(out.dtype, "out")
-    a.out, a.ld_out = _matrix(out, out.dtype, a.n, a.d, "out")
+    n, d = _rows_of(x)
+    dev = _device_of(x, stream)
+    xt, ot = x.dtype, out.dtype
+    pt = weight.dtype if weight is not None else xt if bias is None else bias.dtype
+    px, ld_x = _matrix(x, xt, n, d, "x", dev)
+    po, ld_out = _matrix(out, ot, n, d, "out", dev)
+    a = _abi.gnn_norm(_type(xt, "x"), _type(ot, "out"), _type(pt, "weight"), eps, n, d,
+                      _vector(d_n, torch.int64, 1, "d_n", dev), px, ld_x, _vector(weight, pt, d, "weight", dev),
+                      _vector(bias, pt, d, "bias", dev), po, ld_out, _vector(mean, torch.float32, n, "mean", dev),
+                      _vector(rstd, torch.float32, n, "rstd", dev))
     _ok(lib().gnn_layer_norm(ctypes.byref(a), _stream(stream)), "gnn_layer_norm")
 
 
@@ -966,19 +980,19 @@ def gnn_layer_norm_backward(x: torch.Tensor, weight: Optional[torch.Tensor], mea
     """dx, dweight and dbias (those that are not None) of gnn_layer_norm from its mean and rstd and the
     gradient dout of out; residual_grad, the gradient that reaches x past the norm, is added to dx."""
     n, d = _rows_of(x)
-    param = next((t for t in (weight, dweight, dbias) if t is not None), None)
-    a = _norm(x, weight, None, 0.0, mean, rstd, d_n)
-    if param is not None:
-        a.param_type = _type(param.dtype, "dweight")
-    a.out_type = _type(dout.dtype, "dout")
-    g = _abi.gnn_norm_grad()
-    g.dout, g.ld_dout = _matrix(dout, dout.dtype, n, d, "dout")
-    g.residual_grad, g.ld_residual_grad = _matrix(residual_grad, x.dtype, n, d, "residual_grad")
-    g.dx, g.ld_dx = _matrix(dx, x.dtype, n, d, "dx")
-    if param is not None:
-        g.dweight = _vector(dweight, param.dtype, d, "dweight")
-        g.dbias = _vector(dbias, param.dtype, d, "dbias")
-    p, size = _space(ws)
+    dev = _device_of(x, stream)
+    xt, ot = x.dtype, dout.dtype
+    pt = next((t.dtype for t in (weight, dweight, dbias) if t is not None), xt)
+    px, ld_x = _matrix(x, xt, n, d, "x", dev)
+    a = _abi.gnn_norm(_type(xt, "x"), _type(ot, "dout"), _type(pt, "weight"), 0.0, n, d,
+                      _vector(d_n, torch.int64, 1, "d_n", dev), px, ld_x, _vector(weight, pt, d, "weight", dev), None,
+                      None, d, _vector(mean, torch.float32, n, "mean", dev), _vector(rstd, torch.float32, n, "rstd", dev))
+    pdy, ld_dy = _matrix(dout, ot, n, d, "dout", dev)
+    pr, ld_r = _matrix(residual_grad, xt, n, d, "residual_grad", dev)
+    pdx, ld_dx = _matrix(dx, xt, n, d, "dx", dev)
+    g = _abi.gnn_norm_grad(pdy, ld_dy, pr, ld_r, pdx, ld_dx, _vector(dweight, pt, d, "dweight", dev),
+                           _vector(dbias, pt, d, "dbias", dev))
+    p, size = _space(ws, dev)
     _ok(lib().gnn_layer_norm_backward(ctypes.byref(a), ctypes.byref(g), p, size, _stream(stream)),
         "gnn_layer_norm_backward")
 
@@ -996,15 +1010,16 @@ def _activation(name: str) -> int:
     return a
 
 
-def _layer(layer, x, w, activation, d_n):
-    """The parts that gnn_dense and gnn_gated share; w: any of the layer's weights."""
+def _layer(x, w, activation, d_n, stream):
+    """(type, activation, n, d_in, d_out, d_n, x, ld_x) of a layer, and its device; w: any of its weights."""
     n, d_in = _rows_of(x)
-    if w.dim() != 2:
+    shape = w.shape
+    if len(shape) != 2:
         raise ValueError("weights: must be matrices")
-    a = layer(_type(x.dtype, "x"), _activation(activation), n, d_in, w.shape[1])
-    a.x, a.ld_x = _matrix(x, x.dtype, n, d_in, "x")
-    a.d_n = _vector(d_n, torch.int64, 1, "d_n")
-    return a
+    dt = x.dtype
+    kind, act, dev = _type(dt, "x"), _activation(activation), _device_of(x, stream)
+    return (kind, act, n, d_in, shape[1], _vector(d_n, torch.int64, 1, "d_n", dev),
+            *_matrix(x, dt, n, d_in, "x", dev)), dev
 
 
 def _same_stride(first, second, names: str):
@@ -1032,14 +1047,12 @@ def gnn_linear(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, ws: torch.Te
                d_n: Optional[torch.Tensor] = None, stream=None) -> None:
     """out = act(x w + bias) + residual; pre, if given, receives x w + bias for the backward pass.
     x: [n, d_in], w: [d_in, d_out], the others [n, d_out] and [d_out], one type, float32 or bfloat16."""
-    a = _layer(_abi.gnn_dense, x, w, activation, d_n)
-    n, d_out, dt = a.n, a.d_out, x.dtype
-    a.w, a.ld_w = _matrix(w, dt, a.d_in, d_out, "w")
-    a.bias = _vector(bias, dt, d_out, "bias")
-    a.residual, a.ld_residual = _matrix(residual, dt, n, d_out, "residual")
-    a.out, a.ld_out = _matrix(out, dt, n, d_out, "out")
-    a.pre, a.ld_pre = _matrix(pre, dt, n, d_out, "pre")
-    p, size = _space(ws)
+    head, dev = _layer(x, w, activation, d_n, stream)
+    n, d_in, d_out, dt = head[2], head[3], head[4], x.dtype
+    a = _abi.gnn_dense(*head, *_matrix(w, dt, d_in, d_out, "w", dev), _vector(bias, dt, d_out, "bias", dev),
+                       *_matrix(residual, dt, n, d_out, "residual", dev), *_matrix(out, dt, n, d_out, "out", dev),
+                       *_matrix(pre, dt, n, d_out, "pre", dev))
+    p, size = _space(ws, dev)
     _ok(lib().gnn_linear(ctypes.byref(a), p, size, _stream(stream)), "gnn_linear")
 
 
@@ -1050,16 +1063,13 @@ def gnn_linear_backward(x: torch.Tensor, w: torch.Tensor, dout: torch.Tensor, ws
                         stream=None) -> None:
     """Those of dx, dw and dbias that are given, from the gradient dout of gnn_linear's out and, where
     there is an activation, its pre.  (The residual's gradient is dout.)"""
-    a = _layer(_abi.gnn_dense, x, w, activation, d_n)
-    n, d_in, d_out, dt = a.n, a.d_in, a.d_out, x.dtype
-    a.w, a.ld_w = _matrix(w, dt, d_in, d_out, "w")
-    a.pre, a.ld_pre = _matrix(pre, dt, n, d_out, "pre")
-    g = _abi.gnn_dense_grad()
-    g.dout, g.ld_dout = _matrix(dout, dt, n, d_out, "dout")
-    g.dx, g.ld_dx = _matrix(dx, dt, n, d_in, "dx")
-    g.dw, g.ld_dw = _matrix(dw, dt, d_in, d_out, "dw")
-    g.dbias = _vector(dbias, dt, d_out, "dbias")
-    p, size = _space(ws)
+    head, dev = _layer(x, w, activation, d_n, stream)
+    n, d_in, d_out, dt = head[2], head[3], head[4], x.dtype
+    a = _abi.gnn_dense(*head, *_matrix(w, dt, d_in, d_out, "w", dev), None, None, 0, None, 0,
+                       *_matrix(pre, dt, n, d_out, "pre", dev))
+    g = _abi.gnn_dense_grad(*_matrix(dout, dt, n, d_out, "dout", dev), *_matrix(dx, dt, n, d_in, "dx", dev),
+                            *_matrix(dw, dt, d_in, d_out, "dw", dev), _vector(dbias, dt, d_out, "dbias", dev))
+    p, size = _space(ws, dev)
     _ok(lib().gnn_linear_backward(ctypes.byref(a), ctypes.byref(g), p, size, _stream(stream)),
         "gnn_linear_backward")
 
@@ -1076,15 +1086,14 @@ def gnn_gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, 
     """out = act(x w_gate + bias_gate) * (x w_up + bias_up); gate and up, if given, receive the two sums for
     the backward pass.  x: [n, d_in], weights: [d_in, d_out] of one row stride (halves of one matrix, for
     instance), the others [n, d_out] and [d_out], one type, float32 or bfloat16."""
-    a = _layer(_abi.gnn_gated, x, w_gate, activation, d_n)
-    n, d_in, d_out, dt = a.n, a.d_in, a.d_out, x.dtype
-    a.w_gate, a.w_up, a.ld_w = _same_stride(_matrix(w_gate, dt, d_in, d_out, "w_gate"),
-                                            _matrix(w_up, dt, d_in, d_out, "w_up"), "w_gate, w_up")
-    a.bias_gate, a.bias_up = _vector(bias_gate, dt, d_out, "bias_gate"), _vector(bias_up, dt, d_out, "bias_up")
-    a.out, a.ld_out = _matrix(out, dt, n, d_out, "out")
-    a.gate, a.up, a.ld_pre = _same_stride(_matrix(gate, dt, n, d_out, "gate"),
-                                          _matrix(up, dt, n, d_out, "up"), "gate, up")
-    p, size = _space(ws)
+    head, dev = _layer(x, w_gate, activation, d_n, stream)
+    n, d_in, d_out, dt = head[2], head[3], head[4], x.dtype
+    w = _same_stride(_matrix(w_gate, dt, d_in, d_out, "w_gate", dev), _matrix(w_up, dt, d_in, d_out, "w_up", dev),
+                     "w_gate, w_up")
+    pre = _same_stride(_matrix(gate, dt, n, d_out, "gate", dev), _matrix(up, dt, n, d_out, "up", dev), "gate, up")
+    a = _abi.gnn_gated(*head, *w, _vector(bias_gate, dt, d_out, "bias_gate", dev),
+                       _vector(bias_up, dt, d_out, "bias_up", dev), *_matrix(out, dt, n, d_out, "out", dev), *pre)
+    p, size = _space(ws, dev)
     _ok(lib().gnn_gated_linear(ctypes.byref(a), p, size, _stream(stream)), "gnn_gated_linear")
 
 
@@ -1098,21 +1107,18 @@ def gnn_gated_linear_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch
                               d_n: Optional[torch.Tensor] = None, stream=None) -> None:
     """Those of dx, dw_gate, dw_up, dbias_gate and dbias_up that are given, from the gradient dout of
     gnn_gated_linear's out and its gate and up.  dw_gate and dw_up have one row stride, like gate and up."""
-    a = _layer(_abi.gnn_gated, x, w_gate, activation, d_n)
-    n, d_in, d_out, dt = a.n, a.d_in, a.d_out, x.dtype
-    a.w_gate, a.w_up, a.ld_w = _same_stride(_matrix(w_gate, dt, d_in, d_out, "w_gate"),
-                                            _matrix(w_up, dt, d_in, d_out, "w_up"), "w_gate, w_up")
-    a.gate, a.up, a.ld_pre = _same_stride(_matrix(gate, dt, n, d_out, "gate"),
-                                          _matrix(up, dt, n, d_out, "up"), "gate, up")
-    g = _abi.gnn_gated_grad()
-    g.dout, g.ld_dout = _matrix(dout, dt, n, d_out, "dout")
-    g.dx, g.ld_dx = _matrix(dx, dt, n, d_in, "dx")
-    g.dw_gate, g.dw_up, g.ld_dw = _same_stride(_matrix(dw_gate, dt, d_in, d_out, "dw_gate"),
-                                               _matrix(dw_up, dt, d_in, d_out, "dw_up"),
-                                               "dw_gate, dw_up")
-    g.dbias_gate = _vector(dbias_gate, dt, d_out, "dbias_gate")
-    g.dbias_up = _vector(dbias_up, dt, d_out, "dbias_up")
-    p, size = _space(ws)
+    head, dev = _layer(x, w_gate, activation, d_n, stream)
+    n, d_in, d_out, dt = head[2], head[3], head[4], x.dtype
+    w = _same_stride(_matrix(w_gate, dt, d_in, d_out, "w_gate", dev), _matrix(w_up, dt, d_in, d_out, "w_up", dev),
+                     "w_gate, w_up")
+    pre = _same_stride(_matrix(gate, dt, n, d_out, "gate", dev), _matrix(up, dt, n, d_out, "up", dev), "gate, up")
+    a = _abi.gnn_gated(*head, *w, None, None, None, 0, *pre)
+    dw = _same_stride(_matrix(dw_gate, dt, d_in, d_out, "dw_gate", dev), _matrix(dw_up, dt, d_in, d_out, "dw_up", dev),
+                      "dw_gate, dw_up")
+    g = _abi.gnn_gated_grad(*_matrix(dout, dt, n, d_out, "dout", dev), *_matrix(dx, dt, n, d_in, "dx", dev), *dw,
+                            _vector(dbias_gate, dt, d_out, "dbias_gate", dev),
+                            _vector(dbias_up, dt, d_out, "dbias_up", dev))
+    p, size = _space(ws, dev)
     _ok(lib().gnn_gated_linear_backward(ctypes.byref(a), ctypes.byref(g), p, size, _stream(stream)),
         "gnn_gated_linear_backward")
 

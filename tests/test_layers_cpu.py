@@ -160,6 +160,28 @@ def test_binding_checks_tensors():
     assert gm._same_stride((None, 0), (2, 48), "gate, up") == (None, 2, 48)
 
 
+def test_tensors_on_another_device_are_refused(monkeypatch):
+    """A call runs on the stream's device, the current one's without a stream; every tensor has to be there."""
+    class Tensor:
+        is_cuda = True
+
+        def __init__(self, device):
+            self.device = device
+
+        def get_device(self):
+            return self.device
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert gm._device_of(Tensor(1), None) == 1 and gm._device_of(Tensor(1), 12345) == 1
+    with pytest.raises(ValueError, match="x: is on device 0, the call on device 1"):
+        gm._device_of(Tensor(0), None)
+    with pytest.raises(ValueError, match="ws: is on device 0, the call on device 1"):
+        gm._space(Tensor(0), 1)
+    host = torch.zeros(4)
+    with pytest.raises(ValueError, match="w: must be a device tensor"):
+        gm._vector(host, host.dtype, 4, "w", 1)
+
+
 def test_layouts_match_the_header(tmp_path):
     structs = [_abi.gnn_norm, _abi.gnn_norm_grad, _abi.gnn_dense, _abi.gnn_dense_grad, _abi.gnn_gated,
                _abi.gnn_gated_grad]
