@@ -64,7 +64,9 @@ __device__ __forceinline__ void join_parts(const ProductArgs &p, int64_t rows, i
             }
         }
     }
-    if (there && lane == 0) finish<T, 4, PAIR>(p.e, static_cast<int>(z), m, n, p.cols - n, v, u);
+    if (there && lane == 0)
+        finish<T, 4, PAIR>(p.e, static_cast<int>(z), m, n, p.cols - n, v, u,
+                           load_addends<T, 4, PAIR>(p.e, static_cast<int>(z), m, n, p.cols - n));
 }
 
 struct JoinArgs {
