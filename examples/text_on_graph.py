@@ -6,14 +6,17 @@ Every seed node carries a text of a few tokens.  One step on a mini-batch:
      neighbours' node vectors, both from fp32 tables that are trained;
   3. gnn_cross_attention lets a seed's tokens attend to its own sampled neighbours: the block's indptr
      is the states' indptr, so seeds have different numbers of them, or none;
-  4. the attended tokens are summed and classified;
-  5. backward: gnn_cross_attention_backward, then gnn_embedding_grad for the token table and
-     gnn_embedding_grad_rows for the touched rows of the node table;
-  6. the weight matrices move along their momentum, orthogonalised by gnn_orthogonalize; the tables
+  4. with --hidden, a feed-forward block follows: gnn_layer_norm, gnn_gated_linear and gnn_linear, which
+     adds its input (the residual) in its epilogue;
+  5. the tokens are averaged and classified;
+  6. backward: gnn_linear_backward, gnn_gated_linear_backward and gnn_layer_norm_backward (which adds the
+     residual's gradient), gnn_cross_attention_backward, then gnn_embedding_grad for the token table
+     and gnn_embedding_grad_rows for the touched rows of the node table;
+  7. the weight matrices move along their momentum, orthogonalised by gnn_orthogonalize; the tables
      by plain gradient steps.
 The projections are ordinary torch products.
 
-    python examples/text_on_graph.py [--steps 60]
+    python examples/text_on_graph.py [--steps 60] [--hidden 128]
 """
 from __future__ import annotations
 
@@ -29,12 +32,13 @@ import graph_mini_pipeline_amd as gm  # noqa: E402
 import synth  # noqa: E402
 
 PAD = 0      # the padding token
+EPS = 1e-5   # of the norm
 
 
 class TextOnGraph:
     def __init__(self, graph: gm.DeviceGraph, vocab: int, d: int = 64, heads: int = 4, kv_heads: int = 2,
                  classes: int = 8, seeds: int = 256, fanout: int = 10, tokens: int = 12,
-                 dtype=torch.bfloat16, seed: int = 0):
+                 dtype=torch.bfloat16, seed: int = 0, hidden: int = 0):
         g = torch.Generator(device="cuda").manual_seed(seed)
 
         def normal(*shape, scale):
@@ -48,6 +52,11 @@ class TextOnGraph:
         width = kv_heads * self.hd
         self.weights = {"q": normal(d, d, scale=d ** -0.5), "kv": normal(d, 2 * width, scale=d ** -0.5),
                         "o": normal(d, classes, scale=d ** -0.5)}
+        self.hidden = hidden
+        if hidden:
+            self.weights.update(gate=normal(d, hidden, scale=d ** -0.5), up=normal(d, hidden, scale=d ** -0.5),
+                                down=normal(hidden, d, scale=hidden ** -0.5))
+            self.norm = {"weight": torch.ones(d, device="cuda"), "bias": torch.zeros(d, device="cuda")}
         self.momentum = {k: torch.zeros_like(w) for k, w in self.weights.items()}
 
         # what a program keeps from step to step: blocks, workspaces, outputs
@@ -65,11 +74,43 @@ class TextOnGraph:
         self.ws_nodes = space(gm.gnn_embedding_grad_workspace_size(edges, graph.num_nodes, d))
         self.ws_ortho = {k: space(gm.gnn_orthogonalize_workspace_size(1, *w.shape, w.dtype))
                          for k, w in self.weights.items()}
+        if hidden:
+            self.ws_ff = space(max(
+                gm.gnn_layer_norm_workspace_size(rows, d),
+                *(gm.gnn_gated_linear_workspace_size(rows, d, hidden, dtype, backward=b) for b in (False, True)),
+                *(gm.gnn_linear_workspace_size(rows, hidden, d, dtype, backward=b) for b in (False, True))))
         self.q_indptr = torch.arange(seeds + 1, device="cuda", dtype=torch.int32) * tokens
         self.token_grad = torch.empty_like(self.token_table)
         self.nodes = torch.empty(edges, dtype=torch.int32, device="cuda")
         self.n_nodes = torch.empty(1, dtype=torch.int64, device="cuda")
         self.node_grad = torch.empty(edges, d, device="cuda")
+
+    def feed_forward(self, r: torch.Tensor):
+        """r + down(silu(gate y) * up y) with y the norm of r, and what its backward pass needs."""
+        w = {k: self.weights[k].to(self.dtype) for k in ("gate", "up", "down")}
+        rows = r.shape[0]
+        y, (mean, rstd) = torch.empty_like(r), torch.empty(2, rows, device="cuda")
+        gm.gnn_layer_norm(r, self.norm["weight"], self.norm["bias"], EPS, y, mean=mean, rstd=rstd)
+        h, gate, up = torch.empty(3, rows, self.hidden, device="cuda", dtype=self.dtype)
+        gm.gnn_gated_linear(y, w["gate"], w["up"], h, self.ws_ff, gate=gate, up=up)
+        out = torch.empty_like(r)
+        gm.gnn_linear(h, w["down"], out, self.ws_ff, residual=r)
+        return out, (w, r, mean, rstd, y, gate, up, h)
+
+    def feed_forward_gradients(self, kept, dout: torch.Tensor, grads: dict):
+        """The gradient of feed_forward's input; those of its weights go into grads."""
+        w, r, mean, rstd, y, gate, up, h = kept
+        dw = {k: torch.empty_like(v) for k, v in w.items()}
+        dh, dy, dr = torch.empty_like(h), torch.empty_like(y), torch.empty_like(r)
+        gm.gnn_linear_backward(h, w["down"], dout, self.ws_ff, dx=dh, dw=dw["down"])
+        gm.gnn_gated_linear_backward(y, w["gate"], w["up"], gate, up, dh, self.ws_ff, dx=dy,
+                                     dw_gate=dw["gate"], dw_up=dw["up"])
+        dn = {k: torch.empty_like(v) for k, v in self.norm.items()}
+        gm.gnn_layer_norm_backward(r, self.norm["weight"], mean, rstd, dy, dr, self.ws_ff,
+                                   dweight=dn["weight"], dbias=dn["bias"], residual_grad=dout)
+        grads.update({k: v.float() for k, v in dw.items()})
+        self.norm_grads = dn
+        return dr
 
     def gradients(self, ids: torch.Tensor, texts: torch.Tensor, labels: torch.Tensor, draw: int):
         """The loss of one mini-batch and its gradients: of the weights (a dict), the token table, and
@@ -93,7 +134,11 @@ class TextOnGraph:
         gm.gnn_cross_attention(q, k, v, self.q_indptr, k_indptr, self.tokens, self.fanout, scale, out,
                                self.ws_attend, lse=lse)
         # the tokens' own vectors pass beside what they attended to
-        h = (x.float() + out.view(rows, d).float()).view(self.seeds, self.tokens, d).mean(1)
+        h = x.float() + out.view(rows, d).float()
+        if self.hidden:
+            y2, kept = self.feed_forward(h.to(dt))
+            h = y2.float()
+        h = h.view(self.seeds, self.tokens, d).mean(1)
         logits = h @ self.weights["o"]
         p = torch.softmax(logits, 1)
         loss = -torch.log(p[torch.arange(self.seeds, device="cuda"), labels]).mean()
@@ -101,7 +146,10 @@ class TextOnGraph:
         dlogits = (p - torch.nn.functional.one_hot(labels, p.shape[1])) / self.seeds
         grads = {"o": h.T @ dlogits}
         dh = (dlogits @ self.weights["o"].T / self.tokens).to(dt)
-        dout = dh[:, None, :].expand(-1, self.tokens, -1).contiguous().view(rows, self.heads, self.hd)
+        dout = dh[:, None, :].expand(-1, self.tokens, -1).contiguous().view(rows, d)
+        if self.hidden:
+            dout = self.feed_forward_gradients(kept, dout, grads)
+        dout = dout.view(rows, self.heads, self.hd)
         dq, dstates = torch.empty_like(q), torch.empty_like(states)
         gm.gnn_cross_attention_backward(q, k, v, self.q_indptr, k_indptr, self.tokens, self.fanout, scale,
                                         out, lse, dout, dq, dstates[:, :self.kv],
@@ -123,6 +171,9 @@ class TextOnGraph:
             update = torch.empty_like(w)
             gm.gnn_orthogonalize(grads[k] + beta * m, update, self.ws_ortho[k])
             w.sub_(lr * update)
+        if self.hidden:
+            for k, v in self.norm.items():
+                v.sub_(lr * self.norm_grads[k])
         self.token_table.sub_(table_lr * token_grad)
         n = int(count)
         self.node_table[nodes[:n].long()] -= table_lr * rows[:n]
@@ -159,7 +210,8 @@ def train(steps: int = 60, seed: int = 0, vocab: int = 1001, classes: int = 8, *
 if __name__ == "__main__":
     parser = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     parser.add_argument("--steps", type=int, default=60)
+    parser.add_argument("--hidden", type=int, default=0, help="width of a feed-forward block (0: none)")
     args = parser.parse_args()
-    for i, loss in enumerate(train(args.steps)):
+    for i, loss in enumerate(train(args.steps, hidden=args.hidden)):
         if i % 10 == 0 or i + 1 == args.steps:
             print(f"step {i:4d}  loss {loss:.4f}", flush=True)

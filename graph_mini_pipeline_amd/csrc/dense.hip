@@ -131,6 +131,8 @@ constexpr TileCost kCostF32[4] = {{0, 0, 0, 0}, {2.05, 5, 2.0, 4}, {0.56, 1.8, 0
 constexpr double kJoinLaunch = 2.5;
 double join_us(int64_t parts, double elements) { return kJoinLaunch + static_cast<double>(parts) * elements * (8e-6 / 3.0); }
 
+constexpr double kMostJoined = 1e9;        // sums of a product that is joined (they are counted in 32 bits)
+
 constexpr int kSplitChoices = 12;
 constexpr int64_t kSplits[kSplitChoices] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
 
@@ -150,7 +152,7 @@ Split split_cost(const Shape &s, int type, int tile, bool pair, int64_t parts) {
     const int64_t steps = (s.k + bk - 1) / bk * s.segs;
     const double elements = static_cast<double>(s.rows) * s.cols * s.products * (pair ? 2 : 1);
     Split r;
-    r.sensible = parts == 1 || (parts <= steps && tiles * parts <= 8 * kCus && elements < 1e9);
+    r.sensible = parts == 1 || (parts <= steps && tiles * parts <= 8 * kCus && elements <= kMostJoined);
     r.groups = static_cast<double>(tiles * parts);
     r.each = static_cast<double>((steps + parts - 1) / parts);
     r.chain = r.each * c.alone + c.fixed;
@@ -174,6 +176,7 @@ ForwardPlan plan_forward(const DenseArgs &a) {
         const TileCost &c = a.type == GNN_BF16 ? kCostBf16[tile] : kCostF32[tile];
         // small tiles take a gated pair as two products, whose sums are joined
         const bool pair = a.pair && tile <= kTile128, apart = a.pair && !pair;
+        if (apart && static_cast<double>(a.n) * a.d_out > kMostJoined / 2) continue;
         for (const int64_t parts : kSplits) {
             const Split s = split_cost({kForward, a.n, a.d_out, a.d_in, 1, apart ? 2 : 1}, a.type, tile, pair, parts);
             if (!s.sensible) break;

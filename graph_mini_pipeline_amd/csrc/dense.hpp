@@ -128,7 +128,7 @@ __device__ __forceinline__ vec<float, V> activate_slope(int32_t act, vec<float, 
     case GNN_ACT_RELU:
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            s[i] = z[i] > 0.f ? 1.f : 0.f;
+            s[i] = z[i] > 0.f ? 1.f : z[i] != z[i] ? z[i] : 0.f;
             z[i] = z[i] > 0.f || z[i] != z[i] ? z[i] : 0.f;
         }
         break;
