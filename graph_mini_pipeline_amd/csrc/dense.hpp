@@ -560,27 +560,18 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, int64_t q, ch
             staged = false;
             const void *pa = p.a[seg], *pb0 = p.b[z][seg], *pb1 = PAIR ? p.b[1][seg] : pb0;
             u4 *to = reinterpret_cast<u4 *>(lds + buf * kBuffer) + t;
-            // pieces under way together (beside the largest tile's sums there are registers for two)
-            constexpr int kA = FR * FC > 4 ? 2 : A::kPieces, kB = FR * FC > 4 ? 2 : B::kPieces;
-#pragma unroll 1
-            for (int at = 0; at < A::kPieces; at += kA) {
-                u4 v[kA];
+            // an operand's pieces under way together (all of both: no registers beside the largest tile's sums)
+            u4 va[A::kPieces];
 #pragma unroll
-                for (int i = 0; i < kA; ++i) v[i] = ta.cut(pa, p.ld_a, at + i, k0, k, t);
+            for (int i = 0; i < A::kPieces; ++i) va[i] = ta.cut(pa, p.ld_a, i, k0, k, t);
 #pragma unroll
-                for (int i = 0; i < kA; ++i) to[(at + i) * kThreads] = v[i];
-            }
-            to += A::kBytes / 16;
-#pragma unroll 1
-            for (int at = 0; at < B::kPieces; at += kB) {
-                u4 v[kB];
-                const void *const pb = PAIR && at >= B::kPieces / 2 ? pb1 : pb0;
-                const void *const pe = PAIR && at + kB > B::kPieces / 2 ? pb1 : pb0;     // of the batch's second half
+            for (int i = 0; i < A::kPieces; ++i) to[i * kThreads] = va[i];
+            __builtin_amdgcn_sched_barrier(0);
+            u4 vb[B::kPieces];
 #pragma unroll
-                for (int i = 0; i < kB; ++i) v[i] = tb.cut(i < kB / 2 || kB < B::kPieces ? pb : pe, p.ld_b, at + i, k0, k, t);
+            for (int i = 0; i < B::kPieces; ++i) vb[i] = tb.cut(PAIR && i >= B::kPieces / 2 ? pb1 : pb0, p.ld_b, i, k0, k, t);
 #pragma unroll
-                for (int i = 0; i < kB; ++i) to[(at + i) * kThreads] = v[i];
-            }
+            for (int i = 0; i < B::kPieces; ++i) to[A::kBytes / 16 + i * kThreads] = vb[i];
         }
         k0 += kBk;
         from_a += step_a;
