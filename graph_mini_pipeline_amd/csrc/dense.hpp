@@ -21,7 +21,14 @@
 // LDS read touches spreads over the banks: lds_piece below.  Tiles go from memory into LDS directly, by
 // pieces where both operands' lines start at multiples of 16 bytes and are whole pieces (kByPiece), by words
 // where they are multiples of 4 bytes, fp32 always (kByWord); other bf16 operands go through registers
-// (kThrough).  A tile that the summed length cuts is filled with zeros, element by element where it must be.
+// (kThrough).  A tile that the summed length cuts is loaded through registers, shifted to its place and
+// filled up with zeros.
+//
+// While the products of one tile run, those of the next NB - 1 are under way.  A barrier comes before the last of a
+// tile's four steps, whose operands are in registers by then: the first reads of the next tile hide behind it.
+// 4096 squares in bf16: 1170 TFLOP/s by tiles of 256 (eight wavefronts of 128 x 64), 850 by 128, 640 by 64; fp32
+// 144 by 128 (a library product reaches 1199 and 154 at 8192); LDS has no bank conflicts in any order
+// of operands (SQ_LDS_BANK_CONFLICT 0).
 #pragma once
 
 #include "learn.hpp"

@@ -59,6 +59,12 @@ KERNEL_SOURCES = {
     "k_newton": "csrc/orthogonalize.hip",
     "k_norm_squares": "csrc/orthogonalize.hip",
     "k_first_planes": "csrc/orthogonalize.hip",
+    "k_norm": "csrc/norm.hip",               # (after k_norm_squares, which begins like it)
+    "k_product_join": "csrc/dense.hip",
+    "k_slopes": "csrc/dense.hip",
+    "k_column_sums": "csrc/dense.hip",
+    "k_product": "csrc/dense.hpp",
+    "k_gradients": "csrc/dense.hpp",
 }
 
 
