@@ -138,8 +138,9 @@ struct TileCost {
 constexpr TileCost kCostBf16[4] = {{1.65, 8, 1.4, 8}, {0.62, 5, 0.62, 5}, {0.24, 1, 0.26, 2}, {0.24, 1.6, 0.27, 2}};
 constexpr TileCost kCostF32[4] = {{0, 0, 0, 0}, {2.05, 5, 2.0, 4}, {0.56, 1.8, 0.58, 1.2}, {0.56, 1.8, 0.6, 1.2}};
 
-// Parts of a sum are written and read again, at 3 TB/s, by a launch of its own.
-constexpr double kJoinLaunch = 2.5;
+// Parts of a sum are written and read again, at 3 TB/s, by a launch of its own (which behind the gradients' two
+// others is waited for longer).
+constexpr double kJoinLaunch = 3.0, kGradJoinLaunch = 4.0;
 double join_us(int64_t parts, double elements) { return kJoinLaunch + static_cast<double>(parts) * elements * (8e-6 / 3.0); }
 
 constexpr double kMostJoined = 1e9;        // sums of a product that is joined (they are counted in 32 bits)
@@ -211,14 +212,21 @@ struct GradientPlan {
 };
 
 // Both products' workgroups run in one launch: their parts are chosen together.
-GradientPlan plan_gradients(const Shape &w, const Shape &x, int type) {
+// dW of a few rows does without tiles, and takes what it writes.
+GradientPlan plan_gradients(const Shape &w, const Shape &x, int type, bool few) {
     GradientPlan best{};
     double least = 1e30;
+    const double written = static_cast<double>(w.rows) * w.cols * w.products * (type == GNN_BF16 ? 2 : 4);
     for (int tile = type == GNN_BF16 ? kTile256 : kTile128; tile <= kTile64; ++tile) {
         Split sx[kSplitChoices];
         for (int i = 0; i < kSplitChoices; ++i) sx[i] = split_cost(x, type, tile, false, kSplits[i]);
         for (const int64_t w_parts : kSplits) {
-            const Split sw = split_cost(w, type, tile, false, w_parts);
+            Split sw = split_cost(w, type, tile, false, w_parts);
+            if (few) {
+                sw.sensible = w_parts == 1;
+                sw.chain = 2.0;
+                sw.work = written * (kCus * 1e-6 / 4.0);
+            }
             if (!sw.sensible) break;
             for (int i = 0; i < kSplitChoices && sx[i].sensible; ++i) {
                 const double chain = sw.chain > sx[i].chain ? sw.chain : sx[i].chain;
@@ -226,7 +234,8 @@ GradientPlan plan_gradients(const Shape &w, const Shape &x, int type) {
                 double us = (sw.work + sx[i].work) / kCus;
                 if (sw.groups + sx[i].groups > kCus) us += 0.25 * shorter;      // of the last ones
                 if (us < chain) us = chain;
-                us += sw.join + sx[i].join - (sw.join > 0 && sx[i].join > 0 ? kJoinLaunch : 0.0);
+                us += sw.join + sx[i].join;
+                if (sw.join > 0 || sx[i].join > 0) us += kGradJoinLaunch - (sw.join > 0 && sx[i].join > 0 ? 2 : 1) * kJoinLaunch;
                 if (us < least) {
                     least = us;
                     best = {tile, w_parts, kSplits[i]};
@@ -352,6 +361,7 @@ struct DenseSpace {
     char *dz, *rest, *sums, *w_part, *x_part;
     int64_t ld_dz, second;
     bool wide;               // two planes of every row: dx sums few terms
+    bool few;                // dW by outer_tile
     Shape w, x;
     GradientPlan plan;
     size_t bytes;
@@ -367,7 +377,8 @@ DenseSpace carve_dense(const DenseArgs &a, char *ws) {
     s.wide = bf && a.d_out * mats < kShortSum;
     s.w = {kGradW, a.d_in, a.d_out, a.n, 1, mats};
     s.x = {kGradX, a.n, a.d_in, a.d_out, s.wide ? 2 * mats : mats, 1};
-    s.plan = plan_gradients(s.w, s.x, a.type);
+    s.few = a.n > 0 && a.n <= kFewRows && a.d_out >= 16 / size;
+    s.plan = plan_gradients(s.w, s.x, a.type, s.few);
     size_t at = 0;
     const auto take = [&](char **p, int64_t bytes) {
         *p = ws + at;
@@ -516,6 +527,7 @@ hipError_t launch_dense_backward(const DenseArgs &a, hipStream_t s) {
     pw.short_segs = own && bf ? 2 : 1;
     pw.a[0] = pw.a[1] = a.x;
     pw.e.ld_out = a.ld_dw;
+    pw.few = !w.few ? 0 : bf ? kOuterWide<bf16> : kOuterWide<float>;
     for (int z = 0; z < mats; ++z) {
         if (!a.dw[z]) continue;
         pw.b[pw.products][0] = dz[z];
@@ -533,7 +545,7 @@ hipError_t launch_dense_backward(const DenseArgs &a, hipStream_t s) {
     px.products = inputs ? 1 : 0;
     px.e.out[0] = a.dx;
     px.e.ld_out = a.ld_dx;
-    const int way_w = weights ? way_of(pw, kGradW, false, size) : kByPiece;
+    const int way_w = weights && !w.few ? way_of(pw, kGradW, false, size) : kByPiece;
     const int way_x = inputs ? way_of(px, kGradX, false, size) : kByPiece;
     const int load = way_w > way_x ? way_w : way_x, tile = filled_tile(w.plan.tile, load);
     hipError_t err = bf ? launch_gradients_bf16(pw, px, c, tile, load, s) : launch_gradients_f32(pw, px, c, tile, load, s);

@@ -60,6 +60,7 @@ struct ProductArgs {
     int32_t segs;
     int32_t short_segs;                 // segments where fewer than kShortSum of k count
     int32_t products;                   // products of the launch (one where it is a gated pair)
+    int32_t few;                        // dW of up to kFewRows rows by outer_tile: the columns of one; otherwise 0
     int32_t splits;                     // parts of the summed length, whose sums go to part
     int64_t r_tiles, c_tiles, first_tile;     // set by the launcher
     float *part;                        // [splits][products or pair][rows][ld_part], or NULL: the epilogue follows
@@ -70,6 +71,9 @@ struct ProductArgs {
 // A rounding of a summed operand to bf16 is as large as the result's own rounding where few terms are
 // summed: below this many, the gradients dz are taken in two planes (see dense.hip).
 constexpr int64_t kShortSum = 512;
+
+// dW of so few rows is a sum of so many outer products: written by lanes that hold dz, without tiles to fill.
+constexpr int kFewRows = 8;
 
 // ---- activations ----------------------------------------------------------------------------------
 
@@ -823,6 +827,53 @@ __device__ __forceinline__ void column_sums(const ColumnArgs &p, uint32_t block,
     }
 }
 
+// dW = x^T dz for up to kFewRows rows.  A lane holds its 16 bytes' columns of every row of dz (both planes of it,
+// added), a wavefront writes kOuterHigh lines of dW; x comes from LDS.  What bounds it is the writing.  All gradients
+// of 4 rows of 4096 x 4096 bf16 with gelu take 28 us, 52 where tiles of the matrix units are filled, cut and emptied
+// for dW; of one row of 7168 x 6464 fp32 88 and 168 (floor 76).
+constexpr int kOuterHigh = 16;
+
+template <typename T>
+constexpr int kOuterWide = 64 * 16 / static_cast<int>(sizeof(T));
+
+template <typename T, int THREADS>
+__device__ __forceinline__ void outer_tile(const ProductArgs &p, int64_t q, float *lds) {
+    constexpr int V = 16 / static_cast<int>(sizeof(T)), kHigh = kOuterHigh * THREADS / 64;
+    typedef vec<float, V> Wide;
+    const int64_t tiles = p.r_tiles * p.c_tiles, z = q / tiles;
+    q -= z * tiles;
+    const int64_t tr = q / p.c_tiles, r0 = tr * kHigh, n = load_count(p.d_n, p.k);
+    const int t = threadIdx.x, lane = lane_id(), w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int64_t at = (q - tr * p.c_tiles) * kOuterWide<T> + lane * V;
+    const int64_t c = at < p.cols - V ? at : p.cols - V;      // the last lanes' columns overlap, with the same results
+    for (int e = t; e < kHigh * kFewRows; e += THREADS) {
+        const int i = e % kHigh, row = e / kHigh;
+        const bool there = row < n && r0 + i < p.rows;
+        lds[i * kFewRows + row] = there ? static_cast<float>(static_cast<const T *>(p.a[0])[row * p.ld_a + r0 + i]) : 0.f;
+    }
+    Wide dz[kFewRows];
+#pragma unroll
+    for (int row = 0; row < kFewRows; ++row) {
+        dz[row] = Wide(0.f);
+        if (row < n) {
+            dz[row] = load_f32<T, V>(static_cast<const T *>(p.b[z][0]) + row * p.ld_b + c);
+            if (p.short_segs > 1) dz[row] += load_f32<T, V>(static_cast<const T *>(p.b[z][1]) + row * p.ld_b + c);
+        }
+    }
+    __syncthreads();
+    T *const out = static_cast<T *>(p.e.out[z]) + c;
+#pragma unroll 4
+    for (int i = 0; i < kOuterHigh; ++i) {
+        const int64_t r = r0 + w * kOuterHigh + i;
+        if (r >= p.rows) break;
+        const float *x = lds + (w * kOuterHigh + i) * kFewRows;
+        Wide v = x[0] * dz[0];
+#pragma unroll
+        for (int row = 1; row < kFewRows; ++row) v += x[row] * dz[row];
+        store_f32<T, V>(out + r * p.e.ld_out, v);
+    }
+}
+
 // Wavefronts, buffers of LDS (by the type's bytes) and wavefronts a SIMD of each tile shape.
 struct Tile256 {          // bf16 only, by pieces only
     static constexpr int kRows = 256, kCols = 256, kWr = 2, kWc = 4;
@@ -863,6 +914,8 @@ __global__ __launch_bounds__(TILE::kWr * TILE::kWc * 64, TILE::waves(sizeof(T)))
     const int64_t qw = x_first ? q - x_tiles : q, qx = x_first ? q : q - w_tiles;
     if (q >= all)
         column_sums<TILE::kWr * TILE::kWc * 64>(c, static_cast<uint32_t>(q - all), reinterpret_cast<float *>(lds));
+    else if ((x_first ? qw >= 0 : qx < 0) && w.few)
+        outer_tile<T, TILE::kWr * TILE::kWc * 64>(w, qw, reinterpret_cast<float *>(lds));
     else if (x_first ? qw >= 0 : qx < 0)
         product_tile<T, kGradW, TILE::kRows, TILE::kCols, TILE::kWr, TILE::kWc, NB, false, LOAD>(w, qw, lds);
     else
@@ -886,6 +939,12 @@ hipError_t launch_gradients_bf16(ProductArgs w, ProductArgs x, const ColumnArgs 
 hipError_t launch_gradients_f32(ProductArgs w, ProductArgs x, const ColumnArgs &c, int tile, int load, hipStream_t s);
 
 inline int64_t set_tiles(ProductArgs &a, int tile, bool pair) {
+    if (a.few) {
+        const int64_t high = kOuterHigh * (tile == kTile256 ? 8 : 4);
+        a.r_tiles = (a.rows + high - 1) / high;
+        a.c_tiles = (a.cols + a.few - 1) / a.few;
+        return a.r_tiles * a.c_tiles * a.products;
+    }
     a.r_tiles = (a.rows + tile_rows(tile) - 1) / tile_rows(tile);
     a.c_tiles = (a.cols + tile_cols(tile, pair) - 1) / tile_cols(tile, pair);
     return a.r_tiles * a.c_tiles * a.products * a.splits;
@@ -923,7 +982,7 @@ hipError_t launch_product(ProductArgs a, int tile, bool pair, int load, hipStrea
 template <typename T, typename TILE, int LOAD>
 hipError_t launch_both(ProductArgs &w, ProductArgs &x, const ColumnArgs &c, int64_t w_tiles, int64_t x_tiles, hipStream_t s) {
     constexpr int kThreads = TILE::kWr * TILE::kWc * 64;
-    const bool x_first = x.k * x.segs * w.splits > w.k * w.segs * x.splits;
+    const bool x_first = w.few || x.k * x.segs * w.splits > w.k * w.segs * x.splits;
     return launch_pieces(w_tiles + x_tiles + 2 * c.blocks, kThreads, [&](int64_t first, unsigned blocks) {
         w.first_tile = first;
         k_gradients<T, TILE, LOAD><<<blocks, kThreads, 0, s>>>(w, x, c, w_tiles, x_tiles, x_first);

@@ -135,3 +135,35 @@ def test_the_same_bits_every_time_and_two_streams_at_once(shape, dtype):
     torch.cuda.synchronize()
     for a, b, c in zip(first, second, third):
         assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+@pytest.mark.parametrize("shape", [(1, 515, 1371), (3, 1, 520), (5, 130, 8), (7, 99, 843), (8, 1000, 9), (8, 65, 1032)])
+def test_a_few_rows(shape, dtype):
+    """Gradients of weights that a few rows give: whole and cut lines and columns, rows off any alignment."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    for place in (lambda t: t, lambda t: ref.strided(t, 3, 1)):
+        results = linear_case(*shape, dtype, "gelu", g, place) + gated_case(*shape, dtype, "silu", g, place)
+        for t in results:
+            if t._base is not None and t._base.dim() == 1:
+                n, d = t.shape
+                assert torch.isnan(t._base[1:1 + n * (d + 3)].view(n, d + 3)[:, d:]).all()
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+@pytest.mark.parametrize("count", [0, 1, 5, 8, 9])
+def test_a_few_rows_that_count(count, dtype):
+    g = torch.Generator(device="cuda").manual_seed(9)
+    n, i, o, m = 8, 300, 328, min(count, 8)
+    x, wg, wu = normal(n, i, dtype=dtype, gen=g), *normal(2, i, o, dtype=dtype, gen=g, scale=0.1)
+    dout, gate, up = normal(n, o, dtype=dtype, gen=g), *normal(2, n, o, dtype=dtype, gen=g)
+    for t in (x, dout, gate, up):
+        t[m:] = float("nan")
+    dx, dwg, dwu = torch.full_like(x, 7.0), torch.empty_like(wg), torch.empty_like(wu)
+    gm.gnn_gated_linear_backward(x, wg, wu, gate, up, dout,
+                                 space(gm.gnn_gated_linear_workspace_size, n, i, o, dtype, True), dx=dx, dw_gate=dwg,
+                                 dw_up=dwu, d_n=torch.tensor([count], device="cuda"))
+    want = ref.gated_gradients(d64(x[:m]), d64(wg), d64(wu), d64(dout[:m]), "silu", d64(gate[:m]), d64(up[:m]), dtype)
+    assert (dx[m:] == 7).all()
+    for got, exact in zip((dx[:m], dwg, dwu), (want[0], want[1], want[3])):
+        ref.close(got, exact)
