@@ -293,7 +293,13 @@ __global__ __launch_bounds__(kSlopeWide * kSlopeHigh) void k_slopes(SlopeArgs p)
     const auto keep = [&](int64_t e, Wide v) {
         const Raw r = __builtin_convertvector(v, Raw);
         *reinterpret_cast<Loose *>(static_cast<T *>(p.dz) + e) = r;
-        if (planes) *reinterpret_cast<Loose *>(static_cast<T *>(p.rest) + e) = __builtin_convertvector(v - __builtin_convertvector(r, Wide), Raw);
+        if (planes) {
+            Wide rest = v - __builtin_convertvector(r, Wide);
+            // An infinity leaves nothing: the difference would turn it into NaN.
+#pragma unroll
+            for (int i = 0; i < V; ++i) rest[i] = __builtin_fabsf(rest[i]) < __builtin_inff() ? rest[i] : 0.f;
+            *reinterpret_cast<Loose *>(static_cast<T *>(p.rest) + e) = __builtin_convertvector(rest, Raw);
+        }
     };
     if (there) {
         for (int64_t m0 = static_cast<int64_t>(blockIdx.y) * kSlopeHigh + y; m0 < n; m0 += step * kSlopeRows) {

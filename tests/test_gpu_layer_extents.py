@@ -167,3 +167,32 @@ def test_a_few_rows_that_count(count, dtype):
     assert (dx[m:] == 7).all()
     for got, exact in zip((dx[:m], dwg, dwu), (want[0], want[1], want[3])):
         ref.close(got, exact)
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+@pytest.mark.parametrize("shape", [(4, 40, 24), (20, 70, 50), (300, 64, 640), (600, 136, 72)])
+def test_infinite_gradients_stay_infinite(shape, dtype):
+    """One infinity of dout: its row of dx and its column of dw and dbias are infinite with the sign of the other
+    factor, and all others are what they are without it.  (Sums of one and of two planes of dz.)"""
+    n, i, o = shape
+    g = torch.Generator(device="cuda").manual_seed(10)
+    x, w, dout = normal(n, i, dtype=dtype, gen=g), normal(i, o, dtype=dtype, gen=g), normal(n, o, dtype=dtype, gen=g)
+    x[1] = torch.where(x[1] < 0, x[1] - 0.1, x[1] + 0.1)      # no zeros meet the infinity
+    w[:, 2] = torch.where(w[:, 2] < 0, w[:, 2] - 0.1, w[:, 2] + 0.1)
+    pre = torch.ones_like(dout)      # a slope above 0
+    ws = space(gm.gnn_linear_workspace_size, n, i, o, dtype, True)
+
+    def gradients():
+        dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(o, device="cuda", dtype=dtype)
+        gm.gnn_linear_backward(x, w, dout, ws, activation="gelu", pre=pre, dx=dx, dw=dw, dbias=db)
+        return dx, dw, db
+
+    clean = gradients()
+    dout[1, 2] = float("inf")
+    dx, dw, db = gradients()
+    assert torch.equal(dx[1], w[:, 2].sign() * float("inf"))
+    assert torch.equal(dw[:, 2], x[1].sign() * float("inf"))
+    assert float(db[2]) == float("inf")
+    rows, cols = torch.arange(n, device="cuda") != 1, torch.arange(o, device="cuda") != 2
+    assert torch.equal(dx[rows], clean[0][rows]) and torch.equal(dw[:, cols], clean[1][:, cols])
+    assert torch.equal(db[cols], clean[2][cols])
