@@ -196,3 +196,74 @@ def test_infinite_gradients_stay_infinite(shape, dtype):
     rows, cols = torch.arange(n, device="cuda") != 1, torch.arange(o, device="cuda") != 2
     assert torch.equal(dx[rows], clean[0][rows]) and torch.equal(dw[:, cols], clean[1][:, cols])
     assert torch.equal(db[cols], clean[2][cols])
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+@pytest.mark.parametrize("n, d", [(9, 7), (33, 101), (20, 521), (11, 1031), (5, 4099), (5, 8195), (3, 16383)])
+def test_norms_in_place_at_odd_widths(n, d, dtype):
+    """out over x and dx over residual_grad where a row's last pieces overlap."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    x, w, dout, dres = normal(n, d, dtype=dtype, gen=g), normal(d, dtype=dtype, gen=g), \
+        normal(n, d, dtype=dtype, gen=g), normal(n, d, dtype=dtype, gen=g)
+    out, y, mean, rstd = torch.empty_like(x), x.clone(), *torch.empty(2, n, device="cuda")
+    gm.gnn_layer_norm(x, w, None, 1e-5, out, mean=mean, rstd=rstd)
+    gm.gnn_layer_norm(y, w, None, 1e-5, y)
+    ws = torch.empty(gm.gnn_layer_norm_workspace_size(n, d), dtype=torch.uint8, device="cuda")
+    dx, over = torch.empty_like(x), dres.clone()
+    gm.gnn_layer_norm_backward(x, w, mean, rstd, dout, dx, ws, residual_grad=dres)
+    gm.gnn_layer_norm_backward(x, w, mean, rstd, dout, over, ws, residual_grad=over)
+    assert torch.equal(y, out) and torch.equal(over, dx)
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+@pytest.mark.parametrize("shape", [(1, 512, 256), (3, 1030, 257), (77, 515, 137), (700, 300, 520), (2500, 64, 1032)])
+def test_out_over_the_residual(shape, dtype):
+    n, i, o = shape
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x, w, r = normal(n, i, dtype=dtype, gen=g), normal(i, o, dtype=dtype, gen=g), normal(n, o, dtype=dtype, gen=g)
+    ws = space(gm.gnn_linear_workspace_size, n, i, o, dtype)
+    for place in (lambda t: t.clone(), lambda t: ref.strided(t, 3, 1)):
+        over = place(r)
+        apart = place(torch.zeros_like(r))
+        gm.gnn_linear(x, w, apart, ws, activation="silu", residual=place(r))
+        gm.gnn_linear(x, w, over, ws, activation="silu", residual=over)
+        assert torch.equal(over, apart)
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+def test_a_few_rows_captured(dtype):
+    g = torch.Generator(device="cuda").manual_seed(13)
+    n, i, o = 5, 515, 328
+    x, wg, wu = normal(n, i, dtype=dtype, gen=g), *normal(2, i, o, dtype=dtype, gen=g, scale=0.1)
+    dout, gate, up = normal(n, o, dtype=dtype, gen=g), *normal(2, n, o, dtype=dtype, gen=g)
+    dx, dwg, dwu, db = torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu), \
+        torch.empty(2, o, device="cuda", dtype=dtype)
+    ws, count = space(gm.gnn_gated_linear_workspace_size, n, i, o, dtype, True), torch.tensor([5], device="cuda")
+
+    def step():
+        gm.gnn_gated_linear_backward(x, wg, wu, gate, up, dout, ws, dx=dx, dw_gate=dwg, dw_up=dwu, dbias_gate=db[0],
+                                     dbias_up=db[1], d_n=count)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    results = (dx, dwg, dwu, db)
+    for m in (5, 2, 0):      # the count is read at the replay
+        count.fill_(m)
+        x.copy_(normal(n, i, dtype=dtype, gen=g))
+        for t in results:
+            t.fill_(-1.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = [t.clone() for t in results]
+        for t in results:
+            t.fill_(-1.0)
+        step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(replayed, results)), m
