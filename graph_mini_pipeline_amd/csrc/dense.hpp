@@ -155,7 +155,8 @@ __device__ __forceinline__ vec<float, V> activate_slope(int32_t act, vec<float, 
     case GNN_ACT_GELU_TANH:
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float zz = z[i] * z[i];
+            // where y (1 - y) is 0 the square, which overflows for far z, may be any number
+            const float zz = __builtin_fminf(z[i] * z[i], 1e4f);
             const float y = sigmoid<FAST>(1.595769122f * z[i] * (1.f + 0.044715f * zz));
             s[i] = y + z[i] * y * (1.f - y) * (1.595769122f + 0.2140644488f * zz);
             z[i] *= y;
