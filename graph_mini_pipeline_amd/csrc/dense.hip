@@ -526,27 +526,30 @@ hipError_t launch_dense_backward(const DenseArgs &a, hipStream_t s) {
         q.ld_part = round_up(q.cols, 4);
         q.e.act = GNN_ACT_NONE;
     };
+    // Segments: those of the second plane, where there is one, before the first's.
     sized(pw, w.w, w.plan.w_parts, w.w_part);
     pw.ld_a = a.ld_x;
     pw.ld_b = ld_dz;
     pw.segs = 1;
-    pw.short_segs = own && bf ? 2 : 1;
+    pw.rest = own && bf ? 1 : 0;
+    pw.short_segs = 1 + pw.rest;
     pw.a[0] = pw.a[1] = a.x;
     pw.e.ld_out = a.ld_dw;
     pw.few = !w.few ? 0 : bf ? kOuterWide<bf16> : kOuterWide<float>;
     for (int z = 0; z < mats; ++z) {
         if (!a.dw[z]) continue;
-        pw.b[pw.products][0] = dz[z];
-        pw.b[pw.products][1] = dz[2 + z];
+        pw.b[pw.products][0] = dz[2 * pw.rest + z];
+        pw.b[pw.products][1] = dz[z];
         pw.e.out[pw.products++] = a.dw[z];
     }
     sized(px, w.x, w.plan.x_parts, w.x_part);
     px.ld_a = ld_dz;
     px.ld_b = a.ld_w;
-    px.segs = px.short_segs = own && w.wide ? 2 * mats : mats;
+    px.rest = own && w.wide ? mats : 0;
+    px.segs = px.short_segs = px.rest + mats;
     for (int i = 0; i < px.segs; ++i) {
-        px.a[i] = a.pair ? dz[i] : dz[2 * i];
-        px.b[0][i] = a.w[a.pair ? i & 1 : 0];
+        px.a[i] = dz[(i < px.rest ? 2 : 0) + i % mats];
+        px.b[0][i] = a.w[i % mats];
     }
     px.products = inputs ? 1 : 0;
     px.e.out[0] = a.dx;

@@ -58,7 +58,8 @@ struct ProductArgs {
     int64_t rows, cols, k;              // k: of one segment
     const int64_t *d_n;                 // NULL, or how many of the rows (kGradW: of k) count
     int32_t segs;
-    int32_t short_segs;                 // segments where fewer than kShortSum of k count
+    int32_t short_segs;                 // segments where fewer than kShortSum of k count; otherwise the last `segs` of them
+    int32_t rest;                       // how many of them, the first ones, are of a second plane
     int32_t products;                   // products of the launch (one where it is a gated pair)
     int32_t few;                        // dW of up to kFewRows rows by outer_tile: the columns of one; otherwise 0
     int32_t splits;                     // parts of the summed length, whose sums go to part
@@ -522,7 +523,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, int64_t q, ch
     tb.init(c0, p.cols, p.ld_b, t);
 
     const int64_t seg_tiles = (k + kBk - 1) / kBk;
-    const int segs = k < kShortSum ? p.short_segs : p.segs;
+    const int segs = k < kShortSum ? p.short_segs : p.segs, first_seg = p.short_segs - segs;
     int64_t lo = 0, steps64 = seg_tiles * segs;
     if (p.splits > 1) {
         const int64_t share = (steps64 + p.splits - 1) / p.splits;
@@ -532,8 +533,8 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, int64_t q, ch
     const int steps = static_cast<int>(steps64);
     // Segment and summed index of the next tile to load, and where its loads start (scalars: a look at the
     // arguments for every tile costs 0.1 us of waiting).
-    int seg = seg_tiles > 0 ? static_cast<int>(lo / seg_tiles) : 0;
-    int64_t k0 = (lo - seg * seg_tiles) * kBk;
+    int seg = first_seg + (seg_tiles > 0 ? static_cast<int>(lo / seg_tiles) : 0);
+    int64_t k0 = (lo - (seg - first_seg) * seg_tiles) * kBk;
     const int64_t step_a = A::advance(p.ld_a), step_b = B::advance(p.ld_b);
     const char *from_a, *from_b0, *from_b1;
     const auto place = [&] {
@@ -589,7 +590,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, int64_t q, ch
         from_a += step_a;
         from_b0 += step_b;
         if (PAIR) from_b1 += step_b;
-        if (k0 >= k && seg + 1 < segs) {
+        if (k0 >= k && seg + 1 < p.short_segs) {
             k0 = 0;
             ++seg;
             place();
@@ -617,6 +618,21 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, int64_t q, ch
     for (int i = 0; i < FR; ++i)
 #pragma unroll
         for (int j = 0; j < FC; ++j) acc[i][j] = f16x(0.f);
+    // The products of a second plane come first.  Where one meets an infinity, its sign (or its zero) is not the
+    // gradient's: infinity minus infinity would follow.  What of their sums is not finite is dropped, and the first
+    // plane gives the infinity or the NaN alone.  drop_at: how many tiles follow the last of them.
+    constexpr bool kPlanes = sizeof(T) == 2 && FORM != kForward;
+    const int64_t rest64 = (p.rest - first_seg) * seg_tiles - lo;
+    const int drop_at = steps - static_cast<int>(rest64 < 0 ? 0 : rest64 < steps ? rest64 : steps);
+    const auto drop = [&](int after) {
+        if (!kPlanes || after != drop_at) return;
+#pragma unroll
+        for (int i = 0; i < FR; ++i)
+#pragma unroll
+            for (int j = 0; j < FC; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fabsf(acc[i][j][e]) < __builtin_inff() ? acc[i][j][e] : 0.f;
+    };
     uint32_t at_a[FR], at_b[FC];
 #pragma unroll
     for (int i = 0; i < FR; ++i) at_a[i] = A::read_base(wr * FR + i, lane);
@@ -692,6 +708,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, int64_t q, ch
                 }
 #pragma unroll
                 for (int step = 0; step < 4; ++step) multiply(4 * set + step, false, 0, 0);
+                drop(left);
             };
             read_all(0, 0);
             while (true) {
@@ -703,17 +720,23 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, int64_t q, ch
         } else {
 #pragma unroll
             for (int r = 0; r < kReads; ++r) read(0, 0, 0, r);
-            for (; left > 0; --left) {
-                const int next = buf + 1 == NB ? 0 : buf + 1;
+            // (the second plane's tiles in a loop of their own: with the drop in the loop, sums moved between registers)
+            for (int until = kPlanes && drop_at > 0 && drop_at < steps ? drop_at - 1 : 0;; until = 0) {
+                for (; left > until; --left) {
+                    const int next = buf + 1 == NB ? 0 : buf + 1;
 #pragma unroll
-                for (int step = 0; step < 3; ++step) multiply(step & 1, true, buf, step + 1);
-                turn(buf, next, left);
-                multiply(1, true, next, 0);
-                buf = next;
+                    for (int step = 0; step < 3; ++step) multiply(step & 1, true, buf, step + 1);
+                    turn(buf, next, left);
+                    multiply(1, true, next, 0);
+                    buf = next;
+                }
+                drop(left + 1);
+                if (!kPlanes || left == 0) break;
             }
 #pragma unroll
             for (int step = 0; step < 3; ++step) multiply(step & 1, true, buf, step + 1);
             multiply(1, false, 0, 0);
+            drop(0);
         }
     }
 
@@ -879,26 +902,27 @@ __device__ __forceinline__ void outer_tile(const ProductArgs &p, int64_t q, floa
 struct Tile256 {          // bf16 only, by pieces only
     static constexpr int kRows = 256, kCols = 256, kWr = 2, kWc = 4;
     static constexpr int buffers(int, int) { return 2; }
-    static constexpr int waves(int) { return 2; }
+    static constexpr int waves(int, int) { return 2; }
 };
-struct Tile128 {          // bf16: one workgroup a compute unit (large bf16 products take Tile256)
+struct Tile128 {          // bf16 straight into LDS: one workgroup a compute unit (large bf16 products take Tile256);
+                          // through registers two (gradients of 4096 x 1031 x 4097 186 us, 241 by one)
     static constexpr int kRows = 128, kCols = 128, kWr = 2, kWc = 2;
     static constexpr int buffers(int size, int load) { return size == 4 || load == kThrough ? 2 : load == kByWord ? 3 : 4; }
-    static constexpr int waves(int size) { return size == 2 ? 1 : 2; }
+    static constexpr int waves(int size, int load) { return size == 2 && load != kThrough ? 1 : 2; }
 };
 struct Tile64 {
     static constexpr int kRows = 64, kCols = 64, kWr = 2, kWc = 2;
     static constexpr int buffers(int, int load) { return load == kThrough ? 2 : 4; }
-    static constexpr int waves(int) { return 2; }
+    static constexpr int waves(int, int) { return 2; }
 };
 struct Tile32 {           // few rows
     static constexpr int kRows = 32, kCols = 128, kWr = 1, kWc = 4;
     static constexpr int buffers(int, int load) { return load == kThrough ? 2 : 4; }
-    static constexpr int waves(int) { return 2; }
+    static constexpr int waves(int, int) { return 2; }
 };
 
 template <typename T, typename TILE, bool PAIR, int LOAD>
-__global__ __launch_bounds__(TILE::kWr * TILE::kWc * 64, TILE::waves(sizeof(T))) void k_product(ProductArgs p) {
+__global__ __launch_bounds__(TILE::kWr * TILE::kWc * 64, TILE::waves(sizeof(T), LOAD)) void k_product(ProductArgs p) {
     constexpr int NB = TILE::buffers(sizeof(T), LOAD);
     __shared__ __align__(1024) char lds[NB * (TILE::kRows + TILE::kCols) * 128];
     product_tile<T, kForward, TILE::kRows, TILE::kCols, TILE::kWr, TILE::kWc, NB, PAIR, LOAD>(p, p.first_tile + blockIdx.x, lds);
@@ -907,7 +931,7 @@ __global__ __launch_bounds__(TILE::kWr * TILE::kWc * 64, TILE::waves(sizeof(T)))
 // Both gradients of a layer, and the sums of the bias's: w_tiles workgroups of dW, x_tiles of dx (those whose summed
 // length is longer come first, so that none of them is left at the end), and the last ones add columns.
 template <typename T, typename TILE, int LOAD>
-__global__ __launch_bounds__(TILE::kWr * TILE::kWc * 64, TILE::waves(sizeof(T))) void k_gradients(
+__global__ __launch_bounds__(TILE::kWr * TILE::kWc * 64, TILE::waves(sizeof(T), LOAD)) void k_gradients(
     ProductArgs w, ProductArgs x, ColumnArgs c, int64_t w_tiles, int64_t x_tiles, bool x_first) {
     constexpr int NB = TILE::buffers(sizeof(T), LOAD);
     __shared__ __align__(1024) char lds[NB * (TILE::kRows + TILE::kCols) * 128];

@@ -704,8 +704,8 @@ gnn_status gnn_layer_norm_backward(const gnn_norm *x, const gnn_norm_grad *g, vo
  *   dpre = dout act'(pre),  dx = dpre w^T,  dw = x^T dpre,  dbias = sum over rows of dpre;
  * those of dx [n, ld_dx], dw [d_in, ld_dw] and dbias that are not NULL are written (the residual's gradient
  *   is dout).  act' of relu is 0 at 0.  For GNN_BF16 with an activation, dpre is multiplied as one bf16, or as
- *   two where fewer than 512 terms are summed (an infinity of x or w may then give NaN for an infinite gradient:
- *   the second can be 0); every sum is fp32, in an order that the sizes alone decide.
+ *   two where fewer than 512 terms are summed (their second parts' products first, of which what is not finite is
+ *   dropped: infinities and NaN are those of the first); every sum is fp32, in an order that the sizes alone decide.
  *   bias, residual and out of x are not read.
  *   n and d_n as in gnn_gather_features: rows at or past *d_n are left as they are, and add nothing.
  *   No output may overlap an input or another output, but for out and residual.

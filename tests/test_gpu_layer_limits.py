@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from . import layers as ref
-from .test_gpu_dense import B, F, space
+from .test_gpu_dense import B, F, normal, space
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +30,72 @@ def test_activations_of_the_farthest_arguments(name, dtype):
     else:
         want, slope = torch.where(up, z, 0.0), up.to(dtype)
     assert torch.equal(out, want) and torch.equal(dx, slope)
+
+
+def signs(t):
+    return t.float().sign() * float("inf")
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", [F, B])
+@pytest.mark.parametrize("shape", [(1, 300, 40), (6, 70, 50), (20, 70, 50), (33, 1030, 72), (40, 200, 520), (300, 64, 640),
+                                   (511, 136, 257), (600, 136, 72), (600, 72, 520), (2000, 40, 300)])
+def test_an_infinite_input_or_weight(shape, dtype, bad):
+    """An infinity of x reaches its column's line of dw with the sign of dz, one of w its line's column of dx; a NaN
+    stays NaN there; all else is what it is without it.  (Sums of one and of two planes of dz, whole and split.)"""
+    n, i, o = shape
+    g = torch.Generator(device="cuda").manual_seed(n + i)
+    x, w, dout = normal(n, i, dtype=dtype, gen=g), normal(i, o, dtype=dtype, gen=g), normal(n, o, dtype=dtype, gen=g)
+    pre = normal(n, o, dtype=dtype, gen=g).abs()      # slopes above 0, of full precision
+    ws = space(gm.gnn_linear_workspace_size, n, i, o, dtype, True)
+
+    def gradients():
+        dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(o, device="cuda", dtype=dtype)
+        gm.gnn_linear_backward(x, w, dout, ws, activation="gelu", pre=pre, dx=dx, dw=dw, dbias=db)
+        return dx, dw, db
+
+    clean = gradients()
+    row, col, line, at = n // 2, i // 3, i - 1, o - 2
+    x[row, col], w[line, at] = bad, bad
+    dx, dw, db = gradients()
+    gone = torch.full((1,), float("nan"), device="cuda")
+    want_dw = signs(dout[row]) * (1 if bad > 0 else -1) if bad == bad else gone.expand(o)
+    want_dx = signs(dout[:, at]) * (1 if bad > 0 else -1) if bad == bad else gone.expand(n)
+    torch.testing.assert_close(dw[col].float(), want_dw, rtol=0, atol=0, equal_nan=True)
+    torch.testing.assert_close(dx[:, line].float(), want_dx, rtol=0, atol=0, equal_nan=True)
+    lines = torch.arange(i, device="cuda")
+    assert torch.equal(dw[lines != col], clean[1][lines != col]) and torch.equal(db, clean[2])
+    assert torch.equal(dx[:, lines != line], clean[0][:, lines != line])
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+@pytest.mark.parametrize("n, i, o, count", [(12, 70, 50, 12), (5, 300, 136, 4), (70, 300, 130, 65), (300, 520, 250, 300),
+                                            (700, 200, 328, 300), (700, 64, 96, 700), (2500, 136, 200, 511)])
+def test_an_infinite_input_or_weight_of_a_pair(n, i, o, count, dtype):
+    """The same of the gated pair, whose dx sums both projections' planes, under a device count."""
+    g = torch.Generator(device="cuda").manual_seed(n + i + 1)
+    x, dout, up = (normal(n, c, dtype=dtype, gen=g) for c in (i, o, o))
+    wg, wu = (normal(i, o, dtype=dtype, gen=g) for _ in range(2))
+    gate = 0.1 + normal(n, o, dtype=dtype, gen=g).abs()      # act and its slope above 0
+    d_n = torch.tensor([count], device="cuda")
+    ws = space(gm.gnn_gated_linear_workspace_size, n, i, o, dtype, True)
+
+    def gradients():
+        dx, dwg, dwu = torch.zeros_like(x), torch.empty_like(wg), torch.empty_like(wu)
+        gm.gnn_gated_linear_backward(x, wg, wu, gate, up, dout, ws, activation="gelu_tanh", dx=dx, dw_gate=dwg,
+                                     dw_up=dwu, d_n=d_n)
+        return dx[:count], dwg, dwu
+
+    clean = gradients()
+    row, col, first, second = count // 2, i // 3, i - 1, i // 2
+    x[row, col], wg[first, 3], wu[second, o - 1] = float("inf"), float("inf"), -float("inf")
+    dx, dwg, dwu = gradients()
+    assert torch.equal(dwg[col].float(), signs(dout[row].float() * up[row].float()))
+    assert torch.equal(dwu[col].float(), signs(dout[row]))
+    assert torch.equal(dx[:, first].float(), signs(dout[:count, 3].float() * up[:count, 3].float()))
+    assert torch.equal(dx[:, second].float(), -signs(dout[:count, o - 1]))
+    lines = torch.arange(i, device="cuda")
+    for a, b in zip((dwg, dwu), clean[1:]):
+        assert torch.equal(a[lines != col], b[lines != col])
+    keep = (lines != first) & (lines != second)
+    assert torch.equal(dx[:, keep], clean[0][:, keep])
