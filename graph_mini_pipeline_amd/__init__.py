@@ -1038,6 +1038,7 @@ def _layer_size(layer, call, n, d_in, d_out, dtype, backward):
 
 
 def gnn_linear_workspace_size(n: int, d_in: int, d_out: int, dtype, backward: bool = False) -> int:
+    """Bytes of ws for gnn_linear (or its backward pass) over up to n rows."""
     return _layer_size(_abi.gnn_dense, "gnn_linear_workspace_size", n, d_in, d_out, dtype, backward)
 
 
@@ -1075,6 +1076,7 @@ def gnn_linear_backward(x: torch.Tensor, w: torch.Tensor, dout: torch.Tensor, ws
 
 
 def gnn_gated_linear_workspace_size(n: int, d_in: int, d_out: int, dtype, backward: bool = False) -> int:
+    """Bytes of ws for gnn_gated_linear (or its backward pass) over up to n rows."""
     return _layer_size(_abi.gnn_gated, "gnn_gated_linear_workspace_size", n, d_in, d_out, dtype, backward)
 
 

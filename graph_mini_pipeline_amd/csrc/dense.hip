@@ -143,7 +143,11 @@ constexpr TileCost kCostF32[4] = {{0, 0, 0, 0}, {2.05, 5, 2.0, 4}, {0.56, 1.8, 0
 constexpr double kJoinLaunch = 3.0, kGradJoinLaunch = 4.0;
 double join_us(int64_t parts, double elements) { return kJoinLaunch + static_cast<double>(parts) * elements * (8e-6 / 3.0); }
 
-constexpr double kMostJoined = 1e9;        // sums of a product that is joined (they are counted in 32 bits)
+// The parts of a product take at most what 2048 tiles of 128 x 128 do, half of what the card's last cache holds: a
+// workspace serves every smaller batch, so each large layer's has room for that much.  (Tiles of 256 alone could take
+// more, up to 0.5 GB, for deep sums: 8782 x 16384 x 4096 bf16 1143 us by parts of 288 MB, 1193 without; of 200000 drawn
+// shapes 95 forward plans lose over 3% by the time model, gradients none.)
+constexpr int64_t kMostPartBytes = int64_t(128) << 20;
 
 constexpr int kSplitChoices = 12;
 constexpr int64_t kSplits[kSplitChoices] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
@@ -156,21 +160,49 @@ struct Split {
     bool sensible;
 };
 
+int64_t steps_of(const Shape &s, int type) {
+    const int bk = type == GNN_BF16 ? 64 : 32;
+    return (s.k + bk - 1) / bk * s.segs;
+}
+
+// Bytes of the parts for each row.
+int64_t part_row_bytes(const Shape &s, bool pair, int64_t parts) { return 4 * parts * s.products * (pair ? 2 : 1) * round_up(s.cols, 4); }
+
+// Up to how many rows so many parts are sensible.
+int64_t split_rows(const Shape &s, int tile, bool pair, int64_t parts) {
+    const int64_t tc = tile_cols(tile, pair), across = (s.cols + tc - 1) / tc * s.products * parts;
+    const int64_t filled = 8 * kCus / across * tile_rows(tile), held = kMostPartBytes / part_row_bytes(s, pair, parts);
+    return filled < held ? filled : held;
+}
+
 Split split_cost(const Shape &s, int type, int tile, bool pair, int64_t parts) {
     const TileCost &c = type == GNN_BF16 ? kCostBf16[tile] : kCostF32[tile];
-    const int bk = type == GNN_BF16 ? 64 : 32;
     const int64_t tr = tile_rows(tile), tc = tile_cols(tile, pair);
     const int64_t tiles = ((s.rows + tr - 1) / tr) * ((s.cols + tc - 1) / tc) * s.products;
-    const int64_t steps = (s.k + bk - 1) / bk * s.segs;
+    const int64_t steps = steps_of(s, type);
     const double elements = static_cast<double>(s.rows) * s.cols * s.products * (pair ? 2 : 1);
     Split r;
-    r.sensible = parts == 1 || (parts <= steps && tiles * parts <= 8 * kCus && elements <= kMostJoined);
+    r.sensible = parts == 1 || (parts <= steps && s.rows <= split_rows(s, tile, pair, parts));
     r.groups = static_cast<double>(tiles * parts);
     r.each = static_cast<double>((steps + parts - 1) / parts);
     r.chain = r.each * c.alone + c.fixed;
     r.work = r.groups * (r.each * c.step + c.busy);
     r.join = parts > 1 ? join_us(parts, elements) : 0.0;
     return r;
+}
+
+// Bytes of the parts at most, of a product of up to s.rows rows; kGradW: of s.rows rows, and up to s.k summed ones.
+int64_t most_part_bytes(const Shape &s, int type, int tile, bool pair) {
+    int64_t most = 0;
+    for (const int64_t parts : kSplits) {
+        if (parts > steps_of(s, type)) break;
+        int64_t rows = split_rows(s, tile, pair, parts);
+        if (rows > s.rows) rows = s.rows;
+        if (parts == 1 || (s.form == kGradW && rows < s.rows)) continue;
+        const int64_t bytes = rows * part_row_bytes(s, pair, parts);
+        if (bytes > most) most = bytes;
+    }
+    return most;
 }
 
 struct ForwardPlan {
@@ -180,17 +212,23 @@ struct ForwardPlan {
     bool joined;
 };
 
+constexpr int64_t kFewestRows = 64;       // up to which tiles of 32 rows are looked at
+
+// Tiles of 64 and 32 take a gated pair as two products, whose sums are joined even where they are in one part.
+bool is_apart(const DenseArgs &a, int tile) { return a.pair && tile > kTile128; }
+Shape forward_shape(const DenseArgs &a, int tile) { return {kForward, a.n, a.d_out, a.d_in, 1, is_apart(a, tile) ? 2 : 1}; }
+
 ForwardPlan plan_forward(const DenseArgs &a) {
     ForwardPlan best{};
     double least = 1e30;
     for (int tile = a.type == GNN_BF16 ? kTile256 : kTile128; tile <= kTile32; ++tile) {
-        if (tile == kTile32 && a.n > 64) continue;
+        if (tile == kTile32 && a.n > kFewestRows) continue;
         const TileCost &c = a.type == GNN_BF16 ? kCostBf16[tile] : kCostF32[tile];
-        // small tiles take a gated pair as two products, whose sums are joined
-        const bool pair = a.pair && tile <= kTile128, apart = a.pair && !pair;
-        if (apart && static_cast<double>(a.n) * a.d_out > kMostJoined / 2) continue;
+        const bool apart = is_apart(a, tile), pair = a.pair && !apart;
+        const Shape shape = forward_shape(a, tile);
+        if (apart && a.n * part_row_bytes(shape, false, 1) > kMostPartBytes) continue;
         for (const int64_t parts : kSplits) {
-            const Split s = split_cost({kForward, a.n, a.d_out, a.d_in, 1, apart ? 2 : 1}, a.type, tile, pair, parts);
+            const Split s = split_cost(shape, a.type, tile, pair, parts);
             if (!s.sensible) break;
             // the last round of workgroups may leave compute units idle
             const double rounds = static_cast<double>((static_cast<int64_t>(s.groups) + kCus - 1) / kCus);
@@ -204,6 +242,24 @@ ForwardPlan plan_forward(const DenseArgs &a) {
         }
     }
     return best;
+}
+
+// What the parts of a call of up to a.n rows take.
+int64_t most_forward_bytes(DenseArgs a) {
+    int64_t most = 0;
+    for (int tile = a.type == GNN_BF16 ? kTile256 : kTile128; tile <= kTile32; ++tile) {
+        if (tile == kTile32 && a.n > kFewestRows) a.n = kFewestRows;
+        const bool apart = is_apart(a, tile);
+        const Shape shape = forward_shape(a, tile);
+        int64_t bytes = most_part_bytes(shape, a.type, tile, a.pair && !apart);
+        if (apart) {
+            const int64_t each = part_row_bytes(shape, false, 1), rows = kMostPartBytes / each;
+            const int64_t whole = (a.n < rows ? a.n : rows) * each;
+            if (whole > bytes) bytes = whole;
+        }
+        if (bytes > most) most = bytes;
+    }
+    return most;
 }
 
 struct GradientPlan {
@@ -245,9 +301,6 @@ GradientPlan plan_gradients(const Shape &w, const Shape &x, int type, bool few) 
     }
     return best;
 }
-
-// Floats of the parts of a product.
-int64_t part_floats(int64_t parts, const Shape &s) { return parts * s.products * s.rows * round_up(s.cols, 4); }
 
 // Only pieces fill the largest tile.
 int filled_tile(int tile, int load) { return tile == kTile256 && load != kByPiece ? kTile128 : tile; }
@@ -373,7 +426,8 @@ struct DenseSpace {
     size_t bytes;
 };
 
-DenseSpace carve_dense(const DenseArgs &a, char *ws) {
+// most: as large as any call of up to a.n rows needs it.
+DenseSpace carve_dense(const DenseArgs &a, char *ws, bool most = false) {
     DenseSpace s{};
     const int mats = a.pair ? 2 : 1;
     const bool bf = a.type == GNN_BF16;
@@ -384,7 +438,15 @@ DenseSpace carve_dense(const DenseArgs &a, char *ws) {
     s.w = {kGradW, a.d_in, a.d_out, a.n, 1, mats};
     s.x = {kGradX, a.n, a.d_in, a.d_out, s.wide ? 2 * mats : mats, 1};
     s.few = a.n > 0 && a.n <= kFewRows && a.d_out >= 16 / size;
-    s.plan = plan_gradients(s.w, s.x, a.type, s.few);
+    if (!most) s.plan = plan_gradients(s.w, s.x, a.type, s.few);
+    const auto parts_of = [&](const Shape &shape, int64_t parts) {
+        int64_t bytes = parts > 1 ? shape.rows * part_row_bytes(shape, false, parts) : 0;
+        for (int tile = bf ? kTile256 : kTile128; most && tile <= kTile64; ++tile) {
+            const int64_t by_tile = most_part_bytes(shape, a.type, tile, false);
+            if (by_tile > bytes) bytes = by_tile;
+        }
+        return bytes;
+    };
     size_t at = 0;
     const auto take = [&](char **p, int64_t bytes) {
         *p = ws + at;
@@ -393,8 +455,8 @@ DenseSpace carve_dense(const DenseArgs &a, char *ws) {
     take(&s.dz, a.n * s.ld_dz * size);
     take(&s.rest, !bf ? 0 : (s.wide || a.n < kShortSum ? a.n : kShortSum) * s.ld_dz * size);
     take(&s.sums, static_cast<int64_t>(slope_parts(a.n, a.d_out, a.type)) * s.ld_dz * 4);
-    take(&s.w_part, s.plan.w_parts > 1 ? 4 * part_floats(s.plan.w_parts, s.w) : 0);
-    take(&s.x_part, s.plan.x_parts > 1 ? 4 * part_floats(s.plan.x_parts, s.x) : 0);
+    take(&s.w_part, parts_of(s.w, s.plan.w_parts));
+    take(&s.x_part, parts_of(s.x, s.plan.x_parts));
     s.bytes = at;
     return s;
 }
@@ -423,9 +485,7 @@ hipError_t launch_column_sums(const float *sums, int64_t ld, int parts, int64_t 
 }
 
 size_t dense_bytes(const DenseArgs &a, bool backward) {
-    if (backward) return carve_dense(a, nullptr).bytes;
-    const ForwardPlan p = plan_forward(a);
-    return 256 + (p.joined ? static_cast<size_t>(4 * part_floats(p.parts, {kForward, a.n, a.d_out, a.d_in, 1, a.pair ? 2 : 1})) : 0);
+    return backward ? carve_dense(a, nullptr, true).bytes : 256 + static_cast<size_t>(most_forward_bytes(a));
 }
 
 hipError_t launch_dense(const DenseArgs &a, hipStream_t s) {

@@ -194,7 +194,7 @@ struct DenseArgs {
     void *dbias[2];
     char *ws;
 };
-// Bytes of workspace for type, pair, n, d_in, d_out, whatever the activation and the rows' alignment.
+// Bytes of workspace for type, pair, up to n rows, d_in, d_out, whatever the activation and the rows' alignment.
 size_t dense_bytes(const DenseArgs &a, bool backward);
 hipError_t launch_dense(const DenseArgs &a, hipStream_t s);
 hipError_t launch_dense_backward(const DenseArgs &a, hipStream_t s);

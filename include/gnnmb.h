@@ -710,7 +710,7 @@ gnn_status gnn_layer_norm_backward(const gnn_norm *x, const gnn_norm_grad *g, vo
  *   n and d_n as in gnn_gather_features: rows at or past *d_n are left as they are, and add nothing.
  *   No output may overlap an input or another output, but for out and residual.
  *   ws: 16-byte aligned, ws_bytes >= gnn_linear_workspace_size(x, backward); x->type, n, d_in and d_out
- *   decide it.
+ *   decide it, and it is enough for every smaller n too.
  * Errors: GNN_ERR_INVALID_ARG; GNN_ERR_CAPACITY (ws too small); GNN_ERR_UNSUPPORTED for another type or
  * activation, n over 2^30, d_in or d_out over 2^20, or rows over 2^21 elements apart.
  */

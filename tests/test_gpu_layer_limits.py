@@ -99,3 +99,24 @@ def test_an_infinite_input_or_weight_of_a_pair(n, i, o, count, dtype):
         assert torch.equal(a[lines != col], b[lines != col])
     keep = (lines != first) & (lines != second)
     assert torch.equal(dx[:, keep], clean[0][:, keep])
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+def test_a_workspace_of_the_largest_batch_serves_smaller_ones(dtype):
+    """One workspace, sized once, for a batch that shrinks to a row; results as with a workspace of their own."""
+    i, o, most = 520, 1032, 1100
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, w, wu, dout = (normal(*s, dtype=dtype, gen=g) for s in ((most, i), (i, o), (i, o), (most, o)))
+    calls = (gm.gnn_linear_workspace_size, gm.gnn_gated_linear_workspace_size)
+    shared = [space(c, most, i, o, dtype, b) for c in calls for b in (False, True)]
+    for n in (1100, 1000, 768, 500, 200, 64, 8, 1, 0):
+        results = []
+        for ws in (shared, [space(c, n, i, o, dtype, b) for c in calls for b in (False, True)]):
+            out, gate, up, y = torch.empty(4, n, o, device="cuda", dtype=dtype)
+            dx, dw, dx2, dwg, dwu = (torch.empty(s, device="cuda", dtype=dtype) for s in ((n, i), (i, o), (n, i), (i, o), (i, o)))
+            gm.gnn_linear(x[:n], w, y, ws[0])
+            gm.gnn_linear_backward(x[:n], w, dout[:n], ws[1], dx=dx, dw=dw)
+            gm.gnn_gated_linear(x[:n], w, wu, out, ws[2], gate=gate, up=up)
+            gm.gnn_gated_linear_backward(x[:n], w, wu, gate, up, dout[:n], ws[3], dx=dx2, dw_gate=dwg, dw_up=dwu)
+            results.append((out, gate, up, y, dx, dw, dx2, dwg, dwu))
+        assert all(torch.equal(a, b) for a, b in zip(*results)), n
