@@ -32,6 +32,7 @@
 #pragma once
 
 #include "learn.hpp"
+#include "parts.hpp"
 
 namespace gnnmb {
 
@@ -524,17 +525,12 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, int64_t q, ch
 
     const int64_t seg_tiles = (k + kBk - 1) / kBk;
     const int segs = k < kShortSum ? p.short_segs : p.segs, first_seg = p.short_segs - segs;
-    int64_t lo = 0, steps64 = seg_tiles * segs;
-    if (p.splits > 1) {
-        const int64_t share = (steps64 + p.splits - 1) / p.splits;
-        lo = split * share < steps64 ? split * share : steps64;
-        steps64 = steps64 - lo < share ? steps64 - lo : share;
-    }
-    const int steps = static_cast<int>(steps64);
+    const SumPart part = part_of_sum(seg_tiles, segs, p.splits, split);
+    const int steps = static_cast<int>(part.steps);
     // Segment and summed index of the next tile to load, and where its loads start (scalars: a look at the
     // arguments for every tile costs 0.1 us of waiting).
-    int seg = first_seg + (seg_tiles > 0 ? static_cast<int>(lo / seg_tiles) : 0);
-    int64_t k0 = (lo - (seg - first_seg) * seg_tiles) * kBk;
+    int seg = first_seg + part.seg;
+    int64_t k0 = part.tile * kBk;
     const int64_t step_a = A::advance(p.ld_a), step_b = B::advance(p.ld_b);
     const char *from_a, *from_b0, *from_b1;
     const auto place = [&] {
@@ -622,7 +618,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, int64_t q, ch
     // gradient's: infinity minus infinity would follow.  What of their sums is not finite is dropped, and the first
     // plane gives the infinity or the NaN alone.  drop_at: how many tiles follow the last of them.
     constexpr bool kPlanes = sizeof(T) == 2 && FORM != kForward;
-    const int64_t rest64 = (p.rest - first_seg) * seg_tiles - lo;
+    const int64_t rest64 = (p.rest - first_seg) * seg_tiles - part.first;
     const int drop_at = steps - static_cast<int>(rest64 < 0 ? 0 : rest64 < steps ? rest64 : steps);
     const auto drop = [&](int after) {
         if (!kPlanes || after != drop_at) return;
