@@ -120,3 +120,64 @@ def test_a_workspace_of_the_largest_batch_serves_smaller_ones(dtype):
             gm.gnn_gated_linear_backward(x[:n], w, wu, gate, up, dout[:n], ws[3], dx=dx2, dw_gate=dwg, dw_up=dwu)
             results.append((out, gate, up, y, dx, dw, dx2, dwg, dwu))
         assert all(torch.equal(a, b) for a, b in zip(*results)), n
+
+
+def offset_bounds(x, eps):
+    """(out, its bound, rstd, its bound) of fp32 rows far from zero, without parameters.  A row's mean is off by em at
+    first; the differences from it are exact (numbers within a factor of two of each other), their own mean puts it
+    right, so that what is left of the error is that sum's, of the differences' size."""
+    u, rows = ref.U, ref.ROW
+    m = x.mean(1, keepdim=True)
+    c = x - m
+    em = rows * u * x.abs().mean(1, keepdim=True)
+    ec = (rows + 4) * u * (c.abs().mean(1, keepdim=True) + em) + 2 * u * (c.abs() + em)
+    v = (c * c).mean(1, keepdim=True)
+    ev = (rows + 8) * u * (v + em * em) + 2 * em * (rows + 4) * u * (c.abs().mean(1, keepdim=True) + em)
+    r = (v + eps) ** -0.5
+    er = r * (0.5 * ev / (v + eps) + 4 * u)
+    y = c * r
+    return y, (ec * (r + er) + c.abs() * er + 3 * u * y.abs()) * (1 + u), r[:, 0], er[:, 0]
+
+
+@pytest.mark.parametrize("value", [0.1, -1000.1, 12345.678, 3.0e7])
+@pytest.mark.parametrize("d", [3, 7, 100, 300, 768, 1000, 1025, 4095, 5000, 16383])
+def test_rows_of_one_value(d, value):
+    """Whatever the value and the width, its mean is the value, and the row's result is the bias."""
+    x = torch.full((9, d), value, device="cuda")
+    b = torch.randn(d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    out, mean, rstd = torch.empty_like(x), *torch.empty(2, 9, device="cuda")
+    gm.gnn_layer_norm(x, None, b, 1e-5, out, mean=mean, rstd=rstd)
+    y, ey, r, er = offset_bounds(x.double(), 1e-5)
+    assert torch.equal(mean, x[:, 0])
+    ref.close(out, (b.double().expand_as(x), ey + ref.U * (b.double().abs() + ey)))
+    ref.close(rstd, (r, er))
+    assert float((out - b).abs().max()) < 1e-4
+
+
+@pytest.mark.parametrize("d", [64, 100, 768, 2500, 5000, 16384])
+@pytest.mark.parametrize("shift, scale", [(1000.0, 0.01), (-3.0e4, 1.0), (0.0, 1.0)])
+def test_rows_far_from_zero(d, shift, scale):
+    """What the mean's own rounding takes from rows far from zero is given back."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = normal(33, d, dtype=F, gen=g, scale=scale) + shift
+    out, mean, rstd = torch.empty_like(x), *torch.empty(2, 33, device="cuda")
+    gm.gnn_layer_norm(x, None, None, 0.0, out, mean=mean, rstd=rstd)
+    y, ey, r, er = offset_bounds(x.double(), 0.0)
+    if shift:
+        ref.close(out, (y, ey), "out")
+        ref.close(rstd, (r, er), "rstd")
+        exact = x.double().mean(1)
+        ref.close(mean, (exact, ref.U * exact.abs() + ey.mean(1) / r), "mean")
+    else:      # differences from a mean near zero are rounded
+        want = ref.norm(x.double(), None, None, 0.0, F)
+        for got, bound in zip((out, mean, rstd), want):
+            ref.close(got, bound)
+
+
+def test_the_mean_of_a_row_that_is_not_finite():
+    x = torch.ones(4, 200, device="cuda")
+    x[0, 3], x[1, 4], x[2, 5] = float("inf"), -float("inf"), float("nan")
+    out, mean, rstd = torch.empty_like(x), *torch.empty(2, 4, device="cuda")
+    gm.gnn_layer_norm(x, None, None, 1e-5, out, mean=mean, rstd=rstd)
+    assert mean[0] == float("inf") and mean[1] == -float("inf") and torch.isnan(mean[2]) and mean[3] == 1
+    assert torch.isnan(out[:3]).all() and torch.isnan(rstd[:3]).all() and (out[3] == 0).all()
