@@ -94,3 +94,23 @@ def test_infinities_in_large_tiles(shape, count, dtype):
     lines = torch.arange(i, device="cuda")
     assert torch.equal(dw[lines != col], clean[1][lines != col])
     assert torch.equal(dx[:, lines != line], clean[0][:, lines != line])
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+@pytest.mark.parametrize("n, i, o, count", [(4096, 768, 1024, 4096), (9000, 256, 2048, 9000), (9000, 256, 2048, 7001),
+                                            (2048, 2048, 2048, 1939), (4099, 1030, 1026, 4099), (4097, 1031, 4097, 4001)])
+@pytest.mark.parametrize("name", ["none", "gelu"])
+def test_out_over_the_residual_in_large_tiles(n, i, o, count, name, dtype):
+    """out is the residual itself where rows of it are loaded ahead of the rows that are stored, and where the last
+    rows end inside a wavefront's 32; rows that do not count keep what they hold."""
+    g = torch.Generator(device="cuda").manual_seed(n + count)
+    x, w, r = normal(n, i, dtype=dtype, gen=g), normal(i, o, dtype=dtype, gen=g, scale=i ** -0.5), \
+        normal(n, o, dtype=dtype, gen=g)
+    b = normal(o, dtype=dtype, gen=g)
+    ws, d_n = space(gm.gnn_linear_workspace_size, n, i, o, dtype), torch.tensor([count], device="cuda")
+    over, apart = r.clone(), r.clone()
+    gm.gnn_linear(x, w, over, ws, bias=b, activation=name, residual=over, d_n=d_n)
+    gm.gnn_linear(x, w, apart, ws, bias=b, activation=name, residual=r, d_n=d_n)
+    assert torch.equal(over, apart) and torch.equal(over[count:], r[count:])
+    y, ey, _, _ = ref.linear(d64(x[:count]), d64(w), d64(b), name, d64(r[:count]), dtype)
+    ref.close(over[:count], (y, ey))
