@@ -114,3 +114,12 @@ def test_out_over_the_residual_in_large_tiles(n, i, o, count, name, dtype):
     assert torch.equal(over, apart) and torch.equal(over[count:], r[count:])
     y, ey, _, _ = ref.linear(d64(x[:count]), d64(w), d64(b), name, d64(r[:count]), dtype)
     ref.close(over[:count], (y, ey))
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+@pytest.mark.parametrize("shape", [(4, 4098, 4098), (1, 2050, 1030), (4, 4097, 4099), (1, 2048, 1032), (17, 4098, 4102)])
+def test_wide_layers_of_a_few_rows(shape, dtype):
+    """Tiles of 32 rows by each way, their sums split."""
+    g = torch.Generator(device="cuda").manual_seed(sum(shape))
+    linear_case(*shape, dtype, "gelu_tanh", g)
+    gated_case(*shape, dtype, "silu", g)
