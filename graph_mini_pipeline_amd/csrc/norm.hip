@@ -5,7 +5,9 @@
 // difference of two means loses all digits where m is large) and x is read once.  m as it is first summed is off by
 // some roundings of the row's size: with it alone a row of 768 times 12345.678 had results of 0.3 for 0.  The
 // differences, exact where m is large beside them, have the mean c = sum (x - m) / d by which m is put right:
-//   y = (x - m - c) r w + b,  v = sum (x - m)^2 / d - c^2,  and m + c is the mean.
+//   y = (x - m - c) r w + b,  v = sum (x - m)^2 / d - c^2,  and m + c is the mean,
+// where m^2 > 4 v; of smaller means the differences' roundings are the larger ones (32768 x 4096 bf16 with means of a
+// fiftieth of their spread: these are 4e-8 off, 9e-7 if they were put right, too), and c is 0.
 // (180224 x 100 fp32 19.8 us for 19.1, 32768 x 4096 bf16 110.1 for 109.6, 8192 x 8192 50.5 for 48.0.)
 // Backward, with g = dy w and h = (x - m) r:
 //   dx = r (g - sum g / d - h sum (g h) / d) (+ dres),  dw = sum over rows of dy h,  db = of dy.
@@ -16,11 +18,11 @@
 // elements a lane has at most two pieces of a row and takes two rows at a time: few enough registers for
 // the loads of several workgroups to be under way on a compute unit.
 //
-// What bounds it: memory.  32768 x 4096 bf16: forward 104 us (5.1 TB/s), backward with a residual gradient
-// 210 (5.1 TB/s), its columns' join 5; 180224 x 100 fp32 to bf16: 23, 40 and 5.  (One wavefront a row with eight
+// What bounds it: memory.  32768 x 4096 bf16: forward 106 us (5.1 TB/s), backward with a residual gradient
+// 212 (5.2 TB/s), its columns' join 5; 180224 x 100 fp32 to bf16: 25, 40 and 5.  (One wavefront a row with eight
 // pieces a lane took 214 us forward, rows kept in fp32 between the passes 316 backward.)  Rows over 8192 elements
-// fill the registers of a compute unit one at a time, and the backward pass spills some: 8000 x 16384 both
-// ways 3.8 TB/s in fp32, 2.8 in bf16.  A single row of 4096: 4 us, launch and four dependent turns.
+// fill the registers of a compute unit one at a time, and the backward pass spills half of a lane's 128 (132 to 184 bytes of
+// scratch): 8000 x 16384 3.4 TB/s in fp32, 2.6 in bf16.  A single row of 4096: 4 us, launch and four dependent turns.
 #include <type_traits>
 
 #include "learn.hpp"
@@ -170,13 +172,13 @@ __global__ __launch_bounds__(G > kNormThreads ? G : kNormThreads) void k_norm(No
         for (int r = 0; r < R; ++r) {
             const int64_t m = m0 + r * step;
             if (m >= n) break;
-            const float c = e[2 * r] / d;
-            float v = e[2 * r + 1] * inv_d - c * c;
+            float v = e[2 * r + 1] * inv_d;
+            const float c = mean[r] * mean[r] > 4.f * v ? e[2 * r] / d : 0.f;
+            v -= c * c;
             if (v < 0.f) v = 0.f;                     // (a NaN stays)
             const float rstd = 1.f / sqrtf(v + p.eps);
             if (l == 0) {
-                // (an infinite mean has no c)
-                if (p.mean) p.mean[m] = __builtin_fabsf(c) < __builtin_inff() ? mean[r] + c : mean[r];
+                if (p.mean) p.mean[m] = mean[r] + c;
                 if (p.rstd) p.rstd[m] = rstd;
             }
             TO *out = static_cast<TO *>(p.out) + m * p.ld_out;
@@ -326,8 +328,9 @@ int64_t row_blocks(int64_t n, int g, int r, int64_t most) {
     return blocks < 1 ? 1 : blocks;
 }
 
-// Workgroups of the backward pass: as many as keep memory busy, and no more than their partial sums are
-// worth.
+// Workgroups of the backward pass: one for each turn of its rows, up to as many as keep memory busy.  Each leaves 8 d
+// bytes of sums, a small part of what thousands of rows take; of some hundred wide rows, it is as much again as the
+// rows themselves (512 x 16384 bf16 53 us, 1 TB/s of x, dout and dx, where 8000 rows run at 2.6).
 int64_t backward_blocks(int64_t n, int64_t d) {
     int64_t blocks = 0;
     (void)by_width(d, [&](auto g, auto, auto r, auto) {

@@ -181,3 +181,15 @@ def test_the_mean_of_a_row_that_is_not_finite():
     gm.gnn_layer_norm(x, None, None, 1e-5, out, mean=mean, rstd=rstd)
     assert mean[0] == float("inf") and mean[1] == -float("inf") and torch.isnan(mean[2]) and mean[3] == 1
     assert torch.isnan(out[:3]).all() and torch.isnan(rstd[:3]).all() and (out[3] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F, B])
+def test_small_means_keep_their_digits(dtype):
+    """Rows spread around zero whose sums are exact: multiples of 2^-10 below 8, of which 4000 add up below 2^24 of them
+    in any order.  The mean is their quotient, which the differences' own roundings must not get into."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = normal(500, 4000, dtype=F, gen=g).clamp(-7, 7) + 0.02 * normal(500, 1, dtype=F, gen=g)
+    x = ((x * 1024).round() / 1024).to(dtype)
+    out, mean, rstd = torch.empty_like(x), *torch.empty(2, 500, device="cuda")
+    gm.gnn_layer_norm(x, None, None, 1e-5, out, mean=mean, rstd=rstd)
+    assert torch.equal(mean, (x.double().sum(1) / 4000).float())
