@@ -4,7 +4,7 @@
 // Forward is one product with its epilogue (dense.hpp); a gated layer's two products share the tiles of x
 // and meet in the epilogue's registers.  Backward, with z kept by the forward pass:
 //   dz = dy act'(z)                 (k_slopes; gated: dg = dy u act'(g), du = dy act(g))
-//   db = the sums of dz's columns   (partial sums by k_slopes, k_column_sums)
+//   db = the sums of dz's columns   (partial sums by k_slopes, joined by the last workgroups of k_gradients)
 //   dx = dz W^T, dW = x^T dz        (gated: dx = dg Wg^T + du Wu^T in one product over two segments)
 // Without an activation dz is dy itself.
 //
@@ -105,8 +105,6 @@ uint32_t join_blocks(const ProductArgs &a, bool pair, int32_t *lanes_log2) {
 }
 
 // ---- planning ------------------------------------------------------------------------------------------
-
-bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // The largest unit (16, 4 or 2 bytes) that all operands' lines are multiples of, as the way of their tiles
 // into LDS.
