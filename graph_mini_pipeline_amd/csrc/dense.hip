@@ -14,14 +14,16 @@
 // fewer than kShortSum terms takes dz in two planes, its bf16 and the bf16 of what that leaves (1.7e-3).  No
 // atomic touches a sum: the parts of a split sum are added in their order.
 //
-// What it takes (us; floor at 4.9 TB/s, 1199 TFLOP/s in bf16 and 154 in fp32 in brackets):
-//   16384 x 4096 x 4096 bf16 with a residual 481 (458), gated 16384 x 4096 x 10240 with both sums kept 2298
-//   (2293): the matrix units, at the rate of a large library product.
-//   Gradients of 16384 x 1024 x 4096 bf16 with gelu 317 (229): dz 74 at 5.4 TB/s, products 225, join 10; gated
-//   8192 x 2048 x 5632 756 (630): dz 79 at 5.8 TB/s, products 675.
-//   One row, 4096 x 4096 bf16 13.5 (6.9): two launches, W at 3.3 TB/s.  Four rows, gated 4096 x 10240 35.6 (34.3).
-//   333 x 1030 x 2571 fp32 30.7 (11.5): a tile each for 246 compute units, loads by words; gradients of 16384 x 256 x 128 fp32 43.5 (13.9) and gated 77 x 515 x 1371 fp32 27.7 (2.8): three
-//   launches of a few dependent turns each.
+// What it takes (us a call among others; in brackets the time at 5.4 TB/s, 1360 TFLOP/s in bf16 and 153 in fp32, which a
+// copy of 512 MiB and the library's products of 8192 squares reach on the same card):
+//   16384 x 4096 x 4096 bf16 with a residual 483 (404; the library's product alone 424), gated 16384 x 4096 x 10240 with
+//   both sums kept 2316 (2021; the library's product of both weights alone 2077): the matrix units.
+//   Gradients of 16384 x 1024 x 4096 bf16 with gelu 319 (202): dz 71, products 237, join 9; gated 8192 x 2048 x 5632
+//   743 (556), of it dz 77.
+//   One row, 4096 x 4096 bf16 13.5 (6.3): two launches, W at 3.4 TB/s.  Four rows, gated 4096 x 10240 36.0 (31.4).
+//   333 x 1030 x 2571 fp32 with gelu and a residual 30.8 (11.5): a tile each for 246 compute units, loads by words;
+//   gradients of 16384 x 256 x 128 fp32 43.2 (14.0) and gated 77 x 515 x 1371 fp32 27.6 (2.8): three launches of a few
+//   dependent turns each.
 // (Without matrix instructions, W read straight into registers by strips of columns over the whole summed length: one
 // row of 4096 x 4096 13.5 us too, of 4096 x 10240 33 for 25, four rows 29 for 15; it was left.)
 #include "dense.hpp"

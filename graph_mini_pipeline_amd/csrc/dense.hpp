@@ -26,9 +26,9 @@
 //
 // While the products of one tile run, those of the next NB - 1 are under way.  A barrier comes before the last of a
 // tile's four steps, whose operands are in registers by then: the first reads of the next tile hide behind it.
-// 4096 squares in bf16: 1170 TFLOP/s by tiles of 256 (eight wavefronts of 128 x 64), 850 by 128, 640 by 64; fp32
-// 144 by 128 (a library product reaches 1199 and 154 at 8192); LDS has no bank conflicts in any order
-// of operands (SQ_LDS_BANK_CONFLICT 0).
+// 4096 squares in bf16: 1235 TFLOP/s by tiles of 256 (eight wavefronts of 128 x 64), where tiles of 128 reach 0.73 of
+// that and of 64 0.55; fp32 143 by 128 (the library's products: 1371 and 150).  LDS has no bank conflicts in any order
+// of operands (SQ_LDS_BANK_CONFLICT 0 for each kernel of profiles/layers_counters.txt).
 #pragma once
 
 #include "learn.hpp"
@@ -761,9 +761,8 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, int64_t q, ch
     }
     if (FORM == kForward && sizeof(T) == 2 && FR * FC > 1 && c0 + kPlaces * WC * 32 <= p.cols) {
         // All columns exist, and wavefronts hold many sums: biases are loaded once, a residual's rows a row ahead.
-        // (8192 x 1024 x 4096 bf16 with a bias 98 us, 110 where each is loaded where it is added; 16384 x 4096 x 4096
-        // with a residual 493 and 502.  fp32 and small tiles lose 5 to 8% to the registers: 333 x 1030 x 2571 fp32 37.7
-        // us for 35.0.)
+        // (Where each is loaded where it is added, 8192 x 1024 x 4096 bf16 with a bias takes 12% longer and 16384 x 4096 x
+        // 4096 with a residual 2%.  fp32 and small tiles lose 5 to 8% to the registers.)
         typedef vec<T, 16> Raw;
         typedef typename loose<T, 16>::type Loose;
         const auto load = [](const void *from, int64_t at) -> Raw { return *reinterpret_cast<const Loose *>(static_cast<const T *>(from) + at); };
@@ -850,7 +849,7 @@ __device__ __forceinline__ void column_sums(const ColumnArgs &p, uint32_t block,
 // dW = x^T dz for up to kFewRows rows.  A lane holds its 16 bytes' columns of every row of dz (both planes of it,
 // added), a wavefront writes kOuterHigh lines of dW; x comes from LDS.  What bounds it is the writing.  All gradients
 // of 4 rows of 4096 x 4096 bf16 with gelu take 28 us, 52 where tiles of the matrix units are filled, cut and emptied
-// for dW; of one row of 7168 x 6464 fp32 88 and 168 (floor 76).
+// for dW; of one row of 7168 x 6464 fp32 88 and 168 (70 at 5.4 TB/s).
 constexpr int kOuterHigh = 16;
 
 template <typename T>
