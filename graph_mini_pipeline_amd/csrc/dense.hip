@@ -11,7 +11,8 @@
 // Numbers.  Products are summed in fp32: bf16 on the 16-bit matrix instructions, fp32 on the fp32 ones.
 // The dz of a bf16 layer is rounded to bf16 for its products, which leaves gradients 1.4 times as far from exact
 // as their own rounding does (2.3e-3 for 1.7e-3 in the 2-norm), twice as far where few terms are summed; a sum of
-// fewer than kShortSum terms takes dz in two planes, its bf16 and the bf16 of what that leaves (1.7e-3).  No
+// fewer than kShortSum terms takes dz in two planes, its bf16 and the bf16 of what that leaves (1.7e-3).  (In two planes
+// everywhere, gradients of 16384 x 1024 x 4096 take 762 us for 309, gated 8192 x 2048 x 5632 1417 for 731.)  No
 // atomic touches a sum: the parts of a split sum are added in their order.
 //
 // What it takes (us a call among others; in brackets the time at 5.4 TB/s, 1360 TFLOP/s in bf16 and 153 in fp32, which a
